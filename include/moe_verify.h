@@ -14,6 +14,12 @@
  *   moe_hot_list       hot-expert list (and home-slot table) from profiled routing
  *   s2_expand          S2-MoE utility-driven draft expansion
  *   moe_depth_policy   confidence-gated depth per sequence (ragged speculation)
+ * and, for the attention half of the same step, a paged KV cache in 4 bits:
+ *   kv4_append         quantises keys and values into the cache
+ *   kv4_read           reads them back
+ *   kv4_attend         attention of the verify tokens (tree or chain) over it
+ *   kv4_weigh          accumulates the attention weight of every cached slot
+ *   kv4_evict          brings the cache down to a budget by that weight
  *
  * Conventions shared by every entry point
  *   - Every array argument is a DEVICE pointer owned by the caller, unless a
@@ -65,6 +71,7 @@ enum {
 #define MOE_DEV_BAD_PROB  0x10  /* a path probability / confidence weight is NaN or negative    */
 #define MOE_DEV_TIMEOUT   0x20  /* a bounded device-side wait gave up                            */
 #define MOE_DEV_CAPACITY  0x40  /* a count exceeded the capacity the caller sized buffers for   */
+#define MOE_DEV_BAD_KV    0x80  /* a key or value row is not finite or beyond +-65504            */
 /* With an expert pool, an expert whose slot_of entry is outside [0, n_slots)
  * is reported by the FFN as MOE_DEV_BAD_ID; its weights are not read and the
  * outputs of the tokens routed to it are not valid. */
@@ -602,6 +609,137 @@ int moe_verify_plan(const moe_step_cfg* cfg, const float* P, const int32_t* pare
                     int32_t* perm_token, int32_t* perm_slot, int32_t* inv, float* reuse_ratio,
                     int32_t* dev_err, void* stream);
 
+/* ---------------------------------------------------------------- 4-bit KV cache
+ * A paged cache of keys and values in 4 bits for the attention of the verify
+ * step.  The pages describe its use (S2-MoE write-up, component 2: draft and
+ * target share one KV cache, temporary entries are rolled back and accepted
+ * ones committed); the format is this library's.
+ *
+ * Entry: the D values x of one slot, kv head and K or V are held as
+ *   scale  = fp16(fp32((max x - min x) / 15)),   zero = fp16(min x)
+ *   code_d = clamp(rint((x_d - zero) / scale), 0, 15)   (real quotient, ties
+ *            to even; all 0 when scale is 0),   value_d = zero + scale * code_d
+ * Page p is Hkv blocks of page_size * (D + 8) bytes, one per kv head: K codes
+ * [page_size][D/2], V codes [page_size][D/2] (byte b holds dimension 2b in its
+ * low nibble, 2b + 1 in its high one), parameters [page_size][4] fp16: k
+ * scale, k zero, v scale, v zero.  Slot j of sequence s lies in page
+ * table[s][j / page_size] at row j % page_size.  Slots beyond a sequence's
+ * length may hold anything, NaN included, and table entries beyond its pages
+ * are not used.  A visible slot's scales are finite and not negative, as
+ * kv4_append writes them.
+ *
+ * Drafting, verification and commit: the step's T_s new tokens are appended at
+ * slots base_s .. base_s + T_s - 1, attended with a visibility mask, and those
+ * accepted are appended again at base_s .. ; the rest need no rollback, since
+ * no later call looks beyond the lengths it is given.
+ *
+ * Limits: D = 64 or 128; page_size = 16, 32, 64, 128 or 256; n_kv_heads <=
+ * 1024; n_seq <= 4096; max_pages * page_size <= 2^30.
+ * Errors of every kv4 call: MOE_ERR_ARG for a negative size, a NULL or
+ * misaligned pointer; MOE_ERR_UNSUPPORTED for sizes, types or strides outside
+ * the limits.  A used table entry outside [0, n_pages) flags MOE_DEV_BAD_ID
+ * and its slots are left out; a sequence whose lengths are negative or beyond
+ * max_pages * page_size flags MOE_DEV_CAPACITY and is left out (its outputs
+ * are not written).
+ */
+typedef struct {
+  int32_t n_pages, page_size, n_kv_heads, head_dim;
+  int32_t n_seq, max_pages;
+  void* pages;           /* uint8 [n_pages][n_kv_heads][page_size * (head_dim + 8)], 16-byte aligned */
+  const int32_t* table;  /* [n_seq][max_pages] page ids                                              */
+} kv4_cache;
+
+/* Rows of T tokens x n_kv_heads: dtype MOE_DTYPE_BF16 or MOE_DTYPE_F32;
+ * strides in elements (of kv4_append's k and v; multiples of 16 bytes, the D
+ * values of a row side by side). */
+typedef struct {
+  int32_t T, dtype;
+  int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+} kv4_rows_cfg;
+
+/* kv4_append -- writes the keys and values of T tokens.
+ *   k, v            rows as cfg says.  16-byte aligned.
+ *   seq, slot       [T] int32: where each token goes; slot -1 skips it.  Two
+ *                   tokens must not share a (seq, slot).
+ *   k_held, v_held  [T, Hkv, D] of cfg->dtype, or both NULL: the values that
+ *                   the cache now holds for each token (zeros if skipped).
+ * A row that is not finite or beyond +-65504 flags MOE_DEV_BAD_KV and is held
+ * as NaN.  A (seq, slot) outside the table flags MOE_DEV_BAD_ID and is skipped.
+ */
+int kv4_append(const kv4_cache* cache, const void* k, const void* v, const kv4_rows_cfg* cfg,
+               const int32_t* seq, const int32_t* slot, void* k_held, void* v_held,
+               int32_t* dev_err, void* stream);
+
+/* kv4_read -- the held values of T (seq, slot) pairs: k, v [T, Hkv, D] of
+ * cfg->dtype out (cfg's strides are not read); slot -1, or one outside the
+ * table (MOE_DEV_BAD_ID), gives zeros. */
+int kv4_read(const kv4_cache* cache, const int32_t* seq, const int32_t* slot, const kv4_rows_cfg* cfg,
+             void* k, void* v, int32_t* dev_err, void* stream);
+
+typedef struct {
+  int32_t T;            /* new tokens of all sequences                                          */
+  int32_t n_q_heads;    /* a multiple of n_kv_heads: head h reads kv head h / (n_q / n_kv)      */
+  int32_t max_q;        /* most new tokens of a sequence: chooses the kernel, not the results   */
+  float scale;          /* factor of q . k (finite)                                             */
+  int64_t q_token_stride, q_head_stride; /* in elements, multiples of 8                         */
+} kv4_attn_cfg;
+
+/* kv4_attend -- softmax attention of the new tokens over the cache.
+ *   q         bf16 rows of D, strided as cfg says, 16-byte aligned.
+ *   q_start   [n_seq + 1] int32: sequence s's new tokens are q_start[s] ..
+ *             q_start[s + 1] - 1 (none is fine); token i of them has been
+ *             appended at slot base[s] + i.
+ *   base      [n_seq] int32: context slots, visible to all new tokens of s.
+ *   visible   [T] 64-bit masks or NULL.  Bit j of a token's mask: it sees its
+ *             sequence's new token j (a token of a draft tree: its ancestors
+ *             and itself).  NULL: token i sees 0..i (a chain, or a chunk of
+ *             a prompt).  With masks a sequence has at most 64 new tokens:
+ *             more flag MOE_DEV_CAPACITY, and those past 64 are seen by none.
+ *   out       [T, n_q_heads, D] bf16 out; zeros for a row that sees nothing.
+ *   lse       [T, n_q_heads] fp32 out or NULL: log of the sum of the
+ *             exponentials of the scaled scores, -inf for such a row.
+ * Scores, maxima, sums and outputs are accumulated in fp32; a probability is
+ * rounded to fp16 (relative 2^-12) as the product's operand, the output once
+ * to bf16.  A NaN or infinity in a row of q, or in a slot that a row sees,
+ * makes that row NaN; in slots it does not see it has no effect.
+ * Results do not depend on timing.  Needs kv4_attend_workspace() bytes (0: bad
+ * arguments), 256-byte aligned, of any content. */
+size_t kv4_attend_workspace(const kv4_cache* cache, const kv4_attn_cfg* cfg);
+int kv4_attend(const kv4_cache* cache, const void* q, const int32_t* q_start, const int32_t* base,
+               const uint64_t* visible, const kv4_attn_cfg* cfg, void* out, float* lse, void* workspace,
+               size_t workspace_bytes, int32_t* dev_err, void* stream);
+
+/* kv4_weigh -- accumulates attention weights, the measure kv4_evict goes by:
+ *   mass[s, h, j] += sum over the new tokens i of s and the query heads of kv
+ *   head h of exp(scale * q . k_j - lse), over the slots j that i sees.
+ * Arguments as kv4_attend (of whose call lse is the result; rows with lse
+ * -inf add nothing); mass [n_seq, n_kv_heads, max_pages * page_size] fp32 in
+ * and out.  Slots beyond a sequence's are not touched.  Sums in fp32 in a
+ * fixed order. */
+int kv4_weigh(const kv4_cache* cache, const void* q, const int32_t* q_start, const int32_t* base,
+              const uint64_t* visible, const float* lse, const kv4_attn_cfg* cfg, float* mass,
+              int32_t* dev_err, void* stream);
+
+/* kv4_evict -- keeps at most `keep` slots per sequence and kv head.
+ *   mass      [n_seq, n_kv_heads, max_pages * page_size] fp32.
+ *   lens      [n_seq] int32: slots of each sequence.
+ * Where lens[s] > keep: the last `recent` slots stay, and of the others those
+ * of the largest mass (ties: the lower slot; NaN, which flags
+ * MOE_DEV_BAD_PROB, counts as below everything), keep in all.  Every kv head
+ * chooses for itself; the kept entries move to slots 0 .. keep - 1 in their
+ * old order.  Otherwise nothing moves.
+ *   new_len   [n_seq] int32 out: min(lens, keep).
+ *   origin    [n_seq, n_kv_heads, keep] int32 out: the old slot of each new
+ *             one, -1 past new_len.
+ *   mass_out  as mass, out (may be mass itself): the kept slots' masses, then
+ *             zeros up to lens[s]; not touched beyond.
+ */
+typedef struct {
+  int32_t keep, recent;  /* 1 <= keep, 0 <= recent <= keep */
+} kv4_evict_cfg;
+int kv4_evict(const kv4_cache* cache, const float* mass, const int32_t* lens, const kv4_evict_cfg* cfg,
+              int32_t* new_len, int32_t* origin, float* mass_out, int32_t* dev_err, void* stream);
+
 /* ---------------------------------------------------------------- timing
  * Optional per-kernel timing.  Between moe_profile_begin and moe_profile_end
  * the library records a CUDA event pair on the launching stream around each
@@ -611,10 +749,11 @@ int moe_verify_plan(const moe_step_cfg* cfg, const float* P, const int32_t* pare
  * summed milliseconds and the launch count.  Classes: 0 eco_select, 1 route,
  * 2 union/permute, 3 FFN prep, 4 FFN gate/up, 5 FFN down, 6 combine,
  * 7 router logits, 8 S2-MoE expansion, 9 expert staging, 10 hot list,
- * 11 depth policy.
+ * 11 depth policy, 12 kv4_append, 13 kv4_read, 14 kv4_attend, 15 kv4_weigh,
+ * 16 kv4_evict.
  * Not for use under stream capture.
  */
-enum { MOE_PROF_CLASSES = 12 };
+enum { MOE_PROF_CLASSES = 17 };
 int moe_profile_begin(int32_t max_launches, int32_t class_mask);
 int moe_profile_end(float* ms_per_class, int32_t* launches_per_class, int32_t n_classes);
 

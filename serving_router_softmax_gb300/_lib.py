@@ -11,18 +11,20 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoeverify.so")
 
 MOE_OK, MOE_ERR_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA, MOE_ERR_WORKSPACE = 0, 1, 2, 3, 4
-DEV_NAN_LOGIT, DEV_BAD_ID, DEV_DUP_ID, DEV_BAD_TREE, DEV_BAD_PROB, DEV_TIMEOUT, DEV_CAPACITY = (
-    0x01, 0x02, 0x04, 0x08, 0x10, 0x20, 0x40)
+DEV_NAN_LOGIT, DEV_BAD_ID, DEV_DUP_ID, DEV_BAD_TREE, DEV_BAD_PROB, DEV_TIMEOUT, DEV_CAPACITY, DEV_BAD_KV = (
+    0x01, 0x02, 0x04, 0x08, 0x10, 0x20, 0x40, 0x80)
 DTYPE_F32, DTYPE_BF16, DTYPE_E4M3_B128 = 0, 1, 2
 LAYOUT_ROWMAJOR, LAYOUT_TILED = 0, 1
 TEST_STALL_GATE_UP, TEST_STALL_READY_FLAG = 1, 2
 PROF_CLASSES = ["eco_select", "route", "union_permute", "ffn_prep", "ffn_gate_up", "ffn_down",
-                "combine", "router_logits", "s2_expand", "stage_experts", "hot_list", "depth_policy"]
+                "combine", "router_logits", "s2_expand", "stage_experts", "hot_list", "depth_policy",
+                "kv4_append", "kv4_read", "kv4_attend", "kv4_weigh", "kv4_evict"]
 
 EXPORTED = ["s2_expand", "moe_router_logits", "moe_route", "moe_union_permute", "moe_verify_ffn_workspace", "moe_verify_ffn",
             "eco_select", "moe_verify_step_workspace", "moe_verify_step", "moe_verify_plan", "moe_profile_begin",
             "moe_profile_end", "moe_status_str", "moe_launch_count", "moe_version", "moe_expert_bytes",
-            "moe_stage_experts", "moe_test_set_stall", "moe_hot_list", "moe_depth_policy", "moe_set_nvtx"]
+            "moe_stage_experts", "moe_test_set_stall", "moe_hot_list", "moe_depth_policy", "moe_set_nvtx",
+            "kv4_append", "kv4_read", "kv4_attend_workspace", "kv4_attend", "kv4_weigh", "kv4_evict"]
 
 
 class S2Cfg(C.Structure):
@@ -69,6 +71,26 @@ class StepCfg(C.Structure):
                 ("dtype", C.c_int32), ("layout", C.c_int32), ("T", C.c_int32), ("gamma_max", C.c_int32),
                 ("mode", C.c_int32), ("eps", C.c_float), ("use_bias", C.c_int32),
                 ("cap", C.c_int32), ("alpha", C.c_float)]
+
+
+class Kv4CacheStruct(C.Structure):
+    _fields_ = [("n_pages", C.c_int32), ("page_size", C.c_int32), ("n_kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("n_seq", C.c_int32), ("max_pages", C.c_int32),
+                ("pages", C.c_void_p), ("table", C.c_void_p)]
+
+
+class Kv4RowsCfg(C.Structure):
+    _fields_ = [("T", C.c_int32), ("dtype", C.c_int32), ("k_token_stride", C.c_int64), ("k_head_stride", C.c_int64),
+                ("v_token_stride", C.c_int64), ("v_head_stride", C.c_int64)]
+
+
+class Kv4AttnCfg(C.Structure):
+    _fields_ = [("T", C.c_int32), ("n_q_heads", C.c_int32), ("max_q", C.c_int32), ("scale", C.c_float),
+                ("q_token_stride", C.c_int64), ("q_head_stride", C.c_int64)]
+
+
+class Kv4EvictCfg(C.Structure):
+    _fields_ = [("keep", C.c_int32), ("recent", C.c_int32)]
 
 
 _lib = None
@@ -132,6 +154,18 @@ def load(path: str = LIB_PATH) -> C.CDLL:
     lib.moe_version.restype = C.c_int
     lib.moe_test_set_stall.argtypes = [i32]
     lib.moe_test_set_stall.restype = C.c_int
+    lib.kv4_append.argtypes = [P(Kv4CacheStruct), vp, vp, P(Kv4RowsCfg), vp, vp, vp, vp, vp, vp]
+    lib.kv4_append.restype = C.c_int
+    lib.kv4_read.argtypes = [P(Kv4CacheStruct), vp, vp, P(Kv4RowsCfg), vp, vp, vp, vp]
+    lib.kv4_read.restype = C.c_int
+    lib.kv4_attend_workspace.argtypes = [P(Kv4CacheStruct), P(Kv4AttnCfg)]
+    lib.kv4_attend_workspace.restype = sz
+    lib.kv4_attend.argtypes = [P(Kv4CacheStruct), vp, vp, vp, vp, P(Kv4AttnCfg), vp, vp, vp, sz, vp, vp]
+    lib.kv4_attend.restype = C.c_int
+    lib.kv4_weigh.argtypes = [P(Kv4CacheStruct), vp, vp, vp, vp, vp, P(Kv4AttnCfg), vp, vp, vp]
+    lib.kv4_weigh.restype = C.c_int
+    lib.kv4_evict.argtypes = [P(Kv4CacheStruct), vp, vp, P(Kv4EvictCfg), vp, vp, vp, vp, vp]
+    lib.kv4_evict.restype = C.c_int
     lib.moe_set_nvtx.argtypes = [i32]
     lib.moe_set_nvtx.restype = C.c_int
     _lib = lib

@@ -1,0 +1,562 @@
+// kv4_attend: attention of a batch's new tokens over the 4-bit paged cache.
+//
+// One pass over the cache with a running softmax maximum and sum, in the
+// transposed form: scores S^T [slots x query rows] = C_k Q^T with the key codes as
+// the row operand straight from their nibbles, output O^T [D x query rows] =
+// C_v^T P^T with the value codes.  The query rows of a kv head (its new tokens
+// times the query heads that share it) are the narrow side, in steps of 8, so
+// a single decoded token of 8 query heads wastes nothing.
+//
+// Each CTA owns an even share of all (sequence, head, row block, tile) units;
+// a producer warp keeps a ring of tiles in flight (bulk copies), four consumer
+// warps take 16 slots of each tile.  An item cut between CTAs leaves its
+// partial sums in the workspace and the combine kernel joins them in CTA
+// order, so results do not depend on timing.
+#include "kv4.cuh"
+#include "kv4_sched.cuh"
+
+namespace moe {
+namespace kv4 {
+namespace {
+
+constexpr int kConsumerWarps = 4;
+constexpr int kThreads = 32 * (kConsumerWarps + 1);
+constexpr uint64_t kWaitBudgetNs = 2000000000ull;  // 2 s
+constexpr float kLazy = 8.f;  // the running maximum may lag by this much (log2) before sums are rescaled
+
+struct AttendArgs {
+  Cache c;
+  const uint16_t* q;
+  long long q_ts, q_hs;
+  const int32_t* q_start;
+  const int32_t* base;
+  const uint64_t* visible;
+  uint16_t* out;
+  float* lse;
+  int32_t T, Hq, G;
+  float scale_log2;
+  float* part;     // [CTAs][2][RB][D + 2]: unnormalised outputs, running maximum, sum
+  int32_t* meta;   // [CTAs][8]: a cut item that starts in this CTA
+  int32_t* dev_err;
+};
+
+__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   tc::smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
+               : "memory");
+}
+
+// Query row r of an item: NULL past its last one.
+__device__ __forceinline__ const uint16_t* q_row(const AttendArgs& a, const SeqShape& q, int h, int r) {
+  if (r >= q.nq * a.G) return nullptr;
+  const int i = r / a.G, g = r - i * a.G;
+  return a.q + (q.q0 + i) * a.q_ts + static_cast<long long>(h * a.G + g) * a.q_hs;
+}
+
+template <int D, int NT, int NS>
+struct Smem {
+  static constexpr int RB = 8 * NT;
+  struct Stage {
+    alignas(128) uint8_t k[kTile * D / 2];
+    uint8_t v[kTile * D / 2];
+    uint8_t p[kTile * 8];
+  };
+  Stage st[NS];
+  uint2 frag[NT * (D / 16) * 32];
+  float o[RB][D + 4];
+  float cq[RB], cqs[RB];
+  float m[kConsumerWarps][RB], l[kConsumerWarps][RB], z[kConsumerWarps][RB];
+  uint64_t mask[RB];
+  uint64_t full[NS], empty[NS];
+  uint32_t groups[NS];  // bit g: the page of slots 16g..16g+15 of the tile is valid
+  long long scratch[32];
+  int abort, never;
+  long long cum[1];     // [S + 1]
+};
+
+// MMA layouts: see kv4.cuh.
+template <int D, int NT, int NS>
+__global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
+  using SM = Smem<D, NT, NS>;
+  constexpr int RB = SM::RB;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  SM& sm = *reinterpret_cast<SM*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      tc::mbar_init(&sm.full[i], 1);
+      tc::mbar_init(&sm.empty[i], kConsumerWarps);
+    }
+    sm.abort = sm.never = 0;
+    tc::fence_mbar_init();
+  }
+  pdl_wait();
+  build_units(a.c, a.q_start, a.base, a.T, a.G, RB, kTile, sm.cum, sm.scratch, a.dev_err, blockIdx.x == 0);
+  pdl_trigger();
+  const long long total = sm.cum[a.c.S];
+  // At most one CTA per unit, so that every CTA up to the last one used owns some.
+  const int ncta = static_cast<int>(total < gridDim.x ? total : gridDim.x), cta = blockIdx.x;
+  const long long u0 = cta < ncta ? total * cta / ncta : 0, u1 = cta < ncta ? total * (cta + 1) / ncta : 0;
+  volatile int* abort_flag = &sm.abort;
+
+  if (warp == kConsumerWarps) {
+    // ---------------------------------------------------------- producer
+    Cursor k;
+    int stage = 0, phase = 0, cached_s = -1, cached_at = 0, cached = -1;
+    long long issued = 0;
+    const int seg_rows = a.c.page_size < kTile ? a.c.page_size : kTile;
+    const int nseg = kTile / seg_rows;
+    for (long long u = u0; u < u1; ++u) {
+      if (u == u0 || k.tile == k.nt)
+        cursor_at(k, a.c, a.q_start, a.base, a.T, a.G, RB, kTile, sm.cum, u);
+      const bool ok = tc::mbar_wait_bounded(&sm.empty[stage], phase ^ 1, abort_flag, kWaitBudgetNs);
+      if (__any_sync(0xFFFFFFFFu, !ok)) {
+        *abort_flag = 1;
+        break;
+      }
+      // One table entry per lane, 32 pages ahead.
+      const int p0 = (k.tile * kTile) >> a.c.page_log2;
+      if (k.s != cached_s || p0 < cached_at || p0 + nseg > cached_at + 32) {
+        cached_s = k.s;
+        cached_at = p0;
+        cached = page_of(a.c, k.s, (p0 + lane) << a.c.page_log2);
+      }
+      int page = __shfl_sync(0xFFFFFFFFu, cached, (p0 + lane % nseg - cached_at) & 31);
+      const int j0 = k.tile * kTile + (lane % nseg) * seg_rows;  // first slot of this lane's segment
+      if (j0 >= k.q.total) page = -1;
+      const uint32_t have = __ballot_sync(0xFFFFFFFFu, lane < nseg && page >= 0);
+      const bool broken = __any_sync(0xFFFFFFFFu, lane < nseg && page < 0 && j0 < k.q.total);
+      typename SM::Stage& st = sm.st[stage];
+      if (lane == 0) {
+        uint32_t groups = 0;
+        for (int i = 0; i < nseg; ++i)
+          if ((have >> i) & 1) groups |= ((1u << (seg_rows / 16)) - 1u) << (i * (seg_rows / 16));
+        sm.groups[stage] = groups;
+        if (broken) flag_error(a.dev_err, MOE_DEV_BAD_ID);
+        tc::mbar_arrive_expect_tx(&sm.full[stage], __popc(have) * seg_rows * (D + 8));
+      }
+      __syncwarp();
+      if (lane < nseg && page >= 0) {
+        const uint8_t* b = page_block(a.c, page, k.h);
+        const int r0 = j0 & (a.c.page_size - 1);
+        bulk_copy(st.k + lane * seg_rows * (D / 2), b + static_cast<size_t>(r0) * (D / 2), seg_rows * (D / 2), &sm.full[stage]);
+        bulk_copy(st.v + lane * seg_rows * (D / 2), b + static_cast<size_t>(a.c.page_size + r0) * (D / 2), seg_rows * (D / 2),
+                  &sm.full[stage]);
+        bulk_copy(st.p + lane * seg_rows * 8, b + static_cast<size_t>(a.c.page_size) * D + r0 * 8, seg_rows * 8, &sm.full[stage]);
+      }
+      ++issued;
+      ++k.tile;
+      if (++stage == NS) stage = 0, phase ^= 1;
+    }
+    if (*abort_flag) {
+      // Copies in flight land before the CTA's shared memory goes.
+      for (long long i = issued > NS ? issued - NS : 0; i < issued; ++i)
+        tc::mbar_wait_bounded(&sm.full[i % NS], static_cast<uint32_t>((i / NS) & 1), &sm.never, 100000000ull);
+      if (lane == 0) flag_error(a.dev_err, MOE_DEV_TIMEOUT);
+    }
+    return;
+  }
+
+  // ------------------------------------------------------------ consumers
+  const int g = lane >> 2, c = lane & 3;
+  const int s0 = slot_of_row(g), s1 = slot_of_row(g + 8);
+  int stage = 0, phase = 0;
+  if (tid < 8) a.meta[static_cast<size_t>(cta) * 8 + tid] = 0;
+  for (long long u = u0; u < u1;) {
+    Cursor k;
+    cursor_at(k, a.c, a.q_start, a.base, a.T, a.G, RB, kTile, sm.cum, u);
+    const long long item_end = k.item0 + k.nt;
+    const int n = static_cast<int>((item_end < u1 ? item_end : u1) - u);
+    const int row0 = k.rb * RB, rows = min(RB, k.q.nq * a.G - row0);
+    prep_q<D>([&](int r) { return r < rows ? q_row(a, k.q, k.h, row0 + r) : nullptr; }, RB, a.scale_log2, sm.frag, sm.cq,
+              sm.cqs, tid, 32 * kConsumerWarps);
+    if (tid < RB) {
+      // Bit j: new slot base + j is visible.  Rows past the last one see what row 0 sees.
+      const int i = (row0 + (tid < rows ? tid : 0)) / a.G;
+      uint64_t bits;
+      if (a.visible) bits = a.visible[k.q.q0 + i];
+      else bits = i >= 63 ? ~0ull : (2ull << i) - 1;
+      sm.mask[tid] = bits;
+    }
+    if (a.visible && k.q.nq > kMaxTree && tid == 0) flag_error(a.dev_err, MOE_DEV_CAPACITY);
+    tc::named_bar_sync(1, 32 * kConsumerWarps);
+
+    float o[D / 16][NT][4];
+    float m[NT][2], l[NT][2], z[NT][2], cq[NT][2], cqs[NT][2];
+    uint2 qf[NT == 1 ? D / 16 : 1];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[t][e] = kNone;
+        l[t][e] = z[t][e] = 0.f;
+        cq[t][e] = sm.cq[8 * t + 2 * c + e];
+        cqs[t][e] = sm.cqs[8 * t + 2 * c + e];
+      }
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][t][e] = 0.f;
+    }
+    if constexpr (NT == 1) {
+#pragma unroll
+      for (int t = 0; t < D / 16; ++t) qf[t] = sm.frag[t * 32 + lane];
+    }
+
+    for (int it = 0; it < n; ++it) {
+      const int j0 = (k.tile + it) * kTile + 16 * warp;  // first slot of this warp's group
+      if (!tc::mbar_wait_bounded(&sm.full[stage], phase, abort_flag, kWaitBudgetNs)) *abort_flag = 1;
+      __syncwarp();
+      const typename SM::Stage& st = sm.st[stage];
+      const bool any = j0 < k.q.total && ((sm.groups[stage] >> warp) & 1);
+      if (any) {
+        const bool edge = j0 + 16 > k.q.base;
+        uint32_t ka[D / 32], kb[D / 32];
+        load_k_words<D>(st.k + (16 * warp + s0) * (D / 2), c, ka);
+        load_k_words<D>(st.k + (16 * warp + s1) * (D / 2), c, kb);
+        const uint2 ra = *reinterpret_cast<const uint2*>(st.p + (16 * warp + s0) * 8);
+        const uint2 rb = *reinterpret_cast<const uint2*>(st.p + (16 * warp + s1) * 8);
+        float ks[2], kz[2], lv[2], rs[2], zr[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint2 r = e ? rb : ra;
+          const float2 kp = __half22float2(*reinterpret_cast<const __half2*>(&r.x));
+          const float2 vp = __half22float2(*reinterpret_cast<const __half2*>(&r.y));
+          const float se = fmaxf(vp.x, kMinScale);
+          ks[e] = kp.x;
+          kz[e] = kp.y;
+          lv[e] = lg2(se);
+          rs[e] = rcp(se);
+          zr[e] = vp.y * rs[e];
+        }
+        float t4[NT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+          if constexpr (NT == 1)
+            qk_16x8<D>(acc, ka, kb, [&](int i) { return qf[i]; });
+          else
+            qk_16x8<D>(acc, ka, kb, [&](int i) { return sm.frag[(t * (D / 16) + i) * 32 + lane]; });
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int kk = e >> 1, x = e & 1;
+            t4[t][e] = fmaf(ks[kk], acc[e] * cq[t][x], fmaf(kz[kk], cqs[t][x], lv[kk]));
+          }
+        }
+        uint32_t seen = 0xFFFFFFFFu;  // bit 4t + e: visible
+        if (edge) {
+          seen = 0;
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = j0 + ((e >> 1) ? s1 : s0), d = j - k.q.base;
+              const int r = 8 * t + 2 * c + (e & 1);
+              bool see = d < 0;
+              if (!see && j < k.q.total) {
+                if (d < 64 && (a.visible || (row0 + r) / a.G < 63)) see = (sm.mask[r] >> d) & 1;
+                else see = !a.visible && d <= (row0 + (r < rows ? r : 0)) / a.G;
+              }
+              seen |= static_cast<uint32_t>(see) << (4 * t + e);
+              if (!see) t4[t][e] = -INFINITY;
+            }
+        }
+        bool grow = false;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) grow |= t4[t][e] > m[t][e & 1] + kLazy;
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float nm = fmaxf(m[t][x], fmaxf(t4[t][x], t4[t][2 + x]));
+              nm = fmaxf(nm, __shfl_xor_sync(0xFFFFFFFFu, nm, 4));
+              nm = fmaxf(nm, __shfl_xor_sync(0xFFFFFFFFu, nm, 8));
+              nm = fmaxf(nm, __shfl_xor_sync(0xFFFFFFFFu, nm, 16));
+              const float f = ex2(m[t][x] - nm);
+              m[t][x] = nm;
+              l[t][x] *= f;
+              z[t][x] *= f;
+#pragma unroll
+              for (int j = 0; j < D / 16; ++j) {
+                o[j][t][x] *= f;
+                o[j][t][2 + x] *= f;
+              }
+            }
+        }
+        uint2 pf[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int kk = e >> 1, x = e & 1;
+            p[e] = ex2(t4[t][e] - m[t][x]);
+            if (!edge || ((seen >> (4 * t + e)) & 1)) {
+              l[t][x] = fmaf(p[e], rs[kk], l[t][x]);
+              z[t][x] = fmaf(p[e], zr[kk], z[t][x]);
+            }
+          }
+          pf[t] = make_uint2(transpose_8x8(pack_h2(p[0], p[1])), transpose_8x8(pack_h2(p[2], p[3])));
+        }
+        // Values: lane (g, c) owns k indices 2c, 2c+1, 2c+8, 2c+9 and the
+        // dimensions g * D/8 ..; one byte permute pairs two slots' halves.
+        const uint8_t* vb = st.v + 16 * warp * (D / 2) + g * (D / 16);
+        const int v0 = slot_of_row(2 * c), v1 = slot_of_row(2 * c + 1);
+        if constexpr (D == 128) {
+          uint2 w[4];
+          w[0] = *reinterpret_cast<const uint2*>(vb + v0 * (D / 2));
+          w[1] = *reinterpret_cast<const uint2*>(vb + v1 * (D / 2));
+          w[2] = *reinterpret_cast<const uint2*>(vb + (8 + v0) * (D / 2));
+          w[3] = *reinterpret_cast<const uint2*>(vb + (8 + v1) * (D / 2));
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const uint32_t sel = hf ? 0x7632u : 0x5410u;
+            const uint32_t xa = __byte_perm(w[0].x, w[1].x, sel), ya = __byte_perm(w[0].y, w[1].y, sel);
+            const uint32_t xb = __byte_perm(w[2].x, w[3].x, sel), yb = __byte_perm(w[2].y, w[3].y, sel);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              mma_f16(o[4 * hf + 0][t], nibbles<0>(xa), nibbles<0>(ya), nibbles<0>(xb), nibbles<0>(yb), pf[t]);
+              mma_f16(o[4 * hf + 1][t], nibbles<1>(xa), nibbles<1>(ya), nibbles<1>(xb), nibbles<1>(yb), pf[t]);
+              mma_f16(o[4 * hf + 2][t], nibbles<2>(xa), nibbles<2>(ya), nibbles<2>(xb), nibbles<2>(yb), pf[t]);
+              mma_f16(o[4 * hf + 3][t], nibbles<3>(xa), nibbles<3>(ya), nibbles<3>(xb), nibbles<3>(yb), pf[t]);
+            }
+          }
+        } else {
+          uint32_t w[4];
+          w[0] = *reinterpret_cast<const uint32_t*>(vb + v0 * (D / 2));
+          w[1] = *reinterpret_cast<const uint32_t*>(vb + v1 * (D / 2));
+          w[2] = *reinterpret_cast<const uint32_t*>(vb + (8 + v0) * (D / 2));
+          w[3] = *reinterpret_cast<const uint32_t*>(vb + (8 + v1) * (D / 2));
+          const uint32_t xa = __byte_perm(w[0], w[1], 0x5410u), ya = __byte_perm(w[0], w[1], 0x7632u);
+          const uint32_t xb = __byte_perm(w[2], w[3], 0x5410u), yb = __byte_perm(w[2], w[3], 0x7632u);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            mma_f16(o[0][t], nibbles<0>(xa), nibbles<0>(ya), nibbles<0>(xb), nibbles<0>(yb), pf[t]);
+            mma_f16(o[1][t], nibbles<1>(xa), nibbles<1>(ya), nibbles<1>(xb), nibbles<1>(yb), pf[t]);
+            mma_f16(o[2][t], nibbles<2>(xa), nibbles<2>(ya), nibbles<2>(xb), nibbles<2>(yb), pf[t]);
+            mma_f16(o[3][t], nibbles<3>(xa), nibbles<3>(ya), nibbles<3>(xb), nibbles<3>(yb), pf[t]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.empty[stage]);
+      if (++stage == NS) stage = 0, phase ^= 1;
+    }
+
+    // ---- join the four warps' sums
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+#pragma unroll
+        for (int sft = 4; sft < 32; sft <<= 1) {
+          l[t][x] += __shfl_xor_sync(0xFFFFFFFFu, l[t][x], sft);
+          z[t][x] += __shfl_xor_sync(0xFFFFFFFFu, z[t][x], sft);
+        }
+        if (g == 0) {
+          sm.m[warp][8 * t + 2 * c + x] = m[t][x];
+          sm.l[warp][8 * t + 2 * c + x] = l[t][x];
+          sm.z[warp][8 * t + 2 * c + x] = z[t][x];
+        }
+      }
+    tc::named_bar_sync(1, 32 * kConsumerWarps);
+    float f[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int r = 8 * t + 2 * c + x;
+        float mm = sm.m[0][r];
+#pragma unroll
+        for (int w = 1; w < kConsumerWarps; ++w) mm = fmaxf(mm, sm.m[w][r]);
+        f[t][x] = ex2(m[t][x] - mm);
+      }
+    // Quarter (warp + p) % 4 of the dimensions in phase p.
+    constexpr int QT = D / 16 / kConsumerWarps;
+    for (int p = 0; p < kConsumerWarps; ++p) {
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        if (j / QT != ((warp + p) & 3)) continue;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            // accumulator row g (+ 8 for e >= 2) of tile j is this dimension
+            const int d = D == 128 ? 16 * g + 8 * (e >> 1) + j : 8 * g + 4 * (e >> 1) + j;
+            const int r = 8 * t + 2 * c + (e & 1);
+            const float val = (o[j][t][e] * ((j & 1) ? 1048576.f : 16777216.f) + z[t][e & 1]) * f[t][e & 1];
+            if (p == 0) sm.o[r][d] = val;
+            else sm.o[r][d] += val;
+          }
+      }
+      tc::named_bar_sync(1, 32 * kConsumerWarps);
+    }
+    const bool whole = u == k.item0 && u + n == item_end;
+    for (int i = tid; i < rows * (D / 2); i += 32 * kConsumerWarps) {
+      const int r = i / (D / 2), d = 2 * (i % (D / 2));
+      float mm = sm.m[0][r];
+#pragma unroll
+      for (int w = 1; w < kConsumerWarps; ++w) mm = fmaxf(mm, sm.m[w][r]);
+      float ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < kConsumerWarps; ++w) ll += sm.l[w][r] * ex2(sm.m[w][r] - mm);
+      float x = sm.o[r][d], y = sm.o[r][d + 1];
+      if (whole) {
+        const int ri = row0 + r, tok = ri / a.G, hd = k.h * a.G + ri % a.G;
+        const size_t at = (static_cast<size_t>(k.q.q0) + tok) * a.Hq + hd;
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        x *= inv;
+        y *= inv;
+        uint32_t b;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b) : "f"(y), "f"(x));
+        *reinterpret_cast<uint32_t*>(a.out + at * D + d) = b;
+        if (d == 0 && a.lse) a.lse[at] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+      } else {
+        float* P = a.part + ((static_cast<size_t>(cta) * 2 + (u == u0 ? 0 : 1)) * RB + r) * (D + 2);
+        P[d] = x;
+        P[d + 1] = y;
+        if (d == 0) {
+          P[D] = mm;
+          P[D + 1] = ll;
+        }
+      }
+    }
+    if (!whole && u == k.item0 && tid == 0) {
+      int32_t* M = a.meta + static_cast<size_t>(cta) * 8;
+      const long long last = item_end - 1;
+      M[1] = k.s;
+      M[2] = k.h;
+      M[3] = row0;
+      M[4] = rows;
+      M[5] = static_cast<int>(((last + 1) * ncta - 1) / total);  // the CTA that owns the item's last unit
+      M[6] = u == u0 ? 0 : 1;
+      M[0] = 1;
+    }
+    tc::named_bar_sync(1, 32 * kConsumerWarps);
+    u += n;
+  }
+}
+
+// Joins the partial sums of the item that starts in CTA blockIdx.x and ends
+// in a later one.
+template <int D, int RB>
+__global__ void __launch_bounds__(128) combine_kernel(const AttendArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int c0 = blockIdx.x;
+  const int32_t* M = a.meta + static_cast<size_t>(c0) * 8;
+  if (M[0] == 0) return;
+  const int s = M[1], h = M[2], row0 = M[3], rows = M[4], c1 = M[5], slot0 = M[6];
+  const int q0 = a.q_start[s];
+  for (int i = threadIdx.x; i < rows * (D / 2); i += blockDim.x) {
+    const int r = i / (D / 2), d = 2 * (i % (D / 2));
+    const float* P = a.part + ((static_cast<size_t>(c0) * 2 + slot0) * RB + r) * (D + 2);
+    float m = P[D], l = P[D + 1], x = P[d], y = P[d + 1];
+    for (int c = c0 + 1; c <= c1; ++c) {
+      const float* Q = a.part + (static_cast<size_t>(c) * 2 * RB + r) * (D + 2);
+      const float mq = Q[D], nm = fmaxf(m, mq), f = ex2(m - nm), fq = ex2(mq - nm);
+      l = l * f + Q[D + 1] * fq;
+      x = x * f + Q[d] * fq;
+      y = y * f + Q[d + 1] * fq;
+      m = nm;
+    }
+    const int ri = row0 + r, tok = ri / a.G, hd = h * a.G + ri % a.G;
+    const size_t at = (static_cast<size_t>(q0) + tok) * a.Hq + hd;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint32_t b;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b) : "f"(y * inv), "f"(x * inv));
+    *reinterpret_cast<uint32_t*>(a.out + at * D + d) = b;
+    if (d == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  }
+}
+
+// Ring depth: about 52 KB of tiles, so that three CTAs of an SM keep more than
+// 100 KB in flight.
+template <int D> constexpr int stages() { return D == 128 ? 6 : 10; }
+
+struct Plan {
+  int rb, grid;
+};
+
+// Row block: the fewest steps of 8 rows (up to 32) that hold a sequence's rows.
+Plan plan_of(const kv4_attn_cfg& cfg, const Cache& c) {
+  const long long rows = static_cast<long long>(cfg.max_q) * (cfg.n_q_heads / c.Hkv);
+  Plan p;
+  p.rb = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  p.grid = sm_count() * (p.rb == 32 ? 2 : 3);
+  return p;
+}
+
+size_t part_bytes(const Plan& p, const Cache& c) { return align_up(static_cast<size_t>(p.grid) * 2 * p.rb * (c.D + 2) * 4, 256); }
+
+template <int D, int NT>
+int launch_attend(const AttendArgs& a, const Plan& p, cudaStream_t s) {
+  using SM = Smem<D, NT, stages<D>()>;
+  const size_t smem = sizeof(SM) + static_cast<size_t>(a.c.S) * 8;
+  auto k = attend_kernel<D, NT, stages<D>()>;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  int st;
+  {
+    LaunchScope ls(kProfKv4Attend, s);
+    st = launch_k(k, dim3(p.grid), dim3(kThreads), smem, s, false, a);
+  }
+  if (st != MOE_OK) return st;
+  LaunchScope ls(kProfKv4Attend, s);
+  return launch_k(combine_kernel<D, 8 * NT>, dim3(p.grid), dim3(128), 0, s, true, a);
+}
+
+}  // namespace
+
+int attn_validate(const kv4_attn_cfg* cfg, const Cache& c) {
+  if (!cfg || cfg->T < 0 || cfg->n_q_heads < 1 || cfg->max_q < 1) return MOE_ERR_ARG;
+  if (cfg->n_q_heads % c.Hkv) return MOE_ERR_ARG;
+  if (!(cfg->scale == cfg->scale) || cfg->scale - cfg->scale != 0.f) return MOE_ERR_ARG;
+  if (cfg->n_q_heads > 4096 || static_cast<long long>(cfg->T) * cfg->n_q_heads > (1ll << 30)) return MOE_ERR_UNSUPPORTED;
+  if (cfg->q_token_stride < 0 || cfg->q_head_stride < 0 || cfg->q_token_stride % 8 || cfg->q_head_stride % 8)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace kv4
+}  // namespace moe
+
+extern "C" size_t kv4_attend_workspace(const kv4_cache* cache, const kv4_attn_cfg* cfg) {
+  using namespace moe;
+  using namespace moe::kv4;
+  Cache c;
+  if (cache_validate(cache, &c) != MOE_OK || attn_validate(cfg, c) != MOE_OK) return 0;
+  const Plan p = plan_of(*cfg, c);
+  return part_bytes(p, c) + align_up(static_cast<size_t>(p.grid) * 32, 256);
+}
+
+extern "C" int kv4_attend(const kv4_cache* cache, const void* q, const int32_t* q_start, const int32_t* base,
+                          const uint64_t* visible, const kv4_attn_cfg* cfg, void* out, float* lse, void* workspace,
+                          size_t workspace_bytes, int32_t* dev_err, void* stream) {
+  using namespace moe;
+  using namespace moe::kv4;
+  Cache c;
+  int st = cache_validate(cache, &c);
+  if (st != MOE_OK || (st = attn_validate(cfg, c)) != MOE_OK) return st;
+  if (cfg->T == 0 || c.S == 0) return MOE_OK;
+  if (!q || !q_start || !base || !out) return MOE_ERR_ARG;
+  if ((reinterpret_cast<uintptr_t>(q) & 15) || (reinterpret_cast<uintptr_t>(out) & 15) ||
+      (reinterpret_cast<uintptr_t>(visible) & 7) ||
+      ((reinterpret_cast<uintptr_t>(q_start) | reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(lse)) & 3))
+    return MOE_ERR_ARG;
+  const size_t need = kv4_attend_workspace(cache, cfg);
+  if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)) return MOE_ERR_WORKSPACE;
+  const Plan p = plan_of(*cfg, c);
+  AttendArgs a{c, static_cast<const uint16_t*>(q), cfg->q_token_stride, cfg->q_head_stride, q_start, base, visible,
+               static_cast<uint16_t*>(out), lse, cfg->T, cfg->n_q_heads, cfg->n_q_heads / c.Hkv, cfg->scale * kLog2e,
+               static_cast<float*>(workspace),
+               reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + part_bytes(p, c)), dev_err};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (c.D == 128)
+    return p.rb == 8 ? launch_attend<128, 1>(a, p, s) : p.rb == 16 ? launch_attend<128, 2>(a, p, s) : launch_attend<128, 4>(a, p, s);
+  return p.rb == 8 ? launch_attend<64, 1>(a, p, s) : p.rb == 16 ? launch_attend<64, 2>(a, p, s) : launch_attend<64, 4>(a, p, s);
+}

@@ -152,4 +152,4 @@ extern "C" int moe_set_nvtx(int32_t on) {
   return MOE_OK;
 }
 
-extern "C" int moe_version(void) { return 103; }
+extern "C" int moe_version(void) { return 104; }
