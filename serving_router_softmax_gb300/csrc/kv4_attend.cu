@@ -12,8 +12,7 @@
 // warps take 16 slots of each tile.  An item cut between CTAs leaves its
 // partial sums in the workspace and the combine kernel joins them in CTA
 // order, so results do not depend on timing.
-#include "kv4.cuh"
-#include "kv4_sched.cuh"
+#include "kv4_attend.cuh"
 
 namespace moe {
 namespace kv4 {
@@ -21,48 +20,10 @@ namespace {
 
 constexpr int kConsumerWarps = 4;
 constexpr int kThreads = 32 * (kConsumerWarps + 1);
-constexpr uint64_t kWaitBudgetNs = 2000000000ull;  // 2 s
-constexpr float kLazy = 8.f;  // the running maximum may lag by this much (log2) before sums are rescaled
-
-struct AttendArgs {
-  Cache c;
-  const uint16_t* q;
-  long long q_ts, q_hs;
-  const int32_t* q_start;
-  const int32_t* base;
-  const uint64_t* visible;
-  uint16_t* out;
-  float* lse;
-  int32_t T, Hq, G;
-  float scale_log2;
-  float* part;     // [CTAs][2][RB][D + 2]: unnormalised outputs, running maximum, sum
-  int32_t* meta;   // [CTAs][8]: a cut item that starts in this CTA
-  int32_t* dev_err;
-};
-
-__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   tc::smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
-               : "memory");
-}
-
-// Query row r of an item: NULL past its last one.
-__device__ __forceinline__ const uint16_t* q_row(const AttendArgs& a, const SeqShape& q, int h, int r) {
-  if (r >= q.nq * a.G) return nullptr;
-  const int i = r / a.G, g = r - i * a.G;
-  return a.q + (q.q0 + i) * a.q_ts + static_cast<long long>(h * a.G + g) * a.q_hs;
-}
-
 template <int D, int NT, int NS>
 struct Smem {
   static constexpr int RB = 8 * NT;
-  struct Stage {
-    alignas(128) uint8_t k[kTile * D / 2];
-    uint8_t v[kTile * D / 2];
-    uint8_t p[kTile * 8];
-  };
-  Stage st[NS];
+  Tile<D> st[NS];
   uint2 frag[NT * (D / 16) * 32];
   float o[RB][D + 4];
   float cq[RB], cqs[RB];
@@ -103,10 +64,9 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
   if (warp == kConsumerWarps) {
     // ---------------------------------------------------------- producer
     Cursor k;
-    int stage = 0, phase = 0, cached_s = -1, cached_at = 0, cached = -1;
+    TileLoader<D> loader;
+    int stage = 0, phase = 0;
     long long issued = 0;
-    const int seg_rows = a.c.page_size < kTile ? a.c.page_size : kTile;
-    const int nseg = kTile / seg_rows;
     for (long long u = u0; u < u1; ++u) {
       if (u == u0 || k.tile == k.nt)
         cursor_at(k, a.c, a.q_start, a.base, a.T, a.G, RB, kTile, sm.cum, u);
@@ -115,36 +75,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
         *abort_flag = 1;
         break;
       }
-      // One table entry per lane, 32 pages ahead.
-      const int p0 = (k.tile * kTile) >> a.c.page_log2;
-      if (k.s != cached_s || p0 < cached_at || p0 + nseg > cached_at + 32) {
-        cached_s = k.s;
-        cached_at = p0;
-        cached = page_of(a.c, k.s, (p0 + lane) << a.c.page_log2);
-      }
-      int page = __shfl_sync(0xFFFFFFFFu, cached, (p0 + lane % nseg - cached_at) & 31);
-      const int j0 = k.tile * kTile + (lane % nseg) * seg_rows;  // first slot of this lane's segment
-      if (j0 >= k.q.total) page = -1;
-      const uint32_t have = __ballot_sync(0xFFFFFFFFu, lane < nseg && page >= 0);
-      const bool broken = __any_sync(0xFFFFFFFFu, lane < nseg && page < 0 && j0 < k.q.total);
-      typename SM::Stage& st = sm.st[stage];
-      if (lane == 0) {
-        uint32_t groups = 0;
-        for (int i = 0; i < nseg; ++i)
-          if ((have >> i) & 1) groups |= ((1u << (seg_rows / 16)) - 1u) << (i * (seg_rows / 16));
-        sm.groups[stage] = groups;
-        if (broken) flag_error(a.dev_err, MOE_DEV_BAD_ID);
-        tc::mbar_arrive_expect_tx(&sm.full[stage], __popc(have) * seg_rows * (D + 8));
-      }
-      __syncwarp();
-      if (lane < nseg && page >= 0) {
-        const uint8_t* b = page_block(a.c, page, k.h);
-        const int r0 = j0 & (a.c.page_size - 1);
-        bulk_copy(st.k + lane * seg_rows * (D / 2), b + static_cast<size_t>(r0) * (D / 2), seg_rows * (D / 2), &sm.full[stage]);
-        bulk_copy(st.v + lane * seg_rows * (D / 2), b + static_cast<size_t>(a.c.page_size + r0) * (D / 2), seg_rows * (D / 2),
-                  &sm.full[stage]);
-        bulk_copy(st.p + lane * seg_rows * 8, b + static_cast<size_t>(a.c.page_size) * D + r0 * 8, seg_rows * 8, &sm.full[stage]);
-      }
+      loader.load(a, k, sm.st[stage], &sm.groups[stage], &sm.full[stage]);
       ++issued;
       ++k.tile;
       if (++stage == NS) stage = 0, phase ^= 1;
@@ -169,16 +100,9 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
     const long long item_end = k.item0 + k.nt;
     const int n = static_cast<int>((item_end < u1 ? item_end : u1) - u);
     const int row0 = k.rb * RB, rows = min(RB, k.q.nq * a.G - row0);
-    prep_q<D>([&](int r) { return r < rows ? q_row(a, k.q, k.h, row0 + r) : nullptr; }, RB, a.scale_log2, sm.frag, sm.cq,
+    prep_q<D>([&](int r) { return r < rows ? q_row(a, k.q, k.h, row0 + r) : (const uint16_t*)nullptr; }, RB, a.scale_log2, sm.frag, sm.cq,
               sm.cqs, tid, 32 * kConsumerWarps);
-    if (tid < RB) {
-      // Bit j: new slot base + j is visible.  Rows past the last one see what row 0 sees.
-      const int i = (row0 + (tid < rows ? tid : 0)) / a.G;
-      uint64_t bits;
-      if (a.visible) bits = a.visible[k.q.q0 + i];
-      else bits = i >= 63 ? ~0ull : (2ull << i) - 1;
-      sm.mask[tid] = bits;
-    }
+    if (tid < RB && a.visible) sm.mask[tid] = a.visible[k.q.q0 + (row0 + min(tid, rows - 1)) / a.G];
     if (a.visible && k.q.nq > kMaxTree && tid == 0) flag_error(a.dev_err, MOE_DEV_CAPACITY);
     tc::named_bar_sync(1, 32 * kConsumerWarps);
 
@@ -208,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
       const int j0 = (k.tile + it) * kTile + 16 * warp;  // first slot of this warp's group
       if (!tc::mbar_wait_bounded(&sm.full[stage], phase, abort_flag, kWaitBudgetNs)) *abort_flag = 1;
       __syncwarp();
-      const typename SM::Stage& st = sm.st[stage];
+      const Tile<D>& st = sm.st[stage];
       const bool any = j0 < k.q.total && ((sm.groups[stage] >> warp) & 1);
       if (any) {
         const bool edge = j0 + 16 > k.q.base;
@@ -250,16 +174,13 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = j0 + ((e >> 1) ? s1 : s0), d = j - k.q.base;
-              const int r = 8 * t + 2 * c + (e & 1);
-              bool see = d < 0;
-              if (!see && j < k.q.total) {
-                if (d < 64 && (a.visible || (row0 + r) / a.G < 63)) see = (sm.mask[r] >> d) & 1;
-                else see = !a.visible && d <= (row0 + (r < rows ? r : 0)) / a.G;
-              }
-              seen |= static_cast<uint32_t>(see) << (4 * t + e);
-              if (!see) t4[t][e] = -INFINITY;
+            for (int x = 0; x < 2; ++x) {
+              const int r = 8 * t + 2 * c + x;
+              const uint64_t v = sees(k.q, a.visible != nullptr, sm.mask[r], (row0 + min(r, rows - 1)) / a.G, j0);
+              if ((v >> s0) & 1) seen |= 1u << (4 * t + x);
+              else t4[t][x] = -INFINITY;
+              if ((v >> s1) & 1) seen |= 1u << (4 * t + 2 + x);
+              else t4[t][2 + x] = -INFINITY;
             }
         }
         bool grow = false;
@@ -416,78 +337,80 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
         *reinterpret_cast<uint32_t*>(a.out + at * D + d) = b;
         if (d == 0 && a.lse) a.lse[at] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
       } else {
-        float* P = a.part + ((static_cast<size_t>(cta) * 2 + (u == u0 ? 0 : 1)) * RB + r) * (D + 2);
-        P[d] = x;
-        P[d + 1] = y;
+        float* P = a.part + (static_cast<size_t>(cta) * 2 + (u == u0 ? 0 : 1)) * part_floats<D, RB>();
+        *reinterpret_cast<float2*>(P + r * D + d) = make_float2(x, y);
         if (d == 0) {
-          P[D] = mm;
-          P[D + 1] = ll;
+          P[RB * D + r] = mm;
+          P[RB * D + RB + r] = ll;
         }
       }
     }
-    if (!whole && u == k.item0 && tid == 0) {
-      int32_t* M = a.meta + static_cast<size_t>(cta) * 8;
-      const long long last = item_end - 1;
-      M[1] = k.s;
-      M[2] = k.h;
-      M[3] = row0;
-      M[4] = rows;
-      M[5] = static_cast<int>(((last + 1) * ncta - 1) / total);  // the CTA that owns the item's last unit
-      M[6] = u == u0 ? 0 : 1;
-      M[0] = 1;
-    }
+    if (!whole && u == k.item0 && tid == 0) note_cut(a, cta, ncta, total, k, row0, rows, item_end, u == u0 ? 0 : 1);
     tc::named_bar_sync(1, 32 * kConsumerWarps);
     u += n;
   }
 }
 
 // Joins the partial sums of the item that starts in CTA blockIdx.x and ends
-// in a later one.
+// in a later one: rows 8 * blockIdx.y to + 7 of it, two dimensions a thread.
 template <int D, int RB>
-__global__ void __launch_bounds__(128) combine_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(4 * D) combine_kernel(const AttendArgs a) {
   pdl_wait();
   pdl_trigger();
   const int c0 = blockIdx.x;
   const int32_t* M = a.meta + static_cast<size_t>(c0) * 8;
-  if (M[0] == 0) return;
-  const int s = M[1], h = M[2], row0 = M[3], rows = M[4], c1 = M[5], slot0 = M[6];
+  const int r = blockIdx.y * 8 + threadIdx.x / (D / 2), d = 2 * (threadIdx.x % (D / 2));
+  if (M[0] == 0 || r >= M[4]) return;
+  const int s = M[1], h = M[2], row0 = M[3], c1 = M[5], slot0 = M[6];
   const int q0 = a.q_start[s];
-  for (int i = threadIdx.x; i < rows * (D / 2); i += blockDim.x) {
-    const int r = i / (D / 2), d = 2 * (i % (D / 2));
-    const float* P = a.part + ((static_cast<size_t>(c0) * 2 + slot0) * RB + r) * (D + 2);
-    float m = P[D], l = P[D + 1], x = P[d], y = P[d + 1];
-    for (int c = c0 + 1; c <= c1; ++c) {
-      const float* Q = a.part + (static_cast<size_t>(c) * 2 * RB + r) * (D + 2);
-      const float mq = Q[D], nm = fmaxf(m, mq), f = ex2(m - nm), fq = ex2(mq - nm);
-      l = l * f + Q[D + 1] * fq;
-      x = x * f + Q[d] * fq;
-      y = y * f + Q[d + 1] * fq;
-      m = nm;
-    }
-    const int ri = row0 + r, tok = ri / a.G, hd = h * a.G + ri % a.G;
-    const size_t at = (static_cast<size_t>(q0) + tok) * a.Hq + hd;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint32_t b;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b) : "f"(y * inv), "f"(x * inv));
-    *reinterpret_cast<uint32_t*>(a.out + at * D + d) = b;
-    if (d == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  constexpr size_t PF = part_floats<D, RB>();
+  const float* P = a.part + (static_cast<size_t>(c0) * 2 + slot0) * PF;
+  float m = P[RB * D + r], l = P[RB * D + RB + r];
+  float2 v = *reinterpret_cast<const float2*>(P + r * D + d);
+#pragma unroll 4
+  for (int c = c0 + 1; c <= c1; ++c) {
+    const float* Q = a.part + static_cast<size_t>(c) * 2 * PF;
+    const float mq = Q[RB * D + r], lq = Q[RB * D + RB + r];
+    const float2 w = *reinterpret_cast<const float2*>(Q + r * D + d);
+    const float nm = fmaxf(m, mq), f = ex2(m - nm), fq = ex2(mq - nm);
+    l = l * f + lq * fq;
+    v.x = v.x * f + w.x * fq;
+    v.y = v.y * f + w.y * fq;
+    m = nm;
   }
+  const int ri = row0 + r, tok = ri / a.G, hd = h * a.G + ri % a.G;
+  const size_t at = (static_cast<size_t>(q0) + tok) * a.Hq + hd;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t b;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b) : "f"(v.y * inv), "f"(v.x * inv));
+  *reinterpret_cast<uint32_t*>(a.out + at * D + d) = b;
+  if (d == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+template <int D, int RB>
+int launch_combine(const AttendArgs& a, int grid, cudaStream_t s) {
+  LaunchScope ls(kProfKv4Attend, s);
+  return launch_k(combine_kernel<D, RB>, dim3(grid, RB / 8), dim3(4 * D), 0, s, true, a);
 }
 
 // Ring depth: about 52 KB of tiles, so that three CTAs of an SM keep more than
 // 100 KB in flight.
 template <int D> constexpr int stages() { return D == 128 ? 6 : 10; }
 
+// Rows of a sequence and kv head up to which the kernel here is used.
+constexpr int kNarrowRows = 32;
+
 struct Plan {
   int rb, grid;
 };
 
-// Row block: the fewest steps of 8 rows (up to 32) that hold a sequence's rows.
+// Row block: the fewest steps of 8 rows (up to 32) that hold a sequence's
+// rows, or 128 and the tcgen05 kernel.
 Plan plan_of(const kv4_attn_cfg& cfg, const Cache& c) {
   const long long rows = static_cast<long long>(cfg.max_q) * (cfg.n_q_heads / c.Hkv);
   Plan p;
-  p.rb = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
-  p.grid = sm_count() * (p.rb == 32 ? 2 : 3);
+  p.rb = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= kNarrowRows ? 32 : kWideRows;
+  p.grid = p.rb == kWideRows ? wide_grid() : sm_count() * (p.rb == 32 ? 2 : 3);
   return p;
 }
 
@@ -506,8 +429,7 @@ int launch_attend(const AttendArgs& a, const Plan& p, cudaStream_t s) {
     st = launch_k(k, dim3(p.grid), dim3(kThreads), smem, s, false, a);
   }
   if (st != MOE_OK) return st;
-  LaunchScope ls(kProfKv4Attend, s);
-  return launch_k(combine_kernel<D, 8 * NT>, dim3(p.grid), dim3(128), 0, s, true, a);
+  return launch_combine<D, 8 * NT>(a, p.grid, s);
 }
 
 }  // namespace
@@ -556,6 +478,11 @@ extern "C" int kv4_attend(const kv4_cache* cache, const void* q, const int32_t* 
                static_cast<float*>(workspace),
                reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + part_bytes(p, c)), dev_err};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (p.rb == kWideRows) {
+    st = wide_launch(a, p.grid, s);
+    if (st != MOE_OK) return st;
+    return c.D == 128 ? launch_combine<128, kWideRows>(a, p.grid, s) : launch_combine<64, kWideRows>(a, p.grid, s);
+  }
   if (c.D == 128)
     return p.rb == 8 ? launch_attend<128, 1>(a, p, s) : p.rb == 16 ? launch_attend<128, 2>(a, p, s) : launch_attend<128, 4>(a, p, s);
   return p.rb == 8 ? launch_attend<64, 1>(a, p, s) : p.rb == 16 ? launch_attend<64, 2>(a, p, s) : launch_attend<64, 4>(a, p, s);

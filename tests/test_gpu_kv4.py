@@ -101,7 +101,8 @@ ATTEND = [  # (Hq, Hkv, D, page, base lengths, new tokens, tree)
     (6, 2, 128, 256, [255, 256, 257], [2, 0, 3], False), (16, 16, 64, 32, [77], [28], True),
     (24, 1, 128, 32, [500], [6], True), (4, 2, 64, 64, [70], [64], True), (8, 2, 128, 16, [33, 0], [100, 70], False),
     (8, 1, 64, 64, [190], [150], False), (2, 1, 128, 64, [5000], [1], False), (32, 8, 64, 64, [3000, 1, 700], [1, 1, 1], False),
-    (40, 8, 128, 64, [0, 0, 0, 0], [1, 2, 3, 4], True)]
+    (40, 8, 128, 64, [0, 0, 0, 0], [1, 2, 3, 4], True), (64, 2, 128, 64, [9000, 4000], [5, 3], True),
+    (32, 1, 64, 16, [2500], [17], False), (16, 2, 128, 256, [0], [300], False), (64, 1, 64, 128, [700, 65], [2, 3], True)]
 
 
 @pytest.mark.parametrize("Hq,Hkv,D,page,base,new,tree", ATTEND)
@@ -122,44 +123,49 @@ def test_max_q_chooses_the_kernel_only(mv, max_q):
     check_attention(mv, pg, cache, q, new, base, 0.2, np.concatenate([make_tree(rng, n) for n in new]), max_q=max_q)
 
 
-@pytest.mark.parametrize("spread,scale", [(1e-3, 100.0), (200.0, 1e-4), (1.0, 4.0), (1.0, 0.0), (1.0, -0.3)])
-def test_ranges_of_values_and_scores(mv, spread, scale):
+@pytest.mark.parametrize("max_q", [None, 64])  # the second: the kernel for many rows
+@pytest.mark.parametrize("spread,scale", [(1e-5, 3e3), (1e-3, 100.0), (200.0, 1e-4), (1.0, 4.0), (1.0, 0.0), (1.0, -0.3)])
+def test_ranges_of_values_and_scores(mv, spread, scale, max_q):
     """Tiny and large values (scales across fp16), one-sided softmaxes, a zero and a negative factor."""
     rng = np.random.default_rng(9)
     base, new = [400], [2]
     pg, cache = make_cache(mv, rng, [402], 2, 128, 64, spread=spread)
-    check_attention(mv, pg, cache, rng.standard_normal((2, 8, 128)), new, base, scale, None)
+    check_attention(mv, pg, cache, rng.standard_normal((2, 8, 128)), new, base, scale, None, max_q=max_q)
 
 
-def test_query_magnitudes(mv):
+@pytest.mark.parametrize("max_q", [None, 64])
+def test_query_magnitudes(mv, max_q):
     """Rows of q from 2^-100 to 2^60 beside each other: each is scaled by its own power of two."""
     rng = np.random.default_rng(10)
     pg, cache = make_cache(mv, rng, [130], 1, 128, 64, spread=0.01)
     q = rng.standard_normal((1, 8, 128)) * np.array([2.0 ** e for e in (-100, -40, -10, 0, 4, 6, 8, 10)])[None, :, None]
-    check_attention(mv, pg, cache, q, [1], [129], 0.05, None)
+    check_attention(mv, pg, cache, q, [1], [129], 0.05, None, max_q=max_q)
 
 
-def test_constant_rows_have_zero_scale(mv):
+@pytest.mark.parametrize("max_q", [None, 64])
+def test_constant_rows_have_zero_scale(mv, max_q):
     rng = np.random.default_rng(11)
     pg, cache = make_cache(mv, rng, [40], 1, 64, 16)
     for j in (3, 17, 39):
         pg.write(0, j, 1, np.full((1, 64), 0.75))
         pg.write(0, j, 0, np.full((1, 64), -0.5))
     cache.pages.copy_(torch.from_numpy(pg.raw))
-    check_attention(mv, pg, cache, rng.standard_normal((1, 8, 64)) * 2, [1], [39], 0.125, None)
+    check_attention(mv, pg, cache, rng.standard_normal((1, 8, 64)) * 2, [1], [39], 0.125, None, max_q=max_q)
 
 
-def test_all_rows_constant(mv):
+@pytest.mark.parametrize("max_q", [None, 64])
+def test_all_rows_constant(mv, max_q):
     """Every value row constant: the output is the softmax mean of the zeros."""
     rng = np.random.default_rng(12)
     pg, cache = make_cache(mv, rng, [70], 2, 64, 32)
     for j in range(70):
         pg.write(0, j, 1, np.repeat(rng.standard_normal((2, 1)) * 1e-3, 64, 1))
     cache.pages.copy_(torch.from_numpy(pg.raw))
-    check_attention(mv, pg, cache, rng.standard_normal((3, 8, 64)), [3], [67], 0.125, None)
+    check_attention(mv, pg, cache, rng.standard_normal((3, 8, 64)), [3], [67], 0.125, None, max_q=max_q)
 
 
-def test_empty_rows_and_nan_in_masked_slots(mv):
+@pytest.mark.parametrize("max_q", [5, 64])
+def test_empty_rows_and_nan_in_masked_slots(mv, max_q):
     """A tree token whose key and value are NaN is seen by itself alone; a padding token sees nothing."""
     rng = np.random.default_rng(13)
     base, new = [30, 0], [5, 4]
@@ -171,11 +177,11 @@ def test_empty_rows_and_nan_in_masked_slots(mv):
     cache.pages.copy_(torch.from_numpy(pg.raw))
     q = rng.standard_normal((9, 8, 64))
     q_start = dev(np.array([0, 5, 9], np.int32))
-    out, lse = mv.kv4_attend(cache, bf16(q).cuda(), q_start, dev(np.array(base, np.int32)), 5, visible=dev(vis), scale=0.2)
+    out, lse = mv.kv4_attend(cache, bf16(q).cuda(), q_start, dev(np.array(base, np.int32)), max_q, visible=dev(vis), scale=0.2)
     mass = cache.new_mass()
     clean = lse.clone()
     clean[2] = float("-inf")
-    mv.kv4_weigh(cache, bf16(q).cuda(), q_start, dev(np.array(base, np.int32)), 5, clean, mass, visible=dev(vis), scale=0.2)
+    mv.kv4_weigh(cache, bf16(q).cuda(), q_start, dev(np.array(base, np.int32)), max_q, clean, mass, visible=dev(vis), scale=0.2)
     torch.cuda.synchronize()
     o, l = out.float().cpu().numpy(), lse.cpu().numpy()
     assert np.isnan(o[2]).all() and np.isnan(l[2]).all()
@@ -193,33 +199,35 @@ def test_empty_rows_and_nan_in_masked_slots(mv):
     assert np.all(np.abs(o[keep] - ref[0][keep]) <= ref[3][keep])
 
 
-def test_nan_query_rows_stay_alone(mv):
+@pytest.mark.parametrize("max_q", [2, 64])
+def test_nan_query_rows_stay_alone(mv, max_q):
     rng = np.random.default_rng(14)
     pg, cache = make_cache(mv, rng, [50], 1, 128, 16)
     q = rng.standard_normal((2, 4, 128))
     q[0, 1, 5], q[1, 2, 9] = np.nan, np.inf
-    out, lse = mv.kv4_attend(cache, bf16(q).cuda(), dev(np.array([0, 2], np.int32)), dev(np.array([48], np.int32)), 2)
+    out, lse = mv.kv4_attend(cache, bf16(q).cuda(), dev(np.array([0, 2], np.int32)), dev(np.array([48], np.int32)), max_q)
     o = out.float().cpu().numpy()
     assert np.isnan(o[0, 1]).all() and np.isnan(o[1, 2]).all()
     o[0, 1] = o[1, 2] = 0
     assert np.isfinite(o).all()
 
 
-def test_bad_pages_and_lengths_are_flagged_and_left_out(mv):
+@pytest.mark.parametrize("max_q", [None, 64])
+def test_bad_pages_and_lengths_are_flagged_and_left_out(mv, max_q):
     rng = np.random.default_rng(15)
     base, new = [100, 40], [2, 2]
     pg, cache = make_cache(mv, rng, [102, 42], 2, 64, 16)
     pg.table[0, 2], pg.table[1, 0] = 10 ** 6, -5
     cache.table.copy_(torch.from_numpy(pg.table))
-    check_attention(mv, pg, cache, rng.standard_normal((4, 4, 64)), new, base, 0.2, None, err_want=mv._lib.DEV_BAD_ID)
+    check_attention(mv, pg, cache, rng.standard_normal((4, 4, 64)), new, base, 0.2, None, err_want=mv._lib.DEV_BAD_ID, max_q=max_q)
     err = mv.new_dev_err()
     out = torch.full((4, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
     mv.kv4_attend(cache, bf16(rng.standard_normal((4, 4, 64))).cuda(), dev(np.array([0, 2, 4], np.int32)),
-                  dev(np.array([100, cache.max_slots - 1], np.int32)), 2, out=out, dev_err=err)
+                  dev(np.array([100, cache.max_slots - 1], np.int32)), max_q or 2, out=out, dev_err=err)
     torch.cuda.synchronize()
     assert err.item() & mv._lib.DEV_CAPACITY and bool((out[2:] == 7).all()) and not bool((out[:2] == 7).any())
     err.zero_()
-    mv.kv4_attend(cache, out, dev(np.array([0, 3, 2], np.int32)), dev(np.array([-1, 5], np.int32)), 2, dev_err=err)
+    mv.kv4_attend(cache, out, dev(np.array([0, 3, 2], np.int32)), dev(np.array([-1, 5], np.int32)), max_q or 2, dev_err=err)
     torch.cuda.synchronize()
     assert err.item() & mv._lib.DEV_CAPACITY
 
@@ -257,26 +265,27 @@ def test_pages_beyond_32_bit_offsets(mv):
     assert torch.equal(k, k2) and torch.equal(v, v2) and float((k - x).abs().max()) < 0.5
 
 
-def test_attend_in_a_graph(mv):
+@pytest.mark.parametrize("max_q", [2, 64])
+def test_attend_in_a_graph(mv, max_q):
     rng = np.random.default_rng(18)
     pg, cache = make_cache(mv, rng, [300, 40], 2, 64, 16)
     q = bf16(rng.standard_normal((4, 8, 64))).cuda()
     qs, base = dev(np.array([0, 2, 4], np.int32)), dev(np.array([298, 38], np.int32))
     out = torch.empty((4, 8, 64), dtype=torch.bfloat16, device="cuda")
     lse = torch.empty((4, 8), device="cuda")
-    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
-    want, _ = mv.kv4_attend(cache, q, qs, base, 2)
+    ws = torch.empty(1 << 27, dtype=torch.uint8, device="cuda")
+    want, _ = mv.kv4_attend(cache, q, qs, base, max_q)
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
-        mv.kv4_attend(cache, q, qs, base, 2, out=out, lse=lse, workspace=ws)
+        mv.kv4_attend(cache, q, qs, base, max_q, out=out, lse=lse, workspace=ws)
     out.zero_()
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
     base -= 20  # the lengths are read at replay time
     g.replay()
-    again, _ = mv.kv4_attend(cache, q, qs, base, 2)
+    again, _ = mv.kv4_attend(cache, q, qs, base, max_q)
     torch.cuda.synchronize()
     assert torch.equal(out, again) and not torch.equal(out, want)
 
