@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
     tc::fence_mbar_init();
   }
   pdl_wait();
-  build_units(a.c, a.q_start, a.base, a.T, a.G, RB, kTile, sm.cum, sm.scratch, a.dev_err, blockIdx.x == 0);
+  build_units(a.c, a.q_start, a.base, a.T, a.G, RB, kTile, kItemUnits, sm.cum, sm.scratch, a.dev_err, blockIdx.x == 0);
   pdl_trigger();
   const long long total = sm.cum[a.c.S];
   // At most one CTA per unit, so that every CTA up to the last one used owns some.
@@ -64,21 +64,27 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
   if (warp == kConsumerWarps) {
     // ---------------------------------------------------------- producer
     Cursor k;
-    TileLoader<D> loader;
+    TileLoader<D> loader(a.c);
     int stage = 0, phase = 0;
     long long issued = 0;
-    for (long long u = u0; u < u1; ++u) {
-      if (u == u0 || k.tile == k.nt)
-        cursor_at(k, a.c, a.q_start, a.base, a.T, a.G, RB, kTile, sm.cum, u);
+    if (u0 < u1) cursor_at(k, a.c, a.q_start, a.base, a.T, a.G, RB, kTile, kItemUnits, sm.cum, u0);
+    bool dead = false;
+    for (long long u = u0; u < u1 && !dead;) {
+     const Span sp = span_of<RB>(a, k, u, u1);
+     for (int it = 0; it < sp.tiles; ++it) {
       const bool ok = tc::mbar_wait_bounded(&sm.empty[stage], phase ^ 1, abort_flag, kWaitBudgetNs);
       if (__any_sync(0xFFFFFFFFu, !ok)) {
         *abort_flag = 1;
+        dead = true;
         break;
       }
       loader.load(a, k, sm.st[stage], &sm.groups[stage], &sm.full[stage]);
       ++issued;
       ++k.tile;
       if (++stage == NS) stage = 0, phase ^= 1;
+     }
+     u += sp.n;
+     if (u < u1) cursor_next(k, a.c, a.q_start, a.base, a.T, a.G, RB, kTile, kItemUnits, sm.cum);
     }
     if (*abort_flag) {
       // Copies in flight land before the CTA's shared memory goes.
@@ -92,14 +98,20 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
   // ------------------------------------------------------------ consumers
   const int g = lane >> 2, c = lane & 3;
   const int s0 = slot_of_row(g), s1 = slot_of_row(g + 8);
+  const TileMap<D> map(a.c);
+  const int k_at = map.k(16 * warp), v_at = map.v(16 * warp), p_at = map.p(16 * warp);
   int stage = 0, phase = 0;
   if (tid < 8) a.meta[static_cast<size_t>(cta) * 8 + tid] = 0;
+  Cursor k;
+  if (u0 < u1) cursor_at(k, a.c, a.q_start, a.base, a.T, a.G, RB, kTile, kItemUnits, sm.cum, u0);
   for (long long u = u0; u < u1;) {
-    Cursor k;
-    cursor_at(k, a.c, a.q_start, a.base, a.T, a.G, RB, kTile, sm.cum, u);
-    const long long item_end = k.item0 + k.nt;
-    const int n = static_cast<int>((item_end < u1 ? item_end : u1) - u);
-    const int row0 = k.rb * RB, rows = min(RB, k.q.nq * a.G - row0);
+    const Span sp = span_of<RB>(a, k, u, u1);
+    const int n = sp.tiles, row0 = sp.row0, rows = sp.rows;
+    if (n == 0) {
+      u += sp.n;
+      if (u < u1) cursor_next(k, a.c, a.q_start, a.base, a.T, a.G, RB, kTile, kItemUnits, sm.cum);
+      continue;
+    }
     prep_q<D>([&](int r) { return r < rows ? q_row(a, k.q, k.h, row0 + r) : (const uint16_t*)nullptr; }, RB, a.scale_log2, sm.frag, sm.cq,
               sm.cqs, tid, 32 * kConsumerWarps);
     if (tid < RB && a.visible) sm.mask[tid] = a.visible[k.q.q0 + (row0 + min(tid, rows - 1)) / a.G];
@@ -132,15 +144,15 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
       const int j0 = (k.tile + it) * kTile + 16 * warp;  // first slot of this warp's group
       if (!tc::mbar_wait_bounded(&sm.full[stage], phase, abort_flag, kWaitBudgetNs)) *abort_flag = 1;
       __syncwarp();
-      const Tile<D>& st = sm.st[stage];
+      const uint8_t* st = sm.st[stage].b;
       const bool any = j0 < k.q.total && ((sm.groups[stage] >> warp) & 1);
       if (any) {
         const bool edge = j0 + 16 > k.q.base;
         uint32_t ka[D / 32], kb[D / 32];
-        load_k_words<D>(st.k + (16 * warp + s0) * (D / 2), c, ka);
-        load_k_words<D>(st.k + (16 * warp + s1) * (D / 2), c, kb);
-        const uint2 ra = *reinterpret_cast<const uint2*>(st.p + (16 * warp + s0) * 8);
-        const uint2 rb = *reinterpret_cast<const uint2*>(st.p + (16 * warp + s1) * 8);
+        load_k_words<D>(st + k_at + s0 * (D / 2), c, ka);
+        load_k_words<D>(st + k_at + s1 * (D / 2), c, kb);
+        const uint2 ra = *reinterpret_cast<const uint2*>(st + p_at + s0 * 8);
+        const uint2 rb = *reinterpret_cast<const uint2*>(st + p_at + s1 * 8);
         float ks[2], kz[2], lv[2], rs[2], zr[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -225,7 +237,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
         }
         // Values: lane (g, c) owns k indices 2c, 2c+1, 2c+8, 2c+9 and the
         // dimensions g * D/8 ..; one byte permute pairs two slots' halves.
-        const uint8_t* vb = st.v + 16 * warp * (D / 2) + g * (D / 16);
+        const uint8_t* vb = st + v_at + g * (D / 16);
         const int v0 = slot_of_row(2 * c), v1 = slot_of_row(2 * c + 1);
         if constexpr (D == 128) {
           uint2 w[4];
@@ -316,7 +328,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
       }
       tc::named_bar_sync(1, 32 * kConsumerWarps);
     }
-    const bool whole = u == k.item0 && u + n == item_end;
+    const bool whole = sp.whole;
     for (int i = tid; i < rows * (D / 2); i += 32 * kConsumerWarps) {
       const int r = i / (D / 2), d = 2 * (i % (D / 2));
       float mm = sm.m[0][r];
@@ -345,9 +357,10 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
         }
       }
     }
-    if (!whole && u == k.item0 && tid == 0) note_cut(a, cta, ncta, total, k, row0, rows, item_end, u == u0 ? 0 : 1);
+    if (!whole && sp.first && tid == 0) note_cut(a, cta, ncta, total, k, sp, u, u == u0 ? 0 : 1);
     tc::named_bar_sync(1, 32 * kConsumerWarps);
-    u += n;
+    u += sp.n;
+    if (u < u1) cursor_next(k, a.c, a.q_start, a.base, a.T, a.G, RB, kTile, kItemUnits, sm.cum);
   }
 }
 
@@ -478,11 +491,7 @@ extern "C" int kv4_attend(const kv4_cache* cache, const void* q, const int32_t* 
                static_cast<float*>(workspace),
                reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + part_bytes(p, c)), dev_err};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (p.rb == kWideRows) {
-    st = wide_launch(a, p.grid, s);
-    if (st != MOE_OK) return st;
-    return c.D == 128 ? launch_combine<128, kWideRows>(a, p.grid, s) : launch_combine<64, kWideRows>(a, p.grid, s);
-  }
+  if (p.rb == kWideRows) return wide_launch(a, p.grid, s);
   if (c.D == 128)
     return p.rb == 8 ? launch_attend<128, 1>(a, p, s) : p.rb == 16 ? launch_attend<128, 2>(a, p, s) : launch_attend<128, 4>(a, p, s);
   return p.rb == 8 ? launch_attend<64, 1>(a, p, s) : p.rb == 16 ? launch_attend<64, 2>(a, p, s) : launch_attend<64, 4>(a, p, s);

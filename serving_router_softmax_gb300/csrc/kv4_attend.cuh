@@ -27,7 +27,8 @@ struct AttendArgs {
   int32_t* dev_err;
 };
 
-// One row block's partial sums: outputs [RB][D], running maxima [RB], sums [RB].
+// One row block's partial sums: outputs [RB][D] (the wide kernel: [D][RB], columns as they lie in TMEM), running
+// maxima [RB], sums [RB].
 template <int D, int RB>
 constexpr size_t part_floats() { return static_cast<size_t>(RB) * (D + 2); }
 
@@ -67,65 +68,115 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-// A tile as it lies in the cache: codes and parameters of 64 slots.
+// A tile in shared memory: one segment per page (64 slots of it at most),
+// laid out as a page block is: K codes, V codes, parameters.  So a page of up
+// to 64 slots comes in one copy.
 template <int D>
 struct Tile {
-  alignas(128) uint8_t k[kTile * D / 2];
-  uint8_t v[kTile * D / 2];
-  uint8_t p[kTile * 8];
+  alignas(128) uint8_t b[kTile * (D + 8)];
 };
 
-// Page lookup and copies of tiles, one warp.
+// Where a tile's rows lie.
+template <int D>
+struct TileMap {
+  int seg_log2, seg;
+  __device__ __forceinline__ explicit TileMap(const Cache& c) : seg_log2(min(c.page_log2, 6)), seg(1 << seg_log2) {}
+  __device__ __forceinline__ int base(int r) const { return (r >> seg_log2) * (seg * (D + 8)); }
+  __device__ __forceinline__ int k(int r) const { return base(r) + (r & (seg - 1)) * (D / 2); }
+  __device__ __forceinline__ int v(int r) const { return base(r) + (seg + (r & (seg - 1))) * (D / 2); }
+  __device__ __forceinline__ int p(int r) const { return base(r) + seg * D + (r & (seg - 1)) * 8; }
+};
+
+// Units that an item costs beyond its tiles (query rows in, sums out).
+constexpr int kItemUnits = 2;
+
+// Page lookup and copies of tiles, one warp.  A lone warp's instructions wait
+// for each other, so what does not change from tile to tile is kept.
 template <int D>
 struct TileLoader {
-  int cached_s = -1, cached_at = 0, cached = -1;
+  int seg_log2, nseg, lane;
+  int s = -1, h = -1, cached_at = 0, cached = -1;
+  const uint8_t* head;     // block of page 0, head h
+  size_t stride;           // bytes from page to page
+
+  __device__ __forceinline__ explicit TileLoader(const Cache& c) {
+    seg_log2 = min(c.page_log2, 6);
+    nseg = kTile >> seg_log2;
+    lane = threadIdx.x & 31;
+    stride = static_cast<size_t>(c.Hkv) * c.block_bytes();
+  }
 
   // Starts the copies of the cursor's tile into st; *groups gets the valid
   // slot groups before `full` completes.  Whole warp.
   __device__ __forceinline__ void load(const AttendArgs& a, const Cursor& k, Tile<D>& st, uint32_t* groups, uint64_t* full) {
-    const int lane = threadIdx.x & 31;
-    const int seg_rows = a.c.page_size < kTile ? a.c.page_size : kTile;
-    const int nseg = kTile / seg_rows;
-    // One table entry per lane, 32 pages ahead.
     const int p0 = (k.tile * kTile) >> a.c.page_log2;
-    if (k.s != cached_s || p0 < cached_at || p0 + nseg > cached_at + 32) {
-      cached_s = k.s;
+    if (k.s != s || k.h != h || p0 < cached_at || p0 + nseg > cached_at + 32) {
+      // One table entry per lane, 32 pages ahead.
+      s = k.s;
+      h = k.h;
       cached_at = p0;
       cached = page_of(a.c, k.s, (p0 + lane) << a.c.page_log2);
+      head = a.c.pages + static_cast<size_t>(k.h) * a.c.block_bytes();
     }
-    int page = __shfl_sync(0xFFFFFFFFu, cached, (p0 + lane % nseg - cached_at) & 31);
-    const int j0 = k.tile * kTile + (lane % nseg) * seg_rows;  // first slot of this lane's segment
-    if (j0 >= k.q.total) page = -1;
-    const uint32_t have = __ballot_sync(0xFFFFFFFFu, lane < nseg && page >= 0);
-    const bool broken = __any_sync(0xFFFFFFFFu, lane < nseg && page < 0 && j0 < k.q.total);
+    const int i = lane & (nseg - 1);
+    int page = __shfl_sync(0xFFFFFFFFu, cached, p0 + i - cached_at);
+    const bool want = lane < nseg && k.tile * kTile + (i << seg_log2) < k.q.total;
+    const bool have = want && page >= 0;
+    const uint32_t hv = __ballot_sync(0xFFFFFFFFu, have);
+    const uint32_t bytes = (D + 8) << seg_log2;
     if (lane == 0) {
-      uint32_t gr = 0;
-      for (int i = 0; i < nseg; ++i)
-        if ((have >> i) & 1) gr |= ((1u << (seg_rows / 16)) - 1u) << (i * (seg_rows / 16));
+      uint32_t gr = 15;
+      if (__popc(hv) < nseg) gr = 0;
+      for (uint32_t x = gr ? 0 : hv; x; x &= x - 1) gr |= ((1u << (1 << (seg_log2 - 4))) - 1u) << ((__ffs(x) - 1) << (seg_log2 - 4));
       *groups = gr;
-      if (broken) flag_error(a.dev_err, MOE_DEV_BAD_ID);
-      tc::mbar_arrive_expect_tx(full, __popc(have) * seg_rows * (D + 8));
+      tc::mbar_arrive_expect_tx(full, __popc(hv) * bytes);
     }
+    if (want && page < 0) flag_error(a.dev_err, MOE_DEV_BAD_ID);
     __syncwarp();
-    if (lane < nseg && page >= 0) {
-      const uint8_t* b = page_block(a.c, page, k.h);
-      const int r0 = j0 & (a.c.page_size - 1);
-      bulk_copy(st.k + lane * seg_rows * (D / 2), b + static_cast<size_t>(r0) * (D / 2), seg_rows * (D / 2), full);
-      bulk_copy(st.v + lane * seg_rows * (D / 2), b + static_cast<size_t>(a.c.page_size + r0) * (D / 2), seg_rows * (D / 2), full);
-      bulk_copy(st.p + lane * seg_rows * 8, b + static_cast<size_t>(a.c.page_size) * D + r0 * 8, seg_rows * 8, full);
+    if (!have) return;
+    const uint8_t* b = head + page * stride;
+    uint8_t* dst = st.b + lane * bytes;
+    if (a.c.page_log2 <= 6) {
+      bulk_copy(dst, b, bytes, full);
+    } else {
+      const int r0 = (k.tile * kTile) & (a.c.page_size - 1);
+      bulk_copy(dst, b + r0 * (D / 2), kTile * (D / 2), full);
+      bulk_copy(dst + kTile * (D / 2), b + (a.c.page_size + r0) * (D / 2), kTile * (D / 2), full);
+      bulk_copy(dst + kTile * D, b + a.c.page_size * D + r0 * 8, kTile * 8, full);
     }
   }
 };
 
-// Notes an item that starts in this CTA and ends in a later one.
-__device__ __forceinline__ void note_cut(const AttendArgs& a, int cta, int ncta, long long total, const Cursor& k, int row0,
-                                         int rows, long long item_end, int slot) {
+// The part of the unit order that a CTA does in one item.
+struct Span {
+  int row0, rows;    // the block's query rows
+  int need;          // tiles that one of its rows can see
+  int n, tiles;      // units of the item that are this CTA's, tiles among them
+  bool first, whole; // it has the item's first tile; all of them
+};
+template <int RB>
+__device__ __forceinline__ Span span_of(const AttendArgs& a, const Cursor& k, long long u, long long u1) {
+  Span s;
+  s.n = static_cast<int>(u1 - u < k.nt - k.tile ? u1 - u : k.nt - k.tile);
+  s.row0 = k.rb * RB;
+  s.rows = min(RB, k.q.nq * a.G - s.row0);
+  const int seen = a.visible ? k.q.total : min(k.q.total, k.q.base + (s.row0 + s.rows - 1) / a.G + 1);
+  s.need = (seen + kTile - 1) / kTile;
+  s.tiles = max(0, min(s.n, s.need - k.tile));
+  s.first = k.tile == 0;
+  s.whole = s.first && s.tiles == s.need;
+  return s;
+}
+
+// Notes an item that starts in this CTA and ends in a later one; u is the item's first unit.
+__device__ __forceinline__ void note_cut(const AttendArgs& a, int cta, int ncta, long long total, const Cursor& k,
+                                         const Span& s, long long u, int slot) {
   int32_t* M = a.meta + static_cast<size_t>(cta) * 8;
   M[1] = k.s;
   M[2] = k.h;
-  M[3] = row0;
-  M[4] = rows;
-  M[5] = static_cast<int>((item_end * ncta - 1) / total);  // the CTA that owns the item's last unit
+  M[3] = s.row0;
+  M[4] = s.rows;
+  M[5] = static_cast<int>(((u + s.need) * ncta - 1) / total);  // the CTA that owns the item's last tile
   M[6] = slot;
   M[0] = 1;
 }
@@ -133,7 +184,7 @@ __device__ __forceinline__ void note_cut(const AttendArgs& a, int cta, int ncta,
 constexpr int kWideRows = 128;
 // The tensor-core kernel (tcgen05) for row blocks of 128.
 int wide_grid();
-int wide_launch(const AttendArgs& a, int grid, cudaStream_t s);
+int wide_launch(const AttendArgs& a, int grid, cudaStream_t s);  // with its combine kernel
 
 }  // namespace kv4
 }  // namespace moe

@@ -14,9 +14,10 @@
 // 2^(t - m + E).
 //
 // Roles: warps 0-3 softmax and output (a thread per row), warps 4-7 unpack,
-// warp 8 copies tiles, warp 9 issues the products.  256 TMEM columns (Q, S / P,
-// O) and half the shared memory: two CTAs share an SM, and one's products
-// run while the other's exponentials do.  Bound by the exponentials (16 a
+// warp 8 issues the products, warp 9 copies tiles.  The scores of a tile come in two halves of 32 slots, each with its own
+// columns (its P over its S), so that one half's products run while the other's
+// exponentials do.  256 TMEM columns (Q, S / P, O), half the shared memory and 96
+// registers a thread: two CTAs share an SM.  Bound by the exponentials (16 a
 // clock and SM: 8 clocks per slot of 128 rows) and as much by the products (8).
 #include "kv4_attend.cuh"
 
@@ -24,9 +25,10 @@ namespace moe {
 namespace kv4 {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kRaw = 4;       // tiles in flight
+constexpr int kThreads = 320;
+constexpr int kRaw = 3;       // tiles in flight
 constexpr uint32_t kTmemCols = 256;
+constexpr int kHalf = kTile / 2;
 
 template <int D>
 struct Smem {
@@ -38,8 +40,9 @@ struct Smem {
   alignas(16) float vz[2][kTile];               // times 2^-E
   float e[2];                                    // the tile's E
   uint32_t raw_groups[kRaw], groups[2];
+  alignas(16) uint8_t stage[4][32 * 80];          // per softmax warp: 32 dimensions of its 32 query rows
   alignas(16) uint32_t vs[4][kTile / 2];         // per unpacking warp: scales times 2^-E of slot pairs
-  uint64_t raw_full[kRaw], raw_empty[kRaw], kv_full[2], kv_empty[2], q_full, s_full, p_full, pv_done;
+  uint64_t raw_full[kRaw], raw_empty[kRaw], kv_full[2], kv_empty[2], q_full, s_full[2], p_full[2], pv_done[2];
   long long scratch[32];
   uint32_t tmem;
   int abort, never;
@@ -68,19 +71,19 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
-  uint32_t r[8];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+// 32 columns of the thread's lane, waited for.
+__device__ __forceinline__ void tmem_ld_pairs(uint32_t taddr, float2 (&e)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(e[0].x), "=f"(e[0].y), "=f"(e[1].x), "=f"(e[1].y), "=f"(e[2].x), "=f"(e[2].y), "=f"(e[3].x), "=f"(e[3].y),
+        "=f"(e[4].x), "=f"(e[4].y), "=f"(e[5].x), "=f"(e[5].y), "=f"(e[6].x), "=f"(e[6].y), "=f"(e[7].x), "=f"(e[7].y),
+        "=f"(e[8].x), "=f"(e[8].y), "=f"(e[9].x), "=f"(e[9].y), "=f"(e[10].x), "=f"(e[10].y), "=f"(e[11].x),
+        "=f"(e[11].y), "=f"(e[12].x), "=f"(e[12].y), "=f"(e[13].x), "=f"(e[13].y), "=f"(e[14].x), "=f"(e[14].y),
+        "=f"(e[15].x), "=f"(e[15].y)
+      : "r"(taddr));
+  tc::tmem_ld_wait();
 }
-
-template <int N>
-__device__ __forceinline__ void set_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void set_regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
@@ -103,25 +106,10 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return r;
 }
 
-// The part of the unit order that a CTA does in one item.
-struct Span {
-  Cursor k;
-  int row0, rows;
-  int n;              // units of the item that are this CTA's
-  int tiles;          // of them, those that a row of the block can see
-  long long item_end;
-};
-__device__ __forceinline__ Span span_at(const AttendArgs& a, const long long* cum, long long u, long long u1) {
-  Span s;
-  cursor_at(s.k, a.c, a.q_start, a.base, a.T, a.G, kWideRows, kTile, cum, u);
-  s.item_end = s.k.item0 + s.k.nt;
-  s.n = static_cast<int>((s.item_end < u1 ? s.item_end : u1) - u);
-  s.row0 = s.k.rb * kWideRows;
-  s.rows = min(kWideRows, s.k.q.nq * a.G - s.row0);
-  int need = s.k.nt;
-  if (!a.visible) need = (min(s.k.q.total, s.k.q.base + (s.row0 + s.rows - 1) / a.G + 1) + kTile - 1) / kTile;
-  s.tiles = max(0, min(s.n, need - s.k.tile));
-  return s;
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // Ring position of a pipeline of N stages.
@@ -149,11 +137,11 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sm.kv_full[i], 128);
       tc::mbar_init(&sm.kv_empty[i], 1);
+      tc::mbar_init(&sm.s_full[i], 1);
+      tc::mbar_init(&sm.p_full[i], 128);
+      tc::mbar_init(&sm.pv_done[i], 1);
     }
     tc::mbar_init(&sm.q_full, 128);
-    tc::mbar_init(&sm.s_full, 1);
-    tc::mbar_init(&sm.p_full, 128);
-    tc::mbar_init(&sm.pv_done, 1);
     sm.abort = sm.never = 0;
     tc::fence_mbar_init();
   }
@@ -163,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
   }
   tc::tc_fence_before();
   pdl_wait();
-  build_units(a.c, a.q_start, a.base, a.T, a.G, kWideRows, kTile, sm.cum, sm.scratch, a.dev_err, blockIdx.x == 0);
+  build_units(a.c, a.q_start, a.base, a.T, a.G, kWideRows, kTile, kItemUnits, sm.cum, sm.scratch, a.dev_err, blockIdx.x == 0);
   tc::tc_fence_after();
   pdl_trigger();
   const uint32_t tmem = sm.tmem;
@@ -171,6 +159,8 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
   const int ncta = static_cast<int>(total < gridDim.x ? total : gridDim.x), cta = blockIdx.x;
   const long long u0 = cta < ncta ? total * cta / ncta : 0, u1 = cta < ncta ? total * (cta + 1) / ncta : 0;
   volatile int* abort_flag = &sm.abort;
+  Cursor k;
+  if (u0 < u1) cursor_at(k, a.c, a.q_start, a.base, a.T, a.G, kWideRows, kTile, kItemUnits, sm.cum, u0);
   // Waits give up together: the first to run out tells the others.
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (tc::mbar_wait_bounded(bar, parity, abort_flag, kWaitBudgetNs)) return true;
@@ -178,148 +168,191 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
     return false;
   };
 
+  // The same answer in all lanes.
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
+
   if (warp < 4) {
     // ---------------------------------------------------------- softmax, output
-    set_regs_up<136>();
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t tq = tmem + lanes + kQCol, ts = tmem + lanes + kSCol, to = tmem + lanes + kOCol;
     if (tid < 8) a.meta[static_cast<size_t>(cta) * 8 + tid] = 0;
     Ring<2> kv;
     uint32_t sp = 0;  // parity of s_full, p_full and pv_done
     for (long long u = u0; u < u1;) {
-      const Span s = span_at(a, sm.cum, u, u1);
+      const Span s = span_of<kWideRows>(a, k, u, u1);
+      if (s.tiles == 0) {
+        u += s.n;
+        if (u < u1) cursor_next(k, a.c, a.q_start, a.base, a.T, a.G, kWideRows, kTile, kItemUnits, sm.cum);
+        continue;
+      }
       const int r = s.row0 + tid;
       const bool real = tid < s.rows;
       const int tok = (s.row0 + min(tid, s.rows - 1)) / a.G;
-      const uint64_t bits = a.visible ? a.visible[s.k.q.q0 + tok] : 0;
-      if (a.visible && s.k.q.nq > kMaxTree && tid == 0) flag_error(a.dev_err, MOE_DEV_CAPACITY);
+      const uint64_t bits = a.visible ? a.visible[k.q.q0 + tok] : 0;
+      if (a.visible && k.q.nq > kMaxTree && tid == 0) flag_error(a.dev_err, MOE_DEV_CAPACITY);
       float m = 0.f, l = 0.f, z = 0.f, cq = 0.f, cqs = 0.f;
-      if (s.tiles > 0) {
-        // The row of q, scaled by a power of two and permuted as the key words are (see prep_q), into TMEM.
-        const uint4* src = real ? reinterpret_cast<const uint4*>(q_row(a, s.k.q, s.k.h, r)) : nullptr;
-        float mx = 0.f, sum = 0.f;
-        if (real) {
+      {
+        // The warp's 32 rows of q, scaled by powers of two and permuted as the key words are (see prep_q),
+        // into TMEM: four lanes load a row's 64 bytes together, the lane of the row stores them.
+        constexpr int C = D / 32;
+        const int lr = lane >> 2, x = lane & 3;
+        const uint16_t* src[4];
+        float mx[4] = {}, sum[4] = {};
 #pragma unroll
-          for (int i = 0; i < W; ++i) {
-            const uint4 x = src[i];
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        for (int i = 0; i < 4; ++i) {
+          const int rr = warp * 32 + 8 * i + lr;
+          src[i] = rr < s.rows ? q_row(a, k.q, k.h, s.row0 + rr) + 8 * x : nullptr;
+        }
+#pragma unroll 1
+        for (int c = 0; c < C; ++c) {
+          uint4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = src[i] ? *reinterpret_cast<const uint4*>(src[i] + 32 * c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const float lo = __uint_as_float(w[j] << 16), hi = __uint_as_float(w[j] & 0xFFFF0000u);
-              mx = fmaxf(mx, fmaxf(fabsf(lo), fabsf(hi)));
-              sum += lo + hi;
+              mx[i] = max3(mx[i], fabsf(lo), fabsf(hi));
+              sum[i] += lo + hi;
             }
           }
         }
-        const int ex = static_cast<int>(__float_as_uint(mx) >> 23);
-        const int e = mx > 0.f && ex < 255 ? 14 + 127 - (ex > 0 ? ex : 1) : 0;
-        const float f1 = __uint_as_float(static_cast<uint32_t>(127 + e / 2) << 23);
-        const float f2 = __uint_as_float(static_cast<uint32_t>(127 + e - e / 2) << 23);
-        cq = ldexpf(a.scale_log2, 24 - e);
-        cqs = a.scale_log2 * sum;
 #pragma unroll
-        for (int i = 0; i < W; i += 4) {
-          uint32_t c[16];
+        for (int i = 0; i < 4; ++i) {
+          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 1));
+          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 2));
+          sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 1);
+          sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 2);
+        }
+        int e[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 x = real ? src[i + j] : make_uint4(0, 0, 0, 0);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-            float v[8];
+        for (int i = 0; i < 4; ++i) {
+          const int ex = static_cast<int>(__float_as_uint(mx[i]) >> 23);
+          e[i] = mx[i] > 0.f && ex < 255 ? 14 + 127 - (ex > 0 ? ex : 1) : 0;
+          const int es = __shfl_sync(0xFFFFFFFFu, e[i], 4 * (lane & 7));
+          const float ss = __shfl_sync(0xFFFFFFFFu, sum[i], 4 * (lane & 7));
+          if (lane >> 3 == i) {
+            cq = ldexpf(a.scale_log2, 24 - es);
+            cqs = a.scale_log2 * ss;
+          }
+        }
+#pragma unroll 1
+        for (int c = 0; c < C; ++c) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 v = src[i] ? *reinterpret_cast<const uint4*>(src[i] + 32 * c) : make_uint4(0, 0, 0, 0);
+            const float f1 = __uint_as_float(static_cast<uint32_t>(127 + e[i] / 2) << 23);
+            const float f2 = __uint_as_float(static_cast<uint32_t>(127 + e[i] - e[i] / 2) << 23);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            float y[8];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-              v[2 * t] = __uint_as_float(w[t] << 16) * f1 * f2;
-              v[2 * t + 1] = __uint_as_float(w[t] & 0xFFFF0000u) * f1 * f2;
+              y[2 * t] = __uint_as_float(w[t] << 16) * f1 * f2;
+              y[2 * t + 1] = __uint_as_float(w[t] & 0xFFFF0000u) * f1 * f2;
             }
-            c[4 * j] = pack_h2(v[0], v[4]);
-            c[4 * j + 1] = pack_h2(v[1] * 0.0625f, v[5] * 0.0625f);
-            c[4 * j + 2] = pack_h2(v[2], v[6]);
-            c[4 * j + 3] = pack_h2(v[3] * 0.0625f, v[7] * 0.0625f);
+            *reinterpret_cast<uint4*>(sm.stage[warp] + (8 * i + lr) * 80 + 16 * x) =
+                make_uint4(pack_h2(y[0], y[4]), pack_h2(y[1] * 0.0625f, y[5] * 0.0625f), pack_h2(y[2], y[6]),
+                           pack_h2(y[3] * 0.0625f, y[7] * 0.0625f));
           }
-          tmem_st16(tq + 4 * i, c);
+          __syncwarp();
+          uint32_t o[16];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 y = *reinterpret_cast<const uint4*>(sm.stage[warp] + lane * 80 + 16 * j);
+            o[4 * j] = y.x, o[4 * j + 1] = y.y, o[4 * j + 2] = y.z, o[4 * j + 3] = y.w;
+          }
+          tmem_st16(tq + 16 * c, o);
+          __syncwarp();
         }
         tmem_st_wait();
         tc::tc_fence_before();
         tc::mbar_arrive(&sm.q_full);
       }
       bool dead = false;
-      for (int it = 0; it < s.tiles; ++it) {
-        const int j0 = (s.k.tile + it) * kTile;
-        if (!wait(&sm.kv_full[kv.i], kv.phase) || !wait(&sm.s_full, sp)) {
+      for (int it = 0; it < s.tiles && !dead; ++it) {
+        const int j0 = (k.tile + it) * kTile;
+        if (!wait_warp(&sm.kv_full[kv.i], kv.phase)) {
           dead = true;
           break;
         }
-        tc::tc_fence_after();
-        const float E = sm.e[kv.i];
-        const float4* ks4 = reinterpret_cast<const float4*>(sm.ks[kv.i]);
-        const float4* kz4 = reinterpret_cast<const float4*>(sm.kz[kv.i]);
-        const float off = E - m;
-        const float2 cq2 = make_float2(cq, cq), cqs2 = make_float2(cqs, cqs), off2 = make_float2(off, off);
-        float2 d[kTile / 2];
-#pragma unroll
-        for (int c = 0; c < kTile; c += 16) {
-          float v[16];
-          tc::tmem_ld16(ts + c, v);
-          tc::tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const float4 s4 = ks4[(c + i) / 4], z4 = kz4[(c + i) / 4];
-            d[(c + i) / 2] = fma2(make_float2(s4.x, s4.y), mul2(make_float2(v[i], v[i + 1]), cq2),
-                                  fma2(make_float2(z4.x, z4.y), cqs2, off2));
-            d[(c + i) / 2 + 1] = fma2(make_float2(s4.z, s4.w), mul2(make_float2(v[i + 2], v[i + 3]), cq2),
-                                      fma2(make_float2(z4.z, z4.w), cqs2, off2));
-          }
-        }
+        const float E = sm.e[kv.i], down = ex2(-E);
         const uint32_t groups = sm.groups[kv.i];
-        if (j0 + kTile > s.k.q.base || groups != 15u) {
-          const uint64_t see = sees(s.k.q, a.visible != nullptr, bits, tok, j0) & group_mask(groups);
-          const uint32_t lo = static_cast<uint32_t>(see), hi = static_cast<uint32_t>(see >> 32);
-#pragma unroll
-          for (int i = 0; i < kTile / 2; ++i) {
-            const uint32_t w = i < 16 ? lo : hi;
-            if (!((w >> (2 * i & 31)) & 1)) d[i].x = -INFINITY;
-            if (!((w >> ((2 * i + 1) & 31)) & 1)) d[i].y = -INFINITY;
+        const bool edge = j0 + kTile > k.q.base || groups != 15u;
+        uint64_t see = 0;
+        if (edge) see = sees(k.q, a.visible != nullptr, bits, tok, j0) & group_mask(groups);
+        for (int h = 0; h < 2; ++h) {
+          if (!wait_warp(&sm.s_full[h], sp)) {
+            dead = true;
+            break;
           }
-        }
-        float mx[4];
+          tc::tc_fence_after();
+          const uint32_t tsh = ts + h * kHalf;
+          const float4* ks4 = reinterpret_cast<const float4*>(sm.ks[kv.i] + h * kHalf);
+          const float4* kz4 = reinterpret_cast<const float4*>(sm.kz[kv.i] + h * kHalf);
+          const float4* vz4 = reinterpret_cast<const float4*>(sm.vz[kv.i] + h * kHalf);
+          const float off = E - m;
+          const float2 cq2 = make_float2(cq, cq), cqs2 = make_float2(cqs, cqs), off2 = make_float2(off, off);
+          float2 d[kHalf / 2];
+          tmem_ld_pairs(tsh, d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mx[i] = fmaxf(d[i].x, d[i].y);
+          for (int i = 0; i < kHalf / 2; i += 2) {
+            const float4 s4 = ks4[i / 2], z4 = kz4[i / 2];
+            d[i] = fma2(make_float2(s4.x, s4.y), mul2(d[i], cq2), fma2(make_float2(z4.x, z4.y), cqs2, off2));
+            d[i + 1] = fma2(make_float2(s4.z, s4.w), mul2(d[i + 1], cq2), fma2(make_float2(z4.z, z4.w), cqs2, off2));
+          }
+          if (edge) {
+            const uint32_t w = static_cast<uint32_t>(h ? see >> 32 : see);
 #pragma unroll
-        for (int i = 4; i < kTile / 2; ++i) mx[i & 3] = fmaxf(mx[i & 3], fmaxf(d[i].x, d[i].y));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        // A row's first visible tile sets its maximum; later ones move it when it lags too far.
-        const bool first = l == 0.f && top > -INFINITY;
-        if (__any_sync(0xFFFFFFFFu, first || top > kLazy)) {
-          const float by = first ? top : fmaxf(top, 0.f);
-          const float f = first ? 1.f : ex2(-by);
-          const float2 by2 = make_float2(-by, -by);
-          m += by;
-          l *= f;
-          z *= f;
-#pragma unroll
-          for (int i = 0; i < kTile / 2; ++i) d[i] = add2(d[i], by2);
-          if (it > 0) {
-#pragma unroll
-            for (int c = 0; c < D; c += 8) {
-              float v[8];
-              tmem_ld8(to + c, v);
-              tc::tmem_ld_wait();
-              asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(to + c),
-                           "f"(v[0] * f), "f"(v[1] * f), "f"(v[2] * f), "f"(v[3] * f), "f"(v[4] * f), "f"(v[5] * f),
-                           "f"(v[6] * f), "f"(v[7] * f)
-                           : "memory");
+            for (int i = 0; i < kHalf / 2; ++i) {
+              if (!((w >> (2 * i)) & 1)) d[i].x = -INFINITY;
+              if (!((w >> (2 * i + 1)) & 1)) d[i].y = -INFINITY;
             }
           }
-        }
-        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0, z0 = sum0, z1 = sum0;
-        const float4* vz4 = reinterpret_cast<const float4*>(sm.vz[kv.i]);
+          float mx[4];
 #pragma unroll
-        for (int c = 0; c < kTile / 2; c += 16) {
+          for (int i = 0; i < 4; ++i) mx[i] = fmaxf(d[i].x, d[i].y);
+#pragma unroll
+          for (int i = 4; i < kHalf / 2; ++i) mx[i & 3] = max3(mx[i & 3], d[i].x, d[i].y);
+          const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+          // A row's first visible slots set its maximum; later ones move it when it lags too far.
+          const bool first = l == 0.f && top > -INFINITY;
+          if (__any_sync(0xFFFFFFFFu, first || top > kLazy)) {
+            const float by = first ? top : fmaxf(top, 0.f);
+            const float f = first ? 1.f : ex2(-by);
+            const float2 by2 = make_float2(-by, -by);
+            m += by;
+            l *= f;
+            z *= f;
+#pragma unroll
+            for (int i = 0; i < kHalf / 2; ++i) d[i] = add2(d[i], by2);
+            if (it > 0 || h > 0) {
+              // The half before has been summed into O first.
+              if (!wait_warp(&sm.pv_done[h ^ 1], h ? sp : sp ^ 1)) {
+                dead = true;
+                break;
+              }
+              tc::tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                float v[16];
+                uint32_t x[16];
+                tc::tmem_ld16(to + c, v);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(v[i] * f);
+                tmem_st16(to + c, x);
+              }
+            }
+          }
+          float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0, z0 = sum0, z1 = sum0;
           uint32_t p[16];
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            const float2 x = make_float2(ex2(d[c + i].x), ex2(d[c + i].y));
-            const float2 y = make_float2(ex2(d[c + i + 1].x), ex2(d[c + i + 1].y));
-            const float4 zz = vz4[(c + i) / 2];
+            const float2 x = make_float2(ex2(d[i].x), ex2(d[i].y));
+            const float2 y = make_float2(ex2(d[i + 1].x), ex2(d[i + 1].y));
+            const float4 zz = vz4[i / 2];
             sum0 = add2(sum0, x);
             sum1 = add2(sum1, y);
             z0 = fma2(x, make_float2(zz.x, zz.y), z0);
@@ -327,39 +360,37 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
             p[i] = pack_h2(x.x, x.y);
             p[i + 1] = pack_h2(y.x, y.y);
           }
-          tmem_st16(ts + c, p);
+          tmem_st16(tsh, p);
+          sum0 = add2(sum0, sum1);
+          z0 = add2(z0, z1);
+          z += z0.x + z0.y;
+          l = fmaf(sum0.x + sum0.y, down, l);
+          tmem_st_wait();
+          tc::tc_fence_before();
+          tc::mbar_arrive(&sm.p_full[h]);
         }
-        sum0 = add2(sum0, sum1);
-        z0 = add2(z0, z1);
-        z += z0.x + z0.y;
-        l = fmaf(sum0.x + sum0.y, ex2(-E), l);
-        tmem_st_wait();
-        tc::tc_fence_before();
-        tc::mbar_arrive(&sm.p_full);
         kv.next();
         sp ^= 1;
       }
       if (dead) break;
-      // The item's last product has been summed when pv_done is at the parity of its last tile.
-      if (s.tiles > 0) {
-        if (!wait(&sm.pv_done, sp ^ 1)) break;
-        tc::tc_fence_after();
-      }
-      const bool whole = u == s.k.item0 && u + s.n == s.item_end;
+      // The item's products have been summed when pv_done is at the parity of its last tile.
+      if (!wait_warp(&sm.pv_done[0], sp ^ 1) || !wait_warp(&sm.pv_done[1], sp ^ 1)) break;
+      tc::tc_fence_after();
+      const bool whole = s.whole;
       const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
       float* P = a.part + (static_cast<size_t>(cta) * 2 + (u == u0 ? 0 : 1)) * part_floats<D, kWideRows>();
-      const size_t at = (static_cast<size_t>(s.k.q.q0) + tok) * a.Hq + s.k.h * a.G + r % a.G;
-      // TMEM column n * W + w is dimension 8 w + n.
-#pragma unroll
+      const size_t at = (static_cast<size_t>(k.q.q0) + tok) * a.Hq + k.h * a.G + r % a.G;
+      // TMEM column n * W + w is dimension 8 w + n.  (Loops that run once an item stay rolled: a cold
+      // instruction costs about 10 clocks.)
+#pragma unroll 1
       for (int w0 = 0; w0 < W; w0 += 4) {
         float o[8][4];
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
-          uint32_t x[4] = {0, 0, 0, 0};
-          if (s.tiles > 0)
-            asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                         : "r"(to + n * W + w0));
+          uint32_t x[4];
+          asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                       : "r"(to + n * W + w0));
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[n][j] = __uint_as_float(x[j]);
         }
@@ -369,18 +400,22 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
         for (int n = 0; n < 8; ++n)
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[n][j] += z;
+        if (!whole) {
+          // Lanes are rows: a column of the block is 128 floats side by side.
+#pragma unroll
+          for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) P[(n * W + w0 + j) * kWideRows + tid] = o[n][j];
+          continue;
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if (whole) {
+          {
             uint32_t b[4];
 #pragma unroll
             for (int n = 0; n < 4; ++n)
               asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b[n]) : "f"(o[2 * n + 1][j] * inv), "f"(o[2 * n][j] * inv));
             *reinterpret_cast<uint4*>(a.out + at * D + 8 * (w0 + j)) = make_uint4(b[0], b[1], b[2], b[3]);
-          } else {
-            float4* x = reinterpret_cast<float4*>(P + tid * D + 8 * (w0 + j));
-            x[0] = make_float4(o[0][j], o[1][j], o[2][j], o[3][j]);
-            x[1] = make_float4(o[4][j], o[5][j], o[6][j], o[7][j]);
           }
         }
       }
@@ -392,32 +427,32 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
           P[kWideRows * D + kWideRows + tid] = l;
         }
       }
-      if (!whole && u == s.k.item0 && tid == 0)
-        note_cut(a, cta, ncta, total, s.k, s.row0, s.rows, s.item_end, u == u0 ? 0 : 1);
+      if (!whole && s.first && tid == 0) note_cut(a, cta, ncta, total, k, s, u, u == u0 ? 0 : 1);
       tc::tc_fence_before();
       u += s.n;
+      if (u < u1) cursor_next(k, a.c, a.q_start, a.base, a.T, a.G, kWideRows, kTile, kItemUnits, sm.cum);
     }
   } else if (warp < 8) {
     // ---------------------------------------------------------- unpack
-    set_regs_down<64>();
     const int x = tid - 128;
     Ring<kRaw> raw;
     Ring<2> kv;
     bool dead = false;
+    const TileMap<D> map(a.c);
     for (long long u = u0; u < u1 && !dead;) {
-      const Span s = span_at(a, sm.cum, u, u1);
+      const Span s = span_of<kWideRows>(a, k, u, u1);
       for (int it = 0; it < s.tiles; ++it) {
-        const int j0 = (s.k.tile + it) * kTile;
-        if (!wait(&sm.raw_full[raw.i], raw.phase) || !wait(&sm.kv_empty[kv.i], kv.phase ^ 1)) {
+        const int j0 = (k.tile + it) * kTile;
+        if (!wait_warp(&sm.raw_full[raw.i], raw.phase) || !wait_warp(&sm.kv_empty[kv.i], kv.phase ^ 1)) {
           dead = true;
           break;
         }
-        const Tile<D>& t = sm.raw[raw.i];
+        const uint8_t* t = sm.raw[raw.i].b;
         const uint32_t groups = sm.raw_groups[raw.i];
         // Parameters of slots 2 lane and 2 lane + 1, in every warp.
         {
-          const uint64_t ok = group_mask(groups) & low_ones(static_cast<long long>(s.k.q.total) - j0);
-          const uint4 pr = *reinterpret_cast<const uint4*>(t.p + 16 * lane);
+          const uint64_t ok = group_mask(groups) & low_ones(static_cast<long long>(k.q.total) - j0);
+          const uint4 pr = *reinterpret_cast<const uint4*>(t + map.p(2 * lane));
           const float2 ka = __half22float2(*reinterpret_cast<const __half2*>(&pr.x));
           const float2 kb = __half22float2(*reinterpret_cast<const __half2*>(&pr.z));
           float2 va = __half22float2(*reinterpret_cast<const __half2*>(&pr.y));
@@ -446,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
 #pragma unroll
         for (int q0 = 0; q0 < D / 32; q0 += 2) {
           const int row = x & 63, q = q0 + (x >> 6);
-          const uint4 w = *reinterpret_cast<const uint4*>(t.k + row * (D / 2) + 16 * q);
+          const uint4 w = *reinterpret_cast<const uint4*>(t + map.k(row) + 16 * q);
           const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
           uint8_t* dst = sm.k16[kv.i] + (row >> 3) * 1024 + (row & 7) * 128;
 #pragma unroll
@@ -463,12 +498,13 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
           const int w = x % W, k0 = (x / W) * KP;
           const int swap = (lane / W) & 1;  // lanes of two slot groups read rows of opposite parity
           const uint32_t sel_lo = swap ? 0x1054u : 0x5410u, sel_hi = swap ? 0x3276u : 0x7632u;
+          const uint8_t* tv = t + map.v(k0) + 4 * w;
           uint32_t lo[KP / 2], hi[KP / 2];
           __half2 sc[KP / 2], off[KP / 2];  // scale, -1024 scale
 #pragma unroll
           for (int i = 0; i < KP / 2; ++i) {
-            const uint32_t y0 = *reinterpret_cast<const uint32_t*>(t.v + (k0 + 2 * i + swap) * (D / 2) + 4 * w);
-            const uint32_t y1 = *reinterpret_cast<const uint32_t*>(t.v + (k0 + 2 * i + (swap ^ 1)) * (D / 2) + 4 * w);
+            const uint32_t y0 = *reinterpret_cast<const uint32_t*>(tv + (2 * i + swap) * (D / 2));
+            const uint32_t y1 = *reinterpret_cast<const uint32_t*>(tv + (2 * i + (swap ^ 1)) * (D / 2));
             lo[i] = __byte_perm(y0, y1, sel_lo);
             hi[i] = __byte_perm(y0, y1, sel_hi);
             sc[i] = *reinterpret_cast<const __half2*>(&sm.vs[warp - 4][k0 / 2 + i]);
@@ -498,83 +534,99 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
         kv.next();
       }
       u += s.n;
+      if (u < u1) cursor_next(k, a.c, a.q_start, a.base, a.T, a.G, kWideRows, kTile, kItemUnits, sm.cum);
     }
-  } else {
-    set_regs_down<40>();
-    if (warp == 8) {
-      // -------------------------------------------------------- copies
-      TileLoader<D> loader;
-      Ring<kRaw> raw;
-      long long issued = 0;
-      bool dead = false;
-      for (long long u = u0; u < u1 && !dead;) {
-        Span s = span_at(a, sm.cum, u, u1);
-        for (int it = 0; it < s.tiles; ++it) {
-          if (__any_sync(0xFFFFFFFFu, !wait(&sm.raw_empty[raw.i], raw.phase ^ 1))) {
-            dead = true;
-            break;
-          }
-          loader.load(a, s.k, sm.raw[raw.i], &sm.raw_groups[raw.i], &sm.raw_full[raw.i]);
-          ++s.k.tile;
-          ++issued;
-          raw.next();
+  } else if (warp == 9) {
+    // ---------------------------------------------------------- copies
+    TileLoader<D> loader(a.c);
+    Ring<kRaw> raw;
+    int issued = 0;  // (only its remainder and whether it passed kRaw matter)
+    bool dead = false;
+    for (long long u = u0; u < u1 && !dead;) {
+      const Span s = span_of<kWideRows>(a, k, u, u1);
+      for (int it = 0; it < s.tiles; ++it) {
+        if (!wait_warp(&sm.raw_empty[raw.i], raw.phase ^ 1)) {
+          dead = true;
+          break;
         }
-        u += s.n;
+        loader.load(a, k, sm.raw[raw.i], &sm.raw_groups[raw.i], &sm.raw_full[raw.i]);
+        ++k.tile;
+        issued = min(issued + 1, kRaw);
+        raw.next();
       }
-      // Copies in flight land before the CTA's shared memory goes.
-      for (long long i = issued > kRaw ? issued - kRaw : 0; i < issued; ++i)
-        tc::mbar_wait_bounded(&sm.raw_full[i % kRaw], static_cast<uint32_t>((i / kRaw) & 1), &sm.never, 100000000ull);
-    } else if (warp == 9 && lane == 0) {
-      // -------------------------------------------------------- products
-      const uint32_t is = idesc_f16(kWideRows, kTile), io = idesc_f16(kWideRows, D);
-      Ring<2> kv;
-      uint32_t qp = 0, sp = 0;
-      bool dead = false, any = false;
-      for (long long u = u0; u < u1 && !dead;) {
-        const Span s = span_at(a, sm.cum, u, u1);
-        if (s.tiles > 0) {
-          if (!wait(&sm.q_full, qp)) break;
-          qp ^= 1;
+      u += s.n;
+      if (u < u1) cursor_next(k, a.c, a.q_start, a.base, a.T, a.G, kWideRows, kTile, kItemUnits, sm.cum);
+    }
+    // Copies in flight land before the CTA's shared memory goes.
+    for (int i = 0; i < issued; ++i) {
+      raw.i = raw.i ? raw.i - 1 : kRaw - 1;
+      if (raw.i == kRaw - 1) raw.phase ^= 1;
+      tc::mbar_wait_bounded(&sm.raw_full[raw.i], raw.phase, &sm.never, 100000000ull);
+    }
+  } else if (lane == 0) {
+    // ---------------------------------------------------------- products
+    const uint32_t is = idesc_f16(kWideRows, kHalf), io = idesc_f16(kWideRows, D);
+    const uint64_t kd0 = tc::smem_desc_sw128(tc::smem_u32(sm.k16)), vd0 = tc::smem_desc_sw128(tc::smem_u32(sm.v16));
+    Ring<2> kv;
+    uint32_t qp = 0, sp = 0;
+    bool dead = false, any = false;
+    // Scores of half h of the tile in unpacked buffer b.
+    auto scores = [&](int h, int b) {
+      const uint64_t kd = kd0 + b * (sizeof(sm.k16[0]) >> 4) + h * (kHalf * 128 >> 4);
+#pragma unroll
+      for (int t = 0; t < D / 16; ++t)
+        mma_ts(tmem + kSCol + h * kHalf, tmem + kQCol + 8 * t, kd + (t >> 2) * (kTile * 128 >> 4) + (t & 3) * 2, is, t > 0);
+      tc::mma_commit(&sm.s_full[h]);
+    };
+    for (long long u = u0; u < u1 && !dead;) {
+      const Span s = span_of<kWideRows>(a, k, u, u1);
+      if (s.tiles > 0) {
+        if (!wait(&sm.q_full, qp) || !wait(&sm.kv_full[kv.i], kv.phase)) {
+          dead = true;
+          break;
         }
-        for (int it = 0; it < s.tiles; ++it) {
-          // S shares its columns with the last tile's P: that product comes first.
-          if (!wait(&sm.kv_full[kv.i], kv.phase) || (any && !wait(&sm.pv_done, sp ^ 1))) {
+        qp ^= 1;
+        any = true;
+        tc::tc_fence_after();
+        scores(0, kv.i);
+        scores(1, kv.i);
+      }
+      for (int it = 0; it < s.tiles && !dead; ++it) {
+        const int b = kv.i;
+        kv.next();
+        for (int h = 0; h < 2; ++h) {
+          if (!wait(&sm.p_full[h], sp)) {
             dead = true;
             break;
           }
           tc::tc_fence_after();
-          const uint32_t kb = tc::smem_u32(sm.k16[kv.i]), vb = tc::smem_u32(sm.v16[kv.i]);
+          const uint64_t vd = vd0 + b * (sizeof(sm.v16[0]) >> 4) + h * (kHalf * 2 >> 4);
 #pragma unroll
-          for (int t = 0; t < D / 16; ++t)
-            mma_ts(tmem + kSCol, tmem + kQCol + 8 * t, tc::smem_desc_sw128(kb + (t >> 2) * (kTile * 128) + (t & 3) * 32), is,
-                   t > 0);
-          tc::mma_commit(&sm.s_full);
-          if (!wait(&sm.p_full, sp)) {
-            dead = true;
-            break;
+          for (int t = 0; t < kHalf / 16; ++t)
+            mma_ts(tmem + kOCol, tmem + kSCol + h * kHalf + 8 * t, vd + t * 2, io, it > 0 || h > 0 || t > 0);
+          if (h) tc::mma_commit(&sm.kv_empty[b]);
+          tc::mma_commit(&sm.pv_done[h]);
+          if (it + 1 < s.tiles) {
+            // The next tile's scores go over this P once its product is done.
+            if ((h == 0 && !wait(&sm.kv_full[kv.i], kv.phase)) || !wait(&sm.pv_done[h], sp)) {
+              dead = true;
+              break;
+            }
+            tc::tc_fence_after();
+            scores(h, kv.i);
           }
-          tc::tc_fence_after();
-#pragma unroll
-          for (int t = 0; t < kTile / 16; ++t)
-            mma_ts(tmem + kOCol, tmem + kSCol + 8 * t, tc::smem_desc_sw128(vb + t * 32), io, it > 0 || t > 0);
-          tc::mma_commit(&sm.kv_empty[kv.i]);
-          tc::mma_commit(&sm.pv_done);
-          any = true;
-          kv.next();
-          sp ^= 1;
         }
-        u += s.n;
+        sp ^= 1;
       }
-      // Products in flight end before TMEM is freed.
-      if (any || dead) {
-        if (dead) {
-          tc::mma_commit(&sm.kv_empty[0]);
-          const uint64_t t0 = tc::globaltimer_ns();
-          while (tc::globaltimer_ns() - t0 < 1000000ull) {}
-        } else {
-          tc::mbar_wait_bounded(&sm.pv_done, sp ^ 1, &sm.never, 100000000ull);
-        }
-      }
+      u += s.n;
+      if (u < u1) cursor_next(k, a.c, a.q_start, a.base, a.T, a.G, kWideRows, kTile, kItemUnits, sm.cum);
+    }
+    // Products in flight end before TMEM is freed.
+    if (dead) {
+      const uint64_t t0 = tc::globaltimer_ns();
+      while (tc::globaltimer_ns() - t0 < 1000000ull) {}
+    } else if (any) {
+      tc::mbar_wait_bounded(&sm.pv_done[1], sp ^ 1, &sm.never, 100000000ull);
     }
   }
   __syncthreads();
@@ -585,14 +637,56 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
   }
 }
 
+// Joins the partial sums of the item that starts in CTA blockIdx.x and ends
+// in a later one, in CTA order: rows 8 * blockIdx.y to + 7 of it, a thread per
+// row and code word (8 dimensions).
+template <int D>
+__global__ void __launch_bounds__(D) combine_wide_kernel(const AttendArgs a) {
+  constexpr int W = D / 8;
+  pdl_wait();
+  pdl_trigger();
+  const int c0 = blockIdx.x;
+  const int32_t* M = a.meta + static_cast<size_t>(c0) * 8;
+  const int r = blockIdx.y * 8 + (threadIdx.x & 7), w = threadIdx.x >> 3;
+  if (M[0] == 0 || r >= M[4]) return;
+  const int s = M[1], h = M[2], row0 = M[3], c1 = M[5], slot0 = M[6];
+  const int q0 = a.q_start[s];
+  constexpr size_t PF = part_floats<D, kWideRows>();
+  float m = kNone, l = 0.f, v[8] = {};
+  for (int c = c0; c <= c1; ++c) {
+    const float* Q = a.part + (static_cast<size_t>(c) * 2 + (c == c0 ? slot0 : 0)) * PF;
+    const float mq = Q[kWideRows * D + r], lq = Q[kWideRows * D + kWideRows + r];
+    const float nm = fmaxf(m, mq), f = ex2(m - nm), fq = ex2(mq - nm);
+    l = l * f + lq * fq;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) v[n] = v[n] * f + Q[(n * W + w) * kWideRows + r] * fq;
+    m = nm;
+  }
+  const int ri = row0 + r, tok = ri / a.G, hd = h * a.G + ri % a.G;
+  const size_t at = (static_cast<size_t>(q0) + tok) * a.Hq + hd;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t b[4];
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b[n]) : "f"(v[2 * n + 1] * inv), "f"(v[2 * n] * inv));
+  *reinterpret_cast<uint4*>(a.out + at * D + 8 * w) = make_uint4(b[0], b[1], b[2], b[3]);
+  if (w == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
 template <int D>
 int launch(const AttendArgs& a, int grid, cudaStream_t s) {
   const size_t smem = sizeof(Smem<D>) + static_cast<size_t>(a.c.S) * 8;
   if (cudaFuncSetAttribute(attend_wide_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
       cudaSuccess)
     return MOE_ERR_CUDA;
+  int st;
+  {
+    LaunchScope ls(kProfKv4Attend, s);
+    st = launch_k(attend_wide_kernel<D>, dim3(grid), dim3(kThreads), smem, s, false, a);
+  }
+  if (st != MOE_OK) return st;
   LaunchScope ls(kProfKv4Attend, s);
-  return launch_k(attend_wide_kernel<D>, dim3(grid), dim3(kThreads), smem, s, false, a);
+  return launch_k(combine_wide_kernel<D>, dim3(grid, kWideRows / 8), dim3(D), 0, s, true, a);
 }
 
 }  // namespace

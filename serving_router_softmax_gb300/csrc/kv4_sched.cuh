@@ -1,10 +1,11 @@
 // Work split of the kv4 attention kernels.
 //
 // Sequence s has `nb` row blocks per kv head (its new tokens times the query
-// heads of a kv head, in blocks of RB rows) and `nt` tiles of slots.  Its
-// items (head, row block) have nt units each; all units in order are split
-// evenly over the CTAs, so ragged lengths balance by themselves.  The lengths
-// are device data: every CTA forms the running sum over the sequences itself.
+// heads of a kv head, in blocks of RB rows) and its slots in tiles.  An item
+// (head, row block) counts one unit per tile and `extra` units more for what it
+// costs to begin and end one; all units in order are split evenly over the CTAs,
+// so ragged lengths balance by themselves.  The lengths are device data: every
+// CTA forms the running sum over the sequences itself.
 #pragma once
 
 #include "kv4.cuh"
@@ -31,10 +32,10 @@ __device__ __forceinline__ SeqShape seq_shape(const Cache& c, const int32_t* q_s
 }
 
 // Fills cum[0..S] with the units before each sequence (rows per token G, row
-// blocks of RB, tiles of `tile` slots).  All threads of the block; ends with
+// blocks of RB, tiles of `tile` slots, `extra` units an item).  All threads of the block; ends with
 // a barrier.  scratch: 32 long longs.
 __device__ __forceinline__ void build_units(const Cache& c, const int32_t* q_start, const int32_t* base, int T, int G,
-                                            int RB, int tile, long long* cum, long long* scratch, int32_t* dev_err,
+                                            int RB, int tile, int extra, long long* cum, long long* scratch, int32_t* dev_err,
                                             bool report) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, nw = (blockDim.x + 31) >> 5;
   long long carry = 0;
@@ -45,7 +46,7 @@ __device__ __forceinline__ void build_units(const Cache& c, const int32_t* q_sta
     if (s < c.S) {
       const SeqShape q = seq_shape(c, q_start, base, T, s, &bad);
       const long long nb = (static_cast<long long>(q.nq) * G + RB - 1) / RB;
-      u = static_cast<long long>(c.Hkv) * nb * ((q.total + tile - 1) / tile);
+      u = static_cast<long long>(c.Hkv) * nb * ((q.total + tile - 1) / tile + extra);
     }
     long long incl = u;
 #pragma unroll
@@ -82,24 +83,44 @@ __device__ __forceinline__ int find_seq(const long long* cum, int S, long long u
 
 // A position in the unit order: the item and its next tile.
 struct Cursor {
-  int s, h, rb, tile, nt, nb;
-  long long item0;  // first unit of the item
+  int s, h, rb, tile, nt, nb;  // nt: units of an item, the first of them its tiles
   SeqShape q;
 };
 
-__device__ __forceinline__ void cursor_at(Cursor& k, const Cache& c, const int32_t* q_start, const int32_t* base, int T,
-                                          int G, int RB, int tile, const long long* cum, long long u) {
+__device__ __forceinline__ void cursor_seq(Cursor& k, const Cache& c, const int32_t* q_start, const int32_t* base, int T,
+                                           int G, int RB, int tile, int extra) {
   int32_t bad = 0;
-  k.s = find_seq(cum, c.S, u);
   k.q = seq_shape(c, q_start, base, T, k.s, &bad);
   k.nb = static_cast<int>((static_cast<long long>(k.q.nq) * G + RB - 1) / RB);
-  k.nt = (k.q.total + tile - 1) / tile;
+  k.nt = (k.q.total + tile - 1) / tile + extra;
+}
+
+// The position of unit u (below cum[S]).
+__device__ __forceinline__ void cursor_at(Cursor& k, const Cache& c, const int32_t* q_start, const int32_t* base, int T,
+                                          int G, int RB, int tile, int extra, const long long* cum, long long u) {
+  k.s = find_seq(cum, c.S, u);
+  cursor_seq(k, c, q_start, base, T, G, RB, tile, extra);
   const long long rem = u - cum[k.s];
-  const long long item = rem / k.nt;
+  long long item;
+  if (rem < (1ll << 31)) item = static_cast<uint32_t>(rem) / static_cast<uint32_t>(k.nt);
+  else item = rem / k.nt;
   k.tile = static_cast<int>(rem - item * k.nt);
-  k.h = static_cast<int>(item / k.nb);
+  if (item < (1ll << 31)) k.h = static_cast<int>(static_cast<uint32_t>(item) / static_cast<uint32_t>(k.nb));
+  else k.h = static_cast<int>(item / k.nb);
   k.rb = static_cast<int>(item - static_cast<long long>(k.h) * k.nb);
-  k.item0 = u - k.tile;
+}
+
+// On to the next item; there is one (the caller counts units).
+__device__ __forceinline__ void cursor_next(Cursor& k, const Cache& c, const int32_t* q_start, const int32_t* base, int T,
+                                            int G, int RB, int tile, int extra, const long long* cum) {
+  k.tile = 0;
+  if (++k.rb < k.nb) return;
+  k.rb = 0;
+  if (++k.h < c.Hkv) return;
+  k.h = 0;
+  do ++k.s;
+  while (k.s + 1 < c.S && cum[k.s + 1] == cum[k.s]);
+  cursor_seq(k, c, q_start, base, T, G, RB, tile, extra);
 }
 
 }  // namespace kv4

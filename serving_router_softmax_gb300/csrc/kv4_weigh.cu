@@ -52,14 +52,15 @@ __global__ void __launch_bounds__(32 * kWarps) weigh_kernel(const WeighArgs a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   pdl_wait();
   pdl_trigger();
-  build_units(a.c, a.q_start, a.base, a.T, a.G, kAllRows, kSlots, sm.cum, sm.scratch, a.dev_err, blockIdx.x == 0);
+  build_units(a.c, a.q_start, a.base, a.T, a.G, kAllRows, kSlots, 0, sm.cum, sm.scratch, a.dev_err, blockIdx.x == 0);
   const long long total = sm.cum[a.c.S];
   const long long u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
   const size_t width = static_cast<size_t>(a.c.width) << a.c.page_log2;
   Cursor k;
+  if (u0 < u1) cursor_at(k, a.c, a.q_start, a.base, a.T, a.G, kAllRows, kSlots, 0, sm.cum, u0);
   int held_s = -1, held_h = -1, held_row = -1;  // query rows in shared memory
   for (long long u = u0; u < u1; ++u) {
-    if (u == u0 || k.tile == k.nt) cursor_at(k, a.c, a.q_start, a.base, a.T, a.G, kAllRows, kSlots, sm.cum, u);
+    if (k.tile == k.nt) cursor_next(k, a.c, a.q_start, a.base, a.T, a.G, kAllRows, kSlots, 0, sm.cum);
     const int j0 = k.tile * kSlots + 16 * warp;
     const int page = j0 < k.q.total ? page_of(a.c, k.s, j0) : -1;
     if (page < 0 && j0 < k.q.total && lane == 0) flag_error(a.dev_err, MOE_DEV_BAD_ID);
