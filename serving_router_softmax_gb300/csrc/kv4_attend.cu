@@ -19,6 +19,7 @@ namespace kv4 {
 namespace {
 
 constexpr int kConsumerWarps = 4;
+constexpr int kMinUnits = 1;
 constexpr int kThreads = 32 * (kConsumerWarps + 1);
 template <int D, int NT, int NS>
 struct Smem {
@@ -56,8 +57,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
   build_units(a.c, a.q_start, a.base, a.T, a.G, RB, kTile, kItemUnits, sm.cum, sm.scratch, a.dev_err, blockIdx.x == 0);
   pdl_trigger();
   const long long total = sm.cum[a.c.S];
-  // At most one CTA per unit, so that every CTA up to the last one used owns some.
-  const int ncta = static_cast<int>(total < gridDim.x ? total : gridDim.x), cta = blockIdx.x;
+  const int ncta = used_ctas(total, kMinUnits), cta = blockIdx.x;
   const long long u0 = cta < ncta ? total * cta / ncta : 0, u1 = cta < ncta ? total * (cta + 1) / ncta : 0;
   volatile int* abort_flag = &sm.abort;
 
@@ -364,48 +364,6 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
   }
 }
 
-// Joins the partial sums of the item that starts in CTA blockIdx.x and ends
-// in a later one: rows 8 * blockIdx.y to + 7 of it, two dimensions a thread.
-template <int D, int RB>
-__global__ void __launch_bounds__(4 * D) combine_kernel(const AttendArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  const int c0 = blockIdx.x;
-  const int32_t* M = a.meta + static_cast<size_t>(c0) * 8;
-  const int r = blockIdx.y * 8 + threadIdx.x / (D / 2), d = 2 * (threadIdx.x % (D / 2));
-  if (M[0] == 0 || r >= M[4]) return;
-  const int s = M[1], h = M[2], row0 = M[3], c1 = M[5], slot0 = M[6];
-  const int q0 = a.q_start[s];
-  constexpr size_t PF = part_floats<D, RB>();
-  const float* P = a.part + (static_cast<size_t>(c0) * 2 + slot0) * PF;
-  float m = P[RB * D + r], l = P[RB * D + RB + r];
-  float2 v = *reinterpret_cast<const float2*>(P + r * D + d);
-#pragma unroll 4
-  for (int c = c0 + 1; c <= c1; ++c) {
-    const float* Q = a.part + static_cast<size_t>(c) * 2 * PF;
-    const float mq = Q[RB * D + r], lq = Q[RB * D + RB + r];
-    const float2 w = *reinterpret_cast<const float2*>(Q + r * D + d);
-    const float nm = fmaxf(m, mq), f = ex2(m - nm), fq = ex2(mq - nm);
-    l = l * f + lq * fq;
-    v.x = v.x * f + w.x * fq;
-    v.y = v.y * f + w.y * fq;
-    m = nm;
-  }
-  const int ri = row0 + r, tok = ri / a.G, hd = h * a.G + ri % a.G;
-  const size_t at = (static_cast<size_t>(q0) + tok) * a.Hq + hd;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t b;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b) : "f"(v.y * inv), "f"(v.x * inv));
-  *reinterpret_cast<uint32_t*>(a.out + at * D + d) = b;
-  if (d == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-}
-
-template <int D, int RB>
-int launch_combine(const AttendArgs& a, int grid, cudaStream_t s) {
-  LaunchScope ls(kProfKv4Attend, s);
-  return launch_k(combine_kernel<D, RB>, dim3(grid, RB / 8), dim3(4 * D), 0, s, true, a);
-}
-
 // Ring depth: about 52 KB of tiles, so that three CTAs of an SM keep more than
 // 100 KB in flight.
 template <int D> constexpr int stages() { return D == 128 ? 6 : 10; }
@@ -442,7 +400,7 @@ int launch_attend(const AttendArgs& a, const Plan& p, cudaStream_t s) {
     st = launch_k(k, dim3(p.grid), dim3(kThreads), smem, s, false, a);
   }
   if (st != MOE_OK) return st;
-  return launch_combine<D, 8 * NT>(a, p.grid, s);
+  return launch_combine<D, 8 * NT, false>(a, p.grid, s);
 }
 
 }  // namespace

@@ -87,6 +87,13 @@ struct TileMap {
   __device__ __forceinline__ int p(int r) const { return base(r) + seg * D + (r & (seg - 1)) * 8; }
 };
 
+// CTAs that share `total` units: at least kMinUnits each, so that the sums they
+// leave to be joined stay small beside their work, and at most all.
+__device__ __forceinline__ int used_ctas(long long total, int min_units) {
+  const long long n = total / min_units;
+  return static_cast<int>(n < 1 ? (total > 0) : n < gridDim.x ? n : gridDim.x);
+}
+
 // Units that an item costs beyond its tiles (query rows in, sums out).
 constexpr int kItemUnits = 2;
 
@@ -179,6 +186,80 @@ __device__ __forceinline__ void note_cut(const AttendArgs& a, int cta, int ncta,
   M[5] = static_cast<int>(((u + s.need) * ncta - 1) / total);  // the CTA that owns the item's last tile
   M[6] = slot;
   M[0] = 1;
+}
+
+// Joins the partial sums of the item that starts in CTA blockIdx.x and ends
+// in a later one: rows 8 * blockIdx.y to + 7 of it, eight dimensions a thread,
+// the contributors dealt out to kShare threads whose sums are added in order, so
+// results do not depend on timing.  The maximum comes first, so that the loads
+// of the second loop do not wait for each other.
+// kCols: outputs lie as [D][RB], column n * (D / 8) + w being dimension 8 w + n.
+template <int D, int RB, bool kCols, int kShare>
+__global__ void __launch_bounds__(D * kShare) combine_kernel(const AttendArgs a) {
+  constexpr int W = D / 8;
+  constexpr size_t PF = part_floats<D, RB>();
+  __shared__ float part[kShare - 1][9][D];
+  pdl_wait();
+  pdl_trigger();
+  const int c0 = blockIdx.x, tid = threadIdx.x % D, share = threadIdx.x / D;
+  const int4 M = *reinterpret_cast<const int4*>(a.meta + static_cast<size_t>(c0) * 8);
+  const int4 M2 = *reinterpret_cast<const int4*>(a.meta + static_cast<size_t>(c0) * 8 + 4);
+  if (M.x == 0 || blockIdx.y * 8 >= M2.x) return;
+  const int r = blockIdx.y * 8 + (kCols ? tid & 7 : tid / W), w = kCols ? tid >> 3 : tid % W;
+  // Contributor 0 left its sums in place M2.z of CTA c0, contributor i > 0 in place 0 of CTA c0 + i.
+  const int n = M2.y - c0 + 1;
+  const float* P = a.part + static_cast<size_t>(c0) * 2 * PF;
+  const float* P0 = P + M2.z * PF;
+  const float* ms = P + RB * D + r;
+  float m = P0[RB * D + r];
+#pragma unroll 4
+  for (int i = 1; i < n; ++i) m = fmaxf(m, ms[2 * PF * i]);
+  float l = 0.f, v[8] = {};
+#pragma unroll 2
+  for (int i = share; i < n; i += kShare) {
+    const float* Q = i ? P + 2 * PF * i : P0;
+    const float f = ex2(Q[RB * D + r] - m);
+    l = fmaf(Q[RB * D + RB + r], f, l);
+    float q[8];
+    if (kCols) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[j] = Q[(j * W + w) * RB + r];
+    } else {
+      const float4 x = *reinterpret_cast<const float4*>(Q + r * D + 8 * w), y = *reinterpret_cast<const float4*>(Q + r * D + 8 * w + 4);
+      q[0] = x.x, q[1] = x.y, q[2] = x.z, q[3] = x.w, q[4] = y.x, q[5] = y.y, q[6] = y.z, q[7] = y.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = fmaf(q[j], f, v[j]);
+  }
+  if (share > 0) {
+    part[share - 1][8][tid] = l;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part[share - 1][j][tid] = v[j];
+  }
+  __syncthreads();
+  if (share > 0 || r >= M2.x) return;
+#pragma unroll
+  for (int x = 0; x < kShare - 1; ++x) {
+    l += part[x][8][tid];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += part[x][j][tid];
+  }
+  const int ri = M.w + r, tok = ri / a.G, hd = M.z * a.G + ri - tok * a.G;
+  const size_t at = (static_cast<size_t>(a.q_start[M.y]) + tok) * a.Hq + hd;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t b[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b[j]) : "f"(v[2 * j + 1] * inv), "f"(v[2 * j] * inv));
+  *reinterpret_cast<uint4*>(a.out + at * D + 8 * w) = make_uint4(b[0], b[1], b[2], b[3]);
+  if (w == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2;
+}
+
+template <int D, int RB, bool kCols>
+int launch_combine(const AttendArgs& a, int grid, cudaStream_t s) {
+  // A chain of loads per share: 8 shares read a long list sooner; the wide kernel's many idle CTAs cost less with 4.
+  constexpr int kShare = kCols ? 4 : 8;
+  LaunchScope ls(kProfKv4Attend, s);
+  return launch_k(combine_kernel<D, RB, kCols, kShare>, dim3(grid, RB / 8), dim3(D * kShare), 0, s, true, a);
 }
 
 constexpr int kWideRows = 128;

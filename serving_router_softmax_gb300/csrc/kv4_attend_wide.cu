@@ -5,13 +5,11 @@
 // Per tile of 64 slots: S [128 x 64] = Q K^T with Q as the TMEM operand and
 // the key codes unpacked to fp16 in shared memory, a softmax thread per row,
 // O [128 x D] += P V with P as the TMEM operand (over S's columns) and the
-// value codes unpacked to fp16, transposed.  Keys stay bare codes (their nibbles
-// are fp16 numbers already, see kv4.cuh); their scales and zeros, and the values'
-// zeros, enter per slot in the softmax, in fp32.  Value codes are multiplied by
-// their scale while they are unpacked (one rounding to fp16, relative 2^-11)
-// and by the power of two 2^-E that brings the tile's largest scale to [1, 2), so
-// that no magnitude leaves fp16's range; the exponential takes E back: p' =
-// 2^(t - m + E).
+// value codes unpacked to fp16, transposed.  Both stay bare codes, their nibbles
+// being fp16 numbers already (see kv4.cuh); the scales and zeros enter per slot in
+// the softmax, in fp32.  P holds p * vs, with the tile's largest vs brought to [1, 2)
+// by a power of two 2^-E that the exponential takes back (p = 2^(t - m + E)), so that
+// no magnitude leaves fp16's range.
 //
 // Roles: warps 0-3 softmax and output (a thread per row), warps 4-7 unpack,
 // warp 8 issues the products, warp 9 copies tiles.  The scores of a tile come in two halves of 32 slots, each with its own
@@ -29,6 +27,7 @@ constexpr int kThreads = 320;
 constexpr int kRaw = 3;       // tiles in flight
 constexpr uint32_t kTmemCols = 256;
 constexpr int kHalf = kTile / 2;
+constexpr int kMinUnits = 4;
 
 template <int D>
 struct Smem {
@@ -37,11 +36,10 @@ struct Smem {
   Tile<D> raw[kRaw];
   alignas(16) float ks[2][kTile];
   alignas(16) float kz[2][kTile];
+  alignas(16) float vs[2][kTile];               // times 2^-E
   alignas(16) float vz[2][kTile];               // times 2^-E
   float e[2];                                    // the tile's E
   uint32_t raw_groups[kRaw], groups[2];
-  alignas(16) uint8_t stage[4][32 * 80];          // per softmax warp: 32 dimensions of its 32 query rows
-  alignas(16) uint32_t vs[4][kTile / 2];         // per unpacking warp: scales times 2^-E of slot pairs
   uint64_t raw_full[kRaw], raw_empty[kRaw], kv_full[2], kv_empty[2], q_full, s_full[2], p_full[2], pv_done[2];
   long long scratch[32];
   uint32_t tmem;
@@ -156,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
   pdl_trigger();
   const uint32_t tmem = sm.tmem;
   const long long total = sm.cum[a.c.S];
-  const int ncta = static_cast<int>(total < gridDim.x ? total : gridDim.x), cta = blockIdx.x;
+  const int ncta = used_ctas(total, kMinUnits), cta = blockIdx.x;
   const long long u0 = cta < ncta ? total * cta / ncta : 0, u1 = cta < ncta ? total * (cta + 1) / ncta : 0;
   volatile int* abort_flag = &sm.abort;
   Cursor k;
@@ -185,86 +183,90 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
         if (u < u1) cursor_next(k, a.c, a.q_start, a.base, a.T, a.G, kWideRows, kTile, kItemUnits, sm.cum);
         continue;
       }
-      const int r = s.row0 + tid;
+      // Token and query head of row x of the block (small numbers: a multiplication finds the quotient).
+      const int tok0 = s.row0 / a.G, g0 = s.row0 - tok0 * a.G;
+      const float inv_g = 1.f / static_cast<float>(a.G);
+      auto token = [&](int x) { return static_cast<int>((static_cast<float>(g0 + x) + 0.5f) * inv_g); };
       const bool real = tid < s.rows;
-      const int tok = (s.row0 + min(tid, s.rows - 1)) / a.G;
+      const int tok_rel = token(min(tid, s.rows - 1)), tok = tok0 + tok_rel;
+      const int head = k.h * a.G + g0 + tid - tok_rel * a.G;
       const uint64_t bits = a.visible ? a.visible[k.q.q0 + tok] : 0;
       if (a.visible && k.q.nq > kMaxTree && tid == 0) flag_error(a.dev_err, MOE_DEV_CAPACITY);
       float m = 0.f, l = 0.f, z = 0.f, cq = 0.f, cqs = 0.f;
       {
-        // The warp's 32 rows of q, scaled by powers of two and permuted as the key words are (see prep_q),
-        // into TMEM: four lanes load a row's 64 bytes together, the lane of the row stores them.
-        constexpr int C = D / 32;
+        // The warp's 32 rows of q, scaled by powers of two (see prep_q), into TMEM.  In a half of 16
+        // rows lane 4 a + x takes word x (8 dimensions) of every 32 of rows a and a + 8, which is how the 16 x 256 bit
+        // store wants them: of the 16 columns of 32 dimensions, word x has 2 x, 2 x + 1 (its pairs (0, 4) and
+        // (1, 5)/16) and 8 + 2 x, 9 + 2 x ((2, 6) and (3, 7)/16).
         const int lr = lane >> 2, x = lane & 3;
-        const uint16_t* src[4];
-        float mx[4] = {}, sum[4] = {};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = warp * 32 + 8 * i + lr;
-          src[i] = rr < s.rows ? q_row(a, k.q, k.h, s.row0 + rr) + 8 * x : nullptr;
-        }
 #pragma unroll 1
-        for (int c = 0; c < C; ++c) {
-          uint4 v[4];
+        for (int half = 0; half < 2; ++half) {
+          constexpr int C = D / 32;
+          uint4 v[2][C];
+          float mx[2] = {}, sum[2] = {}, f1[2], f2[2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = src[i] ? *reinterpret_cast<const uint4*>(src[i] + 32 * c) : make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < 2; ++i) {
+            const int rr = warp * 32 + 16 * half + 8 * i + lr, tr = token(rr);
+            const uint16_t* src = a.q + (k.q.q0 + tok0 + tr) * a.q_ts + (k.h * a.G + g0 + rr - tr * a.G) * a.q_hs + 8 * x;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            for (int c = 0; c < C; ++c)
+              v[i][c] = rr < s.rows ? *reinterpret_cast<const uint4*>(src + 32 * c) : make_uint4(0, 0, 0, 0);
+          }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float lo = __uint_as_float(w[j] << 16), hi = __uint_as_float(w[j] & 0xFFFF0000u);
-              mx[i] = max3(mx[i], fabsf(lo), fabsf(hi));
-              sum[i] += lo + hi;
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+              const uint32_t w[4] = {v[i][c].x, v[i][c].y, v[i][c].z, v[i][c].w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float lo = __uint_as_float(w[j] << 16), hi = __uint_as_float(w[j] & 0xFFFF0000u);
+                mx[i] = max3(mx[i], fabsf(lo), fabsf(hi));
+                sum[i] += lo + hi;
+              }
+            }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 1));
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 2));
+            sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 1);
+            sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 2);
+            const int ex = static_cast<int>(__float_as_uint(mx[i]) >> 23);
+            const int e = mx[i] > 0.f && ex < 255 ? 14 + 127 - (ex > 0 ? ex : 1) : 0;
+            f1[i] = __uint_as_float(static_cast<uint32_t>(127 + (e >> 1)) << 23);
+            f2[i] = __uint_as_float(static_cast<uint32_t>(127 + e - (e >> 1)) << 23);
+            // The lane of the row keeps its factors.
+            const int es = __shfl_sync(0xFFFFFFFFu, e, 4 * (lane & 7));
+            const float ss = __shfl_sync(0xFFFFFFFFu, sum[i], 4 * (lane & 7));
+            if (lane >> 3 == 2 * half + i) {
+              const int y = 24 - es;  // the codes carry 2^-24; two factors, as y may pass one fp32's range
+              cq = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + (y >> 1)) << 23) *
+                   __uint_as_float(static_cast<uint32_t>(127 + y - (y >> 1)) << 23);
+              cqs = a.scale_log2 * ss;
             }
           }
-        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 1));
-          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 2));
-          sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 1);
-          sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 2);
-        }
-        int e[4];
+          for (int c = 0; c < C; ++c) {
+            uint32_t o[2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int ex = static_cast<int>(__float_as_uint(mx[i]) >> 23);
-          e[i] = mx[i] > 0.f && ex < 255 ? 14 + 127 - (ex > 0 ? ex : 1) : 0;
-          const int es = __shfl_sync(0xFFFFFFFFu, e[i], 4 * (lane & 7));
-          const float ss = __shfl_sync(0xFFFFFFFFu, sum[i], 4 * (lane & 7));
-          if (lane >> 3 == i) {
-            cq = ldexpf(a.scale_log2, 24 - es);
-            cqs = a.scale_log2 * ss;
-          }
-        }
-#pragma unroll 1
-        for (int c = 0; c < C; ++c) {
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t w[4] = {v[i][c].x, v[i][c].y, v[i][c].z, v[i][c].w};
+              float y[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 v = src[i] ? *reinterpret_cast<const uint4*>(src[i] + 32 * c) : make_uint4(0, 0, 0, 0);
-            const float f1 = __uint_as_float(static_cast<uint32_t>(127 + e[i] / 2) << 23);
-            const float f2 = __uint_as_float(static_cast<uint32_t>(127 + e[i] - e[i] / 2) << 23);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            float y[8];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              y[2 * t] = __uint_as_float(w[t] << 16) * f1 * f2;
-              y[2 * t + 1] = __uint_as_float(w[t] & 0xFFFF0000u) * f1 * f2;
+              for (int t = 0; t < 4; ++t) {
+                y[2 * t] = __uint_as_float(w[t] << 16) * f1[i] * f2[i];
+                y[2 * t + 1] = __uint_as_float(w[t] & 0xFFFF0000u) * f1[i] * f2[i];
+              }
+              o[i][0] = pack_h2(y[0], y[4]);
+              o[i][1] = pack_h2(y[1] * 0.0625f, y[5] * 0.0625f);
+              o[i][2] = pack_h2(y[2], y[6]);
+              o[i][3] = pack_h2(y[3] * 0.0625f, y[7] * 0.0625f);
             }
-            *reinterpret_cast<uint4*>(sm.stage[warp] + (8 * i + lr) * 80 + 16 * x) =
-                make_uint4(pack_h2(y[0], y[4]), pack_h2(y[1] * 0.0625f, y[5] * 0.0625f), pack_h2(y[2], y[6]),
-                           pack_h2(y[3] * 0.0625f, y[7] * 0.0625f));
+            asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+                             tq + (static_cast<uint32_t>(16 * half) << 16) + 16 * c),
+                         "r"(o[0][0]), "r"(o[0][1]), "r"(o[1][0]), "r"(o[1][1]), "r"(o[0][2]), "r"(o[0][3]), "r"(o[1][2]),
+                         "r"(o[1][3])
+                         : "memory");
           }
-          __syncwarp();
-          uint32_t o[16];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 y = *reinterpret_cast<const uint4*>(sm.stage[warp] + lane * 80 + 16 * j);
-            o[4 * j] = y.x, o[4 * j + 1] = y.y, o[4 * j + 2] = y.z, o[4 * j + 3] = y.w;
-          }
-          tmem_st16(tq + 16 * c, o);
-          __syncwarp();
         }
         tmem_st_wait();
         tc::tc_fence_before();
@@ -291,6 +293,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
           const uint32_t tsh = ts + h * kHalf;
           const float4* ks4 = reinterpret_cast<const float4*>(sm.ks[kv.i] + h * kHalf);
           const float4* kz4 = reinterpret_cast<const float4*>(sm.kz[kv.i] + h * kHalf);
+          const float4* vs4 = reinterpret_cast<const float4*>(sm.vs[kv.i] + h * kHalf);
           const float4* vz4 = reinterpret_cast<const float4*>(sm.vz[kv.i] + h * kHalf);
           const float off = E - m;
           const float2 cq2 = make_float2(cq, cq), cqs2 = make_float2(cqs, cqs), off2 = make_float2(off, off);
@@ -352,13 +355,14 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
           for (int i = 0; i < 16; i += 2) {
             const float2 x = make_float2(ex2(d[i].x), ex2(d[i].y));
             const float2 y = make_float2(ex2(d[i + 1].x), ex2(d[i + 1].y));
-            const float4 zz = vz4[i / 2];
+            const float4 zz = vz4[i / 2], sc = vs4[i / 2];
             sum0 = add2(sum0, x);
             sum1 = add2(sum1, y);
             z0 = fma2(x, make_float2(zz.x, zz.y), z0);
             z1 = fma2(y, make_float2(zz.z, zz.w), z1);
-            p[i] = pack_h2(x.x, x.y);
-            p[i + 1] = pack_h2(y.x, y.y);
+            const float2 px = mul2(x, make_float2(sc.x, sc.y)), py = mul2(y, make_float2(sc.z, sc.w));
+            p[i] = pack_h2(px.x, px.y);
+            p[i + 1] = pack_h2(py.x, py.y);
           }
           tmem_st16(tsh, p);
           sum0 = add2(sum0, sum1);
@@ -379,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
       const bool whole = s.whole;
       const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
       float* P = a.part + (static_cast<size_t>(cta) * 2 + (u == u0 ? 0 : 1)) * part_floats<D, kWideRows>();
-      const size_t at = (static_cast<size_t>(k.q.q0) + tok) * a.Hq + k.h * a.G + r % a.G;
+      const size_t at = (static_cast<size_t>(k.q.q0) + tok) * a.Hq + head;
       // TMEM column n * W + w is dimension 8 w + n.  (Loops that run once an item stay rolled: a cold
       // instruction costs about 10 clocks.)
 #pragma unroll 1
@@ -399,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
 #pragma unroll
         for (int n = 0; n < 8; ++n)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) o[n][j] += z;
+          for (int j = 0; j < 4; ++j) o[n][j] = fmaf(o[n][j], (n & 1) ? 1048576.f : 16777216.f, z);
         if (!whole) {
           // Lanes are rows: a column of the block is 128 floats side by side.
 #pragma unroll
@@ -449,8 +453,8 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
         }
         const uint8_t* t = sm.raw[raw.i].b;
         const uint32_t groups = sm.raw_groups[raw.i];
-        // Parameters of slots 2 lane and 2 lane + 1, in every warp.
-        {
+        if (warp == 4) {
+          // Parameters of slots 2 lane and 2 lane + 1.
           const uint64_t ok = group_mask(groups) & low_ones(static_cast<long long>(k.q.total) - j0);
           const uint4 pr = *reinterpret_cast<const uint4*>(t + map.p(2 * lane));
           const float2 ka = __half22float2(*reinterpret_cast<const __half2*>(&pr.x));
@@ -465,16 +469,14 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
           const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(va.x, vb.x)));
           const int E = top ? static_cast<int>(top >> 23) - 127 : -30;
           const float f = __uint_as_float(static_cast<uint32_t>(127 - E) << 23);
-          sm.vs[warp - 4][lane] = pack_h2(va.x * f, vb.x * f);
-          if (warp == 4) {
-            const float nan = __uint_as_float(0x7FC00000u);
-            *reinterpret_cast<float2*>(&sm.ks[kv.i][2 * lane]) = make_float2(fa ? ka.x : nan, fb ? kb.x : nan);
-            *reinterpret_cast<float2*>(&sm.kz[kv.i][2 * lane]) = make_float2(ka.y, kb.y);
-            *reinterpret_cast<float2*>(&sm.vz[kv.i][2 * lane]) = make_float2(va.y * f, vb.y * f);
-            if (lane == 0) {
-              sm.e[kv.i] = static_cast<float>(E);
-              sm.groups[kv.i] = groups;
-            }
+          const float nan = __uint_as_float(0x7FC00000u);
+          *reinterpret_cast<float2*>(&sm.ks[kv.i][2 * lane]) = make_float2(fa ? ka.x : nan, fb ? kb.x : nan);
+          *reinterpret_cast<float2*>(&sm.kz[kv.i][2 * lane]) = make_float2(ka.y, kb.y);
+          *reinterpret_cast<float2*>(&sm.vs[kv.i][2 * lane]) = make_float2(va.x * f, vb.x * f);
+          *reinterpret_cast<float2*>(&sm.vz[kv.i][2 * lane]) = make_float2(va.y * f, vb.y * f);
+          if (lane == 0) {
+            sm.e[kv.i] = static_cast<float>(E);
+            sm.groups[kv.i] = groups;
           }
         }
         // Keys: 16 bytes of a row (32 codes) make four 16-byte pieces.
@@ -483,15 +485,16 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
           const int row = x & 63, q = q0 + (x >> 6);
           const uint4 w = *reinterpret_cast<const uint4*>(t + map.k(row) + 16 * q);
           const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-          uint8_t* dst = sm.k16[kv.i] + (row >> 3) * 1024 + (row & 7) * 128;
+          uint8_t* dst = sm.k16[kv.i] + (row >> 3) * 1024 + (row & 7) * 128 + (q >> 1) * (kTile * 128);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int c = 4 * q + i;
-            *reinterpret_cast<uint4*>(dst + (c >> 3) * (kTile * 128) + (((c & 7) ^ (row & 7)) << 4)) =
-                make_uint4(nibbles<0>(ww[i]), nibbles<1>(ww[i]), nibbles<2>(ww[i]), nibbles<3>(ww[i]));
+            // In the order of Q's columns: first the pairs (0, 4) and (1, 5) of the four words, then the others.
+            const uint32_t y = ww[2 * (i & 1)], z = ww[2 * (i & 1) + 1];
+            *reinterpret_cast<uint4*>(dst + (((4 * (q & 1) + i) ^ (row & 7)) << 4)) =
+                i < 2 ? make_uint4(nibbles<0>(y), nibbles<1>(y), nibbles<0>(z), nibbles<1>(z))
+                      : make_uint4(nibbles<2>(y), nibbles<3>(y), nibbles<2>(z), nibbles<3>(z));
           }
         }
-        __syncwarp();
         // Values: a word of each of KP slots makes, for its 8 dimensions, KP fp16 numbers side by side.
         {
           constexpr int KP = D == 128 ? 8 : 4;
@@ -500,15 +503,12 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
           const uint32_t sel_lo = swap ? 0x1054u : 0x5410u, sel_hi = swap ? 0x3276u : 0x7632u;
           const uint8_t* tv = t + map.v(k0) + 4 * w;
           uint32_t lo[KP / 2], hi[KP / 2];
-          __half2 sc[KP / 2], off[KP / 2];  // scale, -1024 scale
 #pragma unroll
           for (int i = 0; i < KP / 2; ++i) {
             const uint32_t y0 = *reinterpret_cast<const uint32_t*>(tv + (2 * i + swap) * (D / 2));
             const uint32_t y1 = *reinterpret_cast<const uint32_t*>(tv + (2 * i + (swap ^ 1)) * (D / 2));
             lo[i] = __byte_perm(y0, y1, sel_lo);
             hi[i] = __byte_perm(y0, y1, sel_hi);
-            sc[i] = *reinterpret_cast<const __half2*>(&sm.vs[warp - 4][k0 / 2 + i]);
-            off[i] = __hmul2(sc[i], __float2half2_rn(-1024.f));
           }
 #pragma unroll
           for (int n = 0; n < 8; ++n) {
@@ -516,9 +516,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
 #pragma unroll
             for (int i = 0; i < KP / 2; ++i) {
               const uint32_t z = n < 4 ? lo[i] : hi[i];
-              const uint32_t b = ((z >> (4 * (n & 3))) & 0x000F000Fu) | 0x64006400u;  // 1024 + code
-              const __half2 val = __hfma2(*reinterpret_cast<const __half2*>(&b), sc[i], off[i]);
-              y[i] = *reinterpret_cast<const uint32_t*>(&val);
+              y[i] = ((n & 2) ? z >> 8 : z) & ((n & 1) ? 0x00F000F0u : 0x000F000Fu);
             }
             const int row = n * W + w;
             uint8_t* dst = sm.v16[kv.i] + (row >> 3) * 1024 + (row & 7) * 128 + (((k0 / 8) ^ (row & 7)) << 4);
@@ -637,42 +635,6 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
   }
 }
 
-// Joins the partial sums of the item that starts in CTA blockIdx.x and ends
-// in a later one, in CTA order: rows 8 * blockIdx.y to + 7 of it, a thread per
-// row and code word (8 dimensions).
-template <int D>
-__global__ void __launch_bounds__(D) combine_wide_kernel(const AttendArgs a) {
-  constexpr int W = D / 8;
-  pdl_wait();
-  pdl_trigger();
-  const int c0 = blockIdx.x;
-  const int32_t* M = a.meta + static_cast<size_t>(c0) * 8;
-  const int r = blockIdx.y * 8 + (threadIdx.x & 7), w = threadIdx.x >> 3;
-  if (M[0] == 0 || r >= M[4]) return;
-  const int s = M[1], h = M[2], row0 = M[3], c1 = M[5], slot0 = M[6];
-  const int q0 = a.q_start[s];
-  constexpr size_t PF = part_floats<D, kWideRows>();
-  float m = kNone, l = 0.f, v[8] = {};
-  for (int c = c0; c <= c1; ++c) {
-    const float* Q = a.part + (static_cast<size_t>(c) * 2 + (c == c0 ? slot0 : 0)) * PF;
-    const float mq = Q[kWideRows * D + r], lq = Q[kWideRows * D + kWideRows + r];
-    const float nm = fmaxf(m, mq), f = ex2(m - nm), fq = ex2(mq - nm);
-    l = l * f + lq * fq;
-#pragma unroll
-    for (int n = 0; n < 8; ++n) v[n] = v[n] * f + Q[(n * W + w) * kWideRows + r] * fq;
-    m = nm;
-  }
-  const int ri = row0 + r, tok = ri / a.G, hd = h * a.G + ri % a.G;
-  const size_t at = (static_cast<size_t>(q0) + tok) * a.Hq + hd;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t b[4];
-#pragma unroll
-  for (int n = 0; n < 4; ++n)
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b[n]) : "f"(v[2 * n + 1] * inv), "f"(v[2 * n] * inv));
-  *reinterpret_cast<uint4*>(a.out + at * D + 8 * w) = make_uint4(b[0], b[1], b[2], b[3]);
-  if (w == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-}
-
 template <int D>
 int launch(const AttendArgs& a, int grid, cudaStream_t s) {
   const size_t smem = sizeof(Smem<D>) + static_cast<size_t>(a.c.S) * 8;
@@ -685,8 +647,7 @@ int launch(const AttendArgs& a, int grid, cudaStream_t s) {
     st = launch_k(attend_wide_kernel<D>, dim3(grid), dim3(kThreads), smem, s, false, a);
   }
   if (st != MOE_OK) return st;
-  LaunchScope ls(kProfKv4Attend, s);
-  return launch_k(combine_wide_kernel<D>, dim3(grid, kWideRows / 8), dim3(D), 0, s, true, a);
+  return launch_combine<D, kWideRows, true>(a, grid, s);
 }
 
 }  // namespace
