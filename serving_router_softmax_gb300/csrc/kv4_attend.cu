@@ -391,10 +391,9 @@ template <int D, int NT>
 int launch_attend(const AttendArgs& a, const Plan& p, cudaStream_t s) {
   using SM = Smem<D, NT, stages<D>()>;
   const size_t smem = sizeof(SM) + static_cast<size_t>(a.c.S) * 8;
-  auto k = attend_kernel<D, NT, stages<D>()>;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  int st;
+  constexpr auto k = attend_kernel<D, NT, stages<D>()>;
+  int st = allow_smem<k>(smem);
+  if (st != MOE_OK) return st;
   {
     LaunchScope ls(kProfKv4Attend, s);
     st = launch_k(k, dim3(p.grid), dim3(kThreads), smem, s, false, a);

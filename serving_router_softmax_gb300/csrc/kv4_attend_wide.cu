@@ -638,10 +638,8 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
 template <int D>
 int launch(const AttendArgs& a, int grid, cudaStream_t s) {
   const size_t smem = sizeof(Smem<D>) + static_cast<size_t>(a.c.S) * 8;
-  if (cudaFuncSetAttribute(attend_wide_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-      cudaSuccess)
-    return MOE_ERR_CUDA;
-  int st;
+  int st = allow_smem<attend_wide_kernel<D>>(smem);
+  if (st != MOE_OK) return st;
   {
     LaunchScope ls(kProfKv4Attend, s);
     st = launch_k(attend_wide_kernel<D>, dim3(grid), dim3(kThreads), smem, s, false, a);

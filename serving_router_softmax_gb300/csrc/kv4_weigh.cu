@@ -143,9 +143,8 @@ __global__ void __launch_bounds__(32 * kWarps) weigh_kernel(const WeighArgs a) {
 template <int D>
 int launch_weigh(const WeighArgs& a, cudaStream_t s) {
   const size_t smem = sizeof(Smem<D>) + static_cast<size_t>(a.c.S) * 8;
-  if (cudaFuncSetAttribute(weigh_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-      cudaSuccess)
-    return MOE_ERR_CUDA;
+  const int st = allow_smem<weigh_kernel<D>>(smem);
+  if (st != MOE_OK) return st;
   LaunchScope ls(kProfKv4Weigh, s);
   return launch_k(weigh_kernel<D>, dim3(sm_count() * 3), dim3(32 * kWarps), smem, s, false, a);
 }

@@ -1,9 +1,13 @@
 """Binding of the 4-bit paged KV cache (kv4_* of include/moe_verify.h).
 
-Thin like ``api``: argument checks and pointer marshalling; tensors are on one
-CUDA device, calls enqueue on the current stream (or ``stream``) and raise
-``MoEError`` on a non-OK host status.  Device-side error bits land in
+Thin like ``api``: argument checks and pointer marshalling; tensors are on the
+cache's CUDA device, calls enqueue on the current stream (or ``stream``) and
+raise ``MoEError`` on a non-OK host status.  Device-side error bits land in
 ``dev_err`` where one is given.
+
+A small call's host time is of the order of its device time, so what does not
+change from call to call (the argument structs, the workspace) is kept with
+the cache.
 """
 from __future__ import annotations
 
@@ -13,9 +17,11 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib as L
-from .api import MoEError, _check, _need, _ptr, _stream
+from .api import MoEError, _check, _need
 
 _DTYPES = {torch.float32: L.DTYPE_F32, torch.bfloat16: L.DTYPE_BF16}
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 class Kv4Cache:
@@ -23,6 +29,7 @@ class Kv4Cache:
 
     ``pages`` uint8 [n_pages, n_kv_heads, page_size * (head_dim + 8)] and ``table`` int32 [n_seq, max_pages]
     stay the caller's: the table's contents (which page holds a sequence's slots) may change between calls.
+    The object keeps kv4_attend's workspace, one for each stream it is called on.
     """
 
     def __init__(self, pages: torch.Tensor, table: torch.Tensor, page_size: int, head_dim: int):
@@ -32,13 +39,18 @@ class Kv4Cache:
             raise MoEError("table: expected int32 [n_seq, max_pages]")
         if pages.device != table.device:
             raise MoEError("pages and table are on different devices")
+        for t in (pages, table):
+            if not t.is_cuda or not t.is_contiguous():
+                raise MoEError("expected contiguous CUDA tensors")
         self.pages, self.table = pages, table
         self.page_size, self.head_dim = page_size, head_dim
         self.n_kv_heads, self.n_seq = pages.shape[1], table.shape[0]
         self.max_slots = table.shape[1] * page_size
-        self.device = pages.device
+        self.device, self._index = pages.device, pages.device.index
         self._struct = L.Kv4CacheStruct(pages.shape[0], page_size, pages.shape[1], head_dim, table.shape[0],
-                                        table.shape[1], _ptr(pages), _ptr(table))
+                                        table.shape[1], pages.data_ptr(), table.data_ptr())
+        self._ref = C.byref(self._struct)
+        self._plans, self._workspaces = {}, {}
 
     @classmethod
     def new(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, n_seq: int, max_pages: int,
@@ -51,27 +63,53 @@ class Kv4Cache:
         """Accumulated attention weights of every slot, zero: [n_seq, n_kv_heads, max_slots] fp32."""
         return torch.zeros((self.n_seq, self.n_kv_heads, self.max_slots), dtype=torch.float32, device=self.device)
 
+    def _plan(self, key, make):
+        """The argument struct (and what else `make` gives) of calls of one shape."""
+        p = self._plans.get(key)
+        if p is None:
+            if len(self._plans) > 256:
+                self._plans.clear()
+            p = self._plans[key] = make()
+        return p
 
-def _strided(t: torch.Tensor, name: str, shape, dtype: Optional[torch.dtype] = None) -> int:
-    """Pointer of a tensor whose last dimension is contiguous."""
-    if not t.is_cuda:
-        raise MoEError("expected a CUDA tensor")
-    if t.dim() != 3 or tuple(t.shape) != tuple(shape):
-        raise MoEError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise MoEError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.shape[2] > 1 and t.stride(2) != 1:
-        raise MoEError(f"{name}: the last dimension must be contiguous")
+    def _workspace(self, nbytes: int, stream: int) -> torch.Tensor:
+        # A graph's calls must not share a workspace with calls that may run beside its replays.
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        w = self._workspaces.get(stream)
+        if w is None or w.numel() < nbytes:
+            w = self._workspaces[stream] = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        return w
+
+
+def _arg(t: torch.Tensor, dtype: torch.dtype, shape, name: str) -> int:
+    """Pointer of a contiguous CUDA tensor of this type and shape."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _need(t, dtype, shape, name)
+        raise MoEError(f"{name}: expected a contiguous CUDA tensor")
     return t.data_ptr()
 
 
-def _places(cache: Kv4Cache, seq: torch.Tensor, slot: torch.Tensor) -> int:
-    if seq.dim() != 1:
-        raise MoEError("seq: expected one dimension")
-    T = seq.shape[0]
-    _need(seq, torch.int32, (T,), "seq")
-    _need(slot, torch.int32, (T,), "slot")
-    return T
+def _err(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else _arg(t, torch.int32, (1,), "dev_err")
+
+
+def _strided(t: torch.Tensor, name: str, shape, dtype: torch.dtype) -> None:
+    """A CUDA tensor whose last dimension is contiguous."""
+    if not t.is_cuda:
+        raise MoEError("expected a CUDA tensor")
+    if t.dim() != 3 or t.shape != shape:
+        raise MoEError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise MoEError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise MoEError(f"{name}: the last dimension must be contiguous")
+
+
+def _on(stream, call, *args, **kw):
+    """The call with `stream` as the current one, its outputs and workspace allocated there too."""
+    with torch.cuda.stream(stream):
+        return call(*args, **kw)
 
 
 def kv4_append(cache: Kv4Cache, k: torch.Tensor, v: torch.Tensor, seq: torch.Tensor, slot: torch.Tensor,
@@ -81,47 +119,66 @@ def kv4_append(cache: Kv4Cache, k: torch.Tensor, v: torch.Tensor, seq: torch.Ten
 
     ``k`` and ``v`` [T, n_kv_heads, head_dim], bfloat16 or float32; token and head strides are free (multiples of
     16 bytes).  With ``held`` returns the values the cache now holds for them, same shape and type."""
-    T = _places(cache, seq, slot)
-    shape = (T, cache.n_kv_heads, cache.head_dim)
-    dt = _DTYPES.get(k.dtype)
-    if dt is None:
-        raise MoEError(f"k: expected bfloat16 or float32, got {k.dtype}")
-    kp, vp = _strided(k, "k", shape), _strided(v, "v", shape, k.dtype)
-    out = (torch.empty(shape, dtype=k.dtype, device=k.device), torch.empty(shape, dtype=k.dtype, device=k.device)) if held else None
-    ks, vs = k.stride(), v.stride()
-    cfg = L.Kv4RowsCfg(T, dt, ks[0], ks[1], vs[0], vs[1])
-    _check(L.load().kv4_append(C.byref(cache._struct), kp, vp, C.byref(cfg), _ptr(seq), _ptr(slot),
-                               out[0].data_ptr() if held else None, out[1].data_ptr() if held else None,
-                               _ptr(dev_err), _stream(stream)), "kv4_append")
-    return out
+    if stream is not None:
+        return _on(stream, kv4_append, cache, k, v, seq, slot, held, dev_err)
+    T = seq.shape[0] if seq.dim() == 1 else -1
+
+    def make():
+        shape = (T, cache.n_kv_heads, cache.head_dim)
+        if k.dtype not in _DTYPES:
+            raise MoEError(f"k: expected bfloat16 or float32, got {k.dtype}")
+        _strided(k, "k", shape, k.dtype)
+        _strided(v, "v", shape, k.dtype)
+        ks, vs = k.stride(), v.stride()
+        cfg = L.Kv4RowsCfg(T, _DTYPES[k.dtype], ks[0], ks[1], vs[0], vs[1])
+        return C.byref(cfg), shape
+
+    ref, shape = cache._plan(("append", T, k.dtype, v.dtype, k.shape, v.shape, k.stride(), v.stride(), k.is_cuda, v.is_cuda), make)
+    kh = vh = None
+    if held:
+        kh = torch.empty(shape, dtype=k.dtype, device=cache.device)
+        vh = torch.empty(shape, dtype=k.dtype, device=cache.device)
+    _check(L.load().kv4_append(cache._ref, k.data_ptr(), v.data_ptr(), ref, _arg(seq, torch.int32, (T,), "seq"),
+                               _arg(slot, torch.int32, (T,), "slot"), kh.data_ptr() if held else None,
+                               vh.data_ptr() if held else None, _err(dev_err), _raw_stream(cache._index)), "kv4_append")
+    return (kh, vh) if held else None
 
 
 def kv4_read(cache: Kv4Cache, seq: torch.Tensor, slot: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
              dev_err: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """The held keys and values [T, n_kv_heads, head_dim] of T (seq, slot) places (slot -1: zeros)."""
-    T = _places(cache, seq, slot)
-    dt = _DTYPES.get(dtype)
-    if dt is None:
-        raise MoEError(f"dtype: expected bfloat16 or float32, got {dtype}")
-    shape = (T, cache.n_kv_heads, cache.head_dim)
-    k, v = torch.empty(shape, dtype=dtype, device=cache.device), torch.empty(shape, dtype=dtype, device=cache.device)
-    cfg = L.Kv4RowsCfg(T, dt, 0, 0, 0, 0)
-    _check(L.load().kv4_read(C.byref(cache._struct), _ptr(seq), _ptr(slot), C.byref(cfg), k.data_ptr(), v.data_ptr(),
-                             _ptr(dev_err), _stream(stream)), "kv4_read")
+    if stream is not None:
+        return _on(stream, kv4_read, cache, seq, slot, dtype, dev_err)
+    T = seq.shape[0] if seq.dim() == 1 else -1
+
+    def make():
+        if dtype not in _DTYPES:
+            raise MoEError(f"dtype: expected bfloat16 or float32, got {dtype}")
+        return C.byref(L.Kv4RowsCfg(T, _DTYPES[dtype], 0, 0, 0, 0)), (T, cache.n_kv_heads, cache.head_dim)
+
+    sp, jp = _arg(seq, torch.int32, (T,), "seq"), _arg(slot, torch.int32, (T,), "slot")
+    ref, shape = cache._plan(("read", T, dtype), make)
+    k = torch.empty(shape, dtype=dtype, device=cache.device)
+    v = torch.empty(shape, dtype=dtype, device=cache.device)
+    _check(L.load().kv4_read(cache._ref, sp, jp, ref, k.data_ptr(), v.data_ptr(), _err(dev_err),
+                             _raw_stream(cache._index)), "kv4_read")
     return k, v
 
 
-def _attn(cache: Kv4Cache, q, q_start, base, max_q, visible, scale):
-    if q.dim() != 3:
-        raise MoEError("q: expected [T, n_q_heads, head_dim]")
-    T, Hq, _ = q.shape
-    qp = _strided(q, "q", (T, Hq, cache.head_dim), torch.bfloat16)
-    _need(q_start, torch.int32, (cache.n_seq + 1,), "q_start")
-    _need(base, torch.int32, (cache.n_seq,), "base")
-    if visible is not None:
-        _need(visible, torch.int64, (T,), "visible")
-    st = q.stride()
-    return qp, L.Kv4AttnCfg(T, Hq, max_q, cache.head_dim ** -0.5 if scale is None else scale, st[0], st[1])
+def _attn_plan(cache: Kv4Cache, q: torch.Tensor, max_q: int, scale: Optional[float]):
+    """(struct, workspace bytes, shapes of out, lse, q_start, base, visible) of a call with these queries."""
+    def make():
+        if q.dim() != 3:
+            raise MoEError("q: expected [T, n_q_heads, head_dim]")
+        T, Hq, _ = q.shape
+        _strided(q, "q", (T, Hq, cache.head_dim), torch.bfloat16)
+        st = q.stride()
+        cfg = L.Kv4AttnCfg(T, Hq, max_q, cache.head_dim ** -0.5 if scale is None else scale, st[0], st[1])
+        ref = C.byref(cfg)
+        return (ref, int(L.load().kv4_attend_workspace(cache._ref, ref)), (T, Hq, cache.head_dim), (T, Hq),
+                (cache.n_seq + 1,), (cache.n_seq,), (T,))
+
+    return cache._plan(("attn", q.shape, q.stride(), q.dtype, q.is_cuda, max_q, scale), make)
 
 
 def kv4_attend(cache: Kv4Cache, q: torch.Tensor, q_start: torch.Tensor, base: torch.Tensor, max_q: int,
@@ -135,24 +192,27 @@ def kv4_attend(cache: Kv4Cache, q: torch.Tensor, q_start: torch.Tensor, base: to
     multiples of 8), appended at slots ``base[s]`` and on; each sees the ``base[s]`` context slots and, of the new
     ones, those set in its 64-bit mask ``visible`` (int64 [T]; None: itself and those before it).  ``max_q``: the
     most new tokens of a sequence; it chooses the kernel.  ``scale``: head_dim ** -0.5 if None."""
-    lib = L.load()
-    qp, cfg = _attn(cache, q, q_start, base, max_q, visible, scale)
-    T, Hq, D = q.shape
+    if stream is not None:
+        return _on(stream, kv4_attend, cache, q, q_start, base, max_q, visible, scale, out, lse, workspace, dev_err)
+    ref, need, so, sl, sq, sb, sv = _attn_plan(cache, q, max_q, scale)
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty(so, dtype=torch.bfloat16, device=cache.device)
     if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-    _need(out, torch.bfloat16, (T, Hq, D), "out")
-    _need(lse, torch.float32, (T, Hq), "lse")
+        lse = torch.empty(sl, dtype=torch.float32, device=cache.device)
+    st = _raw_stream(cache._index)
     if workspace is None:
-        workspace = torch.empty(kv4_attend_workspace_bytes(cache, cfg), dtype=torch.uint8, device=q.device)
-    _check(lib.kv4_attend(C.byref(cache._struct), qp, _ptr(q_start), _ptr(base), _ptr(visible), C.byref(cfg), _ptr(out),
-                          _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(dev_err), _stream(stream)), "kv4_attend")
+        workspace = cache._workspace(need, st)
+    _check(L.load().kv4_attend(cache._ref, q.data_ptr(), _arg(q_start, torch.int32, sq, "q_start"),
+                               _arg(base, torch.int32, sb, "base"),
+                               None if visible is None else _arg(visible, torch.int64, sv, "visible"), ref,
+                               _arg(out, torch.bfloat16, so, "out"), _arg(lse, torch.float32, sl, "lse"),
+                               workspace.data_ptr(), workspace.numel(), _err(dev_err), st), "kv4_attend")
     return out, lse
 
 
-def kv4_attend_workspace_bytes(cache: Kv4Cache, cfg: L.Kv4AttnCfg) -> int:
-    return int(L.load().kv4_attend_workspace(C.byref(cache._struct), C.byref(cfg)))
+def kv4_attend_workspace_bytes(cache: Kv4Cache, q: torch.Tensor, max_q: int) -> int:
+    """Bytes of workspace that kv4_attend needs for queries of this shape."""
+    return _attn_plan(cache, q, max_q, None)[1]
 
 
 def kv4_weigh(cache: Kv4Cache, q: torch.Tensor, q_start: torch.Tensor, base: torch.Tensor, max_q: int,
@@ -160,11 +220,15 @@ def kv4_weigh(cache: Kv4Cache, q: torch.Tensor, q_start: torch.Tensor, base: tor
               scale: Optional[float] = None, dev_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Adds to ``mass`` [n_seq, n_kv_heads, max_slots] the softmax weight that the new tokens gave each slot
     (arguments as kv4_attend, ``lse`` its result); returns ``mass``."""
-    qp, cfg = _attn(cache, q, q_start, base, max_q, visible, scale)
-    _need(lse, torch.float32, q.shape[:2], "lse")
-    _need(mass, torch.float32, (cache.n_seq, cache.n_kv_heads, cache.max_slots), "mass")
-    _check(L.load().kv4_weigh(C.byref(cache._struct), qp, _ptr(q_start), _ptr(base), _ptr(visible), _ptr(lse),
-                              C.byref(cfg), _ptr(mass), _ptr(dev_err), _stream(stream)), "kv4_weigh")
+    if stream is not None:
+        return _on(stream, kv4_weigh, cache, q, q_start, base, max_q, lse, mass, visible, scale, dev_err)
+    ref, _, _, sl, sq, sb, sv = _attn_plan(cache, q, max_q, scale)
+    _check(L.load().kv4_weigh(cache._ref, q.data_ptr(), _arg(q_start, torch.int32, sq, "q_start"),
+                              _arg(base, torch.int32, sb, "base"),
+                              None if visible is None else _arg(visible, torch.int64, sv, "visible"),
+                              _arg(lse, torch.float32, sl, "lse"), ref,
+                              _arg(mass, torch.float32, (cache.n_seq, cache.n_kv_heads, cache.max_slots), "mass"),
+                              _err(dev_err), _raw_stream(cache._index)), "kv4_weigh")
     return mass
 
 
@@ -174,17 +238,21 @@ def kv4_evict(cache: Kv4Cache, mass: torch.Tensor, lens: torch.Tensor, keep: int
     """Keeps, per sequence and kv head, the last ``recent`` slots and the others of largest mass, ``keep`` in all, and
     moves them to slots 0.. in their old order.  Returns (new_len [n_seq], origin [n_seq, n_kv_heads, keep]: the old
     slot of each new one, -1 past new_len, the masses: ``mass_out``, or ``mass`` itself rewritten where None)."""
-    shape = (cache.n_seq, cache.n_kv_heads, cache.max_slots)
-    _need(mass, torch.float32, shape, "mass")
-    _need(lens, torch.int32, (cache.n_seq,), "lens")
+    if stream is not None:
+        return _on(stream, kv4_evict, cache, mass, lens, keep, recent, mass_out, dev_err)
+
+    def make():
+        if keep < 1 or not 0 <= recent <= keep:
+            raise MoEError("expected 1 <= keep and 0 <= recent <= keep")
+        return (C.byref(L.Kv4EvictCfg(keep, recent)), (cache.n_seq, cache.n_kv_heads, cache.max_slots), (cache.n_seq,),
+                (cache.n_seq, cache.n_kv_heads, keep))
+
+    ref, sm, sn, so = cache._plan(("evict", keep, recent), make)
     if mass_out is None:
         mass_out = mass
-    _need(mass_out, torch.float32, shape, "mass_out")
-    if keep < 1 or not 0 <= recent <= keep:
-        raise MoEError("expected 1 <= keep and 0 <= recent <= keep")
-    new_len = torch.empty(cache.n_seq, dtype=torch.int32, device=cache.device)
-    origin = torch.empty((cache.n_seq, cache.n_kv_heads, keep), dtype=torch.int32, device=cache.device)
-    cfg = L.Kv4EvictCfg(keep, recent)
-    _check(L.load().kv4_evict(C.byref(cache._struct), _ptr(mass), _ptr(lens), C.byref(cfg), _ptr(new_len), _ptr(origin),
-                              _ptr(mass_out), _ptr(dev_err), _stream(stream)), "kv4_evict")
+    new_len = torch.empty(sn, dtype=torch.int32, device=cache.device)
+    origin = torch.empty(so, dtype=torch.int32, device=cache.device)
+    _check(L.load().kv4_evict(cache._ref, _arg(mass, torch.float32, sm, "mass"), _arg(lens, torch.int32, sn, "lens"), ref,
+                              new_len.data_ptr(), origin.data_ptr(), _arg(mass_out, torch.float32, sm, "mass_out"),
+                              _err(dev_err), _raw_stream(cache._index)), "kv4_evict")
     return new_len, origin, mass_out
