@@ -18,10 +18,18 @@
 // registers a thread: two CTAs share an SM.  Bound by the exponentials (16 a
 // clock and SM: 8 clocks per slot of 128 rows) and as much by the products (8).
 #include "kv4_attend.cuh"
+#include "tc_f16.cuh"
 
 namespace moe {
 namespace kv4 {
 namespace {
+
+using tc::add2;
+using tc::fma2;
+using tc::idesc_f16;
+using tc::mul2;
+using tc::tmem_st16;
+using tc::tmem_st_wait;
 
 constexpr int kThreads = 320;
 constexpr int kRaw = 3;       // tiles in flight
@@ -47,28 +55,6 @@ struct Smem {
   long long cum[1];                              // [S + 1]
 };
 
-// D[tmem] (+)= A[tmem] * B[smem]^T, fp16 operands, fp32 sums.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Instruction descriptor of kind::f16 with fp16 A/B, fp32 D, both K-major.
-constexpr uint32_t idesc_f16(int M, int N) {
-  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // 32 columns of the thread's lane, waited for.
 __device__ __forceinline__ void tmem_ld_pairs(uint32_t taddr, float2 (&e)[16]) {
   asm volatile(
@@ -81,27 +67,6 @@ __device__ __forceinline__ void tmem_ld_pairs(uint32_t taddr, float2 (&e)[16]) {
         "=f"(e[15].x), "=f"(e[15].y)
       : "r"(taddr));
   tc::tmem_ld_wait();
-}
-
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
-      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
-      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return r;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
-      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -573,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
       const uint64_t kd = kd0 + b * (sizeof(sm.k16[0]) >> 4) + h * (kHalf * 128 >> 4);
 #pragma unroll
       for (int t = 0; t < D / 16; ++t)
-        mma_ts(tmem + kSCol + h * kHalf, tmem + kQCol + 8 * t, kd + (t >> 2) * (kTile * 128 >> 4) + (t & 3) * 2, is, t > 0);
+        tc::mma_f16_ts(tmem + kSCol + h * kHalf, tmem + kQCol + 8 * t, kd + (t >> 2) * (kTile * 128 >> 4) + (t & 3) * 2, is, t > 0);
       tc::mma_commit(&sm.s_full[h]);
     };
     for (long long u = u0; u < u1 && !dead;) {
@@ -601,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
           const uint64_t vd = vd0 + b * (sizeof(sm.v16[0]) >> 4) + h * (kHalf * 2 >> 4);
 #pragma unroll
           for (int t = 0; t < kHalf / 16; ++t)
-            mma_ts(tmem + kOCol, tmem + kSCol + h * kHalf + 8 * t, vd + t * 2, io, it > 0 || h > 0 || t > 0);
+            tc::mma_f16_ts(tmem + kOCol, tmem + kSCol + h * kHalf + 8 * t, vd + t * 2, io, it > 0 || h > 0 || t > 0);
           if (h) tc::mma_commit(&sm.kv_empty[b]);
           tc::mma_commit(&sm.pv_done[h]);
           if (it + 1 < s.tiles) {

@@ -3,11 +3,19 @@
 //   mass[s, h, j] += sum over the query rows i of kv head h: exp(S_ij - lse_i)
 //
 // with the lse of kv4_attend, so one pass over the keys alone (half the
-// cache): a warp holds the codes of 16 slots in registers as the matrix row
-// operand, goes through all query rows in steps of 8 and sums its slots'
-// weights in fp32 in a fixed order; no atomics.
+// cache).  Slots are the rows of the product on the 5th-generation tensor cores,
+// S^T [128 slots x query rows] = C_k Q^T: a thread owns a slot, unpacks its key
+// into TMEM (the nibbles are fp16 numbers already, see kv4.cuh), keeps its scale and zero in
+// registers, and sums its own columns' exponentials in fp32 in a fixed order: no
+// atomics, no exchange between threads.
+//
+// Four warps and 128 TMEM columns (keys, 64 columns of scores) a CTA, three CTAs
+// an SM (four at D = 64), so that one's products and loads run while the others' exponentials do.
+// Bound by the exponentials (16 a clock and SM) from about 45 query rows a kv
+// head on, by memory (D / 2 + 4 bytes of keys, 8 of mass a slot) below.
 #include "kv4.cuh"
 #include "kv4_sched.cuh"
+#include "tc_f16.cuh"
 
 namespace moe {
 namespace kv4 {
@@ -16,10 +24,19 @@ int attn_validate(const kv4_attn_cfg* cfg, const Cache& c);
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kSlots = 16 * kWarps;  // slots of a unit
-constexpr int kRows = 128;           // query rows held at a time
+using tc::add2;
+using tc::fma2;
+using tc::mul2;
+
+constexpr int kThreads = 128;
+constexpr int kSlots = 128;          // slots of a unit, one a thread
+constexpr int kRows = 128;           // query rows held in shared memory at a time
+constexpr int kCols = 64;            // columns of a product
 constexpr int kAllRows = 1 << 30;    // one row block per kv head
+constexpr int kStages = 3;           // key rows on their way
+constexpr int kGroup = 8;            // units whose sums wait in shared memory where rows come in several blocks
+constexpr uint32_t kTmemCols = 128;
+constexpr uint64_t kWaitBudgetNs = 2000000000ull;  // 2 s
 
 struct WeighArgs {
   Cache c;
@@ -37,106 +54,267 @@ struct WeighArgs {
 
 template <int D>
 struct Smem {
-  uint2 frag[kRows / 8 * (D / 16) * 32];
-  float cq[kRows], cqs[kRows], lse2[kRows];
+  alignas(1024) uint8_t q[kRows * D * 2];                    // panels of 64 dimensions: [128 rows][128 B], 128-byte swizzle
+  alignas(16) uint8_t k[4][kStages][32 * (D / 2 + 16)];      // per warp: key rows, 16 bytes apart so that lanes miss each other's banks
+  uint32_t par[4][kStages][32];                              // their scales and zeros
+  alignas(16) float cq[kRows];
+  alignas(16) float cqs[kRows];
+  alignas(16) float nl[kRows];                               // -lse, in log2; -inf: no weight
   uint64_t mask[kRows];
   int token[kRows];
+  float acc[kGroup][kSlots];
+  uint64_t done;
   long long scratch[32];
+  uint32_t tmem;
+  int abort, never;
   long long cum[1];
 };
 
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Rows row0 .. of the item's queries into shared memory as the product's
+// second operand, in the order of the key words' pairs (see prep_q of kv4.cuh).
 template <int D>
-__global__ void __launch_bounds__(32 * kWarps) weigh_kernel(const WeighArgs a) {
-  extern __shared__ __align__(128) uint8_t smem_raw[];
+__device__ __forceinline__ void load_queries(const WeighArgs& a, const Cursor& k, int row0, int rows, Smem<D>& sm) {
+  constexpr int W = D / 8;  // a row's code words, one a lane
+  const int x = threadIdx.x % W;
+  const int padded = (rows + 15) & ~15;
+#pragma unroll 1
+  for (int r = threadIdx.x / W; r < padded; r += kThreads / W) {
+    const int i = (row0 + r) / a.G, g = (row0 + r) - i * a.G, hd = k.h * a.G + g;
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    float nl = -INFINITY;
+    if (r < rows) {
+      raw = *reinterpret_cast<const uint4*>(a.q + (k.q.q0 + i) * a.q_ts + hd * a.q_hs + 8 * x);
+      nl = a.lse[(static_cast<size_t>(k.q.q0) + i) * a.Hq + hd];
+    }
+    const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+    float v[8], m = 0.f, sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(u[j] << 16);
+      v[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+      m = fmaxf(m, fmaxf(fabsf(v[2 * j]), fabsf(v[2 * j + 1])));
+      sum += v[2 * j] + v[2 * j + 1];
+    }
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) {
+      m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    }
+    const int ex = static_cast<int>(__float_as_uint(m) >> 23);
+    const int e = m > 0.f && ex < 255 ? 14 + 127 - (ex > 0 ? ex : 1) : 0;
+    const float f1 = __uint_as_float(static_cast<uint32_t>(127 + (e >> 1)) << 23);
+    const float f2 = __uint_as_float(static_cast<uint32_t>(127 + e - (e >> 1)) << 23);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = v[j] * f1 * f2;
+    *reinterpret_cast<uint4*>(sm.q + (x >> 3) * (kRows * 128) + (r >> 3) * 1024 + (r & 7) * 128 + (((x & 7) ^ (r & 7)) << 4)) =
+        make_uint4(pack_h2(v[0], v[4]), pack_h2(v[1] * 0.0625f, v[5] * 0.0625f), pack_h2(v[2], v[6]),
+                   pack_h2(v[3] * 0.0625f, v[7] * 0.0625f));
+    if (x == 0) {
+      const int y = 24 - e;  // the codes carry 2^-24
+      sm.cq[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + (y >> 1)) << 23) *
+                 __uint_as_float(static_cast<uint32_t>(127 + y - (y >> 1)) << 23);
+      sm.cqs[r] = a.scale_log2 * sum;
+      const bool none = nl == -INFINITY;  // a row that saw nothing sees no new slot, whatever those hold
+      sm.nl[r] = none ? -INFINITY : -nl * kLog2e;
+      sm.token[r] = none ? -1 : i;
+      sm.mask[r] = a.visible && !none ? a.visible[k.q.q0 + i] : 0;
+    }
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
+  constexpr int P = D / 32, kStride = D / 2 + 16;   // 16-byte pieces of a key row, bytes of it in shared memory
+  constexpr uint32_t kACol = 0, kSCol = D / 2;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    tc::mbar_init(&sm.done, 1);
+    sm.abort = sm.never = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 0) {
+    tc::tmem_alloc(&sm.tmem, kTmemCols);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
   pdl_wait();
   pdl_trigger();
   build_units(a.c, a.q_start, a.base, a.T, a.G, kAllRows, kSlots, 0, sm.cum, sm.scratch, a.dev_err, blockIdx.x == 0);
+  tc::tc_fence_after();
+  const uint32_t tmem = sm.tmem, mine = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+  const uint64_t qd = tc::smem_desc_sw128(tc::smem_u32(sm.q));
+  volatile int* abort_flag = &sm.abort;
   const long long total = sm.cum[a.c.S];
   const long long u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
   const size_t width = static_cast<size_t>(a.c.width) << a.c.page_log2;
+  uint32_t parity = 0;
+  bool dead = false;
   Cursor k;
   if (u0 < u1) cursor_at(k, a.c, a.q_start, a.base, a.T, a.G, kAllRows, kSlots, 0, sm.cum, u0);
-  int held_s = -1, held_h = -1, held_row = -1;  // query rows in shared memory
-  for (long long u = u0; u < u1; ++u) {
-    if (k.tile == k.nt) cursor_next(k, a.c, a.q_start, a.base, a.T, a.G, kAllRows, kSlots, 0, sm.cum);
-    const int j0 = k.tile * kSlots + 16 * warp;
-    const int page = j0 < k.q.total ? page_of(a.c, k.s, j0) : -1;
-    if (page < 0 && j0 < k.q.total && lane == 0) flag_error(a.dev_err, MOE_DEV_BAD_ID);
-    uint32_t ka[D / 32] = {}, kb[D / 32] = {};
-    float2 pa = make_float2(0.f, 0.f), pb = pa;
-    const int sa = slot_of_row(g), sb = slot_of_row(g + 8);
-    float* mass = a.mass + (static_cast<size_t>(k.s) * a.c.Hkv + k.h) * width;
-    if (page >= 0) {
-      const uint8_t* b = page_block(a.c, page, k.h);
-      const int r0 = j0 & (a.c.page_size - 1);
-      load_k_words<D>(b + static_cast<size_t>(r0 + sa) * (D / 2), c, ka);
-      load_k_words<D>(b + static_cast<size_t>(r0 + sb) * (D / 2), c, kb);
-      const uint8_t* p = b + static_cast<size_t>(a.c.page_size) * D;
-      pa = __half22float2(*reinterpret_cast<const __half2*>(p + (r0 + sa) * 8));
-      pb = __half22float2(*reinterpret_cast<const __half2*>(p + (r0 + sb) * 8));
-    }
-    const bool edge = j0 + 16 > k.q.base;
-    float wa = 0.f, wb = 0.f;
-    const int all = k.q.nq * a.G;
+  for (long long u = u0; u < u1 && !dead;) {
+    const int units = static_cast<int>(u1 - u < k.nt - k.tile ? u1 - u : k.nt - k.tile);
+    const int all = k.q.nq * a.G, blocks = (all + kRows - 1) / kRows;
     if (a.visible && k.q.nq > kMaxTree && tid == 0) flag_error(a.dev_err, MOE_DEV_CAPACITY);
-    for (int row0 = 0; row0 < all; row0 += kRows) {
-      const int rows = min(kRows, all - row0), padded = (rows + 7) & ~7;
-      if (k.s != held_s || k.h != held_h || row0 != held_row) {
+    float* mass = a.mass + (static_cast<size_t>(k.s) * a.c.Hkv + k.h) * width;
+    const int group = blocks > 1 ? kGroup : units;
+    for (int g0 = 0; g0 < units && !dead; g0 += group) {
+      const int n = min(group, units - g0), t0 = k.tile + g0;
+      for (int block = 0; block < blocks && !dead; ++block) {
+        const int row0 = block * kRows, rows = min(kRows, all - row0), padded = (rows + 15) & ~15;
+        __syncthreads();  // the rows before have been read
+        load_queries<D>(a, k, row0, rows, sm);
         __syncthreads();
-        prep_q<D>(
-            [&](int r) -> const uint16_t* {
-              if (r >= rows) return nullptr;
-              const int i = (row0 + r) / a.G, x = (row0 + r) - i * a.G;
-              return a.q + (k.q.q0 + i) * a.q_ts + static_cast<long long>(k.h * a.G + x) * a.q_hs;
-            },
-            padded, a.scale_log2, sm.frag, sm.cq, sm.cqs, tid, 32 * kWarps);
-        for (int r = tid; r < padded; r += 32 * kWarps) {
-          const int i = (row0 + min(r, rows - 1)) / a.G, x = (row0 + r) - i * a.G;
-          float v = INFINITY;
-          if (r < rows) {
-            v = a.lse[(static_cast<size_t>(k.q.q0) + i) * a.Hq + k.h * a.G + x] * kLog2e;
-            if (v == -INFINITY) v = INFINITY;  // a row that saw nothing gives no weight
-          }
-          sm.lse2[r] = v;
-          // such a row sees no new slot either, whatever those hold
-          sm.token[r] = v == INFINITY ? -1 : i;
-          sm.mask[r] = a.visible && v != INFINITY ? a.visible[k.q.q0 + i] : 0;
-        }
-        held_s = k.s, held_h = k.h, held_row = row0;
-        __syncthreads();
-      }
-      if (page < 0) continue;
-      for (int t = 0; t < padded / 8; ++t) {
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        qk_16x8<D>(acc, ka, kb, [&](int i) { return sm.frag[(t * (D / 16) + i) * 32 + lane]; });
+        // Key rows: lane l looks up slot l's page, the lanes copy the warp's rows together.
+        int page = -1;
+        uint32_t found = 0;  // bit i: the slot of stage i lies in a valid page
+        auto look = [&](int i) {
+          const int j = (t0 + i) * kSlots + tid;
+          page = i < n && j < k.q.total ? page_of(a.c, k.s, j) : -1;
+          if (i < n && j < k.q.total && page < 0) flag_error(a.dev_err, MOE_DEV_BAD_ID);
+        };
+        auto start = [&](int i, int st) {
+          const int j0 = (t0 + i) * kSlots + warp * 32;
+          found = (found & ~(1u << st)) | (static_cast<uint32_t>(page >= 0) << st);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = 8 * t + 2 * c + (e & 1);
-          const float2 p = e < 2 ? pa : pb;
-          float w = ex2(fmaf(p.x, acc[e] * sm.cq[r], fmaf(p.y, sm.cqs[r], -sm.lse2[r])));
-          if (edge) {
-            const int j = j0 + (e < 2 ? sa : sb), d = j - k.q.base;
-            bool see = d < 0;
-            if (!see && j < k.q.total) see = a.visible ? d < kMaxTree && ((sm.mask[r] >> d) & 1) : d <= sm.token[r];
-            w = see ? w : 0.f;
+          for (int x = 0; x < P; ++x) {
+            const int r = (x * 32 + lane) / P, piece = lane % P;
+            const int pg = __shfl_sync(0xFFFFFFFFu, page, r);
+            if (pg >= 0)
+              copy_async16(sm.k[warp][st] + r * kStride + 16 * piece,
+                           page_block(a.c, pg, k.h) + ((j0 + r) & (a.c.page_size - 1)) * (D / 2) + 16 * piece);
           }
-          if (e < 2) wa += w;
-          else wb += w;
+          if (page >= 0)
+            copy_async4(&sm.par[warp][st][lane],
+                        page_block(a.c, page, k.h) + a.c.page_size * D + ((j0 + lane) & (a.c.page_size - 1)) * 8);
+          copies_commit();
+        };
+        look(0);
+#pragma unroll 1
+        for (int i = 0; i < kStages - 1; ++i) {
+          start(i, i);
+          look(i + 1);
         }
+        int st = 0, st_next = kStages - 1;
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+          copies_wait<kStages - 2>();
+          __syncwarp();
+          const int j0 = (t0 + i) * kSlots, j = j0 + tid;
+          const bool valid = (found >> st) & 1;
+          uint32_t o[16];
+          const uint8_t* row = sm.k[warp][st] + lane * kStride;
+          const float2 kp = __half22float2(*reinterpret_cast<const __half2*>(&sm.par[warp][st][lane]));
+#pragma unroll
+          for (int x = 0; x < P; ++x) {
+            const uint4 w = *reinterpret_cast<const uint4*>(row + 16 * x);
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              o[4 * y] = nibbles<0>(ww[y]);
+              o[4 * y + 1] = nibbles<1>(ww[y]);
+              o[4 * y + 2] = nibbles<2>(ww[y]);
+              o[4 * y + 3] = nibbles<3>(ww[y]);
+            }
+            tc::tmem_st16(mine + kACol + 16 * x, o);
+          }
+          __syncwarp();
+          start(i + kStages - 1, st_next);  // (nothing but its group where there is no such unit)
+          look(i + kStages);
+          st = st + 1 == kStages ? 0 : st + 1;
+          st_next = st_next + 1 == kStages ? 0 : st_next + 1;
+          const bool last = block == blocks - 1;
+          float before = 0.f;
+          if (valid && last) before = mass[j];
+          if (block > 0) before += sm.acc[i][tid];
+          tc::tmem_st_wait();
+          const float2 ks = make_float2(kp.x, kp.x), kz = make_float2(kp.y, kp.y);
+          float2 w0 = make_float2(0.f, 0.f), w1 = w0;
+          for (int c0 = 0; c0 < padded; c0 += kCols) {
+            const int cols = min(kCols, padded - c0);
+            tc::tc_fence_before();
+            __syncthreads();  // keys in place, the scores before have been read
+            if (tid == 0) {
+              tc::tc_fence_after();
+              const uint32_t id = tc::idesc_f16(kSlots, cols);
+              const uint64_t b = qd + c0 * 8;  // 128-byte rows
+#pragma unroll
+              for (int t = 0; t < D / 16; ++t)
+                tc::mma_f16_ts(tmem + kSCol, tmem + kACol + 8 * t, b + (t >> 2) * (kRows * 128 >> 4) + (t & 3) * 2, id, t > 0);
+              tc::mma_commit(&sm.done);
+            }
+            if (!tc::mbar_wait_bounded(&sm.done, parity, abort_flag, kWaitBudgetNs)) *abort_flag = 1;
+            __syncwarp();
+            parity ^= 1;
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < cols; c += 16) {
+              float v[16];
+              tc::tmem_ld16(mine + kSCol + c, v);
+              const float4* cq = reinterpret_cast<const float4*>(sm.cq + c0 + c);
+              const float4* cqs = reinterpret_cast<const float4*>(sm.cqs + c0 + c);
+              const float4* nl = reinterpret_cast<const float4*>(sm.nl + c0 + c);
+              tc::tmem_ld_wait();
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const float4 f = cq[x], z = cqs[x], l = nl[x];
+                float2 t = fma2(ks, mul2(make_float2(v[4 * x], v[4 * x + 1]), make_float2(f.x, f.y)),
+                                fma2(kz, make_float2(z.x, z.y), make_float2(l.x, l.y)));
+                float2 y = fma2(ks, mul2(make_float2(v[4 * x + 2], v[4 * x + 3]), make_float2(f.z, f.w)),
+                                fma2(kz, make_float2(z.z, z.w), make_float2(l.z, l.w)));
+                t = make_float2(ex2(t.x), ex2(t.y));
+                y = make_float2(ex2(y.x), ex2(y.y));
+                if (j0 + kSlots > k.q.base && j >= k.q.base) {
+                  const int d = j - k.q.base, r = c0 + c + 4 * x;
+                  auto see = [&](int e) {
+                    return a.visible ? d < kMaxTree && ((sm.mask[r + e] >> d) & 1) : d <= sm.token[r + e];
+                  };
+                  t.x = see(0) ? t.x : 0.f;
+                  t.y = see(1) ? t.y : 0.f;
+                  y.x = see(2) ? y.x : 0.f;
+                  y.y = see(3) ? y.y : 0.f;
+                }
+                w0 = add2(w0, t);
+                w1 = add2(w1, y);
+              }
+            }
+          }
+          w0 = add2(w0, w1);
+          const float sum = before + (w0.x + w0.y);
+          if (!last) sm.acc[i][tid] = sum;
+          else if (valid) mass[j] = sum;
+          if (*abort_flag) dead = true;
+        }
+        copies_wait<0>();
+        dead = __syncthreads_or(dead);
       }
     }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      wa += __shfl_xor_sync(0xFFFFFFFFu, wa, o);
-      wb += __shfl_xor_sync(0xFFFFFFFFu, wb, o);
-    }
-    if (page >= 0 && c == 0) {
-      if (j0 + sa < k.q.total) mass[j0 + sa] += wa;
-      if (j0 + sb < k.q.total) mass[j0 + sb] += wb;
-    }
-    ++k.tile;
+    u += units;
+    if (u < u1) cursor_next(k, a.c, a.q_start, a.base, a.T, a.G, kAllRows, kSlots, 0, sm.cum);
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *abort_flag) {
+    // A product in flight ends before TMEM is freed.
+    tc::mbar_wait_bounded(&sm.done, parity ^ 1, &sm.never, 100000000ull);
+    flag_error(a.dev_err, MOE_DEV_TIMEOUT);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, kTmemCols);
   }
 }
 
@@ -146,7 +324,7 @@ int launch_weigh(const WeighArgs& a, cudaStream_t s) {
   const int st = allow_smem<weigh_kernel<D>>(smem);
   if (st != MOE_OK) return st;
   LaunchScope ls(kProfKv4Weigh, s);
-  return launch_k(weigh_kernel<D>, dim3(sm_count() * 3), dim3(32 * kWarps), smem, s, false, a);
+  return launch_k(weigh_kernel<D>, dim3(sm_count() * (D == 128 ? 3 : 4)), dim3(kThreads), smem, s, false, a);
 }
 
 }  // namespace
