@@ -30,7 +30,6 @@ using tc::mul2;
 
 constexpr int kThreads = 128;
 constexpr int kSlots = 128;          // slots of a unit, one a thread
-constexpr int kRows = 128;           // query rows held in shared memory at a time
 constexpr int kCols = 64;            // columns of a product
 constexpr int kAllRows = 1 << 30;    // one row block per kv head
 constexpr int kStages = 3;           // key rows on their way
@@ -52,9 +51,9 @@ struct WeighArgs {
   int32_t* dev_err;
 };
 
-template <int D>
+template <int D, int kRows>  // kRows: query rows held at a time
 struct Smem {
-  alignas(1024) uint8_t q[kRows * D * 2];                    // panels of 64 dimensions: [128 rows][128 B], 128-byte swizzle
+  alignas(1024) uint8_t q[kRows * D * 2];                    // panels of 64 dimensions: [kRows][128 B], 128-byte swizzle
   alignas(16) uint8_t k[4][kStages][32 * (D / 2 + 16)];      // per warp: key rows, 16 bytes apart so that lanes miss each other's banks
   uint32_t par[4][kStages][32];                              // their scales and zeros
   alignas(16) float cq[kRows];
@@ -82,8 +81,8 @@ __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_grou
 
 // Rows row0 .. of the item's queries into shared memory as the product's
 // second operand, in the order of the key words' pairs (see prep_q of kv4.cuh).
-template <int D>
-__device__ __forceinline__ void load_queries(const WeighArgs& a, const Cursor& k, int row0, int rows, Smem<D>& sm) {
+template <int D, int kRows>
+__device__ __forceinline__ void load_queries(const WeighArgs& a, const Cursor& k, int row0, int rows, Smem<D, kRows>& sm) {
   constexpr int W = D / 8;  // a row's code words, one a lane
   const int x = threadIdx.x % W;
   const int padded = (rows + 15) & ~15;
@@ -133,12 +132,12 @@ __device__ __forceinline__ void load_queries(const WeighArgs& a, const Cursor& k
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-template <int D>
+template <int D, int kRows>
 __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
   constexpr int P = D / 32, kStride = D / 2 + 16;   // 16-byte pieces of a key row, bytes of it in shared memory
   constexpr uint32_t kACol = 0, kSCol = D / 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw);
+  Smem<D, kRows>& sm = *reinterpret_cast<Smem<D, kRows>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     tc::mbar_init(&sm.done, 1);
@@ -160,6 +159,8 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
   const long long total = sm.cum[a.c.S];
   const long long u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
   const size_t width = static_cast<size_t>(a.c.width) << a.c.page_log2;
+  const size_t stride = static_cast<size_t>(a.c.Hkv) * a.c.block_bytes();
+  const int last_row = a.c.page_size - 1;
   uint32_t parity = 0;
   bool dead = false;
   Cursor k;
@@ -170,12 +171,14 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
     if (a.visible && k.q.nq > kMaxTree && tid == 0) flag_error(a.dev_err, MOE_DEV_CAPACITY);
     float* mass = a.mass + (static_cast<size_t>(k.s) * a.c.Hkv + k.h) * width;
     const int group = blocks > 1 ? kGroup : units;
+    const uint8_t* from = a.c.pages + static_cast<size_t>(k.h) * a.c.block_bytes() + 16 * (lane % P);
+    const uint8_t* from_par = a.c.pages + static_cast<size_t>(k.h) * a.c.block_bytes() + a.c.page_size * D;
     for (int g0 = 0; g0 < units && !dead; g0 += group) {
       const int n = min(group, units - g0), t0 = k.tile + g0;
       for (int block = 0; block < blocks && !dead; ++block) {
         const int row0 = block * kRows, rows = min(kRows, all - row0), padded = (rows + 15) & ~15;
         __syncthreads();  // the rows before have been read
-        load_queries<D>(a, k, row0, rows, sm);
+        load_queries<D, kRows>(a, k, row0, rows, sm);
         __syncthreads();
         // Key rows: lane l looks up slot l's page, the lanes copy the warp's rows together.
         int page = -1;
@@ -188,17 +191,15 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
         auto start = [&](int i, int st) {
           const int j0 = (t0 + i) * kSlots + warp * 32;
           found = (found & ~(1u << st)) | (static_cast<uint32_t>(page >= 0) << st);
+          uint8_t* dst = sm.k[warp][st] + (lane / P) * kStride + 16 * (lane % P);
 #pragma unroll
           for (int x = 0; x < P; ++x) {
-            const int r = (x * 32 + lane) / P, piece = lane % P;
+            const int r = x * (32 / P) + lane / P;
             const int pg = __shfl_sync(0xFFFFFFFFu, page, r);
             if (pg >= 0)
-              copy_async16(sm.k[warp][st] + r * kStride + 16 * piece,
-                           page_block(a.c, pg, k.h) + ((j0 + r) & (a.c.page_size - 1)) * (D / 2) + 16 * piece);
+              copy_async16(dst + x * (32 / P) * kStride, from + pg * stride + ((j0 + r) & last_row) * (D / 2));
           }
-          if (page >= 0)
-            copy_async4(&sm.par[warp][st][lane],
-                        page_block(a.c, page, k.h) + a.c.page_size * D + ((j0 + lane) & (a.c.page_size - 1)) * 8);
+          if (page >= 0) copy_async4(&sm.par[warp][st][lane], from_par + page * stride + ((j0 + lane) & last_row) * 8);
           copies_commit();
         };
         look(0);
@@ -318,13 +319,14 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
   }
 }
 
-template <int D>
-int launch_weigh(const WeighArgs& a, cudaStream_t s) {
-  const size_t smem = sizeof(Smem<D>) + static_cast<size_t>(a.c.S) * 8;
-  const int st = allow_smem<weigh_kernel<D>>(smem);
+// ctas: what fits an SM (TMEM: four).
+template <int D, int kRows>
+int launch_weigh(const WeighArgs& a, int ctas, cudaStream_t s) {
+  const size_t smem = sizeof(Smem<D, kRows>) + static_cast<size_t>(a.c.S) * 8;
+  const int st = allow_smem<weigh_kernel<D, kRows>>(smem);
   if (st != MOE_OK) return st;
   LaunchScope ls(kProfKv4Weigh, s);
-  return launch_k(weigh_kernel<D>, dim3(sm_count() * (D == 128 ? 3 : 4)), dim3(kThreads), smem, s, false, a);
+  return launch_k(weigh_kernel<D, kRows>, dim3(sm_count() * ctas), dim3(kThreads), smem, s, false, a);
 }
 
 }  // namespace
@@ -348,5 +350,8 @@ extern "C" int kv4_weigh(const kv4_cache* cache, const void* q, const int32_t* q
   WeighArgs a{c, static_cast<const uint16_t*>(q), cfg->q_token_stride, cfg->q_head_stride, q_start, base, visible, lse,
               mass, cfg->T, cfg->n_q_heads, cfg->n_q_heads / c.Hkv, cfg->scale * kLog2e, dev_err};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return c.D == 128 ? launch_weigh<128>(a, s) : launch_weigh<64>(a, s);
+  if (c.D == 64) return launch_weigh<64, 128>(a, 4, s);
+  // 64 rows in shared memory leave room for a fourth CTA.
+  const bool few = static_cast<long long>(cfg->max_q) * a.G <= 64;
+  return few ? launch_weigh<128, 64>(a, 4, s) : launch_weigh<128, 128>(a, 3, s);
 }
