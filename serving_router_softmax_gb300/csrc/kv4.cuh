@@ -95,6 +95,13 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   tc::smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
+               : "memory");
+}
+
 // Query rows in the B-operand layout of mma.m16n8k16 (columns = rows of q).
 // Key words are split by masks, so the product's k index follows the nibbles:
 // lane c of a quad owns the D/4 dimensions from c * D/4 on; word w of them

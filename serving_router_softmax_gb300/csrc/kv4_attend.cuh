@@ -61,13 +61,6 @@ __device__ __forceinline__ uint64_t group_mask(uint32_t groups) {
   return m;
 }
 
-__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   tc::smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
-               : "memory");
-}
-
 // A tile in shared memory: one segment per page (64 slots of it at most),
 // laid out as a page block is: K codes, V codes, parameters.  So a page of up
 // to 64 slots comes in one copy.

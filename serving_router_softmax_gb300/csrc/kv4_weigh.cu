@@ -54,30 +54,21 @@ struct WeighArgs {
 template <int D, int kRows>  // kRows: query rows held at a time
 struct Smem {
   alignas(1024) uint8_t q[kRows * D * 2];                    // panels of 64 dimensions: [kRows][128 B], 128-byte swizzle
-  alignas(16) uint8_t k[4][kStages][32 * (D / 2 + 16)];      // per warp: key rows, 16 bytes apart so that lanes miss each other's banks
-  uint32_t par[4][kStages][32];                              // their scales and zeros
+  alignas(16) uint8_t k[4][kStages][32 * (D / 2)];           // per warp: key rows of its 32 slots
+  alignas(16) uint8_t par[4][kStages][32 * 8];               // their parameters
   alignas(16) float cq[kRows];
   alignas(16) float cqs[kRows];
   alignas(16) float nl[kRows];                               // -lse, in log2; -inf: no weight
   uint64_t mask[kRows];
   int token[kRows];
   float acc[kGroup][kSlots];
-  uint64_t done;
+  uint64_t done, full[4][kStages];
+  uint32_t groups[4][kStages];                               // bit x: slots 16 x .. of the warp's lie in a valid page
   long long scratch[32];
   uint32_t tmem;
-  int abort, never;
+  int abort;
   long long cum[1];
 };
-
-__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_async4(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // Rows row0 .. of the item's queries into shared memory as the product's
 // second operand, in the order of the key words' pairs (see prep_q of kv4.cuh).
@@ -86,15 +77,28 @@ __device__ __forceinline__ void load_queries(const WeighArgs& a, const Cursor& k
   constexpr int W = D / 8;  // a row's code words, one a lane
   const int x = threadIdx.x % W;
   const int padded = (rows + 15) & ~15;
+  constexpr int kStep = kThreads / W;  // rows of a pass
 #pragma unroll 1
-  for (int r = threadIdx.x / W; r < padded; r += kThreads / W) {
-    const int i = (row0 + r) / a.G, g = (row0 + r) - i * a.G, hd = k.h * a.G + g;
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    float nl = -INFINITY;
+  for (int r0 = threadIdx.x / W; r0 < padded; r0 += 4 * kStep) {
+  uint4 raws[4];
+  float nls[4];
+#pragma unroll
+  for (int y = 0; y < 4; ++y) {
+    const int r = r0 + y * kStep;
+    raws[y] = make_uint4(0, 0, 0, 0);
+    nls[y] = -INFINITY;
     if (r < rows) {
-      raw = *reinterpret_cast<const uint4*>(a.q + (k.q.q0 + i) * a.q_ts + hd * a.q_hs + 8 * x);
-      nl = a.lse[(static_cast<size_t>(k.q.q0) + i) * a.Hq + hd];
+      const int i = (row0 + r) / a.G, hd = k.h * a.G + (row0 + r) - i * a.G;
+      raws[y] = *reinterpret_cast<const uint4*>(a.q + (k.q.q0 + i) * a.q_ts + hd * a.q_hs + 8 * x);
+      nls[y] = a.lse[(static_cast<size_t>(k.q.q0) + i) * a.Hq + hd];
     }
+  }
+#pragma unroll
+  for (int y = 0; y < 4; ++y) {
+    const int r = r0 + y * kStep, i = (row0 + r) / a.G;
+    if (r >= padded) break;
+    const uint4 raw = raws[y];
+    const float nl = nls[y];
     const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
     float v[8], m = 0.f, sum = 0.f;
 #pragma unroll
@@ -129,19 +133,22 @@ __device__ __forceinline__ void load_queries(const WeighArgs& a, const Cursor& k
       sm.mask[r] = a.visible && !none ? a.visible[k.q.q0 + i] : 0;
     }
   }
+  }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 template <int D, int kRows>
 __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
-  constexpr int P = D / 32, kStride = D / 2 + 16;   // 16-byte pieces of a key row, bytes of it in shared memory
+  constexpr int P = D / 32;   // 16-byte pieces of a key row
   constexpr uint32_t kACol = 0, kSCol = D / 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Smem<D, kRows>& sm = *reinterpret_cast<Smem<D, kRows>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     tc::mbar_init(&sm.done, 1);
-    sm.abort = sm.never = 0;
+    for (int w = 0; w < 4; ++w)
+      for (int i = 0; i < kStages; ++i) tc::mbar_init(&sm.full[w][i], 1);
+    sm.abort = 0;
     tc::fence_mbar_init();
   }
   if (warp == 0) {
@@ -161,6 +168,10 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
   const size_t width = static_cast<size_t>(a.c.width) << a.c.page_log2;
   const size_t stride = static_cast<size_t>(a.c.Hkv) * a.c.block_bytes();
   const int last_row = a.c.page_size - 1;
+  // A warp's 32 slots lie in one page, or in two of 16.
+  const int seg_log2 = min(a.c.page_log2, 5), nseg = 32 >> seg_log2;
+  int st = 0, st_next = 0;       // stages of the copies: read next, started next
+  uint32_t phase = 0;
   uint32_t parity = 0;
   bool dead = false;
   Cursor k;
@@ -171,8 +182,7 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
     if (a.visible && k.q.nq > kMaxTree && tid == 0) flag_error(a.dev_err, MOE_DEV_CAPACITY);
     float* mass = a.mass + (static_cast<size_t>(k.s) * a.c.Hkv + k.h) * width;
     const int group = blocks > 1 ? kGroup : units;
-    const uint8_t* from = a.c.pages + static_cast<size_t>(k.h) * a.c.block_bytes() + 16 * (lane % P);
-    const uint8_t* from_par = a.c.pages + static_cast<size_t>(k.h) * a.c.block_bytes() + a.c.page_size * D;
+    const uint8_t* from = a.c.pages + static_cast<size_t>(k.h) * a.c.block_bytes();
     for (int g0 = 0; g0 < units && !dead; g0 += group) {
       const int n = min(group, units - g0), t0 = k.tile + g0;
       for (int block = 0; block < blocks && !dead; ++block) {
@@ -180,44 +190,51 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
         __syncthreads();  // the rows before have been read
         load_queries<D, kRows>(a, k, row0, rows, sm);
         __syncthreads();
-        // Key rows: lane l looks up slot l's page, the lanes copy the warp's rows together.
+        // Key rows: the lane of each page segment looks its page up, one unit ahead, and copies it.
         int page = -1;
-        uint32_t found = 0;  // bit i: the slot of stage i lies in a valid page
         auto look = [&](int i) {
-          const int j = (t0 + i) * kSlots + tid;
-          page = i < n && j < k.q.total ? page_of(a.c, k.s, j) : -1;
-          if (i < n && j < k.q.total && page < 0) flag_error(a.dev_err, MOE_DEV_BAD_ID);
+          const int j = (t0 + i) * kSlots + warp * 32 + (lane << seg_log2);
+          page = lane < nseg && i < n && j < k.q.total ? page_of(a.c, k.s, j) : -1;
+          if (lane < nseg && i < n && j < k.q.total && page < 0) flag_error(a.dev_err, MOE_DEV_BAD_ID);
         };
-        auto start = [&](int i, int st) {
-          const int j0 = (t0 + i) * kSlots + warp * 32;
-          found = (found & ~(1u << st)) | (static_cast<uint32_t>(page >= 0) << st);
-          uint8_t* dst = sm.k[warp][st] + (lane / P) * kStride + 16 * (lane % P);
-#pragma unroll
-          for (int x = 0; x < P; ++x) {
-            const int r = x * (32 / P) + lane / P;
-            const int pg = __shfl_sync(0xFFFFFFFFu, page, r);
-            if (pg >= 0)
-              copy_async16(dst + x * (32 / P) * kStride, from + pg * stride + ((j0 + r) & last_row) * (D / 2));
+        auto start = [&](int i) {
+          const uint32_t have = __ballot_sync(0xFFFFFFFFu, page >= 0);
+          uint64_t* bar = &sm.full[warp][st_next];
+          if (lane == 0) {
+            sm.groups[warp][st_next] = nseg == 1 ? have * 3 : have;
+            tc::mbar_arrive_expect_tx(bar, (__popc(have) * (D / 2 + 8)) << seg_log2);
           }
-          if (page >= 0) copy_async4(&sm.par[warp][st][lane], from_par + page * stride + ((j0 + lane) & last_row) * 8);
-          copies_commit();
+          __syncwarp();
+          if (page >= 0) {
+            const int r = ((t0 + i) * kSlots + warp * 32 + (lane << seg_log2)) & last_row;
+            const uint8_t* b = from + page * stride;
+            bulk_copy(sm.k[warp][st_next] + (lane << seg_log2) * (D / 2), b + r * (D / 2), (D / 2) << seg_log2, bar);
+            bulk_copy(sm.par[warp][st_next] + (lane << seg_log2) * 8, b + a.c.page_size * D + r * 8, 8u << seg_log2, bar);
+          }
+          st_next = st_next + 1 == kStages ? 0 : st_next + 1;
         };
         look(0);
 #pragma unroll 1
         for (int i = 0; i < kStages - 1; ++i) {
-          start(i, i);
+          start(i);
           look(i + 1);
         }
-        int st = 0, st_next = kStages - 1;
+        const bool last = block == blocks - 1;
+        // The mass of this unit's slot, loaded one unit ahead.
+        auto mass_of = [&](int i) {
+          const int j = (t0 + i) * kSlots + tid;
+          return last && i < n && j < k.q.total ? mass[j] : 0.f;
+        };
+        float next_mass = mass_of(0);
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
-          copies_wait<kStages - 2>();
+          if (!tc::mbar_wait_bounded(&sm.full[warp][st], phase, abort_flag, kWaitBudgetNs)) *abort_flag = 1;
           __syncwarp();
           const int j0 = (t0 + i) * kSlots, j = j0 + tid;
-          const bool valid = (found >> st) & 1;
+          const bool valid = j < k.q.total && ((sm.groups[warp][st] >> (lane >> 4)) & 1);
           uint32_t o[16];
-          const uint8_t* row = sm.k[warp][st] + lane * kStride;
-          const float2 kp = __half22float2(*reinterpret_cast<const __half2*>(&sm.par[warp][st][lane]));
+          const uint8_t* row = sm.k[warp][st] + lane * (D / 2);
+          const float2 kp = __half22float2(*reinterpret_cast<const __half2*>(sm.par[warp][st] + lane * 8));
 #pragma unroll
           for (int x = 0; x < P; ++x) {
             const uint4 w = *reinterpret_cast<const uint4*>(row + 16 * x);
@@ -231,14 +248,12 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
             }
             tc::tmem_st16(mine + kACol + 16 * x, o);
           }
+          if (++st == kStages) st = 0, phase ^= 1;
           __syncwarp();
-          start(i + kStages - 1, st_next);  // (nothing but its group where there is no such unit)
+          start(i + kStages - 1);  // (an empty phase where there is no such unit)
           look(i + kStages);
-          st = st + 1 == kStages ? 0 : st + 1;
-          st_next = st_next + 1 == kStages ? 0 : st_next + 1;
-          const bool last = block == blocks - 1;
-          float before = 0.f;
-          if (valid && last) before = mass[j];
+          float before = next_mass;
+          next_mass = mass_of(i + 1);
           if (block > 0) before += sm.acc[i][tid];
           tc::tmem_st_wait();
           const float2 ks = make_float2(kp.x, kp.x), kz = make_float2(kp.y, kp.y);
@@ -298,7 +313,12 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
           else if (valid) mass[j] = sum;
           if (*abort_flag) dead = true;
         }
-        copies_wait<0>();
+        // The two empty phases beyond the last unit; nothing is in flight after them.
+#pragma unroll 1
+        for (int i = 0; i < kStages - 1; ++i) {
+          if (!tc::mbar_wait_bounded(&sm.full[warp][st], phase, abort_flag, kWaitBudgetNs)) *abort_flag = 1;
+          if (++st == kStages) st = 0, phase ^= 1;
+        }
         dead = __syncthreads_or(dead);
       }
     }
@@ -308,8 +328,9 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
   tc::tc_fence_before();
   __syncthreads();
   if (tid == 0 && *abort_flag) {
-    // A product in flight ends before TMEM is freed.
-    tc::mbar_wait_bounded(&sm.done, parity ^ 1, &sm.never, 100000000ull);
+    // Products and copies in flight end before TMEM and shared memory go.
+    const uint64_t t0 = tc::globaltimer_ns();
+    while (tc::globaltimer_ns() - t0 < 1000000ull) {}
     flag_error(a.dev_err, MOE_DEV_TIMEOUT);
   }
   __syncthreads();
