@@ -77,6 +77,10 @@ __device__ __forceinline__ void load_queries(const WeighArgs& a, const Cursor& k
   constexpr int W = D / 8;  // a row's code words, one a lane
   const int x = threadIdx.x % W;
   const int padded = (rows + 15) & ~15;
+  // Token and query head of row r of the block (small numbers: a multiplication finds the quotient).
+  const int tok0 = row0 / a.G, g0 = row0 - tok0 * a.G;
+  const float inv_g = 1.f / static_cast<float>(a.G);
+  auto token = [&](int r) { return static_cast<int>((static_cast<float>(g0 + r) + 0.5f) * inv_g); };
   constexpr int kStep = kThreads / W;  // rows of a pass
 #pragma unroll 1
   for (int r0 = threadIdx.x / W; r0 < padded; r0 += 4 * kStep) {
@@ -88,14 +92,14 @@ __device__ __forceinline__ void load_queries(const WeighArgs& a, const Cursor& k
     raws[y] = make_uint4(0, 0, 0, 0);
     nls[y] = -INFINITY;
     if (r < rows) {
-      const int i = (row0 + r) / a.G, hd = k.h * a.G + (row0 + r) - i * a.G;
+      const int tr = token(r), i = tok0 + tr, hd = k.h * a.G + g0 + r - tr * a.G;
       raws[y] = *reinterpret_cast<const uint4*>(a.q + (k.q.q0 + i) * a.q_ts + hd * a.q_hs + 8 * x);
       nls[y] = a.lse[(static_cast<size_t>(k.q.q0) + i) * a.Hq + hd];
     }
   }
 #pragma unroll
   for (int y = 0; y < 4; ++y) {
-    const int r = r0 + y * kStep, i = (row0 + r) / a.G;
+    const int r = r0 + y * kStep, i = tok0 + token(min(r, rows - 1));
     if (r >= padded) break;
     const uint4 raw = raws[y];
     const float nl = nls[y];
@@ -183,29 +187,31 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
     float* mass = a.mass + (static_cast<size_t>(k.s) * a.c.Hkv + k.h) * width;
     const int group = blocks > 1 ? kGroup : units;
     const uint8_t* from = a.c.pages + static_cast<size_t>(k.h) * a.c.block_bytes();
+    const int32_t* table = a.c.table + static_cast<size_t>(k.s) * a.c.width;
     for (int g0 = 0; g0 < units && !dead; g0 += group) {
       const int n = min(group, units - g0), t0 = k.tile + g0;
       for (int block = 0; block < blocks && !dead; ++block) {
         const int row0 = block * kRows, rows = min(kRows, all - row0), padded = (rows + 15) & ~15;
-        __syncthreads();  // the rows before have been read
-        load_queries<D, kRows>(a, k, row0, rows, sm);
-        __syncthreads();
         // Key rows: the lane of each page segment looks its page up, one unit ahead, and copies it.
-        int page = -1;
+        // (What it finds is not looked at before it is needed: a use would wait for the load.)
+        int page = 0;
+        bool wanted = false;
         auto look = [&](int i) {
           const int j = (t0 + i) * kSlots + warp * 32 + (lane << seg_log2);
-          page = lane < nseg && i < n && j < k.q.total ? page_of(a.c, k.s, j) : -1;
-          if (lane < nseg && i < n && j < k.q.total && page < 0) flag_error(a.dev_err, MOE_DEV_BAD_ID);
+          wanted = lane < nseg && i < n && j < k.q.total;
+          if (wanted) page = table[j >> a.c.page_log2];
         };
         auto start = [&](int i) {
-          const uint32_t have = __ballot_sync(0xFFFFFFFFu, page >= 0);
+          const bool found = wanted && page >= 0 && page < a.c.n_pages;
+          if (wanted && !found) flag_error(a.dev_err, MOE_DEV_BAD_ID);
+          const uint32_t have = __ballot_sync(0xFFFFFFFFu, found);
           uint64_t* bar = &sm.full[warp][st_next];
           if (lane == 0) {
             sm.groups[warp][st_next] = nseg == 1 ? have * 3 : have;
             tc::mbar_arrive_expect_tx(bar, (__popc(have) * (D / 2 + 8)) << seg_log2);
           }
           __syncwarp();
-          if (page >= 0) {
+          if (found) {
             const int r = ((t0 + i) * kSlots + warp * 32 + (lane << seg_log2)) & last_row;
             const uint8_t* b = from + page * stride;
             bulk_copy(sm.k[warp][st_next] + (lane << seg_log2) * (D / 2), b + r * (D / 2), (D / 2) << seg_log2, bar);
@@ -219,6 +225,9 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
           start(i);
           look(i + 1);
         }
+        __syncthreads();  // the rows before have been read
+        load_queries<D, kRows>(a, k, row0, rows, sm);
+        __syncthreads();
         const bool last = block == blocks - 1;
         // The mass of this unit's slot, loaded one unit ahead.
         auto mass_of = [&](int i) {
