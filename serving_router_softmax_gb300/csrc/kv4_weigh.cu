@@ -86,15 +86,18 @@ __device__ __forceinline__ void load_queries(const WeighArgs& a, const Cursor& k
   for (int r0 = threadIdx.x / W; r0 < padded; r0 += 4 * kStep) {
   uint4 raws[4];
   float nls[4];
+  uint64_t masks[4];
 #pragma unroll
   for (int y = 0; y < 4; ++y) {
     const int r = r0 + y * kStep;
     raws[y] = make_uint4(0, 0, 0, 0);
     nls[y] = -INFINITY;
+    masks[y] = 0;
     if (r < rows) {
       const int tr = token(r), i = tok0 + tr, hd = k.h * a.G + g0 + r - tr * a.G;
       raws[y] = *reinterpret_cast<const uint4*>(a.q + (k.q.q0 + i) * a.q_ts + hd * a.q_hs + 8 * x);
       nls[y] = a.lse[(static_cast<size_t>(k.q.q0) + i) * a.Hq + hd];
+      if (a.visible) masks[y] = a.visible[k.q.q0 + i];
     }
   }
 #pragma unroll
@@ -127,14 +130,14 @@ __device__ __forceinline__ void load_queries(const WeighArgs& a, const Cursor& k
         make_uint4(pack_h2(v[0], v[4]), pack_h2(v[1] * 0.0625f, v[5] * 0.0625f), pack_h2(v[2], v[6]),
                    pack_h2(v[3] * 0.0625f, v[7] * 0.0625f));
     if (x == 0) {
-      const int y = 24 - e;  // the codes carry 2^-24
-      sm.cq[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + (y >> 1)) << 23) *
-                 __uint_as_float(static_cast<uint32_t>(127 + y - (y >> 1)) << 23);
+      const int up = 24 - e;  // the codes carry 2^-24
+      sm.cq[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + (up >> 1)) << 23) *
+                 __uint_as_float(static_cast<uint32_t>(127 + up - (up >> 1)) << 23);
       sm.cqs[r] = a.scale_log2 * sum;
       const bool none = nl == -INFINITY;  // a row that saw nothing sees no new slot, whatever those hold
       sm.nl[r] = none ? -INFINITY : -nl * kLog2e;
       sm.token[r] = none ? -1 : i;
-      sm.mask[r] = a.visible && !none ? a.visible[k.q.q0 + i] : 0;
+      sm.mask[r] = none ? 0 : masks[y];
     }
   }
   }
