@@ -8,8 +8,8 @@
 // a single decoded token of 8 query heads wastes nothing.
 //
 // Each CTA owns an even share of all (sequence, head, row block, tile) units;
-// a producer warp keeps a ring of tiles in flight (bulk copies), four consumer
-// warps take 16 slots of each tile.  An item cut between CTAs leaves its
+// a producer warp keeps a ring of tiles in flight (bulk copies), two consumer
+// warps take 32 slots of each tile, two groups of 16 beside each other.  An item cut between CTAs leaves its
 // partial sums in the workspace and the combine kernel joins them in CTA
 // order, so results do not depend on timing.
 #include "kv4_attend.cuh"
@@ -18,9 +18,13 @@ namespace moe {
 namespace kv4 {
 namespace {
 
-constexpr int kConsumerWarps = 4;
+constexpr int kConsumerWarps = 2;
+constexpr int kGroups = kTile / 16 / kConsumerWarps;  // 16-slot groups of a tile that a warp takes
 constexpr int kMinUnits = 1;
 constexpr int kThreads = 32 * (kConsumerWarps + 1);
+// CTAs that an SM holds, by their registers.
+constexpr int ctas_per_sm(int nt) { return nt == 1 ? 5 : nt == 2 ? 4 : 2; }
+
 template <int D, int NT, int NS>
 struct Smem {
   static constexpr int RB = 8 * NT;
@@ -39,9 +43,10 @@ struct Smem {
 
 // MMA layouts: see kv4.cuh.
 template <int D, int NT, int NS>
-__global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) attend_kernel(const AttendArgs a) {
   using SM = Smem<D, NT, NS>;
   constexpr int RB = SM::RB;
+  constexpr int J = NT == 4 ? 1 : kGroups;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   SM& sm = *reinterpret_cast<SM*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -99,7 +104,14 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
   const int g = lane >> 2, c = lane & 3;
   const int s0 = slot_of_row(g), s1 = slot_of_row(g + 8);
   const TileMap<D> map(a.c);
-  const int k_at = map.k(16 * warp), v_at = map.v(16 * warp), p_at = map.p(16 * warp);
+  int k_at[kGroups], v_at[kGroups], p_at[kGroups];
+#pragma unroll
+  for (int x = 0; x < kGroups; ++x) {
+    const int r = 16 * (kGroups * warp + x);
+    k_at[x] = map.k(r);
+    v_at[x] = map.v(r);
+    p_at[x] = map.p(r);
+  }
   int stage = 0, phase = 0;
   if (tid < 8) a.meta[static_cast<size_t>(cta) * 8 + tid] = 0;
   Cursor k;
@@ -121,12 +133,12 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
     float o[D / 16][NT][4];
     float m[NT][2], l[NT][2], z[NT][2], cq[NT][2], cqs[NT][2];
     uint2 qf[NT == 1 ? D / 16 : 1];
+    uint32_t fresh = (1u << (2 * NT)) - 1;  // rows (of this lane's columns) that have seen nothing
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        m[t][e] = kNone;
-        l[t][e] = z[t][e] = 0.f;
+        m[t][e] = l[t][e] = z[t][e] = 0.f;
         cq[t][e] = sm.cq[8 * t + 2 * c + e];
         cqs[t][e] = sm.cqs[8 * t + 2 * c + e];
       }
@@ -141,137 +153,164 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
     }
 
     for (int it = 0; it < n; ++it) {
-      const int j0 = (k.tile + it) * kTile + 16 * warp;  // first slot of this warp's group
+      const int j0 = (k.tile + it) * kTile + 16 * kGroups * warp;  // first slot of this warp's groups
       if (!tc::mbar_wait_bounded(&sm.full[stage], phase, abort_flag, kWaitBudgetNs)) *abort_flag = 1;
       __syncwarp();
       const uint8_t* st = sm.st[stage].b;
-      const bool any = j0 < k.q.total && ((sm.groups[stage] >> warp) & 1);
-      if (any) {
-        const bool edge = j0 + 16 > k.q.base;
-        uint32_t ka[D / 32], kb[D / 32];
-        load_k_words<D>(st + k_at + s0 * (D / 2), c, ka);
-        load_k_words<D>(st + k_at + s1 * (D / 2), c, kb);
-        const uint2 ra = *reinterpret_cast<const uint2*>(st + p_at + s0 * 8);
-        const uint2 rb = *reinterpret_cast<const uint2*>(st + p_at + s1 * 8);
-        float ks[2], kz[2], lv[2], rs[2], zr[2];
+      const uint32_t groups = sm.groups[stage] >> (kGroups * warp);
+      const bool edge = j0 + 16 * kGroups > k.q.base || (groups & ((1u << kGroups) - 1)) != (1u << kGroups) - 1;
+      // J groups of 16 slots at a time, their chains beside each other.
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint2 r = e ? rb : ra;
-          const float2 kp = __half22float2(*reinterpret_cast<const __half2*>(&r.x));
-          const float2 vp = __half22float2(*reinterpret_cast<const __half2*>(&r.y));
-          const float se = fmaxf(vp.x, kMinScale);
-          ks[e] = kp.x;
-          kz[e] = kp.y;
-          lv[e] = lg2(se);
-          rs[e] = rcp(se);
-          zr[e] = vp.y * rs[e];
-        }
-        float t4[NT][4];
+      for (int x0 = 0; x0 < kGroups; x0 += J) {
+        float d[J][NT][4], rs[J][2], zr[J][2];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
-          if constexpr (NT == 1)
-            qk_16x8<D>(acc, ka, kb, [&](int i) { return qf[i]; });
-          else
-            qk_16x8<D>(acc, ka, kb, [&](int i) { return sm.frag[(t * (D / 16) + i) * 32 + lane]; });
+        for (int x = 0; x < J; ++x) {
+          uint32_t ka[D / 32], kb[D / 32];
+          load_k_words<D>(st + k_at[x0 + x] + s0 * (D / 2), c, ka);
+          load_k_words<D>(st + k_at[x0 + x] + s1 * (D / 2), c, kb);
+          const uint2 ra = *reinterpret_cast<const uint2*>(st + p_at[x0 + x] + s0 * 8);
+          const uint2 rb = *reinterpret_cast<const uint2*>(st + p_at[x0 + x] + s1 * 8);
+          float ks[2], kz[2], lv[2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int kk = e >> 1, x = e & 1;
-            t4[t][e] = fmaf(ks[kk], acc[e] * cq[t][x], fmaf(kz[kk], cqs[t][x], lv[kk]));
+          for (int e = 0; e < 2; ++e) {
+            const uint2 r = e ? rb : ra;
+            const float2 kp = __half22float2(*reinterpret_cast<const __half2*>(&r.x));
+            const float2 vp = __half22float2(*reinterpret_cast<const __half2*>(&r.y));
+            const float se = fmaxf(vp.x, kMinScale);
+            ks[e] = kp.x;
+            kz[e] = kp.y;
+            lv[e] = lg2(se);
+            rs[x][e] = rcp(se);
+            zr[x][e] = vp.y * rs[x][e];
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            if constexpr (NT == 1)
+              qk_16x8<D>(acc, ka, kb, [&](int i) { return qf[i]; });
+            else
+              qk_16x8<D>(acc, ka, kb, [&](int i) { return sm.frag[(t * (D / 16) + i) * 32 + lane]; });
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int kk = e >> 1, y = e & 1;
+              d[x][t][e] = fmaf(ks[kk], acc[e] * cq[t][y], fmaf(kz[kk], cqs[t][y], lv[kk] - m[t][y]));
+            }
           }
         }
-        uint32_t seen = 0xFFFFFFFFu;  // bit 4t + e: visible
+        // Where slots may be out of sight (or out of range): their exponents are -inf, and
+        // what their parameters hold (NaN, say) must not reach the sums.
+        uint32_t seen = 0xFFFFFFFFu;  // bit 4 (NT x + t) + e
         if (edge) {
           seen = 0;
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int r = 8 * t + 2 * c + x;
-              const uint64_t v = sees(k.q, a.visible != nullptr, sm.mask[r], (row0 + min(r, rows - 1)) / a.G, j0);
-              if ((v >> s0) & 1) seen |= 1u << (4 * t + x);
-              else t4[t][x] = -INFINITY;
-              if ((v >> s1) & 1) seen |= 1u << (4 * t + 2 + x);
-              else t4[t][2 + x] = -INFINITY;
-            }
-        }
-        bool grow = false;
+            for (int y = 0; y < 2; ++y) {
+              const int r = 8 * t + 2 * c + y;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) grow |= t4[t][e] > m[t][e & 1] + kLazy;
-        if (__any_sync(0xFFFFFFFFu, grow)) {
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              float nm = fmaxf(m[t][x], fmaxf(t4[t][x], t4[t][2 + x]));
-              nm = fmaxf(nm, __shfl_xor_sync(0xFFFFFFFFu, nm, 4));
-              nm = fmaxf(nm, __shfl_xor_sync(0xFFFFFFFFu, nm, 8));
-              nm = fmaxf(nm, __shfl_xor_sync(0xFFFFFFFFu, nm, 16));
-              const float f = ex2(m[t][x] - nm);
-              m[t][x] = nm;
-              l[t][x] *= f;
-              z[t][x] *= f;
-#pragma unroll
-              for (int j = 0; j < D / 16; ++j) {
-                o[j][t][x] *= f;
-                o[j][t][2 + x] *= f;
+              for (int x = 0; x < J; ++x) {
+                uint64_t v = 0;
+                if ((groups >> (x0 + x)) & 1)
+                  v = sees(k.q, a.visible != nullptr, sm.mask[r], (row0 + min(r, rows - 1)) / a.G, j0 + 16 * (x0 + x));
+                if ((v >> s0) & 1) seen |= 1u << (4 * (NT * x + t) + y);
+                else d[x][t][y] = -INFINITY;
+                if ((v >> s1) & 1) seen |= 1u << (4 * (NT * x + t) + 2 + y);
+                else d[x][t][2 + y] = -INFINITY;
               }
             }
         }
-        uint2 pf[NT];
+        float top = -INFINITY;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float p[4];
+        for (int x = 0; x < J; ++x)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int kk = e >> 1, x = e & 1;
-            p[e] = ex2(t4[t][e] - m[t][x]);
-            if (!edge || ((seen >> (4 * t + e)) & 1)) {
-              l[t][x] = fmaf(p[e], rs[kk], l[t][x]);
-              z[t][x] = fmaf(p[e], zr[kk], z[t][x]);
+          for (int t = 0; t < NT; ++t) top = max3(max3(top, d[x][t][0], d[x][t][1]), d[x][t][2], d[x][t][3]);
+        if (__any_sync(0xFFFFFFFFu, top > kLazy || fresh != 0)) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              float mx = -INFINITY;
+#pragma unroll
+              for (int x = 0; x < J; ++x) mx = max3(mx, d[x][t][y], d[x][t][2 + y]);
+              mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+              // A row's first visible slots set its maximum; later ones only raise it.
+              const bool first = (fresh >> (2 * t + y)) & 1, none = mx == -INFINITY;
+              const float by = none ? 0.f : first ? mx : fmaxf(mx, 0.f);
+              const float f = first ? 1.f : ex2(-by);
+              if (!none) fresh &= ~(1u << (2 * t + y));
+              m[t][y] += by;
+              l[t][y] *= f;
+              z[t][y] *= f;
+#pragma unroll
+              for (int x = 0; x < J; ++x) {
+                d[x][t][y] -= by;
+                d[x][t][2 + y] -= by;
+              }
+#pragma unroll
+              for (int j = 0; j < D / 16; ++j) {
+                o[j][t][y] *= f;
+                o[j][t][2 + y] *= f;
+              }
             }
-          }
-          pf[t] = make_uint2(transpose_8x8(pack_h2(p[0], p[1])), transpose_8x8(pack_h2(p[2], p[3])));
         }
-        // Values: lane (g, c) owns k indices 2c, 2c+1, 2c+8, 2c+9 and the
-        // dimensions g * D/8 ..; one byte permute pairs two slots' halves.
-        const uint8_t* vb = st + v_at + g * (D / 16);
-        const int v0 = slot_of_row(2 * c), v1 = slot_of_row(2 * c + 1);
-        if constexpr (D == 128) {
-          uint2 w[4];
-          w[0] = *reinterpret_cast<const uint2*>(vb + v0 * (D / 2));
-          w[1] = *reinterpret_cast<const uint2*>(vb + v1 * (D / 2));
-          w[2] = *reinterpret_cast<const uint2*>(vb + (8 + v0) * (D / 2));
-          w[3] = *reinterpret_cast<const uint2*>(vb + (8 + v1) * (D / 2));
+        uint2 pf[J][NT];
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const uint32_t sel = hf ? 0x7632u : 0x5410u;
-            const uint32_t xa = __byte_perm(w[0].x, w[1].x, sel), ya = __byte_perm(w[0].y, w[1].y, sel);
-            const uint32_t xb = __byte_perm(w[2].x, w[3].x, sel), yb = __byte_perm(w[2].y, w[3].y, sel);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              mma_f16(o[4 * hf + 0][t], nibbles<0>(xa), nibbles<0>(ya), nibbles<0>(xb), nibbles<0>(yb), pf[t]);
-              mma_f16(o[4 * hf + 1][t], nibbles<1>(xa), nibbles<1>(ya), nibbles<1>(xb), nibbles<1>(yb), pf[t]);
-              mma_f16(o[4 * hf + 2][t], nibbles<2>(xa), nibbles<2>(ya), nibbles<2>(xb), nibbles<2>(yb), pf[t]);
-              mma_f16(o[4 * hf + 3][t], nibbles<3>(xa), nibbles<3>(ya), nibbles<3>(xb), nibbles<3>(yb), pf[t]);
-            }
-          }
-        } else {
-          uint32_t w[4];
-          w[0] = *reinterpret_cast<const uint32_t*>(vb + v0 * (D / 2));
-          w[1] = *reinterpret_cast<const uint32_t*>(vb + v1 * (D / 2));
-          w[2] = *reinterpret_cast<const uint32_t*>(vb + (8 + v0) * (D / 2));
-          w[3] = *reinterpret_cast<const uint32_t*>(vb + (8 + v1) * (D / 2));
-          const uint32_t xa = __byte_perm(w[0], w[1], 0x5410u), ya = __byte_perm(w[0], w[1], 0x7632u);
-          const uint32_t xb = __byte_perm(w[2], w[3], 0x5410u), yb = __byte_perm(w[2], w[3], 0x7632u);
+        for (int x = 0; x < J; ++x)
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            mma_f16(o[0][t], nibbles<0>(xa), nibbles<0>(ya), nibbles<0>(xb), nibbles<0>(yb), pf[t]);
-            mma_f16(o[1][t], nibbles<1>(xa), nibbles<1>(ya), nibbles<1>(xb), nibbles<1>(yb), pf[t]);
-            mma_f16(o[2][t], nibbles<2>(xa), nibbles<2>(ya), nibbles<2>(xb), nibbles<2>(yb), pf[t]);
-            mma_f16(o[3][t], nibbles<3>(xa), nibbles<3>(ya), nibbles<3>(xb), nibbles<3>(yb), pf[t]);
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              p[e] = ex2(d[x][t][e]);
+              if (!edge || ((seen >> (4 * (NT * x + t) + e)) & 1)) {
+                l[t][e & 1] = fmaf(p[e], rs[x][e >> 1], l[t][e & 1]);
+                z[t][e & 1] = fmaf(p[e], zr[x][e >> 1], z[t][e & 1]);
+              }
+            }
+            pf[x][t] = make_uint2(transpose_8x8(pack_h2(p[0], p[1])), transpose_8x8(pack_h2(p[2], p[3])));
+          }
+        // Values: lane (g, c) owns k indices 2c, 2c+1, 2c+8, 2c+9 and the
+        // dimensions g * D/8 ..; one byte permute pairs two slots' halves.
+        const int v0 = slot_of_row(2 * c), v1 = slot_of_row(2 * c + 1);
+#pragma unroll
+        for (int x = 0; x < J; ++x) {
+          const uint8_t* vb = st + v_at[x0 + x] + g * (D / 16);
+          if constexpr (D == 128) {
+            uint2 w[4];
+            w[0] = *reinterpret_cast<const uint2*>(vb + v0 * (D / 2));
+            w[1] = *reinterpret_cast<const uint2*>(vb + v1 * (D / 2));
+            w[2] = *reinterpret_cast<const uint2*>(vb + (8 + v0) * (D / 2));
+            w[3] = *reinterpret_cast<const uint2*>(vb + (8 + v1) * (D / 2));
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const uint32_t sel = hf ? 0x7632u : 0x5410u;
+              const uint32_t xa = __byte_perm(w[0].x, w[1].x, sel), ya = __byte_perm(w[0].y, w[1].y, sel);
+              const uint32_t xb = __byte_perm(w[2].x, w[3].x, sel), yb = __byte_perm(w[2].y, w[3].y, sel);
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+                mma_f16(o[4 * hf + 0][t], nibbles<0>(xa), nibbles<0>(ya), nibbles<0>(xb), nibbles<0>(yb), pf[x][t]);
+                mma_f16(o[4 * hf + 1][t], nibbles<1>(xa), nibbles<1>(ya), nibbles<1>(xb), nibbles<1>(yb), pf[x][t]);
+                mma_f16(o[4 * hf + 2][t], nibbles<2>(xa), nibbles<2>(ya), nibbles<2>(xb), nibbles<2>(yb), pf[x][t]);
+                mma_f16(o[4 * hf + 3][t], nibbles<3>(xa), nibbles<3>(ya), nibbles<3>(xb), nibbles<3>(yb), pf[x][t]);
+              }
+            }
+          } else {
+            uint32_t w[4];
+            w[0] = *reinterpret_cast<const uint32_t*>(vb + v0 * (D / 2));
+            w[1] = *reinterpret_cast<const uint32_t*>(vb + v1 * (D / 2));
+            w[2] = *reinterpret_cast<const uint32_t*>(vb + (8 + v0) * (D / 2));
+            w[3] = *reinterpret_cast<const uint32_t*>(vb + (8 + v1) * (D / 2));
+            const uint32_t xa = __byte_perm(w[0], w[1], 0x5410u), ya = __byte_perm(w[0], w[1], 0x7632u);
+            const uint32_t xb = __byte_perm(w[2], w[3], 0x5410u), yb = __byte_perm(w[2], w[3], 0x7632u);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              mma_f16(o[0][t], nibbles<0>(xa), nibbles<0>(ya), nibbles<0>(xb), nibbles<0>(yb), pf[x][t]);
+              mma_f16(o[1][t], nibbles<1>(xa), nibbles<1>(ya), nibbles<1>(xb), nibbles<1>(yb), pf[x][t]);
+              mma_f16(o[2][t], nibbles<2>(xa), nibbles<2>(ya), nibbles<2>(xb), nibbles<2>(yb), pf[x][t]);
+              mma_f16(o[3][t], nibbles<3>(xa), nibbles<3>(ya), nibbles<3>(xb), nibbles<3>(yb), pf[x][t]);
+            }
           }
         }
       }
@@ -280,7 +319,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
       if (++stage == NS) stage = 0, phase ^= 1;
     }
 
-    // ---- join the four warps' sums
+    // ---- join the warps' sums
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -290,6 +329,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
           l[t][x] += __shfl_xor_sync(0xFFFFFFFFu, l[t][x], sft);
           z[t][x] += __shfl_xor_sync(0xFFFFFFFFu, z[t][x], sft);
         }
+        if ((fresh >> (2 * t + x)) & 1) m[t][x] = kNone;
         if (g == 0) {
           sm.m[warp][8 * t + 2 * c + x] = m[t][x];
           sm.l[warp][8 * t + 2 * c + x] = l[t][x];
@@ -308,12 +348,12 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
         for (int w = 1; w < kConsumerWarps; ++w) mm = fmaxf(mm, sm.m[w][r]);
         f[t][x] = ex2(m[t][x] - mm);
       }
-    // Quarter (warp + p) % 4 of the dimensions in phase p.
+    // Share (warp + p) % kConsumerWarps of the dimensions in phase p.
     constexpr int QT = D / 16 / kConsumerWarps;
     for (int p = 0; p < kConsumerWarps; ++p) {
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
-        if (j / QT != ((warp + p) & 3)) continue;
+        if (j / QT != (warp + p) % kConsumerWarps) continue;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -364,9 +404,9 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
   }
 }
 
-// Ring depth: about 52 KB of tiles, so that three CTAs of an SM keep more than
+// Ring depth: about 35 KB of tiles, so that the CTAs of an SM keep more than
 // 100 KB in flight.
-template <int D> constexpr int stages() { return D == 128 ? 6 : 10; }
+template <int D> constexpr int stages() { return D == 128 ? 4 : 7; }
 
 // Rows of a sequence and kv head up to which the kernel here is used.
 constexpr int kNarrowRows = 32;
@@ -381,7 +421,7 @@ Plan plan_of(const kv4_attn_cfg& cfg, const Cache& c) {
   const long long rows = static_cast<long long>(cfg.max_q) * (cfg.n_q_heads / c.Hkv);
   Plan p;
   p.rb = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= kNarrowRows ? 32 : kWideRows;
-  p.grid = p.rb == kWideRows ? wide_grid() : sm_count() * (p.rb == 32 ? 2 : 3);
+  p.grid = p.rb == kWideRows ? wide_grid() : sm_count() * ctas_per_sm(p.rb / 8);
   return p;
 }
 

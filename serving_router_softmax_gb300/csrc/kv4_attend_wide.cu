@@ -69,12 +69,6 @@ __device__ __forceinline__ void tmem_ld_pairs(uint32_t taddr, float2 (&e)[16]) {
   tc::tmem_ld_wait();
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 // Ring position of a pipeline of N stages.
 template <int N>
 struct Ring {
