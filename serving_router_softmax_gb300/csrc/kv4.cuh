@@ -115,11 +115,11 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t b
 // (1, 5)/16 and k-step 2w + 1 with (2, 6) and (3, 7)/16.  Each row is scaled
 // by the power of two that puts its largest magnitude in [2^14, 2^15), so the
 // fp16 copy of a bf16 row is exact down to 2^-31 of that magnitude.
-//   frag  [n_rows / 8][D / 16][32] uint2
+//   frag  [n_rows / 8][D / 32][32] uint4: k-steps 2w (x, y) and 2w + 1 (z, w)
 //   cq    factor of the accumulator, cqs factor of kz (both times scale * log2 e)
 // `row` gives the source row (NULL: zeros).  Threads 0..nthreads-1 take part.
 template <int D, typename RowPtr>
-__device__ __forceinline__ void prep_q(RowPtr row, int n_rows, float scale_log2, uint2* frag, float* cq, float* cqs,
+__device__ __forceinline__ void prep_q(RowPtr row, int n_rows, float scale_log2, uint4* frag, float* cq, float* cqs,
                                        int tid, int nthreads) {
   constexpr int LPR = D / 8;   // lanes of a row, 8 dimensions each
   constexpr int WPC = D / 32;  // words of a lane's chunk
@@ -155,9 +155,9 @@ __device__ __forceinline__ void prep_q(RowPtr row, int n_rows, float scale_log2,
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = v[i] * f1 * f2;
     const int c = x / WPC, w = x % WPC;
-    uint2* f = frag + (static_cast<size_t>(r >> 3) * (D / 16) + 2 * w) * 32 + (r & 7) * 4 + c;
-    f[0] = make_uint2(pack_h2(v[0], v[4]), pack_h2(v[1] * 0.0625f, v[5] * 0.0625f));
-    f[32] = make_uint2(pack_h2(v[2], v[6]), pack_h2(v[3] * 0.0625f, v[7] * 0.0625f));
+    frag[((r >> 3) * (D / 32) + w) * 32 + (r & 7) * 4 + c] =
+        make_uint4(pack_h2(v[0], v[4]), pack_h2(v[1] * 0.0625f, v[5] * 0.0625f), pack_h2(v[2], v[6]),
+                   pack_h2(v[3] * 0.0625f, v[7] * 0.0625f));
     if (x == 0) {
       cq[r] = ldexpf(scale_log2, 24 - e);  // the codes carry 2^-24
       cqs[r] = scale_log2 * sum;
@@ -196,13 +196,15 @@ __device__ __forceinline__ uint32_t nibbles(uint32_t w) {
 
 // Scores' accumulator of 16 slots against 8 query rows: acc[0..1] = slot of
 // matrix row lane / 4, query columns 2 (lane % 4) and + 1; acc[2..3] = row + 8.
-// ka / kb: the lane's code words of those two slots; q(t): B operand of k-step t.
-template <int D, typename Q>
-__device__ __forceinline__ void qk_16x8(float (&acc)[4], const uint32_t (&ka)[D / 32], const uint32_t (&kb)[D / 32], Q q) {
+// ka / kb: the lane's code words of those two slots; frag: the 8 rows' (prep_q).
+template <int D>
+__device__ __forceinline__ void qk_16x8(float (&acc)[4], const uint32_t (&ka)[D / 32], const uint32_t (&kb)[D / 32],
+                                        const uint4* frag) {
 #pragma unroll
   for (int w = 0; w < D / 32; ++w) {
-    mma_f16(acc, nibbles<0>(ka[w]), nibbles<0>(kb[w]), nibbles<1>(ka[w]), nibbles<1>(kb[w]), q(2 * w));
-    mma_f16(acc, nibbles<2>(ka[w]), nibbles<2>(kb[w]), nibbles<3>(ka[w]), nibbles<3>(kb[w]), q(2 * w + 1));
+    const uint4 q = frag[32 * w + (threadIdx.x & 31)];
+    mma_f16(acc, nibbles<0>(ka[w]), nibbles<0>(kb[w]), nibbles<1>(ka[w]), nibbles<1>(kb[w]), make_uint2(q.x, q.y));
+    mma_f16(acc, nibbles<2>(ka[w]), nibbles<2>(kb[w]), nibbles<3>(ka[w]), nibbles<3>(kb[w]), make_uint2(q.z, q.w));
   }
 }
 

@@ -23,13 +23,13 @@ constexpr int kGroups = kTile / 16 / kConsumerWarps;  // 16-slot groups of a til
 constexpr int kMinUnits = 1;
 constexpr int kThreads = 32 * (kConsumerWarps + 1);
 // CTAs that an SM holds, by their registers.
-constexpr int ctas_per_sm(int nt) { return nt == 1 ? 5 : nt == 2 ? 4 : 2; }
+constexpr int ctas_per_sm(int nt) { return nt <= 2 ? 4 : 2; }
 
 template <int D, int NT, int NS>
 struct Smem {
   static constexpr int RB = 8 * NT;
   Tile<D> st[NS];
-  uint2 frag[NT * (D / 16) * 32];
+  uint4 frag[NT * (D / 32) * 32];
   float o[RB][D + 4];
   float cq[RB], cqs[RB];
   float m[kConsumerWarps][RB], l[kConsumerWarps][RB], z[kConsumerWarps][RB];
@@ -132,7 +132,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) attend_kernel(const
 
     float o[D / 16][NT][4];
     float m[NT][2], l[NT][2], z[NT][2], cq[NT][2], cqs[NT][2];
-    uint2 qf[NT == 1 ? D / 16 : 1];
     uint32_t fresh = (1u << (2 * NT)) - 1;  // rows (of this lane's columns) that have seen nothing
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -146,10 +145,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) attend_kernel(const
       for (int j = 0; j < D / 16; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[j][t][e] = 0.f;
-    }
-    if constexpr (NT == 1) {
-#pragma unroll
-      for (int t = 0; t < D / 16; ++t) qf[t] = sm.frag[t * 32 + lane];
     }
 
     for (int it = 0; it < n; ++it) {
@@ -186,10 +181,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) attend_kernel(const
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            if constexpr (NT == 1)
-              qk_16x8<D>(acc, ka, kb, [&](int i) { return qf[i]; });
-            else
-              qk_16x8<D>(acc, ka, kb, [&](int i) { return sm.frag[(t * (D / 16) + i) * 32 + lane]; });
+            qk_16x8<D>(acc, ka, kb, sm.frag + t * (D / 32) * 32);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int kk = e >> 1, y = e & 1;
@@ -404,9 +396,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) attend_kernel(const
   }
 }
 
-// Ring depth: about 35 KB of tiles, so that the CTAs of an SM keep more than
+// Ring depth: about 43 KB of tiles, so that the CTAs of an SM keep more than
 // 100 KB in flight.
-template <int D> constexpr int stages() { return D == 128 ? 4 : 7; }
+template <int D> constexpr int stages() { return D == 128 ? 5 : 9; }
 
 // Rows of a sequence and kv head up to which the kernel here is used.
 constexpr int kNarrowRows = 32;
