@@ -249,8 +249,9 @@ __global__ void __launch_bounds__(D * kShare) combine_kernel(const AttendArgs a)
 
 template <int D, int RB, bool kCols>
 int launch_combine(const AttendArgs& a, int grid, cudaStream_t s) {
-  // A chain of loads per share: 8 shares read a long list sooner; the wide kernel's many idle CTAs cost less with 4.
-  constexpr int kShare = kCols ? 4 : 8;
+  // A chain of loads per share: four shares read a long list sooner than two (one decoded token over 777 slots: 10.6 us
+  // on the device against 11.4), eight cost more in idle CTAs than they save (48 sequences: 210 us against 204).
+  constexpr int kShare = 4;
   LaunchScope ls(kProfKv4Attend, s);
   return launch_k(combine_kernel<D, RB, kCols, kShare>, dim3(grid, RB / 8), dim3(D * kShare), 0, s, true, a);
 }

@@ -6,8 +6,9 @@ raise ``MoEError`` on a non-OK host status.  Device-side error bits land in
 ``dev_err`` where one is given.
 
 A small call's host time is of the order of its device time, so what does not
-change from call to call (the argument structs, the workspace) is kept with
-the cache.
+change from call to call is kept: the argument structs with the cache, and one
+workspace for each stream (calls on a stream follow each other, so the caches
+of all layers share it).
 """
 from __future__ import annotations
 
@@ -23,13 +24,24 @@ _DTYPES = {torch.float32: L.DTYPE_F32, torch.bfloat16: L.DTYPE_BF16}
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
+_workspaces = {}  # (device, stream) -> the largest workspace that a call there has needed
+
+
+def _workspace(index: int, nbytes: int, stream: int) -> torch.Tensor:
+    # A graph's calls must not share a workspace with calls that may run beside its replays.
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+    w = _workspaces.get((index, stream))
+    if w is None or w.numel() < nbytes:
+        w = _workspaces[index, stream] = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+    return w
+
 
 class Kv4Cache:
     """Pages and page table of a batch's cache.
 
     ``pages`` uint8 [n_pages, n_kv_heads, page_size * (head_dim + 8)] and ``table`` int32 [n_seq, max_pages]
     stay the caller's: the table's contents (which page holds a sequence's slots) may change between calls.
-    The object keeps kv4_attend's workspace, one for each stream it is called on.
     """
 
     def __init__(self, pages: torch.Tensor, table: torch.Tensor, page_size: int, head_dim: int):
@@ -50,7 +62,7 @@ class Kv4Cache:
         self._struct = L.Kv4CacheStruct(pages.shape[0], page_size, pages.shape[1], head_dim, table.shape[0],
                                         table.shape[1], pages.data_ptr(), table.data_ptr())
         self._ref = C.byref(self._struct)
-        self._plans, self._workspaces = {}, {}
+        self._plans = {}
 
     @classmethod
     def new(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, n_seq: int, max_pages: int,
@@ -71,15 +83,6 @@ class Kv4Cache:
                 self._plans.clear()
             p = self._plans[key] = make()
         return p
-
-    def _workspace(self, nbytes: int, stream: int) -> torch.Tensor:
-        # A graph's calls must not share a workspace with calls that may run beside its replays.
-        if torch.cuda.is_current_stream_capturing():
-            return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        w = self._workspaces.get(stream)
-        if w is None or w.numel() < nbytes:
-            w = self._workspaces[stream] = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        return w
 
 
 def _arg(t: torch.Tensor, dtype: torch.dtype, shape, name: str) -> int:
@@ -201,7 +204,7 @@ def kv4_attend(cache: Kv4Cache, q: torch.Tensor, q_start: torch.Tensor, base: to
         lse = torch.empty(sl, dtype=torch.float32, device=cache.device)
     st = _raw_stream(cache._index)
     if workspace is None:
-        workspace = cache._workspace(need, st)
+        workspace = _workspace(cache._index, need, st)
     _check(L.load().kv4_attend(cache._ref, q.data_ptr(), _arg(q_start, torch.int32, sq, "q_start"),
                                _arg(base, torch.int32, sb, "base"),
                                None if visible is None else _arg(visible, torch.int64, sv, "visible"), ref,
