@@ -94,6 +94,9 @@ def check_attention(mv, pg, cache, q, new, base, scale, visible, err_want=0, wei
     return out, lse
 
 
+MANY = 1 << 20  # a number of new tokens (at most) that makes the kernel for many rows the better one for any cache
+
+
 ATTEND = [  # (Hq, Hkv, D, page, base lengths, new tokens, tree)
     (8, 8, 128, 16, [1], [1], False), (8, 1, 64, 32, [0], [1], False), (4, 4, 64, 64, [15, 16, 17], [1, 1, 1], False),
     (32, 4, 128, 64, [63, 64, 65, 0, 200], [1, 1, 1, 1, 1], False), (16, 2, 128, 128, [1000, 3], [7, 5], True),
@@ -114,7 +117,16 @@ def test_attention_and_weights(mv, Hq, Hkv, D, page, base, new, tree):
     check_attention(mv, pg, cache, q, new, base, D ** -0.5, vis)
 
 
-@pytest.mark.parametrize("max_q", [1, 2, 5, 40])
+@pytest.mark.parametrize("Hq,Hkv,D,page,base,new,tree", ATTEND)
+def test_attention_of_the_kernel_for_many_rows(mv, Hq, Hkv, D, page, base, new, tree):
+    rng = np.random.default_rng(Hq * 7 + D + sum(base) + 1)
+    pg, cache = make_cache(mv, rng, [b + n for b, n in zip(base, new)], Hkv, D, page)
+    q = rng.standard_normal((sum(new), Hq, D)) * 1.5
+    vis = np.concatenate([make_tree(rng, n) for n in new]) if tree else None
+    check_attention(mv, pg, cache, q, new, base, D ** -0.5, vis, max_q=MANY)
+
+
+@pytest.mark.parametrize("max_q", [1, 2, 5, 40, MANY])
 def test_max_q_chooses_the_kernel_only(mv, max_q):
     rng = np.random.default_rng(2)
     base, new = [150, 20], [6, 3]
@@ -123,7 +135,7 @@ def test_max_q_chooses_the_kernel_only(mv, max_q):
     check_attention(mv, pg, cache, q, new, base, 0.2, np.concatenate([make_tree(rng, n) for n in new]), max_q=max_q)
 
 
-@pytest.mark.parametrize("max_q", [None, 64])  # the second: the kernel for many rows
+@pytest.mark.parametrize("max_q", [None, 64, MANY])
 @pytest.mark.parametrize("spread,scale", [(1e-5, 3e3), (1e-3, 100.0), (200.0, 1e-4), (1.0, 4.0), (1.0, 0.0), (1.0, -0.3)])
 def test_ranges_of_values_and_scores(mv, spread, scale, max_q):
     """Tiny and large values (scales across fp16), one-sided softmaxes, a zero and a negative factor."""
@@ -133,7 +145,7 @@ def test_ranges_of_values_and_scores(mv, spread, scale, max_q):
     check_attention(mv, pg, cache, rng.standard_normal((2, 8, 128)), new, base, scale, None, max_q=max_q)
 
 
-@pytest.mark.parametrize("max_q", [None, 64])
+@pytest.mark.parametrize("max_q", [None, 64, MANY])
 def test_query_magnitudes(mv, max_q):
     """Rows of q from 2^-100 to 2^60 beside each other: each is scaled by its own power of two."""
     rng = np.random.default_rng(10)
@@ -142,7 +154,7 @@ def test_query_magnitudes(mv, max_q):
     check_attention(mv, pg, cache, q, [1], [129], 0.05, None, max_q=max_q)
 
 
-@pytest.mark.parametrize("max_q", [None, 64])
+@pytest.mark.parametrize("max_q", [None, 64, MANY])
 def test_constant_rows_have_zero_scale(mv, max_q):
     rng = np.random.default_rng(11)
     pg, cache = make_cache(mv, rng, [40], 1, 64, 16)
@@ -153,7 +165,7 @@ def test_constant_rows_have_zero_scale(mv, max_q):
     check_attention(mv, pg, cache, rng.standard_normal((1, 8, 64)) * 2, [1], [39], 0.125, None, max_q=max_q)
 
 
-@pytest.mark.parametrize("max_q", [None, 64])
+@pytest.mark.parametrize("max_q", [None, 64, MANY])
 def test_all_rows_constant(mv, max_q):
     """Every value row constant: the output is the softmax mean of the zeros."""
     rng = np.random.default_rng(12)
@@ -164,7 +176,7 @@ def test_all_rows_constant(mv, max_q):
     check_attention(mv, pg, cache, rng.standard_normal((3, 8, 64)), [3], [67], 0.125, None, max_q=max_q)
 
 
-@pytest.mark.parametrize("max_q", [5, 64])
+@pytest.mark.parametrize("max_q", [5, 64, MANY])
 def test_empty_rows_and_nan_in_masked_slots(mv, max_q):
     """A tree token whose key and value are NaN is seen by itself alone; a padding token sees nothing."""
     rng = np.random.default_rng(13)
@@ -199,7 +211,7 @@ def test_empty_rows_and_nan_in_masked_slots(mv, max_q):
     assert np.all(np.abs(o[keep] - ref[0][keep]) <= ref[3][keep])
 
 
-@pytest.mark.parametrize("max_q", [2, 64])
+@pytest.mark.parametrize("max_q", [2, 64, MANY])
 def test_nan_query_rows_stay_alone(mv, max_q):
     rng = np.random.default_rng(14)
     pg, cache = make_cache(mv, rng, [50], 1, 128, 16)
@@ -212,7 +224,7 @@ def test_nan_query_rows_stay_alone(mv, max_q):
     assert np.isfinite(o).all()
 
 
-@pytest.mark.parametrize("max_q", [None, 64])
+@pytest.mark.parametrize("max_q", [None, 64, MANY])
 def test_bad_pages_and_lengths_are_flagged_and_left_out(mv, max_q):
     rng = np.random.default_rng(15)
     base, new = [100, 40], [2, 2]
@@ -265,7 +277,7 @@ def test_pages_beyond_32_bit_offsets(mv):
     assert torch.equal(k, k2) and torch.equal(v, v2) and float((k - x).abs().max()) < 0.5
 
 
-@pytest.mark.parametrize("max_q", [2, 64])
+@pytest.mark.parametrize("max_q", [2, 64, MANY])
 def test_attend_in_a_graph(mv, max_q):
     rng = np.random.default_rng(18)
     pg, cache = make_cache(mv, rng, [300, 40], 2, 64, 16)
