@@ -59,6 +59,24 @@ int allow_smem(size_t bytes) {
   return MOE_OK;
 }
 
+// Launches `clusters` clusters of `size` CTAs.
+template <typename... KArgs, typename... Args>
+int launch_clusters(void (*kernel)(KArgs...), int clusters, int size, int threads, size_t smem, cudaStream_t s,
+                    Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters) * size);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
 int cache_validate(const kv4_cache* c, Cache* out);
 
 // Block of (page id, head).

@@ -272,19 +272,8 @@ int launch_evict(const EvictArgs& a, cudaStream_t s) {
   const int st = allow_smem<evict_kernel<D>>(sizeof(Smem));
   if (st != MOE_OK) return st;
   const int n = cluster_size(a.c);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.c.S) * a.c.Hkv * n);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = sizeof(Smem);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = n;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   LaunchScope ls(kProfKv4Evict, s);
-  return cudaLaunchKernelEx(&cfg, evict_kernel<D>, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launch_clusters(evict_kernel<D>, a.c.S * a.c.Hkv, n, kThreads, sizeof(Smem), s, a);
 }
 
 }  // namespace

@@ -10,9 +10,15 @@
 // atomics, no exchange between threads.
 //
 // Four warps and 128 TMEM columns (keys, 64 columns of scores) a CTA, three CTAs
-// an SM (four at D = 64), so that one's products and loads run while the others' exponentials do.
+// an SM (four at D = 64 and for few rows), so that one's products and loads run while the others' exponentials do.
 // Bound by the exponentials (16 a clock and SM) from about 45 query rows a kv
 // head on, by memory (D / 2 + 4 bytes of keys, 8 of mass a slot) below.
+//
+// More than 128 query rows (a prompt's chunk) are shared by the CTAs of a cluster, which take the same
+// slots and add up their sums in the order of their ranks: a slot's row blocks one after the
+// other in one CTA took 573 us for 6400 rows and 405 slots, with clusters of 8 81 us.
+#include <cooperative_groups.h>
+
 #include "kv4.cuh"
 #include "kv4_sched.cuh"
 #include "tc_f16.cuh"
@@ -23,6 +29,8 @@ namespace kv4 {
 int attn_validate(const kv4_attn_cfg* cfg, const Cache& c);
 
 namespace {
+
+namespace cg = cooperative_groups;
 
 using tc::add2;
 using tc::fma2;
@@ -60,6 +68,7 @@ struct Smem {
   alignas(16) float cqs[kRows];
   alignas(16) float nl[kRows];                               // -lse, in log2; -inf: no weight
   uint64_t mask[kRows];
+  long long at[kRows];                                       // where in q
   int token[kRows];
   float acc[kGroup][kSlots];
   uint64_t done, full[4][kStages];
@@ -72,79 +81,88 @@ struct Smem {
 
 // Rows row0 .. of the item's queries into shared memory as the product's
 // second operand, in the order of the key words' pairs (see prep_q of kv4.cuh).
+// A thread a row finds its place, lse and mask; W lanes a row convert it.
 template <int D, int kRows>
 __device__ __forceinline__ void load_queries(const WeighArgs& a, const Cursor& k, int row0, int rows, Smem<D, kRows>& sm) {
   constexpr int W = D / 8;  // a row's code words, one a lane
-  const int x = threadIdx.x % W;
   const int padded = (rows + 15) & ~15;
-  // Token and query head of row r of the block (small numbers: a multiplication finds the quotient).
-  const int tok0 = row0 / a.G, g0 = row0 - tok0 * a.G;
-  const float inv_g = 1.f / static_cast<float>(a.G);
-  auto token = [&](int r) { return static_cast<int>((static_cast<float>(g0 + r) + 0.5f) * inv_g); };
-  constexpr int kStep = kThreads / W;  // rows of a pass
+  const int mine = threadIdx.x, tok = (row0 + min(mine, rows - 1)) / a.G;
+  float lse = -INFINITY;
+  uint64_t mask = 0;
+  if (mine < rows) {
+    const int hd = k.h * a.G + (row0 + mine) - tok * a.G;
+    sm.at[mine] = (k.q.q0 + tok) * a.q_ts + hd * a.q_hs;
+    lse = a.lse[(static_cast<size_t>(k.q.q0) + tok) * a.Hq + hd];  // (used below the loop, whose loads go out meanwhile)
+    if (a.visible) mask = a.visible[k.q.q0 + tok];
+  }
+  __syncthreads();
+  const int x = threadIdx.x % W;
+  constexpr int kStep = kThreads / W, kBeside = 4;  // rows of a pass; passes beside each other, step by step
 #pragma unroll 1
-  for (int r0 = threadIdx.x / W; r0 < padded; r0 += 4 * kStep) {
-  uint4 raws[4];
-  float nls[4];
-  uint64_t masks[4];
+  for (int r0 = threadIdx.x / W; r0 < padded; r0 += kBeside * kStep) {
+    uint4 raw[kBeside];
+    float sum[kBeside];
+    uint32_t top[kBeside];  // largest magnitude, as bf16
 #pragma unroll
-  for (int y = 0; y < 4; ++y) {
-    const int r = r0 + y * kStep;
-    raws[y] = make_uint4(0, 0, 0, 0);
-    nls[y] = -INFINITY;
-    masks[y] = 0;
-    if (r < rows) {
-      const int tr = token(r), i = tok0 + tr, hd = k.h * a.G + g0 + r - tr * a.G;
-      raws[y] = *reinterpret_cast<const uint4*>(a.q + (k.q.q0 + i) * a.q_ts + hd * a.q_hs + 8 * x);
-      nls[y] = a.lse[(static_cast<size_t>(k.q.q0) + i) * a.Hq + hd];
-      if (a.visible) masks[y] = a.visible[k.q.q0 + i];
+    for (int y = 0; y < kBeside; ++y) {
+      const int r = r0 + y * kStep;
+      raw[y] = make_uint4(0, 0, 0, 0);
+      if (r < rows) raw[y] = *reinterpret_cast<const uint4*>(a.q + sm.at[r] + 8 * x);
+    }
+#pragma unroll
+    for (int y = 0; y < kBeside; ++y) {
+      const uint32_t u[4] = {raw[y].x, raw[y].y, raw[y].z, raw[y].w};
+      uint32_t t = 0;
+      sum[y] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        t = __vmaxu2(t, u[j] & 0x7FFF7FFFu);
+        sum[y] += __uint_as_float(u[j] << 16) + __uint_as_float(u[j] & 0xFFFF0000u);
+      }
+      top[y] = max(t >> 16, t & 0xFFFFu);
+    }
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int y = 0; y < kBeside; ++y) {
+        top[y] = max(top[y], __shfl_xor_sync(0xFFFFFFFFu, top[y], o));
+        sum[y] += __shfl_xor_sync(0xFFFFFFFFu, sum[y], o);
+      }
+#pragma unroll
+    for (int y = 0; y < kBeside; ++y) {
+      const int r = r0 + y * kStep;
+      if (r >= padded) continue;
+      // (Below 2^-113 a row's largest magnitude lands below 2^14; its scores are zero all the same.)
+      const int ex = static_cast<int>(top[y] >> 7);
+      const int e = ex > 0 && ex < 255 ? min(14 + 127 - ex, 127) : 0;
+      const float f = __uint_as_float(static_cast<uint32_t>(127 + e) << 23), f16 = f * 0.0625f;
+      auto pair = [&](uint32_t lo, uint32_t hi, float by) {
+        const float2 v = mul2(make_float2(__uint_as_float(lo), __uint_as_float(hi)), make_float2(by, by));
+        return pack_h2(v.x, v.y);
+      };
+      const uint4 u = raw[y];
+      *reinterpret_cast<uint4*>(sm.q + (x >> 3) * (kRows * 128) + (r >> 3) * 1024 + (r & 7) * 128 + (((x & 7) ^ (r & 7)) << 4)) =
+          make_uint4(pair(u.x << 16, u.z << 16, f), pair(u.x & 0xFFFF0000u, u.z & 0xFFFF0000u, f16),
+                     pair(u.y << 16, u.w << 16, f), pair(u.y & 0xFFFF0000u, u.w & 0xFFFF0000u, f16));
+      if (x == 0) {
+        const int up = 24 - e;  // the codes carry 2^-24
+        sm.cq[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + (up >> 1)) << 23) *
+                   __uint_as_float(static_cast<uint32_t>(127 + up - (up >> 1)) << 23);
+        sm.cqs[r] = a.scale_log2 * sum[y];
+      }
     }
   }
-#pragma unroll
-  for (int y = 0; y < 4; ++y) {
-    const int r = r0 + y * kStep, i = tok0 + token(min(r, rows - 1));
-    if (r >= padded) break;
-    const uint4 raw = raws[y];
-    const float nl = nls[y];
-    const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-    float v[8], m = 0.f, sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(u[j] << 16);
-      v[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-      m = fmaxf(m, fmaxf(fabsf(v[2 * j]), fabsf(v[2 * j + 1])));
-      sum += v[2 * j] + v[2 * j + 1];
-    }
-#pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) {
-      m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    }
-    const int ex = static_cast<int>(__float_as_uint(m) >> 23);
-    const int e = m > 0.f && ex < 255 ? 14 + 127 - (ex > 0 ? ex : 1) : 0;
-    const float f1 = __uint_as_float(static_cast<uint32_t>(127 + (e >> 1)) << 23);
-    const float f2 = __uint_as_float(static_cast<uint32_t>(127 + e - (e >> 1)) << 23);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = v[j] * f1 * f2;
-    *reinterpret_cast<uint4*>(sm.q + (x >> 3) * (kRows * 128) + (r >> 3) * 1024 + (r & 7) * 128 + (((x & 7) ^ (r & 7)) << 4)) =
-        make_uint4(pack_h2(v[0], v[4]), pack_h2(v[1] * 0.0625f, v[5] * 0.0625f), pack_h2(v[2], v[6]),
-                   pack_h2(v[3] * 0.0625f, v[7] * 0.0625f));
-    if (x == 0) {
-      const int up = 24 - e;  // the codes carry 2^-24
-      sm.cq[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + (up >> 1)) << 23) *
-                 __uint_as_float(static_cast<uint32_t>(127 + up - (up >> 1)) << 23);
-      sm.cqs[r] = a.scale_log2 * sum;
-      const bool none = nl == -INFINITY;  // a row that saw nothing sees no new slot, whatever those hold
-      sm.nl[r] = none ? -INFINITY : -nl * kLog2e;
-      sm.token[r] = none ? -1 : i;
-      sm.mask[r] = none ? 0 : masks[y];
-    }
-  }
+  if (mine < padded) {
+    const bool none = lse == -INFINITY;  // a row that saw nothing sees no new slot, whatever those hold
+    sm.nl[mine] = none ? -INFINITY : -lse * kLog2e;
+    sm.token[mine] = none ? -1 : tok;
+    sm.mask[mine] = none ? 0 : mask;
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-template <int D, int kRows>
+// kShared: the CTAs of a cluster take the same units, each with its share of the query rows.
+template <int D, int kRows, bool kShared>
 __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
   constexpr int P = D / 32;   // 16-byte pieces of a key row
   constexpr uint32_t kACol = 0, kSCol = D / 2;
@@ -171,7 +189,11 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
   const uint64_t qd = tc::smem_desc_sw128(tc::smem_u32(sm.q));
   volatile int* abort_flag = &sm.abort;
   const long long total = sm.cum[a.c.S];
-  const long long u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int cs = kShared ? static_cast<int>(cluster.num_blocks()) : 1;
+  const int rank = kShared ? static_cast<int>(cluster.block_rank()) : 0;
+  const long long team = blockIdx.x / cs, teams = gridDim.x / cs;
+  const long long u0 = total * team / teams, u1 = total * (team + 1) / teams;
   const size_t width = static_cast<size_t>(a.c.width) << a.c.page_log2;
   const size_t stride = static_cast<size_t>(a.c.Hkv) * a.c.block_bytes();
   const int last_row = a.c.page_size - 1;
@@ -183,18 +205,20 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
   bool dead = false;
   Cursor k;
   if (u0 < u1) cursor_at(k, a.c, a.q_start, a.base, a.T, a.G, kAllRows, kSlots, 0, sm.cum, u0);
-  for (long long u = u0; u < u1 && !dead;) {
+  for (long long u = u0; u < u1 && (kShared || !dead);) {  // (to its end in any case: a cluster's CTAs meet in it)
     const int units = static_cast<int>(u1 - u < k.nt - k.tile ? u1 - u : k.nt - k.tile);
-    const int all = k.q.nq * a.G, blocks = (all + kRows - 1) / kRows;
+    const int of_all = k.q.nq * a.G, share = kShared ? ((of_all + cs - 1) / cs + 15) & ~15 : of_all;
+    const int row_at = rank * share, all = min(share, of_all - row_at);  // (none: negative)
+    const int blocks = all > 0 ? (all + kRows - 1) / kRows : 0;
     if (a.visible && k.q.nq > kMaxTree && tid == 0) flag_error(a.dev_err, MOE_DEV_CAPACITY);
     float* mass = a.mass + (static_cast<size_t>(k.s) * a.c.Hkv + k.h) * width;
-    const int group = blocks > 1 ? kGroup : units;
+    const int group = kShared || blocks > 1 ? kGroup : units;
     const uint8_t* from = a.c.pages + static_cast<size_t>(k.h) * a.c.block_bytes();
     const int32_t* table = a.c.table + static_cast<size_t>(k.s) * a.c.width;
-    for (int g0 = 0; g0 < units && !dead; g0 += group) {
+    for (int g0 = 0; g0 < units && (kShared || !dead); g0 += group) {
       const int n = min(group, units - g0), t0 = k.tile + g0;
       for (int block = 0; block < blocks && !dead; ++block) {
-        const int row0 = block * kRows, rows = min(kRows, all - row0), padded = (rows + 15) & ~15;
+        const int row0 = row_at + block * kRows, rows = min(kRows, all - block * kRows), padded = (rows + 15) & ~15;
         // Key rows: the lane of each page segment looks its page up, one unit ahead, and copies it.
         // (What it finds is not looked at before it is needed: a use would wait for the load.)
         int page = 0;
@@ -229,9 +253,9 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
           look(i + 1);
         }
         __syncthreads();  // the rows before have been read
-        load_queries<D, kRows>(a, k, row0, rows, sm);
+        if (!kShared || g0 == 0 || blocks > 1) load_queries<D, kRows>(a, k, row0, rows, sm);
         __syncthreads();
-        const bool last = block == blocks - 1;
+        const bool last = !kShared && block == blocks - 1;
         // The mass of this unit's slot, loaded one unit ahead.
         auto mass_of = [&](int i) {
           const int j = (t0 + i) * kSlots + tid;
@@ -333,6 +357,21 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
         }
         dead = __syncthreads_or(dead);
       }
+      if constexpr (kShared) {
+        // The shares' sums in the order of the ranks; each rank writes its part of the units.
+        cluster.sync();
+        const int shares = (of_all + share - 1) / share;
+        for (int i = rank; i < n; i += cs) {
+          const int j = (t0 + i) * kSlots + tid;
+          const int page = j < k.q.total ? table[j >> a.c.page_log2] : -1;
+          if (page < 0 || page >= a.c.n_pages) continue;
+          const float before = mass[j];
+          float sum = 0.f;
+          for (int r = 0; r < shares; ++r) sum += cluster.map_shared_rank(sm.acc[i], r)[tid];
+          mass[j] = before + sum;
+        }
+        cluster.sync();
+      }
     }
     u += units;
     if (u < u1) cursor_next(k, a.c, a.q_start, a.base, a.T, a.G, kAllRows, kSlots, 0, sm.cum);
@@ -352,14 +391,19 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
   }
 }
 
-// ctas: what fits an SM (TMEM: four).
-template <int D, int kRows>
-int launch_weigh(const WeighArgs& a, int ctas, cudaStream_t s) {
+// ctas: what fits an SM (TMEM: four); cluster: CTAs that share an item's query rows.  Clusters above 2 do not
+// fill every SM, and a grid that does not fit at once takes twice the time (16 sequences of 8k slots,
+// 512 rows, clusters of 4: 286 us with a full grid, 254 with nine tenths).
+template <int D, int kRows, bool kShared>
+int launch_weigh(const WeighArgs& a, int ctas, int cluster, cudaStream_t s) {
+  constexpr auto kernel = weigh_kernel<D, kRows, kShared>;
   const size_t smem = sizeof(Smem<D, kRows>) + static_cast<size_t>(a.c.S) * 8;
-  const int st = allow_smem<weigh_kernel<D, kRows>>(smem);
+  const int st = allow_smem<kernel>(smem);
   if (st != MOE_OK) return st;
   LaunchScope ls(kProfKv4Weigh, s);
-  return launch_k(weigh_kernel<D, kRows>, dim3(sm_count() * ctas), dim3(kThreads), smem, s, false, a);
+  if constexpr (kShared)
+    return launch_clusters(kernel, sm_count() * ctas * (cluster > 2 ? 9 : 10) / (10 * cluster), cluster, kThreads, smem, s, a);
+  return launch_k(kernel, dim3(sm_count() * ctas), dim3(kThreads), smem, s, false, a);
 }
 
 }  // namespace
@@ -383,8 +427,12 @@ extern "C" int kv4_weigh(const kv4_cache* cache, const void* q, const int32_t* q
   WeighArgs a{c, static_cast<const uint16_t*>(q), cfg->q_token_stride, cfg->q_head_stride, q_start, base, visible, lse,
               mass, cfg->T, cfg->n_q_heads, cfg->n_q_heads / c.Hkv, cfg->scale * kLog2e, dev_err};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (c.D == 64) return launch_weigh<64, 128>(a, 4, s);
+  const long long rows = static_cast<long long>(cfg->max_q) * a.G;
+  // At 224 rows clusters of 1 / 2 / 4 / 8 take 194 / 158 / 166 / 245 us, at 400 110 / 96 / 93 / 111, at 2400 244 / 230 / 161 / 160.
+  int cluster = 1;
+  while (cluster < 8 && rows > 128 * cluster) cluster *= 2;
+  if (cluster > 1) return c.D == 128 ? launch_weigh<128, 128, true>(a, 3, cluster, s) : launch_weigh<64, 128, true>(a, 4, cluster, s);
+  if (c.D == 64) return launch_weigh<64, 128, false>(a, 4, 1, s);
   // 64 rows in shared memory leave room for a fourth CTA.
-  const bool few = static_cast<long long>(cfg->max_q) * a.G <= 64;
-  return few ? launch_weigh<128, 64>(a, 4, s) : launch_weigh<128, 128>(a, 3, s);
+  return rows <= 64 ? launch_weigh<128, 64, false>(a, 4, 1, s) : launch_weigh<128, 128, false>(a, 3, 1, s);
 }
