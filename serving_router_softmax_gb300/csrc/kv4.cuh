@@ -119,6 +119,34 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Waits for a phase of an mbarrier.  Gives up, and sets *abort, when 2 s (or `budget_ns`) have passed or another role
+// has set *abort.  A try sleeps in hardware for up to 1 us, so that waiting warps leave the issue slots to the
+// others, and the clock is read only after many tries, as reading it would lengthen every wait.
+// kWarp: all lanes wait, with one answer.
+template <bool kWarp>
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                           uint64_t budget_ns = 2000000000ull) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 1;; ++n) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity), "r"(1000u)
+        : "memory");
+    if (kWarp ? __all_sync(0xFFFFFFFFu, ok) : ok) return true;
+    if ((n & 31) == 0) {
+      const uint64_t now = tc::globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      const bool stop = *abort || now - t0 > budget_ns;
+      if (kWarp ? __any_sync(0xFFFFFFFFu, stop) : stop) {
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
 __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                    tc::smem_u32(dst)),

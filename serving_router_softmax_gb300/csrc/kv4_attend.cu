@@ -72,7 +72,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Atte
   pdl_trigger();
   const long long total = sm.cum[a.c.S];
   const int ncta = used_ctas(total, kMinUnits), cta = blockIdx.x;
-  const long long u0 = cta < ncta ? total * cta / ncta : 0, u1 = cta < ncta ? total * (cta + 1) / ncta : 0;
+  const Shares shares(total, max(ncta, 1));
+  const long long u0 = cta < ncta ? shares.begin(cta) : 0, u1 = cta < ncta ? shares.begin(cta + 1) : 0;
   volatile int* abort_flag = &sm.abort;
   Cursor k;
   if (u0 < u1) cursor_at(k, a.c, a.q_start, a.base, a.T, a.G, kRows, kTile, kItemUnits, sm.cum, u0);
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Atte
         }
       }
     }
-    if (!sp.whole && sp.first && tid == 0) note_cut(a, cta, ncta, total, k, sp, u, u == u0 ? 0 : 1);
+    if (!sp.whole && sp.first && tid == 0) note_cut(a, cta, shares, k, sp, u, u == u0 ? 0 : 1);
     tc::named_bar_sync(1, 32 * kConsumerWarps);
     u += sp.n;
     if (u < u1) cursor_next(k, a.c, a.q_start, a.base, a.T, a.G, kRows, kTile, kItemUnits, sm.cum);

@@ -169,14 +169,14 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, const Cursor& k, lo
 }
 
 // Notes an item that starts in this CTA and ends in a later one; u is the item's first unit.
-__device__ __forceinline__ void note_cut(const AttendArgs& a, int cta, int ncta, long long total, const Cursor& k,
-                                         const Span& s, long long u, int slot) {
+__device__ __forceinline__ void note_cut(const AttendArgs& a, int cta, const Shares& shares, const Cursor& k, const Span& s,
+                                         long long u, int slot) {
   int32_t* M = a.meta + static_cast<size_t>(cta) * 8;
   M[1] = k.s;
   M[2] = k.h;
   M[3] = s.row0;
   M[4] = s.rows;
-  M[5] = static_cast<int>(((u + s.need) * ncta - 1) / total);  // the CTA that owns the item's last tile
+  M[5] = shares.of(u + s.need - 1);  // the CTA that owns the item's last tile
   M[6] = slot;
   M[0] = 1;
 }

@@ -114,19 +114,14 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
   const uint32_t tmem = sm.tmem;
   const long long total = sm.cum[a.c.S];
   const int ncta = used_ctas(total, kMinUnits), cta = blockIdx.x;
-  const long long u0 = cta < ncta ? total * cta / ncta : 0, u1 = cta < ncta ? total * (cta + 1) / ncta : 0;
+  const Shares shares(total, max(ncta, 1));
+  const long long u0 = cta < ncta ? shares.begin(cta) : 0, u1 = cta < ncta ? shares.begin(cta + 1) : 0;
   volatile int* abort_flag = &sm.abort;
   Cursor k;
   if (u0 < u1) cursor_at(k, a.c, a.q_start, a.base, a.T, a.G, kWideRows, kTile, kItemUnits, sm.cum, u0);
   // Waits give up together: the first to run out tells the others.
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (tc::mbar_wait_bounded(bar, parity, abort_flag, kWaitBudgetNs)) return true;
-    *abort_flag = 1;
-    return false;
-  };
-
-  // The same answer in all lanes.
-  auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_phase<false>(bar, parity, abort_flag); };
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return wait_phase<true>(bar, parity, abort_flag); };
 
   if (warp < 4) {
     // ---------------------------------------------------------- softmax, output
@@ -162,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
         for (int half = 0; half < 2; ++half) {
           constexpr int C = D / 32;
           uint4 v[2][C];
-          float mx[2] = {}, sum[2] = {}, f1[2], f2[2];
+          float f[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int rr = warp * 32 + 16 * half + 8 * i + lr, tr = token(rr);
@@ -172,30 +167,30 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
               v[i][c] = rr < s.rows ? *reinterpret_cast<const uint4*>(src + 32 * c) : make_uint4(0, 0, 0, 0);
           }
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < 2; ++i) {
+            uint32_t mag = 0;  // largest magnitudes of the low and the high halves, as bf16
+            float2 both = make_float2(0.f, 0.f);
 #pragma unroll
             for (int c = 0; c < C; ++c) {
               const uint32_t w[4] = {v[i][c].x, v[i][c].y, v[i][c].z, v[i][c].w};
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const float lo = __uint_as_float(w[j] << 16), hi = __uint_as_float(w[j] & 0xFFFF0000u);
-                mx[i] = max3(mx[i], fabsf(lo), fabsf(hi));
-                sum[i] += lo + hi;
+                mag = __vmaxu2(mag, w[j] & 0x7FFF7FFFu);
+                both = add2(both, make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u)));
               }
             }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 1));
-            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 2));
-            sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 1);
-            sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 2);
-            const int ex = static_cast<int>(__float_as_uint(mx[i]) >> 23);
-            const int e = mx[i] > 0.f && ex < 255 ? 14 + 127 - (ex > 0 ? ex : 1) : 0;
-            f1[i] = __uint_as_float(static_cast<uint32_t>(127 + (e >> 1)) << 23);
-            f2[i] = __uint_as_float(static_cast<uint32_t>(127 + e - (e >> 1)) << 23);
+            float sum = both.x + both.y;
+            mag = __vmaxu2(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 1));
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+            mag = __vmaxu2(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 2));
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+            // (Below 2^-113 a row's largest magnitude lands below 2^14; its scores are zero all the same.)
+            const int ex = static_cast<int>(max(mag >> 16, mag & 0xFFFFu) >> 7);
+            const int e = ex > 0 && ex < 255 ? min(14 + 127 - ex, 127) : 0;
+            f[i] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
             // The lane of the row keeps its factors.
             const int es = __shfl_sync(0xFFFFFFFFu, e, 4 * (lane & 7));
-            const float ss = __shfl_sync(0xFFFFFFFFu, sum[i], 4 * (lane & 7));
+            const float ss = __shfl_sync(0xFFFFFFFFu, sum, 4 * (lane & 7));
             if (lane >> 3 == 2 * half + i) {
               const int y = 24 - es;  // the codes carry 2^-24; two factors, as y may pass one fp32's range
               cq = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + (y >> 1)) << 23) *
@@ -208,17 +203,16 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
             uint32_t o[2][4];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const uint32_t w[4] = {v[i][c].x, v[i][c].y, v[i][c].z, v[i][c].w};
-              float y[8];
-#pragma unroll
-              for (int t = 0; t < 4; ++t) {
-                y[2 * t] = __uint_as_float(w[t] << 16) * f1[i] * f2[i];
-                y[2 * t + 1] = __uint_as_float(w[t] & 0xFFFF0000u) * f1[i] * f2[i];
-              }
-              o[i][0] = pack_h2(y[0], y[4]);
-              o[i][1] = pack_h2(y[1] * 0.0625f, y[5] * 0.0625f);
-              o[i][2] = pack_h2(y[2], y[6]);
-              o[i][3] = pack_h2(y[3] * 0.0625f, y[7] * 0.0625f);
+              const uint4 u = v[i][c];
+              const float f16 = f[i] * 0.0625f;
+              auto pair = [](uint32_t lo, uint32_t hi, float by) {
+                const float2 y = mul2(make_float2(__uint_as_float(lo), __uint_as_float(hi)), make_float2(by, by));
+                return pack_h2(y.x, y.y);
+              };
+              o[i][0] = pair(u.x << 16, u.z << 16, f[i]);
+              o[i][1] = pair(u.x & 0xFFFF0000u, u.z & 0xFFFF0000u, f16);
+              o[i][2] = pair(u.y << 16, u.w << 16, f[i]);
+              o[i][3] = pair(u.y & 0xFFFF0000u, u.w & 0xFFFF0000u, f16);
             }
             asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
                              tq + (static_cast<uint32_t>(16 * half) << 16) + 16 * c),
@@ -390,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
           P[kWideRows * D + kWideRows + tid] = l;
         }
       }
-      if (!whole && s.first && tid == 0) note_cut(a, cta, ncta, total, k, s, u, u == u0 ? 0 : 1);
+      if (!whole && s.first && tid == 0) note_cut(a, cta, shares, k, s, u, u == u0 ? 0 : 1);
       tc::tc_fence_before();
       u += s.n;
       if (u < u1) cursor_next(k, a.c, a.q_start, a.base, a.T, a.G, kWideRows, kTile, kItemUnits, sm.cum);
@@ -518,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
     for (int i = 0; i < issued; ++i) {
       raw.i = raw.i ? raw.i - 1 : kRaw - 1;
       if (raw.i == kRaw - 1) raw.phase ^= 1;
-      tc::mbar_wait_bounded(&sm.raw_full[raw.i], raw.phase, &sm.never, 100000000ull);
+      wait_phase<true>(&sm.raw_full[raw.i], raw.phase, &sm.never, 100000000ull);
     }
   } else if (lane == 0) {
     // ---------------------------------------------------------- products
@@ -583,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
       const uint64_t t0 = tc::globaltimer_ns();
       while (tc::globaltimer_ns() - t0 < 1000000ull) {}
     } else if (any) {
-      tc::mbar_wait_bounded(&sm.pv_done[1], sp ^ 1, &sm.never, 100000000ull);
+      wait_phase<false>(&sm.pv_done[1], sp ^ 1, &sm.never, 100000000ull);
     }
   }
   __syncthreads();

@@ -192,8 +192,9 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
   const cg::cluster_group cluster = cg::this_cluster();
   const int cs = kShared ? static_cast<int>(cluster.num_blocks()) : 1;
   const int rank = kShared ? static_cast<int>(cluster.block_rank()) : 0;
-  const long long team = blockIdx.x / cs, teams = gridDim.x / cs;
-  const long long u0 = total * team / teams, u1 = total * (team + 1) / teams;
+  const int team = blockIdx.x / cs;
+  const Shares shares(total, gridDim.x / cs);
+  const long long u0 = shares.begin(team), u1 = shares.begin(team + 1);
   const size_t width = static_cast<size_t>(a.c.width) << a.c.page_log2;
   const size_t stride = static_cast<size_t>(a.c.Hkv) * a.c.block_bytes();
   const int last_row = a.c.page_size - 1;
@@ -353,6 +354,7 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
 #pragma unroll 1
         for (int i = 0; i < kStages - 1; ++i) {
           if (!tc::mbar_wait_bounded(&sm.full[warp][st], phase, abort_flag, kWaitBudgetNs)) *abort_flag = 1;
+          __syncwarp();
           if (++st == kStages) st = 0, phase ^= 1;
         }
         dead = __syncthreads_or(dead);
