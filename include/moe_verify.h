@@ -623,7 +623,8 @@ int moe_verify_plan(const moe_step_cfg* cfg, const float* P, const int32_t* pare
  * [page_size][D/2], V codes [page_size][D/2] (byte b holds dimension 2b in its
  * low nibble, 2b + 1 in its high one), parameters [page_size][4] fp16: k
  * scale, k zero, v scale, v zero.  Slot j of sequence s lies in page
- * table[s][j / page_size] at row j % page_size.  Slots beyond a sequence's
+ * table[s][j / page_size] at row j % page_size.  Sequences may share pages
+ * (a common prefix) that kv4_append and kv4_evict do not write.  Slots beyond a sequence's
  * length may hold anything, NaN included, and table entries beyond its pages
  * are not used.  A visible slot's scales are finite and not negative, as
  * kv4_append writes them.
@@ -698,12 +699,13 @@ typedef struct {
  *   out       [T, n_q_heads, D] bf16 out; zeros for a row that sees nothing.
  *   lse       [T, n_q_heads] fp32 out or NULL: log of the sum of the
  *             exponentials of the scaled scores, -inf for such a row.
- * Scores, maxima, sums and outputs are accumulated in fp32; a probability is
- * rounded to fp16 (relative 2^-12) as the product's operand, the output once
- * to bf16.  A NaN or infinity in a row of q, or in a slot that a row sees,
+ * Scores, maxima, sums and outputs are accumulated in fp32; a probability
+ * times its slot's value scale is rounded to fp16 (by at most 2^-11 of it) as
+ * the product's operand, the output once to bf16.  A NaN or infinity in a row of q, or in a slot that a row sees,
  * makes that row NaN; in slots it does not see it has no effect.
  * Results do not depend on timing.  Needs kv4_attend_workspace() bytes (0: bad
- * arguments), 256-byte aligned, of any content. */
+ * arguments), 256-byte aligned, of any content, that no call running at the
+ * same time uses. */
 size_t kv4_attend_workspace(const kv4_cache* cache, const kv4_attn_cfg* cfg);
 int kv4_attend(const kv4_cache* cache, const void* q, const int32_t* q_start, const int32_t* base,
                const uint64_t* visible, const kv4_attn_cfg* cfg, void* out, float* lse, void* workspace,
@@ -713,7 +715,7 @@ int kv4_attend(const kv4_cache* cache, const void* q, const int32_t* q_start, co
  *   mass[s, h, j] += sum over the new tokens i of s and the query heads of kv
  *   head h of exp(scale * q . k_j - lse), over the slots j that i sees.
  * Arguments as kv4_attend (of whose call lse is the result; rows with lse
- * -inf add nothing); mass [n_seq, n_kv_heads, max_pages * page_size] fp32 in
+ * -inf see no new slot, whatever it holds, and add nothing); mass [n_seq, n_kv_heads, max_pages * page_size] fp32 in
  * and out.  Slots beyond a sequence's are not touched.  Sums in fp32 in a
  * fixed order. */
 int kv4_weigh(const kv4_cache* cache, const void* q, const int32_t* q_start, const int32_t* base,
