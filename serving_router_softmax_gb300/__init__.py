@@ -9,7 +9,7 @@ C ABI in ``include/moe_verify.h``); this package only marshals arguments.
 Importing it loads the library and raises if it has not been built.
 """
 from . import _lib
-from .kv4 import Kv4Cache, kv4_append, kv4_attend, kv4_evict, kv4_read, kv4_weigh  # noqa: F401
+from .kv4 import Kv4Cache, kv4_append, kv4_attend, kv4_attend_workspace_bytes, kv4_evict, kv4_read, kv4_weigh  # noqa: F401
 from .api import (ExpertLayer, ExpertPool, MoEError, StepSpec, VerifyPlan, VerifyStep, depth_policy,  # noqa: F401
                   eco_select,
                   expert_bytes, ffn_workspace_bytes, hot_list, HostExperts, launch_count, new_dev_err, pack_tiled,

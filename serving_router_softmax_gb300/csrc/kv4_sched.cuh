@@ -77,9 +77,9 @@ __device__ __forceinline__ void build_units(const Cache& c, const int32_t* q_sta
 struct Shares {
   long long total, each;
   int n, rest;
-  __device__ __forceinline__ Shares(long long total, int n) : total(total), n(n) {
-    each = total < (1ll << 32) ? static_cast<uint32_t>(total) / static_cast<uint32_t>(n) : total / n;
-    rest = static_cast<int>(total - each * n);
+  __device__ __forceinline__ Shares(long long units, int shares) : total(units), n(shares) {
+    each = units < (1ll << 32) ? static_cast<uint32_t>(units) / static_cast<uint32_t>(shares) : units / shares;
+    rest = static_cast<int>(units - each * shares);
   }
   __device__ __forceinline__ long long begin(int i) const {  // n < 65536
     return each * i + static_cast<uint32_t>(rest) * static_cast<uint32_t>(i) / static_cast<uint32_t>(n);

@@ -41,6 +41,9 @@ constexpr int kSlots = 128;          // slots of a unit, one a thread
 constexpr int kCols = 64;            // columns of a product
 constexpr int kAllRows = 1 << 30;    // one row block per kv head
 constexpr int kStages = 3;           // key rows on their way
+// What beginning an item costs, in units: a CTA with two units whose second begins another item took the longest (4 trees
+// on up to 4000 slots 16.4 us with 0, 12.5 with 1, 14.3 with 2; 16 on up to 16k 50.4, 49.6, 48.5).
+constexpr int kItemUnits = 1;
 constexpr int kGroup = 8;            // units whose sums wait in shared memory where rows come in several blocks
 constexpr uint32_t kTmemCols = 128;
 constexpr uint64_t kWaitBudgetNs = 2000000000ull;  // 2 s
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
   tc::tc_fence_before();
   pdl_wait();
   pdl_trigger();
-  build_units(a.c, a.q_start, a.base, a.T, a.G, kAllRows, kSlots, 0, sm.cum, sm.scratch, a.dev_err, blockIdx.x == 0);
+  build_units(a.c, a.q_start, a.base, a.T, a.G, kAllRows, kSlots, kItemUnits, sm.cum, sm.scratch, a.dev_err, blockIdx.x == 0);
   tc::tc_fence_after();
   const uint32_t tmem = sm.tmem, mine = tmem + (static_cast<uint32_t>(warp * 32) << 16);
   const uint64_t qd = tc::smem_desc_sw128(tc::smem_u32(sm.q));
@@ -205,9 +208,10 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
   uint32_t parity = 0;
   bool dead = false;
   Cursor k;
-  if (u0 < u1) cursor_at(k, a.c, a.q_start, a.base, a.T, a.G, kAllRows, kSlots, 0, sm.cum, u0);
+  if (u0 < u1) cursor_at(k, a.c, a.q_start, a.base, a.T, a.G, kAllRows, kSlots, kItemUnits, sm.cum, u0);
   for (long long u = u0; u < u1 && (kShared || !dead);) {  // (to its end in any case: a cluster's CTAs meet in it)
-    const int units = static_cast<int>(u1 - u < k.nt - k.tile ? u1 - u : k.nt - k.tile);
+    const int span = static_cast<int>(u1 - u < k.nt - k.tile ? u1 - u : k.nt - k.tile);
+    const int units = max(0, min(span, k.nt - kItemUnits - k.tile));  // those with slots
     const int of_all = k.q.nq * a.G, share = kShared ? ((of_all + cs - 1) / cs + 15) & ~15 : of_all;
     const int row_at = rank * share, all = min(share, of_all - row_at);  // (none: negative)
     const int blocks = all > 0 ? (all + kRows - 1) / kRows : 0;
@@ -375,8 +379,8 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
         cluster.sync();
       }
     }
-    u += units;
-    if (u < u1) cursor_next(k, a.c, a.q_start, a.base, a.T, a.G, kAllRows, kSlots, 0, sm.cum);
+    u += span;
+    if (u < u1) cursor_next(k, a.c, a.q_start, a.base, a.T, a.G, kAllRows, kSlots, kItemUnits, sm.cum);
   }
   tc::tc_fence_before();
   __syncthreads();

@@ -205,6 +205,8 @@ def kv4_attend(cache: Kv4Cache, q: torch.Tensor, q_start: torch.Tensor, base: to
     st = _raw_stream(cache._index)
     if workspace is None:
         workspace = _workspace(cache._index, need, st)
+    elif workspace.dtype is not torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
+        raise MoEError("workspace: expected contiguous CUDA bytes (uint8)")
     _check(L.load().kv4_attend(cache._ref, q.data_ptr(), _arg(q_start, torch.int32, sq, "q_start"),
                                _arg(base, torch.int32, sb, "base"),
                                None if visible is None else _arg(visible, torch.int64, sv, "visible"), ref,

@@ -485,3 +485,18 @@ def test_python_refusals(mv):
     assert mv.kv4_append(cache, empty, empty, none, none) is None
     out, lse = mv.kv4_attend(cache, torch.empty((0, 4, 64), dtype=torch.bfloat16, device="cuda"), i32(0, 0), i32(20), 1)
     assert out.shape == (0, 4, 64)
+
+
+def test_workspace_refusals(mv):
+    rng = np.random.default_rng(41)
+    pg, cache = make_cache(mv, rng, [20], 2, 64, 16)
+    q = torch.zeros((1, 4, 64), dtype=torch.bfloat16, device="cuda")
+    q_start, base = dev(np.array([0, 1], np.int32)), dev(np.array([19], np.int32))
+    need = mv.kv4_attend_workspace_bytes(cache, q, 1)
+    for ws in (torch.empty(need, dtype=torch.uint8), torch.empty(need, dtype=torch.float32, device="cuda"),
+               torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2], torch.empty(need - 1, dtype=torch.uint8, device="cuda"),
+               torch.empty(need + 256, dtype=torch.uint8, device="cuda")[1:]):
+        with pytest.raises(mv.MoEError):
+            mv.kv4_attend(cache, q, q_start, base, 1, workspace=ws)
+    mv.kv4_attend(cache, q, q_start, base, 1, workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
