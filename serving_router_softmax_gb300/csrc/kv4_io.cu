@@ -7,9 +7,10 @@
 // of values each, side by side, 4 (fp32) or 8 (bf16) of them, and the 2 or 4
 // bytes of their codes.  A warp's rows share their token's look-up
 // (with one a row the first below took 147 us, the second 72).  Append of 32,768 bf16 tokens of 8 heads of 128 with the
-// held values out: 72 us, 63% of the copy rate (82 before the quotients and held values went two to an instruction; the division, the conversion and the two reductions of every row keep
-// it from more); read of as many to fp32: 55 us, 81%.  7 tokens appended 2.3 us, 333 read 2.0, under the
-// host's 12 a call.
+// held values out: 72 us, 63% of the copy rate (82 before the quotients and held values went two to an
+// instruction; what is left of the conversion and the two reductions a row keep it from more, and so do
+// three or five CTAs an SM, 82 and 76 us); read of as many to fp32: 55 us, 81%.  7 tokens appended 2.3 us, 333
+// read 2.0, under the host's 12 a call.
 #include "kv4.cuh"
 #include "tc_f16.cuh"
 
