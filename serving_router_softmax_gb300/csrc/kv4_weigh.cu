@@ -16,7 +16,7 @@
 //
 // More than 128 query rows (a prompt's chunk) are shared by the CTAs of a cluster, which take the same
 // slots and add up their sums in the order of their ranks: a slot's row blocks one after the
-// other in one CTA took 573 us for 6400 rows and 405 slots, with clusters of 8 81 us.
+// other in one CTA took 543 us for 6400 rows and 405 slots, with clusters of 8 77 us.
 #include <cooperative_groups.h>
 
 #include "kv4.cuh"
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
 
 // ctas: what fits an SM (TMEM: four); cluster: CTAs that share an item's query rows.  Clusters above 2 do not
 // fill every SM, and a grid that does not fit at once takes twice the time (16 sequences of 8k slots,
-// 512 rows, clusters of 4: 286 us with a full grid, 254 with nine tenths).
+// 512 rows, clusters of 4: 285 us with a full grid, 228 with nine tenths).
 template <int D, int kRows, bool kShared>
 int launch_weigh(const WeighArgs& a, int ctas, int cluster, cudaStream_t s) {
   constexpr auto kernel = weigh_kernel<D, kRows, kShared>;
@@ -434,7 +434,8 @@ extern "C" int kv4_weigh(const kv4_cache* cache, const void* q, const int32_t* q
               mass, cfg->T, cfg->n_q_heads, cfg->n_q_heads / c.Hkv, cfg->scale * kLog2e, dev_err};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const long long rows = static_cast<long long>(cfg->max_q) * a.G;
-  // At 224 rows clusters of 1 / 2 / 4 / 8 take 194 / 158 / 166 / 245 us, at 400 110 / 96 / 93 / 111, at 2400 244 / 230 / 161 / 160.
+  // Clusters of 1 / 2 / 4 / 8 take, at 136 rows (2 sequences of 3k slots), 20 / 17 / 18 / 22 us, at 224 (16 of 8k)
+  // 116 / 120 / 153 / 235, at 320 (4 of 4k) 36 / 35 / 32 / 41, at 2400 (4 of 2k) 233 / 199 / 162 / 141.
   int cluster = 1;
   while (cluster < 8 && rows > 128 * cluster) cluster *= 2;
   if (cluster > 1) return c.D == 128 ? launch_weigh<128, 128, true>(a, 3, cluster, s) : launch_weigh<64, 128, true>(a, 4, cluster, s);
