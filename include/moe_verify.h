@@ -700,8 +700,9 @@ typedef struct {
  *   lse       [T, n_q_heads] fp32 out or NULL: log of the sum of the
  *             exponentials of the scaled scores, -inf for such a row.
  * Scores, maxima, sums and outputs are accumulated in fp32; a probability
- * times its slot's value scale is rounded to fp16 (by at most 2^-11 of it) as
- * the product's operand, the output once to bf16.  A NaN or infinity in a row of q, or in a slot that a row sees,
+ * times its slot's value scale is rounded to fp16 as the product's operand (by
+ * at most 2^-11 of it or 2^-25 of the row's largest such product, whichever is
+ * more), the output once to bf16.  A NaN or infinity in a row of q, or in a slot that a row sees,
  * makes that row NaN; in slots it does not see it has no effect.
  * Results do not depend on timing.  Needs kv4_attend_workspace() bytes (0: bad
  * arguments), 256-byte aligned, of any content, that no call running at the

@@ -7,9 +7,10 @@
 // O [128 x D] += P V with P as the TMEM operand (over S's columns) and the
 // value codes unpacked to fp16, transposed.  Both stay bare codes, their nibbles
 // being fp16 numbers already (see kv4.cuh); the scales and zeros enter per slot in
-// the softmax, in fp32.  P holds p * vs, with the tile's largest vs brought to [1, 2)
-// by a power of two 2^-E that the exponential takes back (p = 2^(t - m + E)), so that
-// no magnitude leaves fp16's range.
+// the softmax, in fp32.  P holds the probability times its slot's value scale,
+// 2^(t + log2 vs - m), with the row's running maximum m over that exponent: the
+// row's own largest product is what fp16's range lies around, whatever
+// the scales of the slots are, and of those it does not see.
 //
 // Roles: warps 0-3 softmax and output (a thread per row), warps 4-7 unpack,
 // warp 8 issues the products, warp 9 copies tiles.  The scores of a tile come in two halves of 32 slots, each with its own
@@ -46,9 +47,9 @@ struct Smem {
   Tile<D> raw[kRaw];
   alignas(16) float ks[2][kTile];
   alignas(16) float kz[2][kTile];
-  alignas(16) float vs[2][kTile];               // times 2^-E
-  alignas(16) float vz[2][kTile];               // times 2^-E
-  float e[2];                                    // the tile's E
+  alignas(16) float lv[2][kTile];               // log2 of the value scale vs
+  alignas(16) float rs[2][kTile];               // 1 / vs
+  alignas(16) float zr[2][kTile];               // vz / vs
   uint32_t raw_groups[kRaw], groups[2];
   uint64_t raw_full[kRaw], raw_empty[kRaw], kv_full[2], kv_empty[2], q_full, s_full[2], p_full[2], pv_done[2];
   long long scratch[32];
@@ -234,7 +235,6 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
           dead = true;
           break;
         }
-        const float E = sm.e[kv.i], down = ex2(-E);
         const uint32_t groups = sm.groups[kv.i];
         const bool edge = j0 + kTile > k.q.base || groups != 15u;
         uint64_t see = 0;
@@ -248,17 +248,19 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
           const uint32_t tsh = ts + h * kHalf;
           const float4* ks4 = reinterpret_cast<const float4*>(sm.ks[kv.i] + h * kHalf);
           const float4* kz4 = reinterpret_cast<const float4*>(sm.kz[kv.i] + h * kHalf);
-          const float4* vs4 = reinterpret_cast<const float4*>(sm.vs[kv.i] + h * kHalf);
-          const float4* vz4 = reinterpret_cast<const float4*>(sm.vz[kv.i] + h * kHalf);
-          const float off = E - m;
-          const float2 cq2 = make_float2(cq, cq), cqs2 = make_float2(cqs, cqs), off2 = make_float2(off, off);
+          const float4* lv4 = reinterpret_cast<const float4*>(sm.lv[kv.i] + h * kHalf);
+          const float4* rs4 = reinterpret_cast<const float4*>(sm.rs[kv.i] + h * kHalf);
+          const float4* zr4 = reinterpret_cast<const float4*>(sm.zr[kv.i] + h * kHalf);
+          const float2 cq2 = make_float2(cq, cq), cqs2 = make_float2(cqs, cqs), off2 = make_float2(-m, -m);
           float2 d[kHalf / 2];
           tmem_ld_pairs(tsh, d);
 #pragma unroll
           for (int i = 0; i < kHalf / 2; i += 2) {
-            const float4 s4 = ks4[i / 2], z4 = kz4[i / 2];
-            d[i] = fma2(make_float2(s4.x, s4.y), mul2(d[i], cq2), fma2(make_float2(z4.x, z4.y), cqs2, off2));
-            d[i + 1] = fma2(make_float2(s4.z, s4.w), mul2(d[i + 1], cq2), fma2(make_float2(z4.z, z4.w), cqs2, off2));
+            const float4 s4 = ks4[i / 2], z4 = kz4[i / 2], v4 = lv4[i / 2];
+            d[i] = fma2(make_float2(s4.x, s4.y), mul2(d[i], cq2),
+                        fma2(make_float2(z4.x, z4.y), cqs2, add2(make_float2(v4.x, v4.y), off2)));
+            d[i + 1] = fma2(make_float2(s4.z, s4.w), mul2(d[i + 1], cq2),
+                            fma2(make_float2(z4.z, z4.w), cqs2, add2(make_float2(v4.z, v4.w), off2)));
           }
           if (edge) {
             const uint32_t w = static_cast<uint32_t>(h ? see >> 32 : see);
@@ -310,20 +312,19 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
           for (int i = 0; i < 16; i += 2) {
             const float2 x = make_float2(ex2(d[i].x), ex2(d[i].y));
             const float2 y = make_float2(ex2(d[i + 1].x), ex2(d[i + 1].y));
-            const float4 zz = vz4[i / 2], sc = vs4[i / 2];
-            sum0 = add2(sum0, x);
-            sum1 = add2(sum1, y);
+            const float4 zz = zr4[i / 2], rr = rs4[i / 2];
+            sum0 = fma2(x, make_float2(rr.x, rr.y), sum0);
+            sum1 = fma2(y, make_float2(rr.z, rr.w), sum1);
             z0 = fma2(x, make_float2(zz.x, zz.y), z0);
             z1 = fma2(y, make_float2(zz.z, zz.w), z1);
-            const float2 px = mul2(x, make_float2(sc.x, sc.y)), py = mul2(y, make_float2(sc.z, sc.w));
-            p[i] = pack_h2(px.x, px.y);
-            p[i + 1] = pack_h2(py.x, py.y);
+            p[i] = pack_h2(x.x, x.y);
+            p[i + 1] = pack_h2(y.x, y.y);
           }
           tmem_st16(tsh, p);
           sum0 = add2(sum0, sum1);
           z0 = add2(z0, z1);
           z += z0.x + z0.y;
-          l = fmaf(sum0.x + sum0.y, down, l);
+          l += sum0.x + sum0.y;
           tmem_st_wait();
           tc::tc_fence_before();
           tc::mbar_arrive(&sm.p_full[h]);
@@ -421,18 +422,14 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
           const bool fa = va.x - va.x == 0.f && va.y - va.y == 0.f, fb = vb.x - vb.x == 0.f && vb.y - vb.y == 0.f;
           if (!fa || !((ok >> (2 * lane)) & 1)) va = make_float2(0.f, 0.f);
           if (!fb || !((ok >> (2 * lane + 1)) & 1)) vb = make_float2(0.f, 0.f);
-          const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(va.x, vb.x)));
-          const int E = top ? static_cast<int>(top >> 23) - 127 : -30;
-          const float f = __uint_as_float(static_cast<uint32_t>(127 - E) << 23);
+          const float sa = fmaxf(va.x, kMinScale), sb = fmaxf(vb.x, kMinScale), ra = rcp(sa), rb = rcp(sb);
           const float nan = __uint_as_float(0x7FC00000u);
           *reinterpret_cast<float2*>(&sm.ks[kv.i][2 * lane]) = make_float2(fa ? ka.x : nan, fb ? kb.x : nan);
           *reinterpret_cast<float2*>(&sm.kz[kv.i][2 * lane]) = make_float2(ka.y, kb.y);
-          *reinterpret_cast<float2*>(&sm.vs[kv.i][2 * lane]) = make_float2(va.x * f, vb.x * f);
-          *reinterpret_cast<float2*>(&sm.vz[kv.i][2 * lane]) = make_float2(va.y * f, vb.y * f);
-          if (lane == 0) {
-            sm.e[kv.i] = static_cast<float>(E);
-            sm.groups[kv.i] = groups;
-          }
+          *reinterpret_cast<float2*>(&sm.lv[kv.i][2 * lane]) = make_float2(lg2(sa), lg2(sb));
+          *reinterpret_cast<float2*>(&sm.rs[kv.i][2 * lane]) = make_float2(ra, rb);
+          *reinterpret_cast<float2*>(&sm.zr[kv.i][2 * lane]) = make_float2(va.y * ra, vb.y * rb);
+          if (lane == 0) sm.groups[kv.i] = groups;
         }
         // Keys: 16 bytes of a row (32 codes) make four 16-byte pieces.
 #pragma unroll

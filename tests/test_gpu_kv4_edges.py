@@ -1,0 +1,83 @@
+"""The 4-bit KV cache calls at the edges of their ranges: value scales far apart.
+Helpers and tolerances as in test_gpu_kv4."""
+import numpy as np
+import pytest
+
+from oracle import kv_cache as K
+from test_gpu_kv4 import MANY, bf16, dev, make_cache, mv  # noqa: F401  (mv: fixture)
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+
+def attend(mv, cache, q, new, base, max_q, scale, visible=None):  # noqa: F811
+    q_start = dev(np.concatenate([[0], np.cumsum(new)]).astype(np.int32))
+    out, lse = mv.kv4_attend(cache, bf16(q).cuda(), q_start, dev(np.asarray(base, np.int32)), max_q, scale=scale,
+                             visible=None if visible is None else dev(visible))
+    torch.cuda.synchronize()
+    return out.float().cpu().numpy().astype(np.float64), lse
+
+
+def small_products(pg, q, new, base, scale, visible=None):
+    """What fp16's smallest step adds to the oracle's bound of a row's outputs: half a step (2^-25) of the row's largest
+    probability times value scale, for each code that it sees."""
+    D, G = pg.D, q.shape[1] // pg.raw.shape[1]
+    add = np.zeros(q.shape[:2])
+    qh = bf16(q).double().numpy()
+    at = 0
+    for s, (n, b) in enumerate(zip(new, base)):
+        m = K.seen(b, n, None if visible is None else visible[at:at + n].astype(np.uint64)) & pg.valid(s, b + n)[None]
+        for h in range(pg.raw.shape[1]):
+            kc, ks, kz = pg.entries(s, h, b + n, 0)
+            vc, vs, _ = pg.entries(s, h, b + n, 1)
+            for i in range(n):
+                for g in range(h * G, (h + 1) * G):
+                    S = scale * ((kz[:, None] + ks[:, None] * kc)[m[i]] @ qh[at + i, g])
+                    p = np.exp(S - S.max())
+                    add[at + i, g] = 2.0 ** -25 * np.max(p / p.sum() * vs[m[i]]) * vc[m[i]].sum(0).max()
+        at += n
+    return add[..., None]
+
+
+# ------------------------------------------------------------------ value scales far apart
+@pytest.mark.parametrize("max_q", [1, MANY])
+@pytest.mark.parametrize("D,page,base", [(64, 64, 3000), (128, 32, 32767)])
+@pytest.mark.parametrize("ratio", [0.02, 1e-4])
+def test_a_dominant_slot_of_small_values(mv, max_q, D, page, base, ratio):  # noqa: F811
+    """Nearly all weight lies on one slot whose values are far smaller than the others' (an attention sink).  Many sequences on
+    the same pages, so that one CTA takes a long run of slots with it."""
+    rng = np.random.default_rng(D + base)
+    pg, _ = make_cache(mv, rng, [base + 1], 1, D, page)
+    q = bf16(rng.standard_normal((1, 1, D))).double().numpy()
+    scale, S = D ** -0.5, 320
+    want = np.log(999.0 * base) + 1.0  # its score, the others' being of variance 1 or so
+    pg.write(0, 5, 0, q[0] * (want / scale / np.sum(q * q)))
+    pg.write(0, 5, 1, rng.standard_normal((1, D)) * ratio)
+    cache = mv.Kv4Cache(dev(pg.raw), dev(np.repeat(pg.table, S, 0)), page, D)
+    got, lse = attend(mv, cache, np.repeat(q, S, 0), [1] * S, [base] * S, max_q, scale)
+    o, l, _, ot, lt, _ = K.attend(pg, q, [0, 1], [base], scale)
+    assert np.all(np.abs(lse.cpu().numpy() - l) <= lt)
+    off = np.abs(got - o) / (ot + small_products(pg, q, [1], [base], scale))
+    assert off.max() <= 1, off.max((1, 2)).round(2).tolist()
+
+
+@pytest.mark.parametrize("max_q", [5, MANY])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("small", [1e-3, 0.05])
+def test_a_hidden_slot_of_large_values(mv, max_q, D, page, small):  # noqa: F811
+    """New tokens whose values are in the tens of thousands, beside a context of small ones: rows that see none of
+    them are as exact as without them."""
+    rng = np.random.default_rng(D)
+    base, new = [150], [5]
+    pg, cache = make_cache(mv, rng, [155], 2, D, page, spread=small)
+    q = rng.standard_normal((5, 8, D))
+    for j in (151, 153):
+        pg.write(0, j, 1, rng.uniform(-30000, 30000, (2, D)))
+    cache.pages.copy_(torch.from_numpy(pg.raw))
+    visible = np.array([1, 2, 0b101, 0b1000, 0b10101], dtype=np.int64)  # tokens 1 and 3 see themselves
+    got, lse = attend(mv, cache, q, new, base, max_q, 1.0, visible)
+    o, l, _, ot, lt, _ = K.attend(pg, bf16(q).double().numpy(), [0, 5], base, 1.0, visible.astype(np.uint64))
+    assert np.all(np.abs(lse.cpu().numpy() - l) <= lt)
+    off = np.abs(got - o) / (ot + small_products(pg, q, new, base, 1.0, visible))
+    assert off.max() <= 1, off.max((1, 2))
