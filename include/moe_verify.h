@@ -702,8 +702,10 @@ typedef struct {
  * Scores, maxima, sums and outputs are accumulated in fp32; a probability
  * times its slot's value scale is rounded to fp16 as the product's operand (by
  * at most 2^-11 of it or 2^-25 of the row's largest such product, whichever is
- * more), the output once to bf16.  A NaN or infinity in a row of q, or in a slot that a row sees,
- * makes that row NaN; in slots it does not see it has no effect.
+ * more), the output once to bf16.  A NaN or
+ * infinity in a row of q, or in a key that a row sees, makes that row NaN, out
+ * and lse; in a value row it makes out NaN alone; in slots that a row does not
+ * see it has no effect.
  * Results do not depend on timing.  Needs kv4_attend_workspace() bytes (0: bad
  * arguments), 256-byte aligned, of any content, that no call running at the
  * same time uses. */

@@ -51,6 +51,7 @@ struct Smem {
   alignas(16) float rs[2][kTile];               // 1 / vs
   alignas(16) float zr[2][kTile];               // vz / vs
   uint32_t raw_groups[kRaw], groups[2];
+  uint2 bad[2];                                  // slots whose values are not finite: the even ones, the odd ones
   uint64_t raw_full[kRaw], raw_empty[kRaw], kv_full[2], kv_empty[2], q_full, s_full[2], p_full[2], pv_done[2];
   long long scratch[32];
   uint32_t tmem;
@@ -239,6 +240,13 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
         const bool edge = j0 + kTile > k.q.base || groups != 15u;
         uint64_t see = 0;
         if (edge) see = sees(k.q, a.visible != nullptr, bits, tok, j0) & group_mask(groups);
+        const uint2 bad = sm.bad[kv.i];
+        if (bad.x | bad.y) {
+          // Values that are not finite reach the outputs of the rows that see them, and nothing else.
+          const uint64_t sight = edge ? see : ~0ull;
+          for (int i = 0; i < 32; ++i)
+            if (((bad.x >> i) & (sight >> (2 * i)) & 1) || ((bad.y >> i) & (sight >> (2 * i + 1)) & 1)) z = __uint_as_float(0x7FC00000u);
+        }
         for (int h = 0; h < 2; ++h) {
           if (!wait_warp(&sm.s_full[h], sp)) {
             dead = true;
@@ -418,18 +426,21 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
           float2 va = __half22float2(*reinterpret_cast<const __half2*>(&pr.y));
           float2 vb = __half22float2(*reinterpret_cast<const __half2*>(&pr.w));
           // A value row that is not finite must not reach other rows through 0 * NaN: it counts as
-          // zeros, and its key makes the rows that see it NaN.
+          // zeros here, and the softmax threads add it to the rows that see it.
           const bool fa = va.x - va.x == 0.f && va.y - va.y == 0.f, fb = vb.x - vb.x == 0.f && vb.y - vb.y == 0.f;
           if (!fa || !((ok >> (2 * lane)) & 1)) va = make_float2(0.f, 0.f);
           if (!fb || !((ok >> (2 * lane + 1)) & 1)) vb = make_float2(0.f, 0.f);
           const float sa = fmaxf(va.x, kMinScale), sb = fmaxf(vb.x, kMinScale), ra = rcp(sa), rb = rcp(sb);
-          const float nan = __uint_as_float(0x7FC00000u);
-          *reinterpret_cast<float2*>(&sm.ks[kv.i][2 * lane]) = make_float2(fa ? ka.x : nan, fb ? kb.x : nan);
+          const uint2 bad = make_uint2(__ballot_sync(0xFFFFFFFFu, !fa), __ballot_sync(0xFFFFFFFFu, !fb));
+          *reinterpret_cast<float2*>(&sm.ks[kv.i][2 * lane]) = make_float2(ka.x, kb.x);
           *reinterpret_cast<float2*>(&sm.kz[kv.i][2 * lane]) = make_float2(ka.y, kb.y);
           *reinterpret_cast<float2*>(&sm.lv[kv.i][2 * lane]) = make_float2(lg2(sa), lg2(sb));
           *reinterpret_cast<float2*>(&sm.rs[kv.i][2 * lane]) = make_float2(ra, rb);
           *reinterpret_cast<float2*>(&sm.zr[kv.i][2 * lane]) = make_float2(va.y * ra, vb.y * rb);
-          if (lane == 0) sm.groups[kv.i] = groups;
+          if (lane == 0) {
+            sm.groups[kv.i] = groups;
+            sm.bad[kv.i] = bad;
+          }
         }
         // Keys: 16 bytes of a row (32 codes) make four 16-byte pieces.
 #pragma unroll

@@ -1,4 +1,4 @@
-"""The 4-bit KV cache calls at the edges of their ranges: value scales far apart.
+"""The 4-bit KV cache calls at the edges of their ranges: value scales far apart, values that are not finite.
 Helpers and tolerances as in test_gpu_kv4."""
 import numpy as np
 import pytest
@@ -81,3 +81,37 @@ def test_a_hidden_slot_of_large_values(mv, max_q, D, page, small):  # noqa: F811
     assert np.all(np.abs(lse.cpu().numpy() - l) <= lt)
     off = np.abs(got - o) / (ot + small_products(pg, q, new, base, 1.0, visible))
     assert off.max() <= 1, off.max((1, 2))
+
+
+# ------------------------------------------------------------------ values that are not finite
+@pytest.mark.parametrize("max_q", [4, 64, MANY])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 64)])
+def test_a_value_row_that_is_not_finite_spoils_outputs_alone(mv, max_q, D, page):  # noqa: F811
+    """A context slot and a tree token whose values were beyond fp16 (held as scale 0 and zero NaN): outputs of the rows that
+    see one are NaN; lse and weights go by the keys."""
+    rng = np.random.default_rng(51 + D)
+    base, new = [90, 70], [3, 4]
+    pg, cache = make_cache(mv, rng, [93, 74], 2, D, page)
+    bad = np.zeros((2, D))
+    bad[:, 3] = 1e6
+    pg.write(0, 20, 1, bad)      # seen by all of sequence 0
+    pg.write(1, 71, 1, bad)      # new token 1 of sequence 1
+    cache.pages.copy_(torch.from_numpy(pg.raw))
+    visible = np.array([1, 3, 5, 1, 3, 5, 0b1011], dtype=np.int64)
+    q = rng.standard_normal((7, 8, D))
+    qh = bf16(q).double().numpy()
+    got, lse = attend(mv, cache, q, new, base, max_q, 0.1, visible)
+    got_lse = lse.cpu().numpy().astype(np.float64)
+    with np.errstate(invalid="ignore"):
+        o, l, mass, ot, lt, mt = K.attend(pg, qh, [0, 3, 7], base, 0.1, visible.astype(np.uint64), lse_in=got_lse)
+    nan = np.isnan(o).all((1, 2))
+    assert nan.tolist() == [True, True, True, False, True, False, True]
+    assert np.isnan(got[nan]).all()
+    assert np.all(np.abs(got[~nan] - o[~nan]) <= ot[~nan])
+    assert np.all(np.abs(got_lse - l) <= lt)
+    m = cache.new_mass()
+    mv.kv4_weigh(cache, bf16(q).cuda(), dev(np.array([0, 3, 7], np.int32)), dev(np.array(base, np.int32)), max_q, lse, m,
+                 visible=dev(visible), scale=0.1)
+    m = m.cpu().numpy().astype(np.float64)
+    for (s, h), w in mass.items():
+        assert np.all(np.abs(m[s, h, :len(w)] - w) <= mt[s, h] + 2.0 ** -23 * w)
