@@ -7,12 +7,14 @@ raise ``MoEError`` on a non-OK host status.  Device-side error bits land in
 
 A small call's host time is of the order of its device time, so what does not
 change from call to call is kept: the argument structs with the cache, and one
-workspace for each stream (calls on a stream follow each other, so the caches
-of all layers share it).
+workspace for each stream and host thread.  A thread's calls on a stream follow
+each other, so the caches of all layers share it; another thread's may come
+between the two launches of a kv4_attend.
 """
 from __future__ import annotations
 
 import ctypes as C
+import threading
 from typing import Optional, Tuple
 
 import torch
@@ -24,16 +26,28 @@ _DTYPES = {torch.float32: L.DTYPE_F32, torch.bfloat16: L.DTYPE_BF16}
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-_workspaces = {}  # (device, stream) -> the largest workspace that a call there has needed
+_STREAMS_KEPT = 16
+
+
+class _Workspaces(threading.local):
+    def __init__(self):
+        self.held = {}  # (device, stream) -> the largest workspace that this thread's calls there have needed
+
+
+_workspaces = _Workspaces()
 
 
 def _workspace(index: int, nbytes: int, stream: int) -> torch.Tensor:
     # A graph's calls must not share a workspace with calls that may run beside its replays.
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
-    w = _workspaces.get((index, stream))
+    held = _workspaces.held
+    w = held.get((index, stream))
     if w is None or w.numel() < nbytes:
-        w = _workspaces[index, stream] = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+        # (What is dropped goes back to the allocator's blocks of its own stream, behind the calls that use it.)
+        if w is None and len(held) >= _STREAMS_KEPT:
+            del held[next(iter(held))]
+        w = held[index, stream] = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
     return w
 
 

@@ -1,4 +1,5 @@
-"""The 4-bit KV cache calls at the edges of their ranges: value scales far apart, values that are not finite.
+"""The 4-bit KV cache calls at the edges of their ranges: value scales far apart, values that are not finite, several threads and
+streams at once.
 Helpers and tolerances as in test_gpu_kv4."""
 import numpy as np
 import pytest
@@ -115,3 +116,72 @@ def test_a_value_row_that_is_not_finite_spoils_outputs_alone(mv, max_q, D, page)
     m = m.cpu().numpy().astype(np.float64)
     for (s, h), w in mass.items():
         assert np.all(np.abs(m[s, h, :len(w)] - w) <= mt[s, h] + 2.0 ** -23 * w)
+
+
+# ------------------------------------------------------------------ the binding's workspaces
+def cut_calls(mv, rng):  # noqa: F811
+    """Calls of different shapes whose items are cut between CTAs: (cache, arguments of kv4_attend)."""
+    calls = []
+    for Hkv, D, base, new, max_q in ((2, 128, 5000, 1, 1), (1, 64, 9000, 3, MANY), (4, 64, 3000, 2, 2), (1, 128, 4000, 4, MANY)):
+        _, cache = make_cache(mv, rng, [base + new], Hkv, D, 64)
+        q = bf16(rng.standard_normal((new, 8, D))).cuda()
+        calls.append((cache, (q, dev(np.array([0, new], np.int32)), dev(np.array([base], np.int32)), max_q)))
+    return calls
+
+
+def test_two_threads_on_one_stream(mv):  # noqa: F811
+    import threading
+    calls = cut_calls(mv, np.random.default_rng(81))
+    want = [mv.kv4_attend(c, *a) for c, a in calls]
+    torch.cuda.synchronize()
+    off, start = [], threading.Barrier(2)
+
+    def work(first):
+        start.wait()
+        got = []
+        for i in range(400):
+            n = (first + i) % len(calls)
+            got.append((n, mv.kv4_attend(calls[n][0], *calls[n][1])))
+        torch.cuda.synchronize()
+        off.extend(n for n, (o, l) in got if not (torch.equal(o, want[n][0]) and torch.equal(l, want[n][1])))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not off
+
+
+def test_two_streams_at_once(mv):  # noqa: F811
+    calls = cut_calls(mv, np.random.default_rng(82))
+    want = [mv.kv4_attend(c, *a) for c, a in calls]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(200):
+        n = i % len(calls)
+        got.append((n, mv.kv4_attend(calls[n][0], *calls[n][1], stream=streams[i % 3])))
+    torch.cuda.synchronize()
+    for n, (o, l) in got:
+        assert torch.equal(o, want[n][0]) and torch.equal(l, want[n][1])
+
+
+def test_a_graph_has_workspaces_of_its_own(mv):  # noqa: F811
+    """Captured calls with the binding's workspace: replays beside other calls on the stream that they were captured from."""
+    calls = cut_calls(mv, np.random.default_rng(83))
+    want = [mv.kv4_attend(c, *a) for c, a in calls]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = [mv.kv4_attend(c, *a) for c, a in calls]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        with torch.cuda.stream(side):
+            g.replay()
+        beside = [mv.kv4_attend(c, *a) for c, a in calls]
+    torch.cuda.synchronize()
+    for x in (got, beside):
+        for (o, l), w in zip(x, want):
+            assert torch.equal(o, w[0]) and torch.equal(l, w[1])
