@@ -138,3 +138,75 @@ def test_workspaces_are_kept_for_a_few_streams_only(machine, monkeypatch):
         seen.append(machine.lib.calls[-1][2][8])
     assert seen[-1] == seen[-2] == seen[-3] and len(set(seen)) == 100
     assert len(kv4._workspaces.held) <= 16
+
+
+# ------------------------------------------------------------------ devices
+def rows(index, heads=2):
+    return Tensor((3, heads, 128), torch.bfloat16, index)
+
+
+def i32(n, index):
+    return Tensor((n,), torch.int32, index)
+
+
+def f32(shape, index):
+    return Tensor(shape, torch.float32, index)
+
+
+def calls(c, index, at=None, other=None, **kw):
+    """Every call on cache c with tensors of device `index`; those named in `at` on device `other` instead."""
+    d = lambda name: other if at == name else index  # noqa: E731
+    q = lambda: (Tensor((3, 8, 128), torch.bfloat16, d("q")), i32(3, d("q_start")), i32(2, d("base")), 2)  # noqa: E731
+    vis = lambda: Tensor((3,), torch.int64, d("visible"))  # noqa: E731
+    err, mass = i32(1, d("dev_err")), f32((2, 2, 256), d("mass"))
+    return {
+        "kv4_append": lambda: kv4.kv4_append(c, rows(d("k")), rows(d("v")), i32(3, d("seq")), i32(3, d("slot")), held=True, dev_err=err, **kw),
+        "kv4_read": lambda: kv4.kv4_read(c, i32(3, d("seq")), i32(3, d("slot")), dev_err=err, **kw),
+        "kv4_attend": lambda: kv4.kv4_attend(c, *q(), visible=vis(), out=Tensor((3, 8, 128), torch.bfloat16, d("out")),
+                                             lse=f32((3, 8), d("lse")), workspace=Tensor((4096,), torch.uint8, d("workspace")), dev_err=err, **kw),
+        "kv4_weigh": lambda: kv4.kv4_weigh(c, *q(), f32((3, 8), d("lse")), mass, visible=vis(), dev_err=err, **kw),
+        "kv4_evict": lambda: kv4.kv4_evict(c, mass, i32(2, d("lens")), 4, 1, mass_out=f32((2, 2, 256), d("mass_out")), dev_err=err, **kw),
+    }
+
+
+NAMED = {"kv4_append": ["k", "v", "seq", "slot", "dev_err"], "kv4_read": ["seq", "slot", "dev_err"],
+         "kv4_attend": ["q", "q_start", "base", "visible", "out", "lse", "workspace", "dev_err"],
+         "kv4_weigh": ["q", "q_start", "base", "visible", "lse", "mass", "dev_err"], "kv4_evict": ["mass", "lens", "mass_out", "dev_err"]}
+
+
+class Stream:
+    def __init__(self, index):
+        self.device_index, self.device = index, torch.device("cuda", index)
+
+
+@pytest.mark.parametrize("name", sorted(NAMED))
+def test_calls_run_on_the_device_of_the_cache(machine, name):
+    for index, current, kw in ((0, 0, {}), (1, 0, {}), (0, 1, {}), (1, 0, dict(stream=Stream(1))), (1, 1, dict(stream=Stream(1)))):
+        with machine.on(current):
+            calls(cache_on(index), index, **kw)[name]()
+            assert machine.current() == current
+        got, on, args = machine.lib.calls[-1]
+        assert (got, on, args[-1]) == (name, index, 16 * index)
+    c = cache_on(1)
+    need = []
+    machine.lib.kv4_attend_workspace = lambda *a: need.append(machine.current()) or 4096
+    kv4.kv4_attend_workspace_bytes(c, Tensor((3, 8, 128), torch.bfloat16, 1), 2)
+    assert need == [1]
+
+
+@pytest.mark.parametrize("name,at", [(n, a) for n in sorted(NAMED) for a in NAMED[n]])
+def test_tensors_of_another_device_are_refused(machine, name, at):
+    c = cache_on(1)
+    calls(c, 1)[name]()  # a call of this shape has been made before
+    n = len(machine.lib.calls)
+    for other in (0, -1):
+        with pytest.raises(MoEError):
+            calls(c, 1, at, other)[name]()
+    assert len(machine.lib.calls) == n
+
+
+@pytest.mark.parametrize("name", sorted(NAMED))
+def test_streams_of_another_device_are_refused(machine, name):
+    with pytest.raises(MoEError):
+        calls(cache_on(1), 1, stream=Stream(0))[name]()
+    assert not machine.lib.calls
