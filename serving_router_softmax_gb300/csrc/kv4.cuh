@@ -21,9 +21,8 @@
 
 #include <cuda_fp16.h>
 
-#include <atomic>
-
 #include "common.cuh"
+#include "smem_limit.cuh"
 #include "tc_ptx.cuh"
 
 namespace moe {
@@ -45,19 +44,6 @@ struct Cache {
   int32_t n_pages, page_size, page_log2, Hkv, D, S, width;
   __host__ __device__ size_t block_bytes() const { return static_cast<size_t>(page_size) * (D + 8); }
 };
-
-// Lets kernel K use `bytes` of dynamic shared memory; asks the driver once per device and size.
-template <auto K>
-int allow_smem(size_t bytes) {
-  static std::atomic<size_t> allowed[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
-  if (dev >= 0 && dev < 64 && allowed[dev].load(std::memory_order_relaxed) >= bytes) return MOE_OK;
-  if (cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  if (dev >= 0 && dev < 64) allowed[dev].store(bytes, std::memory_order_relaxed);
-  return MOE_OK;
-}
 
 // Launches `clusters` clusters of `size` CTAs.
 template <typename... KArgs, typename... Args>
