@@ -776,10 +776,13 @@ uint64_t moe_launch_count(void);
  *                              the launch reports MOE_DEV_TIMEOUT;
  *   MOE_TEST_STALL_READY_FLAG  the step's layer heads do not publish the
  *                              union, so gate/up takes its slower fallback
- *                              (results unchanged).
+ *                              (results unchanged);
+ *   MOE_TEST_STALL_KV4_ATTEND  kv4_attend does not copy the last tile of each
+ *                              CTA's share, so the wait for it runs out and the
+ *                              call reports MOE_DEV_TIMEOUT.
  * Process-wide; read by the host at each launch.  Returns MOE_ERR_ARG for
  * unknown bits. */
-enum { MOE_TEST_STALL_GATE_UP = 1, MOE_TEST_STALL_READY_FLAG = 2 };
+enum { MOE_TEST_STALL_GATE_UP = 1, MOE_TEST_STALL_READY_FLAG = 2, MOE_TEST_STALL_KV4_ATTEND = 4 };
 int moe_test_set_stall(int32_t mask);
 
 /* Trace ranges for a timeline tool (NVTX; the pages have no counterpart).

@@ -86,7 +86,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Atte
     bool dead = false;
     for (long long u = u0; u < u1 && !dead;) {
       const Span sp = span_of<kRows>(a, k, u, u1);
-      for (int it = 0; it < sp.tiles; ++it) {
+      const int tiles = copied_tiles(a, sp, u + sp.n == u1);
+      for (int it = 0; it < tiles; ++it) {
         if (__any_sync(0xFFFFFFFFu, !tc::mbar_wait_bounded(&sm.empty[stage], phase ^ 1, abort_flag, kWaitBudgetNs))) {
           *abort_flag = 1;
           dead = true;
@@ -100,6 +101,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Atte
       u += sp.n;
       if (u < u1) cursor_next(k, a.c, a.q_start, a.base, a.T, a.G, kRows, kTile, kItemUnits, sm.cum);
     }
+    // A consumer may give up long after the last copy has been started, so this warp stays until they are done.
+    tc::named_bar_sync(2, kThreads);
     if (*abort_flag) {
       // Copies in flight land before the CTA's shared memory goes.
       for (int i = 0; i < issued; ++i) {
@@ -365,6 +368,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Atte
     u += sp.n;
     if (u < u1) cursor_next(k, a.c, a.q_start, a.base, a.T, a.G, kRows, kTile, kItemUnits, sm.cum);
   }
+  tc::named_bar_sync(2, kThreads);  // (the producer waits for it)
 }
 
 // Whether blocks of 128 rows on the tcgen05 kernel take less time than blocks of
@@ -452,10 +456,11 @@ extern "C" int kv4_attend(const kv4_cache* cache, const void* q, const int32_t* 
   const size_t need = kv4_attend_workspace(cache, cfg);
   if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)) return MOE_ERR_WORKSPACE;
   const Plan p = plan_of(*cfg, c);
+  const bool withhold = (test_stall_mask() & MOE_TEST_STALL_KV4_ATTEND) != 0;
   AttendArgs a{c, static_cast<const uint16_t*>(q), cfg->q_token_stride, cfg->q_head_stride, q_start, base, visible,
                static_cast<uint16_t*>(out), lse, cfg->T, cfg->n_q_heads, cfg->n_q_heads / c.Hkv, cfg->scale * kLog2e,
                static_cast<float*>(workspace),
-               reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + part_bytes(p, c)), dev_err};
+               reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + part_bytes(p, c)), dev_err, withhold};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (p.rb == kWideRows) return wide_launch(a, p.grid, s);
   return c.D == 128 ? launch_attend<128>(a, p, s) : launch_attend<64>(a, p, s);

@@ -25,6 +25,7 @@ struct AttendArgs {
   float* part;     // [CTAs][2] partial sums of row blocks, see part_floats
   int32_t* meta;   // [CTAs][8]: a cut item that starts in this CTA
   int32_t* dev_err;
+  bool withhold;   // test hook: each CTA's last tile is not copied, so that the wait for it runs out
 };
 
 // One row block's partial sums: outputs [RB][D] (the wide kernel: [D][RB], columns as they lie in TMEM), running
@@ -167,6 +168,11 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, const Cursor& k, lo
   s.first = k.tile == 0;
   s.whole = s.first && s.tiles == s.need;
   return s;
+}
+
+// Tiles of a span to copy; the test hook keeps back the last one of the CTA's last span (`last`).
+__device__ __forceinline__ int copied_tiles(const AttendArgs& a, const Span& s, bool last) {
+  return s.tiles - (a.withhold && last && s.tiles > 0 ? 1 : 0);
 }
 
 // Notes an item that starts in this CTA and ends in a later one; u is the item's first unit.
