@@ -718,8 +718,8 @@ int kv4_attend(const kv4_cache* cache, const void* q, const int32_t* q_start, co
  *   mass[s, h, j] += sum over the new tokens i of s and the query heads of kv
  *   head h of exp(scale * q . k_j - lse), over the slots j that i sees.
  * Arguments as kv4_attend (of whose call lse is the result; rows with lse
- * -inf see no new slot, whatever it holds, and add nothing); mass [n_seq, n_kv_heads, max_pages * page_size] fp32 in
- * and out.  Slots beyond a sequence's are not touched.  Sums in fp32 in a
+ * -inf add nothing, whatever they and the slots hold); mass
+ * [n_seq, n_kv_heads, max_pages * page_size] fp32 in and out.  Slots beyond a sequence's are not touched.  Sums in fp32 in a
  * fixed order. */
 int kv4_weigh(const kv4_cache* cache, const void* q, const int32_t* q_start, const int32_t* base,
               const uint64_t* visible, const float* lse, const kv4_attn_cfg* cfg, float* mass,

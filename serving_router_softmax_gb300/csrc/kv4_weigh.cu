@@ -45,6 +45,7 @@ constexpr int kStages = 3;           // key rows on their way
 // What beginning an item costs, in units: a CTA with two units whose second begins another item took the longest (4 trees
 // on up to 4000 slots 16.4 us with 0, 12.5 with 1, 14.3 with 2; 16 on up to 16k 50.4, 49.6, 48.5).
 constexpr int kItemUnits = 1;
+constexpr int kNoToken = -(1 << 30) - 1;  // of a row that has seen nothing: below every slot's distance from the new ones
 constexpr int kGroup = 8;            // units whose sums wait in shared memory where rows come in several blocks
 constexpr uint32_t kTmemCols = 128;
 constexpr uint64_t kWaitBudgetNs = 2000000000ull;  // 2 s
@@ -86,8 +87,9 @@ struct Smem {
 // Rows row0 .. of the item's queries into shared memory as the product's
 // second operand, in the order of the key words' pairs (see prep_q of kv4.cuh).
 // A thread a row finds its place, lse and mask; W lanes a row convert it.
+// Returns whether the thread's row has seen nothing (an lse of -inf).
 template <int D, int kRows>
-__device__ __forceinline__ void load_queries(const WeighArgs& a, const Cursor& k, int row0, int rows, Smem<D, kRows>& sm) {
+__device__ __forceinline__ bool load_queries(const WeighArgs& a, const Cursor& k, int row0, int rows, Smem<D, kRows>& sm) {
   constexpr int W = D / 8;  // a row's code words, one a lane
   const int padded = (rows + 15) & ~15;
   const int mine = threadIdx.x, tok = (row0 + min(mine, rows - 1)) / a.G;
@@ -157,12 +159,13 @@ __device__ __forceinline__ void load_queries(const WeighArgs& a, const Cursor& k
     }
   }
   if (mine < padded) {
-    const bool none = lse == -INFINITY;  // a row that saw nothing sees no new slot, whatever those hold
+    const bool none = lse == -INFINITY;  // a row that saw nothing sees no slot, whatever those hold
     sm.nl[mine] = none ? -INFINITY : -lse * kLog2e;
-    sm.token[mine] = none ? -1 : tok;
+    sm.token[mine] = none ? kNoToken : tok;
     sm.mask[mine] = none ? 0 : mask;
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  return mine < rows && lse == -INFINITY;
 }
 
 // kShared: the CTAs of a cluster take the same units, each with its share of the query rows.
@@ -208,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
   uint32_t phase = 0;
   uint32_t parity = 0;
   bool dead = false;
+  int told = 0;  // first slot that not all rows held see: the context's end, or 0 where a row has seen nothing
   Cursor k;
   if (u0 < u1) cursor_at(k, a.c, a.q_start, a.base, a.T, a.G, kAllRows, kSlots, kItemUnits, sm.cum, u0);
   for (long long u = u0; u < u1 && (kShared || !dead);) {  // (to its end in any case: a cluster's CTAs meet in it)
@@ -259,8 +263,10 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
           look(i + 1);
         }
         __syncthreads();  // the rows before have been read
-        if (!kShared || g0 == 0 || blocks > 1) load_queries<D, kRows>(a, k, row0, rows, sm);
-        __syncthreads();
+        if (!kShared || g0 == 0 || blocks > 1)
+          told = __syncthreads_or(load_queries<D, kRows>(a, k, row0, rows, sm)) ? 0 : k.q.base;
+        else
+          __syncthreads();
         const bool last = !kShared && block == blocks - 1;
         // The mass of this unit's slot, loaded one unit ahead.
         auto mass_of = [&](int i) {
@@ -334,10 +340,11 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
                                 fma2(kz, make_float2(z.z, z.w), make_float2(l.z, l.w)));
                 t = make_float2(ex2(t.x), ex2(t.y));
                 y = make_float2(ex2(y.x), ex2(y.y));
-                if (j0 + kSlots > k.q.base && j >= k.q.base) {
+                if (j0 + kSlots > told && j >= told) {
                   const int d = j - k.q.base, r = c0 + c + 4 * x;
                   auto see = [&](int e) {
-                    return a.visible ? d < kMaxTree && ((sm.mask[r + e] >> d) & 1) : d <= sm.token[r + e];
+                    if (!a.visible || d < 0) return d <= sm.token[r + e];
+                    return d < kMaxTree && ((sm.mask[r + e] >> d) & 1);
                   };
                   t.x = see(0) ? t.x : 0.f;
                   t.y = see(1) ? t.y : 0.f;

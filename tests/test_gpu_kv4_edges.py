@@ -1,11 +1,11 @@
 """The 4-bit KV cache calls at the edges of their ranges: value scales far apart, values that are not finite, several threads and
-streams at once.
+streams at once, rows left out of the weights.
 Helpers and tolerances as in test_gpu_kv4."""
 import numpy as np
 import pytest
 
 from oracle import kv_cache as K
-from test_gpu_kv4 import MANY, bf16, dev, make_cache, mv  # noqa: F401  (mv: fixture)
+from test_gpu_kv4 import MANY, bf16, dev, make_cache, make_tree, mv  # noqa: F401  (mv: fixture)
 
 torch = pytest.importorskip("torch")
 
@@ -185,3 +185,35 @@ def test_a_graph_has_workspaces_of_its_own(mv):  # noqa: F811
     for x in (got, beside):
         for (o, l), w in zip(x, want):
             assert torch.equal(o, w[0]) and torch.equal(l, w[1])
+
+
+# ------------------------------------------------------------------ rows left out of the weights
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("Hq,D,page,new,max_q", [(8, 64, 16, 5, 5), (8, 128, 64, 5, 5), (32, 128, 64, 5, 5), (16, 64, 32, 60, 60), (8, 128, 16, 5, MANY)])
+def test_rows_without_a_sum_add_no_weight(mv, tree, Hq, D, page, new, max_q):  # noqa: F811
+    """Rows whose lse is -inf add nothing whatever they hold, NaN and infinities in q, and whatever the slots hold."""
+    rng = np.random.default_rng(61 + Hq + D)
+    base, none = 200, [1, new - 1]
+    pg, cache = make_cache(mv, rng, [base + new], 2, D, page)
+    q = rng.standard_normal((new, Hq, D))
+    visible = make_tree(rng, new) if tree else None
+    _, lse = attend(mv, cache, q, [new], [base], max_q, 0.1, visible)
+    lse[none] = float("-inf")
+    clean = q.copy()
+    clean[none] = 0.0
+    q[1, :, 7], q[new - 1, :, 9] = np.nan, np.inf
+    q_start, b = dev(np.array([0, new], np.int32)), dev(np.array([base], np.int32))
+    vis = None if visible is None else dev(visible)
+    got, want = cache.new_mass(), cache.new_mass()
+    mv.kv4_weigh(cache, bf16(q).cuda(), q_start, b, max_q, lse, got, visible=vis, scale=0.1)
+    mv.kv4_weigh(cache, bf16(clean).cuda(), q_start, b, max_q, lse, want, visible=vis, scale=0.1)
+    assert torch.equal(got, want) and bool(torch.isfinite(got).all())
+    assert np.allclose(got.sum(2).cpu().numpy(), Hq // 2 * (new - 2), rtol=1e-3)  # a row's weights add up to 1
+    # No row has a sum: keys that are not finite, of the context and of new tokens, reach nothing either.
+    for j in (3, base, base + new - 1):
+        pg.par[pg.table[0][j // page], :, j % page, :2] = np.float16("nan")
+    cache.pages.copy_(torch.from_numpy(pg.raw))
+    held = torch.rand_like(got)
+    got = held.clone()
+    mv.kv4_weigh(cache, bf16(q).cuda(), q_start, b, max_q, torch.full_like(lse, float("-inf")), got, visible=vis, scale=0.1)
+    assert torch.equal(got, held)
