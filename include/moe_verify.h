@@ -704,8 +704,9 @@ typedef struct {
  * at most 2^-11 of it or 2^-25 of the row's largest such product, whichever is
  * more), the output once to bf16.  A NaN or
  * infinity in a row of q, or in a key that a row sees, makes that row NaN, out
- * and lse; in a value row it makes out NaN alone; in slots that a row does not
- * see it has no effect.
+ * and lse (but scores that come out as -inf for every slot make it a row that
+ * sees nothing); in a value row it makes out NaN alone; in slots that a row
+ * does not see it has no effect.
  * Results do not depend on timing.  Needs kv4_attend_workspace() bytes (0: bad
  * arguments), 256-byte aligned, of any content, that no call running at the
  * same time uses. */

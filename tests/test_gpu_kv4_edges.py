@@ -217,3 +217,24 @@ def test_rows_without_a_sum_add_no_weight(mv, tree, Hq, D, page, new, max_q):  #
     got = held.clone()
     mv.kv4_weigh(cache, bf16(q).cuda(), q_start, b, max_q, torch.full_like(lse, float("-inf")), got, visible=vis, scale=0.1)
     assert torch.equal(got, held)
+
+
+# ------------------------------------------------------------------ infinities in q
+@pytest.mark.parametrize("max_q", [1, 64, MANY])
+def test_an_infinity_in_q_gives_nan_or_an_empty_row(mv, max_q):  # noqa: F811
+    """Scores that are -inf for every slot make a row of zeros with lse -inf; a score of +inf or NaN among them makes the row NaN."""
+    rng = np.random.default_rng(65)
+    pg, cache = make_cache(mv, rng, [40], 1, 64, 16)
+    for j in range(40):
+        k = rng.uniform(1.0, 2.0, (1, 64))
+        k[0, 5], k[0, 6] = 3.0, 1.0  # the largest code, the smallest
+        pg.write(0, j, 0, k)
+    cache.pages.copy_(torch.from_numpy(pg.raw))
+    q = rng.standard_normal((1, 4, 64))
+    q[0, 0, 5], q[0, 1, 5], q[0, 2, 6] = -np.inf, np.inf, -np.inf  # -inf; +inf; infinity times code 0
+    got, lse = attend(mv, cache, q, [1], [39], max_q, 0.125)
+    lse = lse.cpu().numpy()
+    assert not got[0, 0].any() and np.isneginf(lse[0, 0])
+    assert np.isnan(got[0, 1:3]).all() and np.isnan(lse[0, 1:3]).all()
+    o, l, _, ot, lt, _ = K.attend(pg, bf16(np.nan_to_num(q, posinf=0, neginf=0)).double().numpy(), [0, 1], [39], 0.125)
+    assert np.all(np.abs(got[0, 3] - o[0, 3]) <= ot[0, 3]) and abs(lse[0, 3] - l[0, 3]) <= lt[0, 3]
