@@ -652,7 +652,8 @@ typedef struct {
 
 /* Rows of T tokens x n_kv_heads: dtype MOE_DTYPE_BF16 or MOE_DTYPE_F32;
  * strides in elements (of kv4_append's k and v; multiples of 16 bytes, the D
- * values of a row side by side). */
+ * values of a row side by side; the token stride of one token and the head
+ * stride of one head are not used). */
 typedef struct {
   int32_t T, dtype;
   int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
@@ -682,7 +683,7 @@ typedef struct {
   int32_t n_q_heads;    /* a multiple of n_kv_heads: head h reads kv head h / (n_q / n_kv)      */
   int32_t max_q;        /* most new tokens of a sequence: chooses the kernel, not the results   */
   float scale;          /* factor of q . k (finite)                                             */
-  int64_t q_token_stride, q_head_stride; /* in elements, multiples of 8                         */
+  int64_t q_token_stride, q_head_stride; /* in elements, multiples of 8 (not used for one token, one head) */
 } kv4_attn_cfg;
 
 /* kv4_attend -- softmax attention of the new tokens over the cache.

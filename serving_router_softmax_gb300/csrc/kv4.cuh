@@ -65,6 +65,9 @@ int launch_clusters(void (*kernel)(KArgs...), int clusters, int size, int thread
 
 int cache_validate(const kv4_cache* c, Cache* out);
 
+// A stride over n tokens or heads (of one: never used, so anything goes).
+inline bool stride_ok(long long stride, int n, int multiple) { return n <= 1 || (stride >= 0 && stride % multiple == 0); }
+
 // Block of (page id, head).
 __device__ __forceinline__ uint8_t* page_block(const Cache& c, int page, int h) {
   return c.pages + (static_cast<size_t>(page) * c.Hkv + h) * c.block_bytes();

@@ -422,7 +422,7 @@ int attn_validate(const kv4_attn_cfg* cfg, const Cache& c) {
   if (cfg->n_q_heads % c.Hkv) return MOE_ERR_ARG;
   if (!(cfg->scale == cfg->scale) || cfg->scale - cfg->scale != 0.f) return MOE_ERR_ARG;
   if (cfg->n_q_heads > 4096 || static_cast<long long>(cfg->T) * cfg->n_q_heads > (1ll << 30)) return MOE_ERR_UNSUPPORTED;
-  if (cfg->q_token_stride < 0 || cfg->q_head_stride < 0 || cfg->q_token_stride % 8 || cfg->q_head_stride % 8)
+  if (!stride_ok(cfg->q_token_stride, cfg->T, 8) || !stride_ok(cfg->q_head_stride, cfg->n_q_heads, 8))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

@@ -348,8 +348,9 @@ extern "C" int kv4_append(const kv4_cache* cache, const void* k, const void* v, 
   if (misaligned(k, 16) || misaligned(v, 16) || misaligned(k_held, 16) || misaligned(v_held, 16) ||
       misaligned(seq, 4) || misaligned(slot, 4))
     return MOE_ERR_ARG;
-  for (long long x : {cfg->k_token_stride, cfg->k_head_stride, cfg->v_token_stride, cfg->v_head_stride})
-    if (x < 0 || x % per) return MOE_ERR_UNSUPPORTED;
+  if (!stride_ok(cfg->k_token_stride, cfg->T, per) || !stride_ok(cfg->v_token_stride, cfg->T, per) ||
+      !stride_ok(cfg->k_head_stride, c.Hkv, per) || !stride_ok(cfg->v_head_stride, c.Hkv, per))
+    return MOE_ERR_UNSUPPORTED;
   IoArgs a{c, {k, v}, {cfg->k_token_stride, cfg->v_token_stride}, {cfg->k_head_stride, cfg->v_head_stride},
            seq, slot, cfg->T, 0, {k_held, v_held}, dev_err};
   return launch_io<true>(a, cfg->dtype == MOE_DTYPE_F32, static_cast<cudaStream_t>(stream));

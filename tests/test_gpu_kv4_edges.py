@@ -1,5 +1,5 @@
 """The 4-bit KV cache calls at the edges of their ranges: value scales far apart, values that are not finite, several threads and
-streams at once, rows left out of the weights.
+streams at once, rows left out of the weights, strides that nothing is reached by.
 Helpers and tolerances as in test_gpu_kv4."""
 import numpy as np
 import pytest
@@ -238,3 +238,30 @@ def test_an_infinity_in_q_gives_nan_or_an_empty_row(mv, max_q):  # noqa: F811
     assert np.isnan(got[0, 1:3]).all() and np.isnan(lse[0, 1:3]).all()
     o, l, _, ot, lt, _ = K.attend(pg, bf16(np.nan_to_num(q, posinf=0, neginf=0)).double().numpy(), [0, 1], [39], 0.125)
     assert np.all(np.abs(got[0, 3] - o[0, 3]) <= ot[0, 3]) and abs(lse[0, 3] - l[0, 3]) <= lt[0, 3]
+
+
+# ------------------------------------------------------------------ strides that no element is reached by
+def test_strides_of_a_lone_token_and_a_lone_head_are_free(mv):  # noqa: F811
+    rng = np.random.default_rng(71)
+    D, page = 64, 16
+    pg, cache = make_cache(mv, rng, [20], 1, D, page)
+    lone = lambda x, strides: torch.as_strided(x, (1, 1, D), strides)  # noqa: E731
+    k = torch.from_numpy(rng.standard_normal((1, 1, D)).astype(np.float32)).cuda()
+    i32 = lambda *a: dev(np.array(a, np.int32))  # noqa: E731
+    for t in (k, k.to(torch.bfloat16)):
+        want = mv.kv4_append(cache, t, t, i32(0), i32(7), held=True)
+        got = mv.kv4_append(cache, lone(t, (67, 1, 1)), lone(t, (1, 3, 1)), i32(0), i32(7), held=True)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    three = torch.from_numpy(rng.standard_normal((3, 1, D)).astype(np.float32)).cuda()
+    got = mv.kv4_append(cache, torch.as_strided(three, (3, 1, D), (D, 5, 1)), three, i32(0, 0, 0), i32(1, 2, 3), held=True)
+    assert torch.equal(got[0], got[1])
+    q = bf16(rng.standard_normal((1, 1, D))).cuda()
+    want = mv.kv4_attend(cache, q, i32(0, 1), i32(19), 1)
+    got = mv.kv4_attend(cache, lone(q, (3, 7, 1)), i32(0, 1), i32(19), 1)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    a, b = cache.new_mass(), cache.new_mass()
+    mv.kv4_weigh(cache, q, i32(0, 1), i32(19), 1, want[1], a)
+    mv.kv4_weigh(cache, lone(q, (3, 7, 1)), i32(0, 1), i32(19), 1, want[1], b)
+    assert torch.equal(a, b) and float(a.sum()) > 0.99
+    with pytest.raises(mv.MoEError):  # two heads: their stride counts
+        mv.kv4_attend(cache, torch.as_strided(bf16(rng.standard_normal((1, 3, D))).cuda(), (1, 2, D), (2 * D, 67, 1)), i32(0, 1), i32(19), 1)

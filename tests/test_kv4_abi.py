@@ -100,6 +100,14 @@ def test_attention_refuses_bad_shapes(lib, kw, want):
     assert lib.kv4_weigh(c, FAKE, FAKE, FAKE, None, FAKE, a, FAKE, None, None) == want
 
 
+def test_strides_of_a_lone_token_or_head_are_not_looked_at(lib):
+    c = C.byref(cache(n_kv_heads=1))
+    assert lib.kv4_attend_workspace(c, C.byref(attn(T=1, q_token_stride=-3))) > 0
+    assert lib.kv4_attend_workspace(c, C.byref(attn(n_q_heads=1, q_head_stride=7))) > 0
+    assert lib.kv4_attend_workspace(c, C.byref(attn(T=2, q_token_stride=7))) == 0
+    assert lib.kv4_attend_workspace(c, C.byref(attn(n_q_heads=2, q_head_stride=7))) == 0
+
+
 def test_attention_refuses_bad_pointers_and_workspaces(lib):
     c, a = C.byref(cache()), C.byref(attn())
     need = lib.kv4_attend_workspace(c, a)
