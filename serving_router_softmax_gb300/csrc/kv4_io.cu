@@ -26,7 +26,7 @@ int cache_validate(const kv4_cache* c, Cache* out) {
   if ((1 << lg) != c->page_size) return MOE_ERR_UNSUPPORTED;
   if (c->n_kv_heads > 1024 || c->n_seq > kMaxSeq) return MOE_ERR_UNSUPPORTED;
   if (static_cast<long long>(c->max_pages) * c->page_size > (1ll << 30)) return MOE_ERR_UNSUPPORTED;
-  if (!c->table || (c->n_pages > 0 && !c->pages)) return MOE_ERR_ARG;
+  if ((c->n_seq > 0 && !c->table) || (c->n_pages > 0 && !c->pages)) return MOE_ERR_ARG;
   if ((reinterpret_cast<uintptr_t>(c->pages) & 15) || (reinterpret_cast<uintptr_t>(c->table) & 3)) return MOE_ERR_ARG;
   *out = Cache{static_cast<uint8_t*>(c->pages), c->table, c->n_pages, c->page_size, lg,
                c->n_kv_heads, c->head_dim, c->n_seq, c->max_pages};

@@ -265,3 +265,19 @@ def test_strides_of_a_lone_token_and_a_lone_head_are_free(mv):  # noqa: F811
     assert torch.equal(a, b) and float(a.sum()) > 0.99
     with pytest.raises(mv.MoEError):  # two heads: their stride counts
         mv.kv4_attend(cache, torch.as_strided(bf16(rng.standard_normal((1, 3, D))).cuda(), (1, 2, D), (2 * D, 67, 1)), i32(0, 1), i32(19), 1)
+
+
+# ------------------------------------------------------------------ nothing in the cache
+def test_a_cache_without_sequences(mv):  # noqa: F811
+    cache = mv.Kv4Cache.new(0, 2, 16, 64, 0, 4)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    new_len, origin, mass = mv.kv4_evict(cache, cache.new_mass(), i32(), 4, 1)
+    assert new_len.shape == (0,) and origin.shape == (0, 2, 4) and mass.shape == (0, 2, 64)
+    q = torch.empty((0, 4, 64), dtype=torch.bfloat16, device="cuda")
+    out, lse = mv.kv4_attend(cache, q, i32(0), i32(), 1)
+    assert out.shape == (0, 4, 64) and mv.kv4_weigh(cache, q, i32(0), i32(), 1, lse, mass) is mass
+    err = mv.new_dev_err()
+    x = torch.ones((2, 2, 64), device="cuda")
+    k, v = mv.kv4_append(cache, x, x, i32(0, 0), i32(-1, 0), held=True, dev_err=err)  # there is no sequence 0
+    torch.cuda.synchronize()
+    assert err.item() == mv._lib.DEV_BAD_ID and not bool(k.any()) and not bool(v.any())

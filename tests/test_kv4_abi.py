@@ -131,6 +131,17 @@ def test_attention_refuses_bad_pointers_and_workspaces(lib):
     assert lib.kv4_weigh(c, None, None, None, None, None, z, None, None, None) == L.MOE_OK
 
 
+def test_a_cache_without_sequences_needs_no_table(lib):
+    c = C.byref(cache(n_seq=0, table=None, n_pages=0, pages=None))
+    assert lib.kv4_evict(c, None, None, C.byref(L.Kv4EvictCfg(4, 2)), None, None, None, None, None) == L.MOE_OK
+    a = C.byref(attn(T=0))
+    assert lib.kv4_attend_workspace(c, a) > 0
+    assert lib.kv4_attend(c, None, None, None, None, a, None, None, None, 0, None, None) == L.MOE_OK
+    assert lib.kv4_weigh(c, None, None, None, None, None, a, None, None, None) == L.MOE_OK
+    assert lib.kv4_append(c, None, None, C.byref(rows(T=0)), None, None, None, None, None, None) == L.MOE_OK
+    assert lib.kv4_read(c, None, None, C.byref(rows(T=0)), None, None, None, None) == L.MOE_OK
+
+
 def test_evict_refusals(lib):
     c = C.byref(cache())
     for keep, recent in ((0, 0), (4, -1), (4, 5), (-1, 0)):
