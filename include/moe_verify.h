@@ -641,7 +641,7 @@ int moe_verify_plan(const moe_step_cfg* cfg, const float* P, const int32_t* pare
  * the limits.  A used table entry outside [0, n_pages) flags MOE_DEV_BAD_ID
  * and its slots are left out; a sequence whose lengths are negative or beyond
  * max_pages * page_size flags MOE_DEV_CAPACITY and is left out (its outputs
- * are not written).
+ * are not written; kv4_evict gives it a length of 0).
  */
 typedef struct {
   int32_t n_pages, page_size, n_kv_heads, head_dim;
@@ -681,7 +681,7 @@ int kv4_read(const kv4_cache* cache, const int32_t* seq, const int32_t* slot, co
 typedef struct {
   int32_t T;            /* new tokens of all sequences                                          */
   int32_t n_q_heads;    /* a multiple of n_kv_heads: head h reads kv head h / (n_q / n_kv)      */
-  int32_t max_q;        /* most new tokens of a sequence: chooses the kernel, not the results   */
+  int32_t max_q;        /* most new tokens of a sequence: chooses the kernel (and its roundings) */
   float scale;          /* factor of q . k (finite)                                             */
   int64_t q_token_stride, q_head_stride; /* in elements, multiples of 8 (not used for one token, one head) */
 } kv4_attn_cfg;
@@ -734,7 +734,8 @@ int kv4_weigh(const kv4_cache* cache, const void* q, const int32_t* q_start, con
  * of the largest mass (ties: the lower slot; NaN, which flags
  * MOE_DEV_BAD_PROB, counts as below everything), keep in all.  Every kv head
  * chooses for itself; the kept entries move to slots 0 .. keep - 1 in their
- * old order.  Otherwise nothing moves.
+ * old order.  Otherwise nothing moves.  (A kept entry whose old or new slot has
+ * a bad table entry is not moved: its new slot holds what it held before.)
  *   new_len   [n_seq] int32 out: min(lens, keep).
  *   origin    [n_seq, n_kv_heads, keep] int32 out: the old slot of each new
  *             one, -1 past new_len.

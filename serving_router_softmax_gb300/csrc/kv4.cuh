@@ -149,7 +149,7 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t b
 // (dimensions 8w..8w+7, n = nibble) gives k-step 2w with the pairs (0, 4) and
 // (1, 5)/16 and k-step 2w + 1 with (2, 6) and (3, 7)/16.  Each row is scaled
 // by the power of two that puts its largest magnitude in [2^14, 2^15), so the
-// fp16 copy of a bf16 row is exact down to 2^-31 of that magnitude.
+// fp16 copy of a bf16 row is exact down to 2^-27 of that magnitude.
 //   frag  [n_rows / 8][D / 32][32] uint4: k-steps 2w (x, y) and 2w + 1 (z, w)
 //   cq    factor of the accumulator, cqs factor of kz (both times scale * log2 e)
 // `row` gives the source row (NULL: zeros).  Threads 0..nthreads-1 take part.

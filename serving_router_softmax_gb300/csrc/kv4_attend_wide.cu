@@ -16,10 +16,10 @@
 // warp 8 issues the products, warp 9 copies tiles.  The scores of a tile come in two halves of 32 slots, each with its own
 // columns (its P over its S), so that one half's products run while the other's
 // exponentials do.  256 TMEM columns (Q, S / P, O), half the shared memory and 96
-// registers a thread: two CTAs share an SM.  The exponentials (16 a clock and SM) and the products
-// would each allow 8 clocks per slot of 128 rows; it takes about 30, in the chain of a half (scores out of TMEM, maximum,
-// exponentials, P into TMEM, product), which two CTAs do not hide: 148 us for 2 chunks of up to 500 tokens of 32 query heads on
-// up to 6000 slots of 8 kv heads, D = 64 (285 TFLOP/s).  Two threads a row with 72 registers took 155.
+// registers a thread: two CTAs share an SM.  The exponentials (32 a clock and SM) would allow 4 clocks per slot of
+// 128 rows, the products (D = 64) 5; it takes about 30, in the chain of a half (scores out of TMEM, maximum,
+// exponentials, P into TMEM, product), which two CTAs do not hide: 145 us for 2 chunks of up to 500 tokens of 32 query heads on
+// up to 6000 slots of 8 kv heads, D = 64 (294 TFLOP/s, issue slots 51% busy, tensor pipe 14%).
 #include "kv4_attend.cuh"
 #include "tc_f16.cuh"
 

@@ -12,8 +12,8 @@
 // rounds in ascending order, each read whole by the cluster before any of it is
 // written: a slot never moves up, so a round writes nothing that a later
 // one reads.  What it moves is far below the memory's rate; the time is in the
-// chain of phases, which is why few rows get clusters of up to 8 CTAs.  On the device 25.7 us for 32 rows of
-// 2304 slots to 2048 (35 MB, 5 us at the copy rate; one CTA a row took 68), 61 us for 32 of up to 40k to 4096.
+// chain of phases, which is why few rows get clusters of up to 8 CTAs.  On the device 17 us for 32 rows of
+// 2304 slots to 2048 (9.4 MB, 1.4 us at the copy rate), 35 us for 32 of up to 40k to 4096 (35 MB, 5.2 us).
 #include <cooperative_groups.h>
 
 #include "kv4.cuh"
@@ -259,8 +259,10 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
 }
 
 // CTAs of a row: as many as keep the GPU's two places an SM filled, but no
-// fewer than 512 slots each (32 rows of 2304 slots: 31 us with 2 CTAs a row, 26 with 4,
-// 32 with 8).
+// fewer than 512 slots each.  On the device, with 2, 4 and 8 CTAs a row: 32 rows of 2304
+// slots 21.7, 16.6 and 24.5 us, 32 of up to 40k 59.7, 32.4 and 34.9.  The lengths
+// are device data, so it goes by the slots that the table can hold: the former in
+// a table of 36,864 slots take 24.9 us.
 int cluster_size(const Cache& c) {
   const long long rows = static_cast<long long>(c.S) * c.Hkv, slots = static_cast<long long>(c.width) << c.page_log2;
   int n = 8;

@@ -7,10 +7,10 @@
 // of values each, side by side, 4 (fp32) or 8 (bf16) of them, and the 2 or 4
 // bytes of their codes.  A warp's rows share their token's look-up
 // (with one a row the first below took 147 us, the second 72).  Append of 32,768 bf16 tokens of 8 heads of 128 with the
-// held values out: 72 us, 63% of the copy rate (82 before the quotients and held values went two to an
-// instruction; what is left of the conversion and the two reductions a row keep it from more, and so do
-// three or five CTAs an SM, 82 and 76 us); read of as many to fp32: 55 us, 81%.  7 tokens appended 2.3 us, 333
-// read 2.0, under the host's 12 a call.
+// held values out: 72 us, 62% of the copy rate (82 before the quotients and held values went two to an
+// instruction).  What is left of the conversion and the two reductions a row keep it from more: issue slots 72% busy,
+// the ALU pipe 70%.  On the device four CTAs an SM take 70 us, three 79, five 73, six 75.  Read of as many to fp32: 55 us,
+// 81%.  7 tokens appended 2.3 us, 333 read 2.0, under the host's 12 to 16 a call.
 #include "kv4.cuh"
 #include "tc_f16.cuh"
 
@@ -136,7 +136,8 @@ __device__ __forceinline__ void extremes(const uint4& r, const float (&v)[E], fl
 }
 
 // (hi - lo) / 15 rounded to fp32: the difference as an unrounded sum of two
-// numbers, the quotient corrected by its remainder.
+// numbers (Knuth's TwoSum, The Art of Computer Programming vol. 2, 4.2.2), the
+// quotient corrected by its remainder (Markstein 1990).
 __device__ __forceinline__ float fifteenth(float hi, float lo) {
   const float d = hi - lo, b = d - hi;
   const float tail = (hi - (d - b)) + (-lo - b);
@@ -147,7 +148,7 @@ __device__ __forceinline__ float fifteenth(float hi, float lo) {
 // Which of k and k + 1 is the whole number nearest to the real quotient
 // (x - zero) / scale, known to lie within 1e-5 of k + 1/2; ties to even.  Exact
 // in fp32: (k + 1/2) scale has 16 bits, x - zero is an unrounded sum of two
-// numbers, and the larger of them is so near to the former that their
+// numbers (TwoSum), and the larger of them is so near to the former that their
 // difference has no rounding.
 __device__ __forceinline__ float nearer(float x, float zero, float scale, float k) {
   const float d = x - zero, b = d - x;
