@@ -87,7 +87,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Atte
     for (long long u = u0; u < u1 && !dead;) {
       const Span sp = span_of<kRows>(a, k, u, u1);
       const int tiles = copied_tiles(a, sp, u + sp.n == u1);
-      for (int it = 0; it < tiles; ++it) {
+      int it = 0;
+      if (a.withhold == kWithholdFirst && u == u0 && tiles > 0) it = issued = stage = 1, ++k.tile;
+      for (; it < tiles; ++it) {
         if (__any_sync(0xFFFFFFFFu, !tc::mbar_wait_bounded(&sm.empty[stage], phase ^ 1, abort_flag, kWaitBudgetNs))) {
           *abort_flag = 1;
           dead = true;
@@ -128,6 +130,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Atte
   }
   int stage = 0;
   uint32_t phase = 0;
+  bool lost = false;  // a tile has not come: no later one is looked at, nor a stage freed that may still be filling
   if (tid < 8) a.meta[static_cast<size_t>(cta) * 8 + tid] = 0;
   for (long long u = u0; u < u1;) {
     const Span sp = span_of<kRows>(a, k, u, u1);
@@ -150,10 +153,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Atte
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
 
-    for (int it = 0; it < n; ++it) {
+    for (int it = 0; it < n && !lost; ++it) {
       const int j0 = (k.tile + it) * kTile + 16 * kGroups * warp;  // first slot of this warp's groups
-      if (!tc::mbar_wait_bounded(&sm.full[stage], phase, abort_flag, kWaitBudgetNs)) *abort_flag = 1;
-      __syncwarp();
+      if (__any_sync(0xFFFFFFFFu, !tc::mbar_wait_bounded(&sm.full[stage], phase, abort_flag, kWaitBudgetNs))) {
+        *abort_flag = 1;
+        lost = true;
+        break;
+      }
       const uint8_t* st = sm.st[stage].b;
       const uint32_t groups = sm.groups[stage] >> (kGroups * warp);
       const bool edge = j0 + 16 * kGroups > k.q.base || (groups & ((1u << kGroups) - 1)) != (1u << kGroups) - 1;
@@ -463,7 +469,8 @@ extern "C" int kv4_attend(const kv4_cache* cache, const void* q, const int32_t* 
   const size_t need = kv4_attend_workspace(cache, cfg);
   if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)) return MOE_ERR_WORKSPACE;
   const Plan p = plan_of(*cfg, c);
-  const bool withhold = (test_stall_mask() & MOE_TEST_STALL_KV4_ATTEND) != 0;
+  const int stall = test_stall_mask();
+  const int withhold = stall & MOE_TEST_STALL_KV4_ATTEND ? kWithholdLast : stall & MOE_TEST_STALL_KV4_FIRST ? kWithholdFirst : 0;
   AttendArgs a{c, static_cast<const uint16_t*>(q), cfg->q_token_stride, cfg->q_head_stride, q_start, base, visible,
                static_cast<uint16_t*>(out), lse, cfg->T, cfg->n_q_heads, cfg->n_q_heads / c.Hkv, cfg->scale * kLog2e,
                static_cast<float*>(workspace),

@@ -25,8 +25,9 @@ struct AttendArgs {
   float* part;     // [CTAs][2] partial sums of row blocks, see part_floats
   int32_t* meta;   // [CTAs][8]: a cut item that starts in this CTA
   int32_t* dev_err;
-  bool withhold;   // test hook: each CTA's last tile is not copied, so that the wait for it runs out
+  int32_t withhold;  // test hook: each CTA's last or first tile is not copied, so that the wait for it runs out
 };
+constexpr int kWithholdLast = 1, kWithholdFirst = 2;
 
 // One row block's partial sums: outputs [RB][D] (the wide kernel: [D][RB], columns as they lie in TMEM), running
 // maxima [RB], sums [RB].
@@ -172,7 +173,7 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, const Cursor& k, lo
 
 // Tiles of a span to copy; the test hook keeps back the last one of the CTA's last span (`last`).
 __device__ __forceinline__ int copied_tiles(const AttendArgs& a, const Span& s, bool last) {
-  return s.tiles - (a.withhold && last && s.tiles > 0 ? 1 : 0);
+  return s.tiles - (a.withhold == kWithholdLast && last && s.tiles > 0 ? 1 : 0);
 }
 
 // Notes an item that starts in this CTA and ends in a later one; u is the item's first unit.

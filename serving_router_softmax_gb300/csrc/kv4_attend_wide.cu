@@ -506,7 +506,9 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
     for (long long u = u0; u < u1 && !dead;) {
       const Span s = span_of<kWideRows>(a, k, u, u1);
       const int tiles = copied_tiles(a, s, u + s.n == u1);
-      for (int it = 0; it < tiles; ++it) {
+      int it = 0;
+      if (a.withhold == kWithholdFirst && u == u0 && tiles > 0) it = issued = 1, ++k.tile, raw.next();
+      for (; it < tiles; ++it) {
         if (!wait_warp(&sm.raw_empty[raw.i], raw.phase ^ 1)) {
           dead = true;
           break;

@@ -1,6 +1,6 @@
-"""Failure path of kv4_attend without any GPU fault: with the test hook MOE_TEST_STALL_KV4_ATTEND the last tile of each CTA's
-share is not copied, so the wait for it runs out after its budget (2 s), long after everything else of the CTA has been
-started.  The call must report MOE_DEV_TIMEOUT and leave the context usable: the next one gives the same result as before."""
+"""Failure path of kv4_attend without any GPU fault: with the test hooks MOE_TEST_STALL_KV4_ATTEND and MOE_TEST_STALL_KV4_FIRST
+the last or the first tile of each CTA's share is not copied, so the wait for it runs out after its budget (2 s): long after
+everything else of the CTA has been started, or with the pipeline full behind it.  The call must report MOE_DEV_TIMEOUT and leave the context usable: the next one gives the same result as before."""
 import time
 
 import numpy as np
@@ -13,9 +13,10 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 
+@pytest.mark.parametrize("hook", ["TEST_STALL_KV4_ATTEND", "TEST_STALL_KV4_FIRST"])
 @pytest.mark.parametrize("max_q", [2, MANY])
 @pytest.mark.parametrize("D,base", [(64, [3000, 40]), (128, [20000, 7])])
-def test_a_wait_that_runs_out_is_reported(mv, max_q, D, base):  # noqa: F811
+def test_a_wait_that_runs_out_is_reported(mv, hook, max_q, D, base):  # noqa: F811
     rng = np.random.default_rng(91)
     new = [2, 1]
     _, cache = make_cache(mv, rng, [b + n for b, n in zip(base, new)], 2, D, 64)
@@ -26,7 +27,7 @@ def test_a_wait_that_runs_out_is_reported(mv, max_q, D, base):  # noqa: F811
     torch.cuda.synchronize()
     assert err.item() == 0
     lib = mv._lib.load()
-    assert lib.moe_test_set_stall(mv._lib.TEST_STALL_KV4_ATTEND) == mv._lib.MOE_OK
+    assert lib.moe_test_set_stall(getattr(mv._lib, hook)) == mv._lib.MOE_OK
     try:
         t0 = time.time()
         mv.kv4_attend(*args, dev_err=err)
