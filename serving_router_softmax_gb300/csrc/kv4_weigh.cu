@@ -63,6 +63,7 @@ struct WeighArgs {
   int32_t T, Hq, G;
   float scale_log2;
   int32_t* dev_err;
+  bool withhold;   // test hook: the first stage of a CTA's first warp never looks full, so that the wait for it runs out
 };
 
 template <int D, int kRows>  // kRows: query rows held at a time
@@ -81,7 +82,7 @@ struct Smem {
   uint32_t groups[4][kStages];                               // bit x: slots 16 x .. of the warp's lie in a valid page
   long long scratch[32];
   uint32_t tmem;
-  int abort;
+  int abort, never;
   long long cum[1];
 };
 
@@ -180,8 +181,8 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
   if (tid == 0) {
     tc::mbar_init(&sm.done, 1);
     for (int w = 0; w < 4; ++w)
-      for (int i = 0; i < kStages; ++i) tc::mbar_init(&sm.full[w][i], 1);
-    sm.abort = 0;
+      for (int i = 0; i < kStages; ++i) tc::mbar_init(&sm.full[w][i], a.withhold && w + i == 0 ? 2 : 1);
+    sm.abort = sm.never = 0;
     tc::fence_mbar_init();
   }
   if (warp == 0) {
@@ -257,6 +258,11 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
           }
           st_next = st_next + 1 == kStages ? 0 : st_next + 1;
         };
+        // Another role's giving up does not end the copies of this warp's stage, which is filled again before long.
+        auto give_up = [&] {
+          *abort_flag = 1;
+          tc::mbar_wait_bounded(&sm.full[warp][st], phase, &sm.never, 100000000ull);
+        };
         look(0);
 #pragma unroll 1
         for (int i = 0; i < kStages - 1; ++i) {
@@ -277,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
         float next_mass = mass_of(0);
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
-          if (!tc::mbar_wait_bounded(&sm.full[warp][st], phase, abort_flag, kWaitBudgetNs)) *abort_flag = 1;
+          if (!tc::mbar_wait_bounded(&sm.full[warp][st], phase, abort_flag, kWaitBudgetNs)) give_up();
           __syncwarp();
           const int j0 = (t0 + i) * kSlots, j = j0 + tid;
           const bool valid = j < k.q.total && ((sm.groups[warp][st] >> (lane >> 4)) & 1);
@@ -366,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
         // The two empty phases beyond the last unit; nothing is in flight after them.
 #pragma unroll 1
         for (int i = 0; i < kStages - 1; ++i) {
-          if (!tc::mbar_wait_bounded(&sm.full[warp][st], phase, abort_flag, kWaitBudgetNs)) *abort_flag = 1;
+          if (!tc::mbar_wait_bounded(&sm.full[warp][st], phase, abort_flag, kWaitBudgetNs)) give_up();
           __syncwarp();
           if (++st == kStages) st = 0, phase ^= 1;
         }
@@ -440,7 +446,8 @@ extern "C" int kv4_weigh(const kv4_cache* cache, const void* q, const int32_t* q
         reinterpret_cast<uintptr_t>(mass)) & 3))
     return MOE_ERR_ARG;
   WeighArgs a{c, static_cast<const uint16_t*>(q), cfg->q_token_stride, cfg->q_head_stride, q_start, base, visible, lse,
-              mass, cfg->T, cfg->n_q_heads, cfg->n_q_heads / c.Hkv, cfg->scale * kLog2e, dev_err};
+              mass, cfg->T, cfg->n_q_heads, cfg->n_q_heads / c.Hkv, cfg->scale * kLog2e, dev_err,
+              (test_stall_mask() & MOE_TEST_STALL_KV4_WEIGH) != 0};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const long long rows = static_cast<long long>(cfg->max_q) * a.G;
   // Clusters of 1 / 2 / 4 / 8 take, on the device, at 136 rows (2 sequences of 3k slots) 25 / 18 / 18 / 22 us, at 224 (16

@@ -141,7 +141,9 @@ extern "C" const char* moe_status_str(int status) {
 extern "C" uint64_t moe_launch_count(void) { return moe::g_launches.load(); }
 
 extern "C" int moe_test_set_stall(int32_t mask) {
-  if (mask & ~(MOE_TEST_STALL_GATE_UP | MOE_TEST_STALL_READY_FLAG | MOE_TEST_STALL_KV4_ATTEND | MOE_TEST_STALL_KV4_FIRST)) return MOE_ERR_ARG;
+  constexpr int32_t kKnown = MOE_TEST_STALL_GATE_UP | MOE_TEST_STALL_READY_FLAG | MOE_TEST_STALL_KV4_ATTEND |
+                             MOE_TEST_STALL_KV4_FIRST | MOE_TEST_STALL_KV4_WEIGH;
+  if (mask & ~kKnown) return MOE_ERR_ARG;
   moe::g_test_stall.store(mask, std::memory_order_relaxed);
   return MOE_OK;
 }

@@ -1,6 +1,7 @@
-"""Failure path of kv4_attend without any GPU fault: with the test hooks MOE_TEST_STALL_KV4_ATTEND and MOE_TEST_STALL_KV4_FIRST
+"""Failure paths of kv4_attend and kv4_weigh without any GPU fault: with the test hooks MOE_TEST_STALL_KV4_ATTEND and MOE_TEST_STALL_KV4_FIRST
 the last or the first tile of each CTA's share is not copied, so the wait for it runs out after its budget (2 s): long after
-everything else of the CTA has been started, or with the pipeline full behind it.  The call must report MOE_DEV_TIMEOUT and leave the context usable: the next one gives the same result as before."""
+everything else of the CTA has been started, or with the pipeline full behind it.  MOE_TEST_STALL_KV4_WEIGH does so with the first keys
+of a CTA.  The call must report MOE_DEV_TIMEOUT and leave the context usable: the next one gives the same result as before."""
 import time
 
 import numpy as np
@@ -42,3 +43,34 @@ def test_a_wait_that_runs_out_is_reported(mv, hook, max_q, D, base):  # noqa: F8
     torch.cuda.synchronize()
     assert err.item() == 0
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("max_q", [2, 40, MANY])
+@pytest.mark.parametrize("Hq,D,base", [(8, 64, [3000, 40]), (8, 128, [20000, 7]), (128, 128, [300, 1000])])
+def test_a_wait_for_keys_that_runs_out_is_reported(mv, max_q, Hq, D, base):  # noqa: F811
+    """One CTA an item, and clusters that share its rows."""
+    rng = np.random.default_rng(92)
+    new = [2, 1]
+    _, cache = make_cache(mv, rng, [b + n for b, n in zip(base, new)], 2, D, 64)
+    q = bf16(rng.standard_normal((3, Hq, D))).cuda()
+    args = (q, dev(np.array([0, 2, 3], np.int32)), dev(np.array(base, np.int32)), max_q)
+    _, lse = mv.kv4_attend(cache, *args)
+    err = mv.new_dev_err()
+    want = mv.kv4_weigh(cache, *args, lse, cache.new_mass(), dev_err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    lib = mv._lib.load()
+    assert lib.moe_test_set_stall(mv._lib.TEST_STALL_KV4_WEIGH) == mv._lib.MOE_OK
+    try:
+        t0 = time.time()
+        mv.kv4_weigh(cache, *args, lse, cache.new_mass(), dev_err=err)
+        torch.cuda.synchronize()
+        waited = time.time() - t0
+    finally:
+        lib.moe_test_set_stall(0)
+    assert err.item() == mv._lib.DEV_TIMEOUT
+    assert 1.5 < waited < 30.0, waited
+    err.zero_()
+    got = mv.kv4_weigh(cache, *args, lse, cache.new_mass(), dev_err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0 and torch.equal(got, want)
