@@ -783,7 +783,8 @@ uint64_t moe_launch_count(void);
  *   MOE_TEST_STALL_KV4_ATTEND  kv4_attend does not copy the last tile of each
  *                              CTA's share, so the wait for it runs out and the
  *                              call reports MOE_DEV_TIMEOUT;
- *   MOE_TEST_STALL_KV4_FIRST   the same for the first tile;
+ *   MOE_TEST_STALL_KV4_FIRST   kv4_attend does not take the first tile of each
+ *                              CTA's share as copied, to the same effect;
  *   MOE_TEST_STALL_KV4_WEIGH   kv4_weigh does not take the first keys of one
  *                              warp of each CTA as copied, to the same effect.
  * Process-wide; read by the host at each launch.  Returns MOE_ERR_ARG for

@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Atte
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      tc::mbar_init(&sm.full[i], 1);
+      tc::mbar_init(&sm.full[i], arrivals_of_stage(a, i));
       tc::mbar_init(&sm.empty[i], kConsumerWarps);
     }
     sm.abort = sm.never = 0;
@@ -87,9 +87,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Atte
     for (long long u = u0; u < u1 && !dead;) {
       const Span sp = span_of<kRows>(a, k, u, u1);
       const int tiles = copied_tiles(a, sp, u + sp.n == u1);
-      int it = 0;
-      if (a.withhold == kWithholdFirst && u == u0 && tiles > 0) it = issued = stage = 1, ++k.tile;
-      for (; it < tiles; ++it) {
+      for (int it = 0; it < tiles; ++it) {
         if (__any_sync(0xFFFFFFFFu, !tc::mbar_wait_bounded(&sm.empty[stage], phase ^ 1, abort_flag, kWaitBudgetNs))) {
           *abort_flag = 1;
           dead = true;

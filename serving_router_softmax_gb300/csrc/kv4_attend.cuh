@@ -25,7 +25,7 @@ struct AttendArgs {
   float* part;     // [CTAs][2] partial sums of row blocks, see part_floats
   int32_t* meta;   // [CTAs][8]: a cut item that starts in this CTA
   int32_t* dev_err;
-  int32_t withhold;  // test hook: each CTA's last or first tile is not copied, so that the wait for it runs out
+  int32_t withhold;  // test hook: each CTA's last or first tile does not come, so that the wait for it runs out
 };
 constexpr int kWithholdLast = 1, kWithholdFirst = 2;
 
@@ -169,6 +169,11 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, const Cursor& k, lo
   s.first = k.tile == 0;
   s.whole = s.first && s.tiles == s.need;
   return s;
+}
+
+// Arrivals that fill stage i of the tile ring; with the test hook on the first tile its stage never looks full.
+__device__ __forceinline__ uint32_t arrivals_of_stage(const AttendArgs& a, int i) {
+  return a.withhold == kWithholdFirst && i == 0 ? 2 : 1;
 }
 
 // Tiles of a span to copy; the test hook keeps back the last one of the CTA's last span (`last`).

@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kRaw; ++i) {
-      tc::mbar_init(&sm.raw_full[i], 1);
+      tc::mbar_init(&sm.raw_full[i], arrivals_of_stage(a, i));
       tc::mbar_init(&sm.raw_empty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
@@ -506,9 +506,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_wide_kernel(const AttendAr
     for (long long u = u0; u < u1 && !dead;) {
       const Span s = span_of<kWideRows>(a, k, u, u1);
       const int tiles = copied_tiles(a, s, u + s.n == u1);
-      int it = 0;
-      if (a.withhold == kWithholdFirst && u == u0 && tiles > 0) it = issued = 1, ++k.tile, raw.next();
-      for (; it < tiles; ++it) {
+      for (int it = 0; it < tiles; ++it) {
         if (!wait_warp(&sm.raw_empty[raw.i], raw.phase ^ 1)) {
           dead = true;
           break;

@@ -1,5 +1,5 @@
 """Failure paths of kv4_attend and kv4_weigh without any GPU fault: with the test hooks MOE_TEST_STALL_KV4_ATTEND and MOE_TEST_STALL_KV4_FIRST
-the last or the first tile of each CTA's share is not copied, so the wait for it runs out after its budget (2 s): long after
+the last tile of each CTA's share is not copied, or the first one not taken as copied, so the wait for it runs out after its budget (2 s): long after
 everything else of the CTA has been started, or with the pipeline full behind it.  MOE_TEST_STALL_KV4_WEIGH does so with the first keys
 of a CTA.  The call must report MOE_DEV_TIMEOUT and leave the context usable: the next one gives the same result as before."""
 import time
