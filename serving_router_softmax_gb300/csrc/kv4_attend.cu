@@ -17,8 +17,8 @@
 // joins them in CTA order, so results do not depend on timing.
 //
 // Bound by memory for long contexts (48 sequences of 8k to 32k slots, 64 query
-// heads on 8: 1.09 GB in 205 us with the joining, 78% of the copy rate); what keeps it
-// from more is the unpacking's integer operations (the ALU pipe is 57% busy, the issue slots 54%) and
+// heads on 8: 1.09 GB in 201 us with the joining, 79% of the copy rate); what keeps it
+// from more is the unpacking's integer operations (the ALU pipe is 59% busy, the issue slots 55%) and
 // the registers, which hold four CTAs an SM.
 #include "kv4_attend.cuh"
 
@@ -31,7 +31,7 @@ constexpr int kConsumerWarps = 2;
 constexpr int kThreads = 32 * (kConsumerWarps + 1);
 constexpr int kGroups = kTile / 16 / kConsumerWarps;  // 16-slot groups of a tile that a warp takes
 constexpr int kMinUnits = 1;
-constexpr int kCtasPerSm = 4;  // the above on the device: 202 us; with five, which spill registers, 301, with three 258
+constexpr int kCtasPerSm = 4;  // the above on the device: 199 us; with five, which spill registers, 306, with three 250
 
 // About 43 KB of tiles in flight a CTA.
 template <int D> constexpr int stages() { return D == 128 ? 5 : 9; }
@@ -380,23 +380,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_kernel(const Atte
 // (here / wide), rows of a sequence and kv head against sequences x longest
 // context (lengths and tokens ragged but in the last column, 8 kv heads, the
 // table as wide as the longest context):
-//            rows    2 x 2,000     1 x 30,000    16 x 8,192     16 x 8,192, all full
-//   D = 128    24   13.7 / 20.3   30.2 / 47.6    66.7 /  82.9    88.0 / 126.6
-//              32   14.1 / 20.7   33.3 / 48.0    68.4 /  79.7   113.1 / 127.1
-//              40   13.6 / 20.4   39.2 / 48.9    90.3 /  88.6   137.0 / 127.9
-//              48   13.9 / 21.2   43.8 / 49.1   110.3 /  84.7   163.8 / 128.8
-//              64   15.7 / 21.6   53.9 / 49.3   184.6 /  93.6   215.4 / 130.1
-//             128   20.4 / 24.5   98.7 / 54.2   294.1 / 101.4   418.8 / 139.5
-//   D = 64     24   11.7 / 17.7   23.6 / 42.0    44.9 /  68.0    60.8 / 106.3
-//              32   12.0 / 18.2   26.0 / 42.1    46.5 /  63.7    77.2 / 106.5
-//              40   11.9 / 17.7   29.8 / 42.8    59.9 /  71.4    94.2 / 106.6
-//              48   11.7 / 18.0   33.1 / 42.8    72.3 /  67.9   111.9 / 106.6
-//              64   12.9 / 18.3   40.0 / 43.0   114.2 /  73.7   146.1 / 106.9
-//             128   15.9 / 21.2   69.9 / 46.3   190.3 /  72.1   284.0 / 110.9
-// The rule below takes up to 19% more there than the better one.  The lengths are
+//            rows    2 x 2,000     1 x 30,000     16 x 8,192    16 x 8,192, all full
+//   D = 128    24   13.8 / 20.2   30.2 / 47.4    68.0 /  83.9     87.1 / 127.5
+//              32   14.0 / 20.7   33.7 / 47.9    69.2 /  79.1    112.0 / 127.8
+//              40   13.8 / 20.4   39.4 / 48.8    90.4 /  89.6    135.8 / 128.8
+//              48   14.0 / 20.9   44.1 / 49.1   111.2 /  85.3    163.0 / 129.3
+//              64   16.0 / 21.4   54.0 / 49.2   183.6 /  93.8    213.2 / 130.8
+//             128   20.7 / 24.3   98.1 / 54.1   294.8 / 101.1    414.0 / 139.8
+//   D = 64     24   11.9 / 17.8   23.8 / 42.2    45.5 /  67.9     61.8 / 106.3
+//              32   12.0 / 18.1   26.4 / 42.3    47.1 /  63.4     78.4 / 106.2
+//              40   12.0 / 17.9   30.3 / 43.0    60.7 /  71.5     95.8 / 106.5
+//              48   11.8 / 18.0   33.6 / 43.0    73.6 /  67.7    113.6 / 106.5
+//              64   13.0 / 18.2   40.6 / 43.1   115.6 /  73.7    148.5 / 106.8
+//             128   16.1 / 21.1   71.1 / 46.5   192.7 /  71.7    288.0 / 111.0
+// The rule below takes up to 18% more there than the better one.  The lengths are
 // device data, so it goes by the slots that the table can hold: a table far
 // wider than what is in use costs more (32 rows, 4 x 2,000 slots, a table of
-// 131,072 slots: 21.8 us where the kernel here takes 14.2).
+// 131,072 slots: 22.0 us where the kernel here takes 14.2).
 bool wide_pays(long long rows, const Cache& c) {
   const double slots = static_cast<double>(c.S) * c.Hkv * (static_cast<double>(c.width) * c.page_size);
   return rows > 24 && slots * static_cast<double>(rows - 24) * c.D >= 576e6;

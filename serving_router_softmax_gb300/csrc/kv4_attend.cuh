@@ -90,7 +90,7 @@ __device__ __forceinline__ int used_ctas(long long total, int min_units) {
 }
 
 // Units that an item costs beyond its tiles (query rows in, sums out).  With 1, 2, 3 and 4, on the device: 4 trees of up to 7
-// tokens on up to 8192 slots 38.5, 35.3, 34.8 and 34.8 us, 48 tokens on up to 32,768 each 203.5, 201.8, 201.9 and 201.5.
+// tokens on up to 8192 slots 38.4, 35.2, 34.9 and 35.0 us, 48 tokens on up to 32,768 each 206.4, 202.4, 199.1 and 198.6.
 constexpr int kItemUnits = 3;
 
 // Page lookup and copies of tiles, one warp.  A lone warp's instructions wait
@@ -262,9 +262,9 @@ __global__ void __launch_bounds__(D * kShare) combine_kernel(const AttendArgs a)
 
 template <int D, int RB, bool kCols>
 int launch_combine(const AttendArgs& a, int grid, cudaStream_t s) {
-  // A chain of loads per share: four shares read a long list sooner than two (one decoded token over 777 slots: 10.3 us
-  // on the device against 11.1, 4 trees on up to 8192 34.9 against 39.1), eight cost more in idle CTAs than they save
-  // (10.2 and 37.3; 48 sequences: 207.6 us against 201.9).
+  // A chain of loads per share: four shares read a long list sooner than two (one decoded token over 777 slots: 10.4 us
+  // on the device against 11.4, 4 trees on up to 8192 34.8 against 38.9), eight cost more in idle CTAs than they save
+  // (10.4 and 37.3; 48 sequences: 204.8 us against 199.1).
   constexpr int kShare = 4;
   LaunchScope ls(kProfKv4Attend, s);
   return launch_k(combine_kernel<D, RB, kCols, kShare>, dim3(grid, RB / 8), dim3(D * kShare), 0, s, true, a);

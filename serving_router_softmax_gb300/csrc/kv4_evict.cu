@@ -260,9 +260,9 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
 
 // CTAs of a row: as many as keep the GPU's two places an SM filled, but no
 // fewer than 512 slots each.  On the device, with 2, 4 and 8 CTAs a row: 32 rows of 2304
-// slots 21.7, 16.6 and 24.5 us, 32 of up to 40k 59.7, 32.4 and 34.9.  The lengths
+// slots 21.8, 16.6 and 22.6 us, 32 of up to 40k 59.8, 32.4 and 35.2.  The lengths
 // are device data, so it goes by the slots that the table can hold: the former in
-// a table of 36,864 slots take 24.9 us.
+// a table of 36,864 slots take 22.9 us.
 int cluster_size(const Cache& c) {
   const long long rows = static_cast<long long>(c.S) * c.Hkv, slots = static_cast<long long>(c.width) << c.page_log2;
   int n = 8;

@@ -18,7 +18,7 @@
 //
 // More than 128 query rows (a prompt's chunk) are shared by the CTAs of a cluster, which take the same
 // slots and add up their sums in the order of their ranks: a slot's row blocks one after the
-// other in one CTA take 626 us for 6400 rows and 405 slots, with clusters of 8 84 us.
+// other in one CTA take 621 us for 6400 rows and 405 slots, with clusters of 8 85 us.
 #include <cooperative_groups.h>
 
 #include "kv4.cuh"
@@ -44,7 +44,7 @@ constexpr int kCols = 64;            // columns of a product
 constexpr int kAllRows = 1 << 30;    // one row block per kv head
 constexpr int kStages = 3;           // key rows on their way
 // What beginning an item costs, in units: a CTA with two units whose second begins another item took the longest (on
-// the device, 4 trees on up to 4000 slots 14.4 us with 0, 11.5 with 1, 12.4 with 2; 16 on up to 16k 47.4, 46.9, 45.6).
+// the device, 4 trees on up to 4000 slots 14.6 us with 0, 11.4 with 1, 12.5 with 2; 16 on up to 16k 47.4, 46.8, 45.5).
 constexpr int kItemUnits = 1;
 constexpr int kNoToken = -(1 << 30) - 1;  // of a row that has seen nothing: below every slot's distance from the new ones
 constexpr int kGroup = 8;            // units whose sums wait in shared memory where rows come in several blocks
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const WeighArgs a) {
 
 // ctas: what fits an SM (TMEM: four); cluster: CTAs that share an item's query rows.  Clusters above 2 do not
 // fill every SM, and a grid that does not fit at once takes twice the time (16 sequences of 8k slots,
-// 512 rows, clusters of 4: 290 us with a full grid, 228 with nine tenths).
+// 512 rows, clusters of 4: 291 us with a full grid, 237 with nine tenths).
 template <int D, int kRows, bool kShared>
 int launch_weigh(const WeighArgs& a, int ctas, int cluster, cudaStream_t s) {
   constexpr auto kernel = weigh_kernel<D, kRows, kShared>;
@@ -450,9 +450,9 @@ extern "C" int kv4_weigh(const kv4_cache* cache, const void* q, const int32_t* q
               (test_stall_mask() & MOE_TEST_STALL_KV4_WEIGH) != 0};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const long long rows = static_cast<long long>(cfg->max_q) * a.G;
-  // Clusters of 1 / 2 / 4 / 8 take, on the device, at 136 rows (2 sequences of 3k slots) 25 / 18 / 18 / 22 us, at 224 (16
-  // of 8k) 114 / 127 / 154 / 242, at 320 (4 of 4k) 45 / 37 / 33 / 41, at 512 (16 of 8k) 246 / 249 / 227 / 273, at 2400 (4 of
-  // 2k) 274 / 185 / 152 / 134.
+  // Clusters of 1 / 2 / 4 / 8 take, on the device, at 136 rows (2 sequences of 3k slots) 24 / 18 / 18 / 22 us, at 224 (16
+  // of 8k) 114 / 128 / 157 / 241, at 320 (4 of 4k) 45 / 37 / 33 / 41, at 512 (16 of 8k) 241 / 249 / 237 / 274, at 2400 (4 of
+  // 2k) 275 / 186 / 152 / 132.
   int cluster = 1;
   while (cluster < 8 && rows > 128 * cluster) cluster *= 2;
   if (cluster > 1) return c.D == 128 ? launch_weigh<128, 128, true>(a, 3, cluster, s) : launch_weigh<64, 128, true>(a, 4, cluster, s);
