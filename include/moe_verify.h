@@ -20,6 +20,11 @@
  *   kv4_attend         attention of the verify tokens (tree or chain) over it
  *   kv4_weigh          accumulates the attention weight of every cached slot
  *   kv4_evict          brings the cache down to a budget by that weight
+ * and, for a prompt's pass through a layer before the first verify step:
+ *   moe_rotate         rotary positions (one or several axes) of queries and keys
+ *   moe_prompt_attend  causal attention of packed prompts over their own keys
+ *   moe_group_gate_up  the experts' first products and SwiGLU, grouped by expert
+ *   moe_group_down     their second product and each token's weighted sum
  *
  * Conventions shared by every entry point
  *   - Every array argument is a DEVICE pointer owned by the caller, unless a
@@ -748,6 +753,110 @@ typedef struct {
 int kv4_evict(const kv4_cache* cache, const float* mass, const int32_t* lens, const kv4_evict_cfg* cfg,
               int32_t* new_len, int32_t* origin, float* mass_out, int32_t* dev_err, void* stream);
 
+/* ---------------------------------------------------------------- a prompt's pass
+ * What a prompt needs of a layer before the first verify step, at a prompt's
+ * number of tokens: rotated queries and keys, attention over the whole prompt,
+ * and the experts' products over the same layer weights and the same union as
+ * the verify step's.  The write-ups start from a prefilled context and have no
+ * counterpart; the calls below are the plain mathematics.
+ */
+
+/* moe_rotate -- rotary positions of T tokens' queries and keys.
+ *   pair i < rotary_dim / 2 of a head's row turns by the angle
+ *     2 pi * turns[i] / 2^64 * pos[axis[i]][t]:
+ *   (a, b) -> (a cos - b sin, a sin + b cos)   (inverse: by minus the angle,
+ *   which is also the gradient of the rotation with respect to its input).
+ *   Pair i is dimensions i and i + rotary_dim / 2, or 2i and 2i + 1 where
+ *   `interleaved` is 1.  Dimensions from rotary_dim on are copied.
+ *   q, k        rows of head_dim values, dtype MOE_DTYPE_BF16 or MOE_DTYPE_F32,
+ *               strided as cfg says; k may be NULL (n_k_heads 0).
+ *   pos         [n_axes][T] int32, any value: a text token's position, or
+ *               time, height and width of an image's or a video's patch.
+ *   turns       [rotary_dim / 2] 64-bit: the angle of one position as a part of
+ *               a full turn, times 2^64 (mod 2^64).  Positions multiply it as
+ *               integers, so an angle is exact to 2^-34 of a turn however far
+ *               the position is.
+ *   axis        [rotary_dim / 2] int32, each in [0, n_axes).
+ *   out_q, out_k  rows as q and k, with their own strides; either the input
+ *               itself (same pointer and strides) or memory apart from it.
+ * Arithmetic in fp32; cosine and sine within 2^-22, each output rounded once.
+ * Limits: 0 <= T <= 2^24; head_dim a multiple of 8 up to 512; rotary_dim a
+ * multiple of 16, 16 <= rotary_dim <= head_dim; 1 <= n_axes <= 4; 1 <= n_q_heads,
+ * 0 <= n_k_heads, together <= 4096; strides multiples of 16 bytes, not negative, and no two rows of
+ * an output share a value (the token stride of one token and the head stride of one head are not used).
+ * Device errors: MOE_DEV_BAD_ID (an axis outside [0, n_axes): its pair is
+ * copied as it is). */
+typedef struct {
+  int32_t T, n_q_heads, n_k_heads, head_dim, rotary_dim, n_axes, interleaved, inverse, dtype;
+  int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;             /* in elements */
+  int64_t oq_token_stride, oq_head_stride, ok_token_stride, ok_head_stride;
+} moe_rotate_cfg;
+int moe_rotate(const void* q, const void* k, const int32_t* pos, const uint64_t* turns, const int32_t* axis,
+               const moe_rotate_cfg* cfg, void* out_q, void* out_k, int32_t* dev_err, void* stream);
+
+/* moe_prompt_attend -- causal attention of whole prompts, packed one behind the
+ * other: out_i = sum over j <= i of exp(scale q_i . k_j - lse_i) v_j within each
+ * sequence, lse_i the log of the sum of the exponentials.
+ *   q           [T, n_q_heads, D] bf16; k, v [T, n_kv_heads, D] bf16, strided as
+ *               cfg says, 16-byte aligned.
+ *   start       [n_seq + 1] int32: sequence s is rows start[s] .. start[s + 1] - 1
+ *               (none is fine).  Rows before start[0] and from start[n_seq] on
+ *               are not read, and their outputs are left as they are.
+ *   out         [T, n_q_heads, D] bf16 out.
+ *   lse         [T, n_q_heads] fp32 out or NULL.
+ * Scores, maxima, sums and outputs are accumulated in fp32; the probabilities
+ * enter the second product as bf16 (relative to a reference within 2^8 of the
+ * row's largest), the output is rounded once.
+ * A NaN or infinity in a row of q, or in a key that a row sees, makes that row
+ * NaN, out and lse (a key whose score is -inf counts as not seen; a row without
+ * any gives zeros and -inf).  In a value it makes that dimension of out NaN or infinite for the
+ * rows that see it.  What a row does not see has no effect on it.
+ * Results do not depend on timing.
+ * Limits: D = 64 or 128; 0 <= T <= 2^24, n_seq <= 4096; n_q_heads a multiple of
+ * n_kv_heads, at most 128 times as many, n_q_heads <= 1024; strides multiples
+ * of 8, those of one token or one head not used.
+ * Device errors: MOE_DEV_CAPACITY (starts outside [0, T] or out of order:
+ * nothing is written), MOE_DEV_TIMEOUT. */
+typedef struct {
+  int32_t T, n_seq, n_q_heads, n_kv_heads, head_dim;
+  float scale;          /* finite */
+  int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+} moe_prompt_cfg;
+int moe_prompt_attend(const void* q, const void* k, const void* v, const int32_t* start,
+                      const moe_prompt_cfg* cfg, void* out, float* lse, int32_t* dev_err, void* stream);
+
+/* moe_group_gate_up -- h[p] = silu(W_gate,e x_t) * (W_up,e x_t) for every row p
+ * of the union's groups (offsets[u] <= p < offsets[u+1], e = unique[u],
+ * t = perm_token[p]): the first half of moe_verify_ffn, for any number of tokens.
+ *   x           [T, H] bf16.
+ *   lw          a bf16 layer, either layout, with or without a pool.
+ *   n_unique .. perm_token   as written by moe_union_permute.
+ *   h           [T * k, I] bf16 out, rows in the groups' order; rows that no
+ *               group holds are left as they are.
+ * fp32 accumulation on the tensor cores, one rounding per output.
+ * Limits: 0 <= T, T * k <= 2^22, 1 <= k <= 16, H and I multiples of 64, E <= 1024.
+ * Device errors: MOE_DEV_CAPACITY (n_unique outside [0, min(E, T*k)]: nothing is
+ * written), MOE_DEV_BAD_ID (an expert id, pool slot or group ends out of range:
+ * that group's rows are not written; a token out of range: its row is that of
+ * some token), MOE_DEV_TIMEOUT. */
+int moe_group_gate_up(const void* x, int32_t T, int32_t k, const moe_layer_weights* lw, const int32_t* n_unique,
+                      const int32_t* unique, const int32_t* offsets, const int32_t* perm_token, void* h,
+                      int32_t* dev_err, void* stream);
+
+/* moe_group_down -- y_t = sum_j w[t, j] * (W_down,e h[inv[t, j]]), e the expert
+ * whose group holds that row: the second half.
+ *   h           [T * k, I] bf16 in the groups' order (moe_group_gate_up's).
+ *   inv, w      [T, k] int32 and fp32 as moe_union_permute and moe_route write them.
+ *   y           [T, H] bf16 out.  The products, rounded to bf16 in the workspace,
+ *               are summed in slot order in fp32 and rounded once.
+ * Needs moe_group_down_workspace() bytes (0: bad arguments), 256-byte aligned.
+ * With n_unique outside its range (MOE_DEV_CAPACITY) or 0, y is zeros; a term whose inv is out
+ * of range (MOE_DEV_BAD_ID) is left out.  Other limits and errors as above. */
+size_t moe_group_down_workspace(const moe_layer_weights* lw, int32_t T, int32_t k);
+int moe_group_down(const void* h, int32_t T, int32_t k, const moe_layer_weights* lw, const int32_t* n_unique,
+                   const int32_t* unique, const int32_t* offsets, const int32_t* inv, const float* w, void* y,
+                   void* workspace, size_t ws_bytes, int32_t* dev_err, void* stream);
+
 /* ---------------------------------------------------------------- timing
  * Optional per-kernel timing.  Between moe_profile_begin and moe_profile_end
  * the library records a CUDA event pair on the launching stream around each
@@ -758,10 +867,11 @@ int kv4_evict(const kv4_cache* cache, const float* mass, const int32_t* lens, co
  * 2 union/permute, 3 FFN prep, 4 FFN gate/up, 5 FFN down, 6 combine,
  * 7 router logits, 8 S2-MoE expansion, 9 expert staging, 10 hot list,
  * 11 depth policy, 12 kv4_append, 13 kv4_read, 14 kv4_attend, 15 kv4_weigh,
- * 16 kv4_evict.
+ * 16 kv4_evict, 17 rotate, 18 prompt_attend, 19 group_gate_up, 20 group_down
+ * (product and sum).
  * Not for use under stream capture.
  */
-enum { MOE_PROF_CLASSES = 17 };
+enum { MOE_PROF_CLASSES = 21 };
 int moe_profile_begin(int32_t max_launches, int32_t class_mask);
 int moe_profile_end(float* ms_per_class, int32_t* launches_per_class, int32_t n_classes);
 

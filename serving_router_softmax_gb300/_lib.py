@@ -18,13 +18,15 @@ LAYOUT_ROWMAJOR, LAYOUT_TILED = 0, 1
 TEST_STALL_GATE_UP, TEST_STALL_READY_FLAG, TEST_STALL_KV4_ATTEND, TEST_STALL_KV4_FIRST, TEST_STALL_KV4_WEIGH = 1, 2, 4, 8, 16
 PROF_CLASSES = ["eco_select", "route", "union_permute", "ffn_prep", "ffn_gate_up", "ffn_down",
                 "combine", "router_logits", "s2_expand", "stage_experts", "hot_list", "depth_policy",
-                "kv4_append", "kv4_read", "kv4_attend", "kv4_weigh", "kv4_evict"]
+                "kv4_append", "kv4_read", "kv4_attend", "kv4_weigh", "kv4_evict", "rotate", "prompt_attend",
+                "group_gate_up", "group_down"]
 
 EXPORTED = ["s2_expand", "moe_router_logits", "moe_route", "moe_union_permute", "moe_verify_ffn_workspace", "moe_verify_ffn",
             "eco_select", "moe_verify_step_workspace", "moe_verify_step", "moe_verify_plan", "moe_profile_begin",
             "moe_profile_end", "moe_status_str", "moe_launch_count", "moe_version", "moe_expert_bytes",
             "moe_stage_experts", "moe_test_set_stall", "moe_hot_list", "moe_depth_policy", "moe_set_nvtx",
-            "kv4_append", "kv4_read", "kv4_attend_workspace", "kv4_attend", "kv4_weigh", "kv4_evict"]
+            "kv4_append", "kv4_read", "kv4_attend_workspace", "kv4_attend", "kv4_weigh", "kv4_evict",
+            "moe_rotate", "moe_prompt_attend", "moe_group_gate_up", "moe_group_down_workspace", "moe_group_down"]
 
 
 class S2Cfg(C.Structure):
@@ -91,6 +93,20 @@ class Kv4AttnCfg(C.Structure):
 
 class Kv4EvictCfg(C.Structure):
     _fields_ = [("keep", C.c_int32), ("recent", C.c_int32)]
+
+
+class RotateCfg(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("T", "n_q_heads", "n_k_heads", "head_dim", "rotary_dim", "n_axes", "interleaved",
+                                         "inverse", "dtype")] + [
+        (n, C.c_int64) for n in ("q_token_stride", "q_head_stride", "k_token_stride", "k_head_stride",
+                                 "oq_token_stride", "oq_head_stride", "ok_token_stride", "ok_head_stride")]
+
+
+class PromptCfg(C.Structure):
+    _fields_ = [("T", C.c_int32), ("n_seq", C.c_int32), ("n_q_heads", C.c_int32), ("n_kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("scale", C.c_float)] + [
+        (n, C.c_int64) for n in ("q_token_stride", "q_head_stride", "k_token_stride", "k_head_stride",
+                                 "v_token_stride", "v_head_stride")]
 
 
 _lib = None
@@ -166,6 +182,16 @@ def load(path: str = LIB_PATH) -> C.CDLL:
     lib.kv4_weigh.restype = C.c_int
     lib.kv4_evict.argtypes = [P(Kv4CacheStruct), vp, vp, P(Kv4EvictCfg), vp, vp, vp, vp, vp]
     lib.kv4_evict.restype = C.c_int
+    lib.moe_rotate.argtypes = [vp, vp, vp, vp, vp, P(RotateCfg), vp, vp, vp, vp]
+    lib.moe_rotate.restype = C.c_int
+    lib.moe_prompt_attend.argtypes = [vp, vp, vp, vp, P(PromptCfg), vp, vp, vp, vp]
+    lib.moe_prompt_attend.restype = C.c_int
+    lib.moe_group_gate_up.argtypes = [vp, i32, i32, P(LayerWeights), vp, vp, vp, vp, vp, vp, vp]
+    lib.moe_group_gate_up.restype = C.c_int
+    lib.moe_group_down_workspace.argtypes = [P(LayerWeights), i32, i32]
+    lib.moe_group_down_workspace.restype = sz
+    lib.moe_group_down.argtypes = [vp, i32, i32, P(LayerWeights), vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]
+    lib.moe_group_down.restype = C.c_int
     lib.moe_set_nvtx.argtypes = [i32]
     lib.moe_set_nvtx.restype = C.c_int
     _lib = lib

@@ -23,7 +23,8 @@ struct LaunchScope {
 enum ProfClass { kProfEco = 0, kProfRoute = 1, kProfUnion = 2, kProfPrep = 3, kProfGateUp = 4,
                  kProfDown = 5, kProfCombine = 6, kProfRouter = 7, kProfS2 = 8, kProfStage = 9,
                  kProfHot = 10, kProfDepth = 11, kProfKv4Append = 12, kProfKv4Read = 13,
-                 kProfKv4Attend = 14, kProfKv4Weigh = 15, kProfKv4Evict = 16 };
+                 kProfKv4Attend = 14, kProfKv4Weigh = 15, kProfKv4Evict = 16, kProfRotate = 17,
+                 kProfPrompt = 18, kProfGroupGateUp = 19, kProfGroupDown = 20 };
 
 int sm_count();
 // Test-hook bits set by moe_test_set_stall (0 in normal operation).
