@@ -896,11 +896,15 @@ uint64_t moe_launch_count(void);
  *   MOE_TEST_STALL_KV4_FIRST   kv4_attend does not take the first tile of each
  *                              CTA's share as copied, to the same effect;
  *   MOE_TEST_STALL_KV4_WEIGH   kv4_weigh does not take the first keys of one
- *                              warp of each CTA as copied, to the same effect.
+ *                              warp of each CTA as copied, to the same effect;
+ *   MOE_TEST_STALL_GROUP       the moe_group_* products copy nothing, to the same effect;
+ *   MOE_TEST_STALL_PROMPT      moe_prompt_attend does not copy the last keys of
+ *                              each CTA's rows, to the same effect.
  * Process-wide; read by the host at each launch.  Returns MOE_ERR_ARG for
  * unknown bits. */
 enum { MOE_TEST_STALL_GATE_UP = 1, MOE_TEST_STALL_READY_FLAG = 2, MOE_TEST_STALL_KV4_ATTEND = 4,
-       MOE_TEST_STALL_KV4_FIRST = 8, MOE_TEST_STALL_KV4_WEIGH = 16 };
+       MOE_TEST_STALL_KV4_FIRST = 8, MOE_TEST_STALL_KV4_WEIGH = 16, MOE_TEST_STALL_GROUP = 32,
+       MOE_TEST_STALL_PROMPT = 64 };
 int moe_test_set_stall(int32_t mask);
 
 /* Trace ranges for a timeline tool (NVTX; the pages have no counterpart).

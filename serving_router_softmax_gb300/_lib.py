@@ -16,6 +16,7 @@ DEV_NAN_LOGIT, DEV_BAD_ID, DEV_DUP_ID, DEV_BAD_TREE, DEV_BAD_PROB, DEV_TIMEOUT, 
 DTYPE_F32, DTYPE_BF16, DTYPE_E4M3_B128 = 0, 1, 2
 LAYOUT_ROWMAJOR, LAYOUT_TILED = 0, 1
 TEST_STALL_GATE_UP, TEST_STALL_READY_FLAG, TEST_STALL_KV4_ATTEND, TEST_STALL_KV4_FIRST, TEST_STALL_KV4_WEIGH = 1, 2, 4, 8, 16
+TEST_STALL_GROUP, TEST_STALL_PROMPT = 32, 64
 PROF_CLASSES = ["eco_select", "route", "union_permute", "ffn_prep", "ffn_gate_up", "ffn_down",
                 "combine", "router_logits", "s2_expand", "stage_experts", "hot_list", "depth_policy",
                 "kv4_append", "kv4_read", "kv4_attend", "kv4_weigh", "kv4_evict", "rotate", "prompt_attend",

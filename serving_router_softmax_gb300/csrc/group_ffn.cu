@@ -1,74 +1,334 @@
 // moe_group_gate_up, moe_group_down: the experts' products of a prompt's
-// tokens, grouped by expert.
+// tokens, grouped by expert, on pairs of CTAs.
 //
-// First form: 64 x 64 tiles of a group's rows and a matrix's rows on the CUDA
-// cores.
+// A tile is 256 weight rows of one expert times up to 256 rows of its group
+// (N, a multiple of 32): a group of any size pads by 31 rows at most, whereas
+// tokens as the product's M would pad to 128 or 256.  gate/up takes 128 gate and
+// the same 128 up rows, half of each in either CTA: gate in the CTA's TMEM lanes
+// 0-63, up in 64-127.  K goes through a ring of stages of 64 columns, 16 KB of
+// weights and up to 16 KB of rows each; the sums are kept twice, so that a
+// tile's epilogue runs beside the next one's products.
+//
+// The group's rows are gathered by TMA where they lie: lane l of the loading
+// warp copies rows 4l .. 4l+3 of each stage (gate/up: the tokens' rows of x
+// through perm_token; down: the group's own rows of h).
+//
+// Persistent: pair i takes tiles i, i + pairs, ..., in an order that has a
+// matrix's rows go over all of their group's chunks before the next rows come,
+// and an expert's before the next expert's: what runs at the same time shares
+// weights and rows in L2.
+//
+// Roles of a CTA: warp 0 loads, warp 1 owns TMEM and (in the pair's first CTA)
+// issues the products, warps 2-5 take the sums out.  Every wait is bounded.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
 #include "common.cuh"
+#include "smem_limit.cuh"
+#include "tc_pair.cuh"
 
 namespace moe {
 namespace {
 
+constexpr int kThreads = 192;
+constexpr int kStages = 6;
+constexpr int kABytes = 128 * 128, kBBytes = 128 * 128;
+constexpr int kMaxU = 1024;
+constexpr uint64_t kWaitNs = 2000000000ull;
+
 struct GroupArgs {
-  const uint16_t* x;          // rows of K values
-  const uint16_t* w;
   const int32_t *n_unique, *unique, *offsets, *perm, *slot_of;
   uint16_t* out;              // [rows][N]
   int32_t* dev_err;
-  int T, rows, E, cap, n_slots, N, K, tiled;
+  int T, rows, E, cap, n_slots;
+  int N, K;                   // rows of a matrix (gate/up: of one of its halves), reduction length
+  int tiled, MT, stall;
 };
 
-// Weight rows of (slot, row) in either layout: `half` is 0 for a gate row, 1 for an up row.
-template <bool kGateUp>
-__device__ __forceinline__ const uint16_t* weight(const GroupArgs& a, int slot, int row, int half, int col) {
-  if (!a.tiled) return a.w + (static_cast<size_t>(slot) * a.N * (kGateUp ? 2 : 1) + (half ? a.N : 0) + row) * a.K + col;
-  const int MT = (a.N + 127) / 128, R = kGateUp ? 256 : 128;
-  return a.w + (((static_cast<size_t>(slot) * MT + row / 128) * (a.K / 64) + col / 64) * R + half * 128 + row % 128) * 64 + col % 64;
+struct Smem {
+  alignas(1024) uint8_t a[kStages][kABytes];
+  alignas(1024) uint8_t b[kStages][kBBytes];
+  float swap[2][4][16][32];   // gate/up: what a warp hands to its partner, twice
+  int cum[kMaxU + 1];         // chunks before each expert of the union
+  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drain;
+  uint32_t tmem;
+  int abort;
+  int part[kThreads / 32];
+};
+constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+// Chunks of a group of n rows, and rows of a chunk (all but the last).
+__host__ __device__ __forceinline__ int chunks_of(int n) { return (n + 255) / 256; }
+__device__ __forceinline__ int chunk_rows(int n) {
+  const int c = chunks_of(n);
+  return ((n + c - 1) / c + 31) & ~31;
 }
 
-template <bool kGateUp>
-__global__ void __launch_bounds__(256) group_tile_kernel(const GroupArgs a) {
-  __shared__ float xs[64][17], ws[2][64][17];
-  const int U = *a.n_unique;
-  if (U < 0 || U > a.cap) {
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) flag_error(a.dev_err, MOE_DEV_CAPACITY);
-    return;
-  }
-  const int u = blockIdx.y, n0 = blockIdx.x * 64, tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  if (u >= U) return;
-  const int e = a.unique[u], p0 = a.offsets[u], p1 = a.offsets[u + 1];
-  const bool ok = e >= 0 && e < a.E && p0 >= 0 && p0 <= p1 && p1 <= a.rows;
-  const int slot = ok ? weight_slot(a.slot_of, a.n_slots, e) : -1;
-  if (slot < 0) {
-    if (threadIdx.x == 0) flag_error(a.dev_err, MOE_DEV_BAD_ID);
-    return;
-  }
-  for (int p = p0; p < p1; p += 64) {
-    float acc[2][4][4] = {};
-    for (int k = 0; k < a.K; k += 16) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < 1024; i += 256) {
-        const int r = i / 16, c = i % 16, row = min(p + r, p1 - 1);
-        int t = kGateUp ? a.perm[row] : row;
-        if (kGateUp && (t < 0 || t >= a.T)) flag_error(a.dev_err, MOE_DEV_BAD_ID), t = 0;
-        xs[r][c] = bf16_bits_to_float(a.x[static_cast<size_t>(t) * a.K + k + c]);
-        for (int half = 0; half < (kGateUp ? 2 : 1); ++half)
-          ws[half][r][c] = n0 + r < a.N ? bf16_bits_to_float(*weight<kGateUp>(a, slot, n0 + r, half, k + c)) : 0.f;
-      }
-      __syncthreads();
-      for (int c = 0; c < 16; ++c)
-        for (int half = 0; half < (kGateUp ? 2 : 1); ++half)
-          for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) acc[half][i][j] += xs[ty + 16 * i][c] * ws[half][tx + 16 * j][c];
+struct Tile {
+  int u, slot, m, p, n, N;  // expert's place in the union, its weights, row tile, first row of the chunk, its rows, padded
+};
+
+// Group u's expert slot and rows, or n = 0 if any of it is out of range.
+__device__ __forceinline__ void group_of(const GroupArgs& a, int u, int* slot, int* p0, int* n) {
+  const int e = a.unique[u], b = a.offsets[u], q = a.offsets[u + 1];
+  const bool ok = e >= 0 && e < a.E && b >= 0 && b <= q && q <= a.rows;
+  *slot = ok ? weight_slot(a.slot_of, a.n_slots, e) : -1;
+  *p0 = b;
+  *n = *slot >= 0 ? q - b : -1;
+}
+
+// Walks the tiles of one pair.
+struct Walk {
+  const GroupArgs& a;
+  const int* cum;
+  int U, u = 0, first = -1, slot, p0, n, rows, nc;
+  __device__ __forceinline__ Walk(const GroupArgs& args, const int* c, int us) : a(args), cum(c), U(us) {}
+  __device__ __forceinline__ bool at(long long t, Tile* x) {
+    while (u < U && static_cast<long long>(cum[u + 1]) * a.MT <= t) ++u;
+    if (u >= U) return false;
+    if (first != u) {
+      group_of(a, u, &slot, &p0, &n);
+      first = u;
+      nc = cum[u + 1] - cum[u];
+      rows = chunk_rows(n);
     }
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) {
-        const int row = p + ty + 16 * i, n = n0 + tx + 16 * j;
-        if (row >= p1 || n >= a.N) continue;
-        float v = acc[0][i][j];
-        if (kGateUp) v = v / (1.f + expf(-v)) * acc[1][i][j];
-        a.out[static_cast<size_t>(row) * a.N + n] = v == v ? float_to_bf16_bits_rn(v) : 0x7FFF;
-      }
+    const int r = static_cast<int>(t - static_cast<long long>(cum[u]) * a.MT), c = r % nc;
+    x->u = u, x->slot = slot, x->m = r / nc;
+    x->p = p0 + c * rows;
+    x->n = min(rows, n - c * rows);
+    x->N = (x->n + 31) & ~31;
+    return true;
   }
+};
+
+template <bool kGateUp>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    group_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, const GroupArgs a) {
+  extern __shared__ uint8_t raw[];
+  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = tc::cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) tc::mbar_init(&sm.full[i], 1), tc::mbar_init(&sm.empty[i], 1);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.acc_full[i], 1), tc::mbar_init(&sm.acc_empty[i], 8);
+    tc::mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc_pair(&sm.tmem, 512);
+    tc::tmem_relinquish_pair();
+  }
+  // The union's chunks, added up.
+  const int U0 = *a.n_unique;
+  const bool counted = U0 >= 0 && U0 <= a.cap;
+  const int U = counted ? U0 : 0;
+  if (!counted && blockIdx.x == 0 && tid == 0) flag_error(a.dev_err, MOE_DEV_CAPACITY);
+  int before = 0;
+  for (int base = 0; base < U; base += kThreads) {
+    const int u = base + tid;
+    int c = 0;
+    if (u < U) {
+      int slot, p0, n;
+      group_of(a, u, &slot, &p0, &n);
+      if (n < 0 && blockIdx.x == 0) flag_error(a.dev_err, MOE_DEV_BAD_ID);
+      c = n > 0 ? chunks_of(n) : 0;
+    }
+    const int inc = warp_inclusive_sum(c, lane);
+    if (lane == 31) sm.part[warp] = inc;
+    __syncthreads();
+    int sum = before;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) sum += sm.part[w];
+      before += sm.part[w];
+    }
+    if (u < U) sm.cum[u + 1] = sum + inc;
+    __syncthreads();
+  }
+  if (tid == 0) sm.cum[0] = 0;
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::cluster_sync();
+  tc::tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  const long long total = static_cast<long long>(before) * a.MT;
+  const int KB = a.K / 64;
+  volatile int* gave_up = &sm.abort;
+  Walk walk(a, sm.cum, U);
+  Tile x;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- loads
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (long long t = pair; t < total && ok; t += pairs) {
+      walk.at(t, &x);
+      const int half = x.N / 2;
+      int row[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = min(static_cast<int>(rank) * half + 4 * lane + i, x.n - 1);
+        row[i] = x.p + r;
+        if (kGateUp) {
+          row[i] = a.perm[x.p + r];
+          if (row[i] < 0 || row[i] >= a.T) flag_error(a.dev_err, MOE_DEV_BAD_ID), row[i] = 0;
+        }
+      }
+      const uint32_t bytes = 2u * (kABytes + half * 128);
+      // First weight row of the tile in the map, and rows from one block of columns to the next.
+      int wr, step, wx = 0;
+      if (a.tiled) {
+        const int block = kGateUp ? (x.slot * a.MT + x.m) * KB : (x.slot * ((a.N + 127) / 128) + 2 * x.m + static_cast<int>(rank)) * KB;
+        wr = block * (kGateUp ? 256 : 128) + (kGateUp ? static_cast<int>(rank) * 64 : 0);
+        step = kGateUp ? 256 : 128;
+      } else {
+        wr = kGateUp ? x.slot * 2 * a.N + x.m * 128 + static_cast<int>(rank) * 64 : x.slot * a.N + x.m * 256 + static_cast<int>(rank) * 128;
+        step = 0;
+      }
+      const int up = a.tiled ? 128 : a.N;
+      for (int kb = 0; kb < KB; ++kb) {
+        ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait_bounded(&sm.empty[s], ph ^ 1, gave_up, kWaitNs));
+        if (!ok) break;
+        const uint32_t bar = tc::smem_of(&sm.full[s], 0);
+        if (lane == 0 && rank == 0) tc::mbar_arrive_expect_tx(&sm.full[s], bytes);
+        __syncwarp();
+        if (!a.stall) {
+          if (lane == 0) {
+            if (kGateUp) {
+              tc::tma_load_2d_pair(sm.a[s], &wmap, wx, wr, bar);
+              tc::tma_load_2d_pair(sm.a[s] + 64 * 128, &wmap, wx, wr + up, bar);
+            } else {
+              tc::tma_load_2d_pair(sm.a[s], &wmap, wx, wr, bar);
+            }
+          }
+          if (4 * lane < half) tc::tma_gather4_pair(sm.b[s] + lane * 512, &xmap, kb * 64, row, bar);
+        }
+        wr += step;
+        if (!a.tiled) wx += 64;
+        if (++s == kStages) s = 0, ph ^= 1;
+      }
+    }
+    if (!ok) {
+      // Copies in flight land in microseconds; nothing tells this CTA of those that report to the other one.
+      if (lane == 0) {
+        *gave_up = 1;
+        flag_error(a.dev_err, MOE_DEV_TIMEOUT);
+        const uint64_t t0 = tc::globaltimer_ns();
+        while (tc::globaltimer_ns() - t0 < 5000000ull) __nanosleep(1000);
+      }
+      __syncwarp();
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- products
+    if (rank == 0 && lane == 0) {
+      int s = 0, acc = 0;
+      uint32_t ph = 0, aph = 0;
+      bool ok = true;
+      for (long long t = pair; t < total && ok; t += pairs) {
+        walk.at(t, &x);
+        const uint32_t idesc = tc::idesc_bf16_f32(256, x.N), d = tmem + acc * 256;
+        ok = tc::mbar_wait_bounded(&sm.acc_empty[acc], aph ^ 1, gave_up, kWaitNs);
+        tc::tc_fence_after();
+        for (int kb = 0; kb < KB && ok; ++kb) {
+          ok = tc::mbar_wait_bounded(&sm.full[s], ph, gave_up, kWaitNs);
+          if (!ok) break;
+          tc::tc_fence_after();
+          const uint64_t ad = tc::smem_desc_sw128(tc::smem_u32(sm.a[s])), bd = tc::smem_desc_sw128(tc::smem_u32(sm.b[s]));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tc::mma_bf16_pair(d, ad + 2 * i, bd + 2 * i, idesc, kb || i);
+          tc::mma_commit_pair(&sm.empty[s]);
+          if (++s == kStages) s = 0, ph ^= 1;
+        }
+        if (ok) tc::mma_commit_pair(&sm.acc_full[acc]);
+        if (++acc == 2) acc = 0, aph ^= 1;
+      }
+      if (!ok) {
+        *gave_up = 1;
+        flag_error(a.dev_err, MOE_DEV_TIMEOUT);
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(tc::smem_u32(&sm.drain)) : "memory");
+        int never = 0;
+        tc::mbar_wait_bounded(&sm.drain, 0, &never, kWaitNs / 100);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------- sums out
+    const int q = warp & 3;
+    const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+    int acc = 0, flip = 0;
+    uint32_t aph = 0;
+    bool ok = true;
+    for (long long t = pair; t < total && ok; t += pairs) {
+      walk.at(t, &x);
+      ok = tc::mbar_wait_bounded(&sm.acc_full[acc], aph, gave_up, kWaitNs);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      // (Partners give up together: a barrier is between them.)
+      if (kGateUp) {
+        int both;
+        asm volatile("{\n\t.reg .pred p, r;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.red.and.pred r, %2, 64, p;\n\tselp.b32 %0, 1, 0, r;\n\t}"
+                     : "=r"(both) : "r"(static_cast<int>(ok)), "r"(1 + (q & 1)) : "memory");
+        ok = both != 0;
+      }
+      if (!ok) break;
+      tc::tc_fence_after();
+      const uint32_t src = tmem + acc * 256 + lanes;
+      uint16_t* out = a.out + static_cast<size_t>(x.p) * a.N;
+      if (kGateUp) {
+        const int i = x.m * 128 + static_cast<int>(rank) * 64 + (q & 1) * 32 + lane;
+        for (int c = 0; c < x.N; c += 32) {
+          float v0[16], v1[16];
+          tc::tmem_ld16(src + c, v0);
+          tc::tmem_ld16(src + c + 16, v1);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sm.swap[flip][q][j][lane] = q < 2 ? v1[j] : v0[j];
+          tc::named_bar_sync(1 + (q & 1), 64);
+          const int c0 = c + (q < 2 ? 0 : 16);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float other = sm.swap[flip][q ^ 2][j][lane];
+            const float g = q < 2 ? v0[j] : other, w = q < 2 ? other : v1[j];
+            const float h = __fdividef(g, 1.f + __expf(-g)) * w;
+            if (c0 + j < x.n && i < a.N) out[static_cast<size_t>(c0 + j) * a.N + i] = __bfloat16_as_ushort(__float2bfloat16_rn(h));
+          }
+          flip ^= 1;
+        }
+      } else {
+        const int i = x.m * 256 + static_cast<int>(rank) * 128 + q * 32 + lane;
+        for (int c = 0; c < x.N; c += 32) {
+          float v0[16], v1[16];
+          tc::tmem_ld16(src + c, v0);
+          tc::tmem_ld16(src + c + 16, v1);
+          tc::tmem_ld_wait();
+          if (i < a.N) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              if (c + j < x.n) out[static_cast<size_t>(c + j) * a.N + i] = __bfloat16_as_ushort(__float2bfloat16_rn(v0[j]));
+              if (c + 16 + j < x.n) out[static_cast<size_t>(c + 16 + j) * a.N + i] = __bfloat16_as_ushort(__float2bfloat16_rn(v1[j]));
+            }
+          }
+        }
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive_at(tc::smem_of(&sm.acc_empty[acc], 0));
+      if (++acc == 2) acc = 0, aph ^= 1;
+    }
+    if (!ok && lane == 0) {
+      *gave_up = 1;
+      flag_error(a.dev_err, MOE_DEV_TIMEOUT);
+    }
+    __syncwarp();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::cluster_sync();
+  if (warp == 1) tc::tmem_dealloc_pair(tmem, 512);
 }
 
 // y_t = sum_j w_tj o[inv_tj] in slot order, eight values a thread.
@@ -82,22 +342,40 @@ __global__ void __launch_bounds__(256) group_sum_kernel(const uint16_t* __restri
   const int U = *n_unique;
   float acc[8] = {};
   if (U > 0 && U <= cap) {
-    for (int j = 0; j < k; ++j) {
-      const long long p = inv[static_cast<long long>(t) * k + j];
-      const float f = w[static_cast<long long>(t) * k + j];
-      if (p < 0 || p >= static_cast<long long>(T) * k) {
-        flag_error(dev_err, MOE_DEV_BAD_ID);
-        continue;
+    // Four terms' rows are asked for before the first is used.
+    for (int j0 = 0; j0 < k; j0 += 4) {
+      uint4 v[4];
+      float f[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[j] = 0.f, v[j] = make_uint4(0, 0, 0, 0);
+        if (j0 + j >= k) continue;
+        const long long p = inv[static_cast<long long>(t) * k + j0 + j];
+        if (p < 0 || p >= static_cast<long long>(T) * k) {
+          if (c == 0) flag_error(dev_err, MOE_DEV_BAD_ID);
+          continue;
+        }
+        f[j] = w[static_cast<long long>(t) * k + j0 + j];
+        v[j] = __ldg(reinterpret_cast<const uint4*>(o + p * H + c));
       }
-      const uint4 v = *reinterpret_cast<const uint4*>(o + p * H + c);
-      const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
-      for (int q = 0; q < 4; ++q) {
-        acc[2 * q] += f * __uint_as_float(vw[q] << 16);
-        acc[2 * q + 1] += f * __uint_as_float(vw[q] & 0xFFFF0000u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t vw[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          acc[2 * q] += f[j] * __uint_as_float(vw[q] << 16);
+          acc[2 * q + 1] += f[j] * __uint_as_float(vw[q] & 0xFFFF0000u);
+        }
       }
     }
   }
-  for (int q = 0; q < 8; ++q) y[static_cast<size_t>(t) * H + c + q] = acc[q] == acc[q] ? float_to_bf16_bits_rn(acc[q]) : 0x7FFF;
+  uint32_t r[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(acc[2 * q], acc[2 * q + 1]);
+    r[q] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint4*>(y + static_cast<size_t>(t) * H + c) = make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 int group_validate(const moe_layer_weights& lw, int T, int k, const void* w) {
@@ -113,6 +391,29 @@ int group_validate(const moe_layer_weights& lw, int T, int k, const void* w) {
                                                       : (2ll * lw.I > lw.H ? 2ll * lw.I : lw.H);
   if (weight_slots(lw) * per >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
+}
+
+// The maps of the weights and of the rows they multiply, and the launch.
+template <bool kGateUp>
+int group_launch(const moe_layer_weights& lw, const void* rows, int n_rows, const void* w, GroupArgs a, cudaStream_t s) {
+  a.tiled = lw.layout == MOE_LAYOUT_TILED;
+  a.MT = kGateUp ? (a.N + 127) / 128 : (a.N + 255) / 256;
+  a.stall = (test_stall_mask() & MOE_TEST_STALL_GROUP) != 0;
+  CUtensorMap wmap, xmap;
+  const uint64_t K = a.K, slots = a.n_slots;
+  const uint64_t tall = a.tiled ? slots * ((a.N + 127) / 128) * (K / 64) * (kGateUp ? 256 : 128) : slots * a.N * (kGateUp ? 2 : 1);
+  const uint64_t wd[2] = {a.tiled ? 64 : K, tall}, ws[1] = {a.tiled ? 128 : K * 2};
+  const uint64_t xd[2] = {K, static_cast<uint64_t>(n_rows)}, xs[1] = {K * 2};
+  const uint32_t wb[2] = {64, kGateUp ? 64u : 128u}, xb[2] = {64, 1};
+  if (!tc::make_bf16_map(&wmap, w, 2, wd, ws, wb) || !tc::make_bf16_map(&xmap, rows, 2, xd, xs, xb)) return MOE_ERR_CUDA;
+  const int e = allow_smem<group_kernel<kGateUp>>(kSmemBytes);
+  if (e != MOE_OK) return e;
+  // At most this many tiles (a chunk a full 256 rows, and one more for each expert).
+  const long long most = (a.rows / 256 + static_cast<long long>(a.cap)) * a.MT;
+  const int pairs = static_cast<int>(std::min<long long>(sm_count() / 2, most));
+  LaunchScope ls(kGateUp ? kProfGroupGateUp : kProfGroupDown, s);
+  group_kernel<kGateUp><<<2 * pairs, kThreads, kSmemBytes, s>>>(wmap, xmap, a);
+  return check_launch();
 }
 
 bool misaligned(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) & (n - 1); }
@@ -133,13 +434,11 @@ extern "C" int moe_group_gate_up(const void* x, int32_t T, int32_t k, const moe_
       misaligned(perm_token, 4) || misaligned(dev_err, 4))
     return MOE_ERR_ARG;
   const int rows = T * k, cap = lw->E < rows ? lw->E : rows;
-  const GroupArgs a{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(lw->w_gate_up), n_unique, unique, offsets, perm_token,
-                    slot_table(*lw), static_cast<uint16_t*>(h), dev_err, T, rows, lw->E, cap, weight_slots(*lw), lw->I, lw->H,
-                    lw->layout == MOE_LAYOUT_TILED};
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  LaunchScope ls(kProfGroupGateUp, s);
-  group_tile_kernel<true><<<dim3((lw->I + 63) / 64, cap), 256, 0, s>>>(a);
-  return check_launch();
+  GroupArgs a = {};
+  a.n_unique = n_unique, a.unique = unique, a.offsets = offsets, a.perm = perm_token, a.slot_of = slot_table(*lw);
+  a.out = static_cast<uint16_t*>(h), a.dev_err = dev_err;
+  a.T = T, a.rows = rows, a.E = lw->E, a.cap = cap, a.n_slots = weight_slots(*lw), a.N = lw->I, a.K = lw->H;
+  return group_launch<true>(*lw, x, T, lw->w_gate_up, a, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t moe_group_down_workspace(const moe_layer_weights* lw, int32_t T, int32_t k) {
@@ -164,15 +463,12 @@ extern "C" int moe_group_down(const void* h, int32_t T, int32_t k, const moe_lay
   if (misaligned(workspace, 256)) return MOE_ERR_ARG;
   const int rows = T * k, cap = lw->E < rows ? lw->E : rows;
   uint16_t* o = static_cast<uint16_t*>(workspace);
-  const GroupArgs a{static_cast<const uint16_t*>(h), static_cast<const uint16_t*>(lw->w_down), n_unique, unique, offsets, nullptr,
-                    slot_table(*lw), o, dev_err, T, rows, lw->E, cap, weight_slots(*lw), lw->H, lw->I, lw->layout == MOE_LAYOUT_TILED};
+  GroupArgs a = {};
+  a.n_unique = n_unique, a.unique = unique, a.offsets = offsets, a.slot_of = slot_table(*lw), a.out = o, a.dev_err = dev_err;
+  a.T = T, a.rows = rows, a.E = lw->E, a.cap = cap, a.n_slots = weight_slots(*lw), a.N = lw->H, a.K = lw->I;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  {
-    LaunchScope ls(kProfGroupDown, s);
-    group_tile_kernel<false><<<dim3((lw->H + 63) / 64, cap), 256, 0, s>>>(a);
-    const int e = check_launch();
-    if (e != MOE_OK) return e;
-  }
+  const int e = group_launch<false>(*lw, h, rows, lw->w_down, a, s);
+  if (e != MOE_OK) return e;
   LaunchScope ls(kProfGroupDown, s);
   const long long n = static_cast<long long>(T) * (lw->H / 8);
   group_sum_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(o, inv, w, n_unique, static_cast<uint16_t*>(y), T, k, lw->H, cap,

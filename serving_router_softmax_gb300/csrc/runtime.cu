@@ -142,7 +142,7 @@ extern "C" uint64_t moe_launch_count(void) { return moe::g_launches.load(); }
 
 extern "C" int moe_test_set_stall(int32_t mask) {
   constexpr int32_t kKnown = MOE_TEST_STALL_GATE_UP | MOE_TEST_STALL_READY_FLAG | MOE_TEST_STALL_KV4_ATTEND |
-                             MOE_TEST_STALL_KV4_FIRST | MOE_TEST_STALL_KV4_WEIGH;
+                             MOE_TEST_STALL_KV4_FIRST | MOE_TEST_STALL_KV4_WEIGH | MOE_TEST_STALL_GROUP | MOE_TEST_STALL_PROMPT;
   if (mask & ~kKnown) return MOE_ERR_ARG;
   moe::g_test_stall.store(mask, std::memory_order_relaxed);
   return MOE_OK;
