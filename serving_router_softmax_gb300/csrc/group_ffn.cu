@@ -9,9 +9,13 @@
 // weights and up to 16 KB of rows each; the sums are kept twice, so that a
 // tile's epilogue runs beside the next one's products.
 //
-// The group's rows are gathered by TMA where they lie: lane l of the loading
-// warp copies rows 4l .. 4l+3 of each stage (gate/up: the tokens' rows of x
-// through perm_token; down: the group's own rows of h).
+// The rows come by TMA in boxes of 16.  gate/up's are the tokens' rows of x
+// through perm_token, copied side by side into the workspace first (0.1 ms of
+// 1.4 for 65,536 rows of 4096).  Small groups (64 rows on the average, or fewer)
+// do without: lane l of the loading warp copies rows 4l .. 4l+3 of each stage out
+// of x by TMA's gather of four rows, which takes about 65 cycles each, nothing
+// beside the 700 that a stage's weights take from memory, but 2100 a stage for full
+// chunks whose products take 512 (3.63 ms for those 65,536 rows).
 //
 // Persistent: pair i takes tiles i, i + pairs, ..., in an order that has a
 // matrix's rows go over all of their group's chunks before the next rows come,
@@ -44,6 +48,7 @@ struct GroupArgs {
   int T, rows, E, cap, n_slots;
   int N, K;                   // rows of a matrix (gate/up: of one of its halves), reduction length
   int tiled, MT, stall;
+  int gather;                 // gate/up: rows straight out of x
 };
 
 struct Smem {
@@ -103,6 +108,34 @@ struct Walk {
   }
 };
 
+// gate/up's rows side by side: a warp a row.
+__global__ void __launch_bounds__(256) group_rows_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ n_unique,
+                                                         const int32_t* __restrict__ offsets, const int32_t* __restrict__ perm,
+                                                         uint4* __restrict__ xp, int T, int rows, int cap, int per, int32_t* dev_err) {
+  pdl_trigger();
+  const int U = *n_unique;
+  if (U < 1 || U > cap) return;
+  const int p0 = max(offsets[0], 0), p1 = min(offsets[U], rows), lane = threadIdx.x & 31;
+  for (int p = p0 + blockIdx.x * 8 + (threadIdx.x >> 5); p < p1; p += gridDim.x * 8) {
+    int t = perm[p];
+    if (t < 0 || t >= T) {
+      if (lane == 0) flag_error(dev_err, MOE_DEV_BAD_ID);
+      t = 0;
+    }
+    const uint4* src = x + static_cast<size_t>(t) * per;
+    uint4* dst = xp + static_cast<size_t>(p) * per;
+    for (int i = lane; i < per; i += 128) {
+      uint4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + 32 * j < per) v[j] = __ldg(src + i + 32 * j);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + 32 * j < per) dst[i + 32 * j] = v[j];
+    }
+  }
+}
+
 template <bool kGateUp>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     group_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, const GroupArgs a) {
@@ -155,6 +188,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc::cluster_sync();
   tc::tc_fence_after();
   const uint32_t tmem = sm.tmem;
+  if (kGateUp) tc::griddep_wait();  // the rows' copies
   const long long total = static_cast<long long>(before) * a.MT;
   const int KB = a.K / 64;
   volatile int* gave_up = &sm.abort;
@@ -174,7 +208,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 4; ++i) {
         const int r = min(static_cast<int>(rank) * half + 4 * lane + i, x.n - 1);
         row[i] = x.p + r;
-        if (kGateUp) {
+        if (kGateUp && a.gather) {
           row[i] = a.perm[x.p + r];
           if (row[i] < 0 || row[i] >= a.T) flag_error(a.dev_err, MOE_DEV_BAD_ID), row[i] = 0;
         }
@@ -206,7 +240,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               tc::tma_load_2d_pair(sm.a[s], &wmap, wx, wr, bar);
             }
           }
-          if (4 * lane < half) tc::tma_gather4_pair(sm.b[s] + lane * 512, &xmap, kb * 64, row, bar);
+          if (kGateUp && a.gather) {
+            if (4 * lane < half) tc::tma_gather4_pair(sm.b[s] + lane * 512, &xmap, kb * 64, row, bar);
+          } else if (16 * lane < half) {
+            tc::tma_load_2d_pair(sm.b[s] + lane * 2048, &xmap, kb * 64, x.p + static_cast<int>(rank) * half + 16 * lane, bar);
+          }
         }
         wr += step;
         if (!a.tiled) wx += 64;
@@ -232,10 +270,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (long long t = pair; t < total && ok; t += pairs) {
         walk.at(t, &x);
         const uint32_t idesc = tc::idesc_bf16_f32(256, x.N), d = tmem + acc * 256;
-        ok = tc::mbar_wait_bounded(&sm.acc_empty[acc], aph ^ 1, gave_up, kWaitNs);
+        ok = tc::mbar_wait_pair(&sm.acc_empty[acc], aph ^ 1, gave_up, kWaitNs);
         tc::tc_fence_after();
         for (int kb = 0; kb < KB && ok; ++kb) {
-          ok = tc::mbar_wait_bounded(&sm.full[s], ph, gave_up, kWaitNs);
+          ok = tc::mbar_wait_pair(&sm.full[s], ph, gave_up, kWaitNs);
           if (!ok) break;
           tc::tc_fence_after();
           const uint64_t ad = tc::smem_desc_sw128(tc::smem_u32(sm.a[s])), bd = tc::smem_desc_sw128(tc::smem_u32(sm.b[s]));
@@ -404,7 +442,7 @@ int group_launch(const moe_layer_weights& lw, const void* rows, int n_rows, cons
   const uint64_t tall = a.tiled ? slots * ((a.N + 127) / 128) * (K / 64) * (kGateUp ? 256 : 128) : slots * a.N * (kGateUp ? 2 : 1);
   const uint64_t wd[2] = {a.tiled ? 64 : K, tall}, ws[1] = {a.tiled ? 128 : K * 2};
   const uint64_t xd[2] = {K, static_cast<uint64_t>(n_rows)}, xs[1] = {K * 2};
-  const uint32_t wb[2] = {64, kGateUp ? 64u : 128u}, xb[2] = {64, 1};
+  const uint32_t wb[2] = {64, kGateUp ? 64u : 128u}, xb[2] = {64, a.gather ? 1u : 16u};
   if (!tc::make_bf16_map(&wmap, w, 2, wd, ws, wb) || !tc::make_bf16_map(&xmap, rows, 2, xd, xs, xb)) return MOE_ERR_CUDA;
   const int e = allow_smem<group_kernel<kGateUp>>(kSmemBytes);
   if (e != MOE_OK) return e;
@@ -412,18 +450,27 @@ int group_launch(const moe_layer_weights& lw, const void* rows, int n_rows, cons
   const long long most = (a.rows / 256 + static_cast<long long>(a.cap)) * a.MT;
   const int pairs = static_cast<int>(std::min<long long>(sm_count() / 2, most));
   LaunchScope ls(kGateUp ? kProfGroupGateUp : kProfGroupDown, s);
-  group_kernel<kGateUp><<<2 * pairs, kThreads, kSmemBytes, s>>>(wmap, xmap, a);
-  return check_launch();
+  return launch_k(group_kernel<kGateUp>, dim3(2 * pairs), dim3(kThreads), kSmemBytes, s, kGateUp && !a.gather, wmap, xmap, a);
 }
+
+// Whether gate/up's groups are small enough (on the average) to gather their rows in the product.
+bool gathers(long long rows, int cap) { return rows <= 64ll * cap; }
 
 bool misaligned(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) & (n - 1); }
 
 }  // namespace
 }  // namespace moe
 
+extern "C" size_t moe_group_gate_up_workspace(const moe_layer_weights* lw, int32_t T, int32_t k) {
+  using namespace moe;
+  if (!lw || group_validate(*lw, T, k, lw->w_gate_up) != MOE_OK) return 0;
+  const long long rows = static_cast<long long>(T) * k;
+  return 256 + (gathers(rows, static_cast<int>(std::min<long long>(lw->E, rows))) ? 0 : align_up(static_cast<size_t>(rows) * lw->H * 2, 256));
+}
+
 extern "C" int moe_group_gate_up(const void* x, int32_t T, int32_t k, const moe_layer_weights* lw, const int32_t* n_unique,
                                  const int32_t* unique, const int32_t* offsets, const int32_t* perm_token, void* h,
-                                 int32_t* dev_err, void* stream) {
+                                 void* workspace, size_t ws_bytes, int32_t* dev_err, void* stream) {
   using namespace moe;
   if (!lw) return MOE_ERR_ARG;
   const int st = group_validate(*lw, T, k, lw->w_gate_up);
@@ -433,12 +480,24 @@ extern "C" int moe_group_gate_up(const void* x, int32_t T, int32_t k, const moe_
   if (misaligned(x, 16) || misaligned(h, 16) || misaligned(n_unique, 4) || misaligned(unique, 4) || misaligned(offsets, 4) ||
       misaligned(perm_token, 4) || misaligned(dev_err, 4))
     return MOE_ERR_ARG;
+  if (!workspace || ws_bytes < moe_group_gate_up_workspace(lw, T, k)) return MOE_ERR_WORKSPACE;
+  if (misaligned(workspace, 256)) return MOE_ERR_ARG;
   const int rows = T * k, cap = lw->E < rows ? lw->E : rows;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
   GroupArgs a = {};
+  a.gather = gathers(rows, cap);
+  if (!a.gather) {
+    LaunchScope ls(kProfGroupGateUp, s);
+    const int blocks = static_cast<int>(std::min<long long>((rows + 7) / 8, sm_count() * 8ll));
+    group_rows_kernel<<<blocks, 256, 0, s>>>(static_cast<const uint4*>(x), n_unique, offsets, perm_token, static_cast<uint4*>(workspace), T,
+                                             rows, cap, lw->H / 8, dev_err);
+    const int e = check_launch();
+    if (e != MOE_OK) return e;
+  }
   a.n_unique = n_unique, a.unique = unique, a.offsets = offsets, a.perm = perm_token, a.slot_of = slot_table(*lw);
   a.out = static_cast<uint16_t*>(h), a.dev_err = dev_err;
   a.T = T, a.rows = rows, a.E = lw->E, a.cap = cap, a.n_slots = weight_slots(*lw), a.N = lw->I, a.K = lw->H;
-  return group_launch<true>(*lw, x, T, lw->w_gate_up, a, static_cast<cudaStream_t>(stream));
+  return a.gather ? group_launch<true>(*lw, x, T, lw->w_gate_up, a, s) : group_launch<true>(*lw, workspace, rows, lw->w_gate_up, a, s);
 }
 
 extern "C" size_t moe_group_down_workspace(const moe_layer_weights* lw, int32_t T, int32_t k) {
