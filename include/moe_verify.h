@@ -834,17 +834,14 @@ int moe_prompt_attend(const void* q, const void* k, const void* v, const int32_t
  *   h           [T * k, I] bf16 out, rows in the groups' order; rows that no
  *               group holds are left as they are.
  * fp32 accumulation on the tensor cores, one rounding per output.
- * Needs moe_group_gate_up_workspace() bytes (0: bad arguments), 256-byte aligned,
- * of any content, that no call running at the same time uses.
  * Limits: 0 <= T, T * k <= 2^22, 1 <= k <= 16, H and I multiples of 64, E <= 1024.
  * Device errors: MOE_DEV_CAPACITY (n_unique outside [0, min(E, T*k)]: nothing is
  * written), MOE_DEV_BAD_ID (an expert id, pool slot or group ends out of range:
  * that group's rows are not written; a token out of range: its row is that of
  * some token), MOE_DEV_TIMEOUT. */
-size_t moe_group_gate_up_workspace(const moe_layer_weights* lw, int32_t T, int32_t k);
 int moe_group_gate_up(const void* x, int32_t T, int32_t k, const moe_layer_weights* lw, const int32_t* n_unique,
                       const int32_t* unique, const int32_t* offsets, const int32_t* perm_token, void* h,
-                      void* workspace, size_t ws_bytes, int32_t* dev_err, void* stream);
+                      int32_t* dev_err, void* stream);
 
 /* moe_group_down -- y_t = sum_j w[t, j] * (W_down,e h[inv[t, j]]), e the expert
  * whose group holds that row: the second half.
@@ -852,7 +849,7 @@ int moe_group_gate_up(const void* x, int32_t T, int32_t k, const moe_layer_weigh
  *   inv, w      [T, k] int32 and fp32 as moe_union_permute and moe_route write them.
  *   y           [T, H] bf16 out.  The products, rounded to bf16 in the workspace,
  *               are summed in slot order in fp32 and rounded once.
- * Needs moe_group_down_workspace() bytes, as above.
+ * Needs moe_group_down_workspace() bytes (0: bad arguments), 256-byte aligned.
  * With n_unique outside its range (MOE_DEV_CAPACITY) or 0, y is zeros; a term whose inv is out
  * of range (MOE_DEV_BAD_ID) is left out.  Other limits and errors as above. */
 size_t moe_group_down_workspace(const moe_layer_weights* lw, int32_t T, int32_t k);

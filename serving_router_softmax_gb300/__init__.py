@@ -11,8 +11,7 @@ Importing it loads the library and raises if it has not been built.
 """
 from . import _lib
 from .kv4 import Kv4Cache, kv4_append, kv4_attend, kv4_attend_workspace_bytes, kv4_evict, kv4_read, kv4_weigh  # noqa: F401
-from .prompt import (Rotary, group_down, group_down_workspace_bytes, group_gate_up, group_gate_up_workspace_bytes,  # noqa: F401
-                     prompt_attend, rotate)
+from .prompt import Rotary, group_down, group_down_workspace_bytes, group_gate_up, prompt_attend, rotate  # noqa: F401
 from .api import (ExpertLayer, ExpertPool, MoEError, StepSpec, VerifyPlan, VerifyStep, depth_policy,  # noqa: F401
                   eco_select,
                   expert_bytes, ffn_workspace_bytes, hot_list, HostExperts, launch_count, new_dev_err, pack_tiled,

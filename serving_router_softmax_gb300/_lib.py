@@ -27,7 +27,7 @@ EXPORTED = ["s2_expand", "moe_router_logits", "moe_route", "moe_union_permute", 
             "moe_profile_end", "moe_status_str", "moe_launch_count", "moe_version", "moe_expert_bytes",
             "moe_stage_experts", "moe_test_set_stall", "moe_hot_list", "moe_depth_policy", "moe_set_nvtx",
             "kv4_append", "kv4_read", "kv4_attend_workspace", "kv4_attend", "kv4_weigh", "kv4_evict",
-            "moe_rotate", "moe_prompt_attend", "moe_group_gate_up_workspace", "moe_group_gate_up", "moe_group_down_workspace", "moe_group_down"]
+            "moe_rotate", "moe_prompt_attend", "moe_group_gate_up", "moe_group_down_workspace", "moe_group_down"]
 
 
 class S2Cfg(C.Structure):
@@ -187,9 +187,7 @@ def load(path: str = LIB_PATH) -> C.CDLL:
     lib.moe_rotate.restype = C.c_int
     lib.moe_prompt_attend.argtypes = [vp, vp, vp, vp, P(PromptCfg), vp, vp, vp, vp]
     lib.moe_prompt_attend.restype = C.c_int
-    lib.moe_group_gate_up_workspace.argtypes = [P(LayerWeights), i32, i32]
-    lib.moe_group_gate_up_workspace.restype = sz
-    lib.moe_group_gate_up.argtypes = [vp, i32, i32, P(LayerWeights), vp, vp, vp, vp, vp, vp, sz, vp, vp]
+    lib.moe_group_gate_up.argtypes = [vp, i32, i32, P(LayerWeights), vp, vp, vp, vp, vp, vp, vp]
     lib.moe_group_gate_up.restype = C.c_int
     lib.moe_group_down_workspace.argtypes = [P(LayerWeights), i32, i32]
     lib.moe_group_down_workspace.restype = sz

@@ -9,21 +9,21 @@
 // weights and up to 16 KB of rows each; the sums are kept twice, so that a
 // tile's epilogue runs beside the next one's products.
 //
-// The rows come by TMA in boxes of 16.  gate/up's are the tokens' rows of x
-// through perm_token, copied side by side into the workspace first (0.1 ms of
-// 1.4 for 65,536 rows of 4096).  Small groups (64 rows on the average, or fewer)
-// do without: lane l of the loading warp copies rows 4l .. 4l+3 of each stage out
-// of x by TMA's gather of four rows, which takes about 65 cycles each, nothing
-// beside the 700 that a stage's weights take from memory, but 2100 a stage for full
-// chunks whose products take 512 (3.63 ms for those 65,536 rows).
+// The rows come by TMA where they lie: down's in one box a stage (a map for each
+// multiple of 16 rows), gate/up's, the tokens' rows of x through perm_token, by
+// its gather of four rows a copy.  What a bulk copy costs is its thread's time,
+// 65 cycles and more, so eight warps share the gather's 32 copies of a stage.
+// (One warp: 3.63 ms for 65,536 rows of 4096 x 1536 matrices; four warps: 1.31.
+// Rows copied side by side first: 0.1 ms for that alone.)
 //
 // Persistent: pair i takes tiles i, i + pairs, ..., in an order that has a
 // matrix's rows go over all of their group's chunks before the next rows come,
 // and an expert's before the next expert's: what runs at the same time shares
 // weights and rows in L2.
 //
-// Roles of a CTA: warp 0 loads, warp 1 owns TMEM and (in the pair's first CTA)
-// issues the products, warps 2-5 take the sums out.  Every wait is bounded.
+// Roles of a CTA: warp 0 loads weights, warp 1 owns TMEM and (in the pair's first
+// CTA) issues the products, warps 2-5 take the sums out, the warps from 6 on load
+// rows.  Every wait is bounded.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -35,7 +35,8 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 192;
+template <bool kGateUp>
+constexpr int kThreads = 192 + (kGateUp ? 256 : 32);
 constexpr int kStages = 6;
 constexpr int kABytes = 128 * 128, kBBytes = 128 * 128;
 constexpr int kMaxU = 1024;
@@ -48,7 +49,11 @@ struct GroupArgs {
   int T, rows, E, cap, n_slots;
   int N, K;                   // rows of a matrix (gate/up: of one of its halves), reduction length
   int tiled, MT, stall;
-  int gather;                 // gate/up: rows straight out of x
+};
+
+// Maps of the rows with boxes of 16, 32, ... 128 of them (gate/up: the first, of one).
+struct RowMaps {
+  CUtensorMap m[8];
 };
 
 struct Smem {
@@ -59,7 +64,7 @@ struct Smem {
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
   int abort;
-  int part[kThreads / 32];
+  int part[14];
 };
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -108,37 +113,20 @@ struct Walk {
   }
 };
 
-// gate/up's rows side by side: a warp a row.
-__global__ void __launch_bounds__(256) group_rows_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ n_unique,
-                                                         const int32_t* __restrict__ offsets, const int32_t* __restrict__ perm,
-                                                         uint4* __restrict__ xp, int T, int rows, int cap, int per, int32_t* dev_err) {
-  pdl_trigger();
-  const int U = *n_unique;
-  if (U < 1 || U > cap) return;
-  const int p0 = max(offsets[0], 0), p1 = min(offsets[U], rows), lane = threadIdx.x & 31;
-  for (int p = p0 + blockIdx.x * 8 + (threadIdx.x >> 5); p < p1; p += gridDim.x * 8) {
-    int t = perm[p];
-    if (t < 0 || t >= T) {
-      if (lane == 0) flag_error(dev_err, MOE_DEV_BAD_ID);
-      t = 0;
-    }
-    const uint4* src = x + static_cast<size_t>(t) * per;
-    uint4* dst = xp + static_cast<size_t>(p) * per;
-    for (int i = lane; i < per; i += 128) {
-      uint4 v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (i + 32 * j < per) v[j] = __ldg(src + i + 32 * j);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (i + 32 * j < per) dst[i + 32 * j] = v[j];
-    }
+// A loading warp's way out.  Copies in flight land in microseconds; nothing tells this CTA of those that report to the other one.
+__device__ __noinline__ void give_up_loading(Smem& sm, const GroupArgs& a, int lane) {
+  if (lane == 0) {
+    *static_cast<volatile int*>(&sm.abort) = 1;
+    flag_error(a.dev_err, MOE_DEV_TIMEOUT);
+    const uint64_t t0 = tc::globaltimer_ns();
+    while (tc::globaltimer_ns() - t0 < 5000000ull) __nanosleep(1000);
   }
+  __syncwarp();
 }
 
 template <bool kGateUp>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    group_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, const GroupArgs a) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kGateUp>, 1)
+    group_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ RowMaps xmap, const GroupArgs a) {
   extern __shared__ uint8_t raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -162,7 +150,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int U = counted ? U0 : 0;
   if (!counted && blockIdx.x == 0 && tid == 0) flag_error(a.dev_err, MOE_DEV_CAPACITY);
   int before = 0;
-  for (int base = 0; base < U; base += kThreads) {
+  for (int base = 0; base < U; base += kThreads<kGateUp>) {
     const int u = base + tid;
     int c = 0;
     if (u < U) {
@@ -175,7 +163,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 31) sm.part[warp] = inc;
     __syncthreads();
     int sum = before;
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < kThreads<kGateUp> / 32; ++w) {
       if (w < warp) sum += sm.part[w];
       before += sm.part[w];
     }
@@ -188,7 +176,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc::cluster_sync();
   tc::tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  if (kGateUp) tc::griddep_wait();  // the rows' copies
   const long long total = static_cast<long long>(before) * a.MT;
   const int KB = a.K / 64;
   volatile int* gave_up = &sm.abort;
@@ -196,71 +183,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   Tile x;
 
   if (warp == 0) {
-    // ---------------------------------------------------------- loads
+    // ---------------------------------------------------------- weights
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
     for (long long t = pair; t < total && ok; t += pairs) {
       walk.at(t, &x);
-      const int half = x.N / 2;
-      int row[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = min(static_cast<int>(rank) * half + 4 * lane + i, x.n - 1);
-        row[i] = x.p + r;
-        if (kGateUp && a.gather) {
-          row[i] = a.perm[x.p + r];
-          if (row[i] < 0 || row[i] >= a.T) flag_error(a.dev_err, MOE_DEV_BAD_ID), row[i] = 0;
-        }
-      }
-      const uint32_t bytes = 2u * (kABytes + half * 128);
-      // First weight row of the tile in the map, and rows from one block of columns to the next.
-      int wr, step, wx = 0;
-      if (a.tiled) {
-        const int block = kGateUp ? (x.slot * a.MT + x.m) * KB : (x.slot * ((a.N + 127) / 128) + 2 * x.m + static_cast<int>(rank)) * KB;
-        wr = block * (kGateUp ? 256 : 128) + (kGateUp ? static_cast<int>(rank) * 64 : 0);
-        step = kGateUp ? 256 : 128;
+      const uint32_t bytes = 2u * (kABytes + x.N / 2 * 128);
+      // Where the tile's rows begin in the map, and its steps from one block of columns to the next.
+      int wx = 0, wy, wz = 0, dx = 0, dy = 0, dz = 0;
+      const int r = static_cast<int>(rank);
+      if (kGateUp) {
+        wy = r * 64 + (a.tiled ? 0 : x.m * 128);
+        wz = 2 * (a.tiled ? (x.slot * a.MT + x.m) * KB : x.slot);
+        (a.tiled ? dz : dx) = a.tiled ? 2 : 64;
       } else {
-        wr = kGateUp ? x.slot * 2 * a.N + x.m * 128 + static_cast<int>(rank) * 64 : x.slot * a.N + x.m * 256 + static_cast<int>(rank) * 128;
-        step = 0;
+        wy = a.tiled ? (x.slot * ((a.N + 127) / 128) + 2 * x.m + r) * KB * 128 : x.slot * a.N + x.m * 256 + r * 128;
+        (a.tiled ? dy : dx) = a.tiled ? 128 : 64;
       }
-      const int up = a.tiled ? 128 : a.N;
       for (int kb = 0; kb < KB; ++kb) {
         ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait_bounded(&sm.empty[s], ph ^ 1, gave_up, kWaitNs));
         if (!ok) break;
-        const uint32_t bar = tc::smem_of(&sm.full[s], 0);
-        if (lane == 0 && rank == 0) tc::mbar_arrive_expect_tx(&sm.full[s], bytes);
-        __syncwarp();
-        if (!a.stall) {
-          if (lane == 0) {
-            if (kGateUp) {
-              tc::tma_load_2d_pair(sm.a[s], &wmap, wx, wr, bar);
-              tc::tma_load_2d_pair(sm.a[s] + 64 * 128, &wmap, wx, wr + up, bar);
-            } else {
-              tc::tma_load_2d_pair(sm.a[s], &wmap, wx, wr, bar);
-            }
-          }
-          if (kGateUp && a.gather) {
-            if (4 * lane < half) tc::tma_gather4_pair(sm.b[s] + lane * 512, &xmap, kb * 64, row, bar);
-          } else if (16 * lane < half) {
-            tc::tma_load_2d_pair(sm.b[s] + lane * 2048, &xmap, kb * 64, x.p + static_cast<int>(rank) * half + 16 * lane, bar);
+        if (lane == 0) {
+          if (rank == 0) tc::mbar_arrive_expect_tx(&sm.full[s], bytes);
+          const uint32_t bar = tc::smem_of(&sm.full[s], 0);
+          if (!a.stall) {
+            if (kGateUp)
+              tc::tma_load_3d_pair(sm.a[s], &wmap, wx, wy, wz, bar);
+            else
+              tc::tma_load_2d_pair(sm.a[s], &wmap, wx, wy, bar);
           }
         }
-        wr += step;
-        if (!a.tiled) wx += 64;
+        __syncwarp();
+        wx += dx, wy += dy, wz += dz;
         if (++s == kStages) s = 0, ph ^= 1;
       }
     }
-    if (!ok) {
-      // Copies in flight land in microseconds; nothing tells this CTA of those that report to the other one.
-      if (lane == 0) {
-        *gave_up = 1;
-        flag_error(a.dev_err, MOE_DEV_TIMEOUT);
-        const uint64_t t0 = tc::globaltimer_ns();
-        while (tc::globaltimer_ns() - t0 < 5000000ull) __nanosleep(1000);
-      }
-      __syncwarp();
-    }
+    if (!ok) give_up_loading(sm, a, lane);
   } else if (warp == 1) {
     // ---------------------------------------------------------- products
     if (rank == 0 && lane == 0) {
@@ -294,6 +253,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
+  } else if (warp >= 6) {
+    // ---------------------------------------------------------- rows
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (long long t = pair; t < total && ok; t += pairs) {
+      walk.at(t, &x);
+      const int half = x.N / 2, first = static_cast<int>(rank) * half;
+      const int four = (warp - 6) * 4 + lane;  // gate/up: rows 4 four .. 4 four + 3, by lanes 0-3
+      const bool mine = kGateUp ? lane < 4 && 4 * four < half : lane == 0;
+      int row[4] = {x.p + first, 0, 0, 0};
+      if (kGateUp && mine) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          row[i] = a.perm[x.p + min(first + 4 * four + i, x.n - 1)];  // the last row stands in for those behind it
+          if (row[i] < 0 || row[i] >= a.T) flag_error(a.dev_err, MOE_DEV_BAD_ID), row[i] = 0;
+        }
+      }
+      const CUtensorMap* map = &xmap.m[kGateUp ? 0 : half / 16 - 1];
+      for (int kb = 0; kb < KB; ++kb) {
+        ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait_bounded(&sm.empty[s], ph ^ 1, gave_up, kWaitNs));
+        if (!ok) break;
+        if (mine && !a.stall) {
+          const uint32_t bar = tc::smem_of(&sm.full[s], 0);
+          if (kGateUp)
+            tc::tma_gather4_pair(sm.b[s] + four * 512, map, kb * 64, row, bar);
+          else
+            tc::tma_load_2d_pair(sm.b[s], map, kb * 64, row[0], bar);
+        }
+        __syncwarp();
+        if (++s == kStages) s = 0, ph ^= 1;
+      }
+    }
+    if (!ok) give_up_loading(sm, a, lane);
   } else {
     // ---------------------------------------------------------- sums out
     const int q = warp & 3;
@@ -437,40 +430,38 @@ int group_launch(const moe_layer_weights& lw, const void* rows, int n_rows, cons
   a.tiled = lw.layout == MOE_LAYOUT_TILED;
   a.MT = kGateUp ? (a.N + 127) / 128 : (a.N + 255) / 256;
   a.stall = (test_stall_mask() & MOE_TEST_STALL_GROUP) != 0;
-  CUtensorMap wmap, xmap;
+  CUtensorMap wmap;
+  RowMaps xmap = {};
   const uint64_t K = a.K, slots = a.n_slots;
-  const uint64_t tall = a.tiled ? slots * ((a.N + 127) / 128) * (K / 64) * (kGateUp ? 256 : 128) : slots * a.N * (kGateUp ? 2 : 1);
-  const uint64_t wd[2] = {a.tiled ? 64 : K, tall}, ws[1] = {a.tiled ? 128 : K * 2};
+  // gate/up: rows of a half, then the halves (of every slot, or of every block of a slot): a box takes 64 of both.
+  const uint64_t blocks = slots * ((a.N + 127) / 128) * (K / 64);
+  const uint64_t N = a.N, wide = a.tiled ? 64 : K, high = kGateUp ? (a.tiled ? 128 : N) : a.tiled ? blocks * 128 : slots * N;
+  const uint64_t wd[3] = {wide, high, 2 * (a.tiled ? blocks : slots)}, ws[2] = {wide * 2, wide * high * 2};
   const uint64_t xd[2] = {K, static_cast<uint64_t>(n_rows)}, xs[1] = {K * 2};
-  const uint32_t wb[2] = {64, kGateUp ? 64u : 128u}, xb[2] = {64, a.gather ? 1u : 16u};
-  if (!tc::make_bf16_map(&wmap, w, 2, wd, ws, wb) || !tc::make_bf16_map(&xmap, rows, 2, xd, xs, xb)) return MOE_ERR_CUDA;
+  const uint32_t wb[3] = {64, kGateUp ? 64u : 128u, 2};
+  if (!tc::make_bf16_map(&wmap, w, kGateUp ? 3 : 2, wd, ws, wb)) return MOE_ERR_CUDA;
+  for (uint32_t i = 0; i < (kGateUp ? 1 : 8); ++i) {
+    const uint32_t xb[2] = {64, kGateUp ? 1 : 16 * (i + 1)};
+    if (!tc::make_bf16_map(&xmap.m[i], rows, 2, xd, xs, xb)) return MOE_ERR_CUDA;
+  }
   const int e = allow_smem<group_kernel<kGateUp>>(kSmemBytes);
   if (e != MOE_OK) return e;
   // At most this many tiles (a chunk a full 256 rows, and one more for each expert).
   const long long most = (a.rows / 256 + static_cast<long long>(a.cap)) * a.MT;
   const int pairs = static_cast<int>(std::min<long long>(sm_count() / 2, most));
   LaunchScope ls(kGateUp ? kProfGroupGateUp : kProfGroupDown, s);
-  return launch_k(group_kernel<kGateUp>, dim3(2 * pairs), dim3(kThreads), kSmemBytes, s, kGateUp && !a.gather, wmap, xmap, a);
+  group_kernel<kGateUp><<<2 * pairs, kThreads<kGateUp>, kSmemBytes, s>>>(wmap, xmap, a);
+  return check_launch();
 }
-
-// Whether gate/up's groups are small enough (on the average) to gather their rows in the product.
-bool gathers(long long rows, int cap) { return rows <= 64ll * cap; }
 
 bool misaligned(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) & (n - 1); }
 
 }  // namespace
 }  // namespace moe
 
-extern "C" size_t moe_group_gate_up_workspace(const moe_layer_weights* lw, int32_t T, int32_t k) {
-  using namespace moe;
-  if (!lw || group_validate(*lw, T, k, lw->w_gate_up) != MOE_OK) return 0;
-  const long long rows = static_cast<long long>(T) * k;
-  return 256 + (gathers(rows, static_cast<int>(std::min<long long>(lw->E, rows))) ? 0 : align_up(static_cast<size_t>(rows) * lw->H * 2, 256));
-}
-
 extern "C" int moe_group_gate_up(const void* x, int32_t T, int32_t k, const moe_layer_weights* lw, const int32_t* n_unique,
                                  const int32_t* unique, const int32_t* offsets, const int32_t* perm_token, void* h,
-                                 void* workspace, size_t ws_bytes, int32_t* dev_err, void* stream) {
+                                 int32_t* dev_err, void* stream) {
   using namespace moe;
   if (!lw) return MOE_ERR_ARG;
   const int st = group_validate(*lw, T, k, lw->w_gate_up);
@@ -480,24 +471,12 @@ extern "C" int moe_group_gate_up(const void* x, int32_t T, int32_t k, const moe_
   if (misaligned(x, 16) || misaligned(h, 16) || misaligned(n_unique, 4) || misaligned(unique, 4) || misaligned(offsets, 4) ||
       misaligned(perm_token, 4) || misaligned(dev_err, 4))
     return MOE_ERR_ARG;
-  if (!workspace || ws_bytes < moe_group_gate_up_workspace(lw, T, k)) return MOE_ERR_WORKSPACE;
-  if (misaligned(workspace, 256)) return MOE_ERR_ARG;
   const int rows = T * k, cap = lw->E < rows ? lw->E : rows;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   GroupArgs a = {};
-  a.gather = gathers(rows, cap);
-  if (!a.gather) {
-    LaunchScope ls(kProfGroupGateUp, s);
-    const int blocks = static_cast<int>(std::min<long long>((rows + 7) / 8, sm_count() * 8ll));
-    group_rows_kernel<<<blocks, 256, 0, s>>>(static_cast<const uint4*>(x), n_unique, offsets, perm_token, static_cast<uint4*>(workspace), T,
-                                             rows, cap, lw->H / 8, dev_err);
-    const int e = check_launch();
-    if (e != MOE_OK) return e;
-  }
   a.n_unique = n_unique, a.unique = unique, a.offsets = offsets, a.perm = perm_token, a.slot_of = slot_table(*lw);
   a.out = static_cast<uint16_t*>(h), a.dev_err = dev_err;
   a.T = T, a.rows = rows, a.E = lw->E, a.cap = cap, a.n_slots = weight_slots(*lw), a.N = lw->I, a.K = lw->H;
-  return a.gather ? group_launch<true>(*lw, x, T, lw->w_gate_up, a, s) : group_launch<true>(*lw, workspace, rows, lw->w_gate_up, a, s);
+  return group_launch<true>(*lw, x, T, lw->w_gate_up, a, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t moe_group_down_workspace(const moe_layer_weights* lw, int32_t T, int32_t k) {

@@ -160,22 +160,8 @@ def _layer(dev: int, layer: ExpertLayer) -> L.LayerWeights:
     return layer.struct()
 
 
-def _bytes(dev: int, workspace: Optional[torch.Tensor], need: int, like: torch.Tensor) -> torch.Tensor:
-    if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=like.device)
-    if workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
-        raise MoEError(f"workspace: expected contiguous bytes (uint8) on cuda:{dev}")
-    return workspace
-
-
-def group_gate_up_workspace_bytes(layer: ExpertLayer, T: int, k: int) -> int:
-    """Bytes of workspace that group_gate_up needs for T tokens of k experts each."""
-    st = layer.struct()
-    return int(L.load().moe_group_gate_up_workspace(C.byref(st), T, k))
-
-
 def group_gate_up(x: torch.Tensor, layer: ExpertLayer, union: Dict[str, torch.Tensor], k: int, out: Optional[torch.Tensor] = None,
-                  workspace: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                  dev_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """h [T * k, I] bf16: silu(W_gate x) * (W_up x) for every row of the groups of ``union`` (``union_permute``'s, for the
     same T tokens' k experts), in the groups' order.  ``x`` [T, H] bf16, any T; ``layer``: bf16, either layout."""
     if x.dim() != 2 or x.shape[1] != layer.H:
@@ -187,11 +173,9 @@ def group_gate_up(x: torch.Tensor, layer: ExpertLayer, union: Dict[str, torch.Te
             raise MoEError("k < 1")
         st = _layer(dev, layer)
         h = torch.empty((T * k, layer.I), dtype=torch.bfloat16, device=x.device) if out is None else out
-        ws = _bytes(dev, workspace, L.load().moe_group_gate_up_workspace(C.byref(st), T, k), x)
         args = _union_args(dev, union, ("n_unique", "unique", "offsets", "perm_token"), T * k, layer.E)
         _check(L.load().moe_group_gate_up(_arg(dev, x, torch.bfloat16, x.shape, "x"), T, k, C.byref(st), *args,
-                                          _arg(dev, h, torch.bfloat16, (T * k, layer.I), "out"), ws.data_ptr(), ws.numel(),
-                                          _err(dev, dev_err), _raw_stream(dev)),
+                                          _arg(dev, h, torch.bfloat16, (T * k, layer.I), "out"), _err(dev, dev_err), _raw_stream(dev)),
                "moe_group_gate_up")
         return h
 
@@ -217,7 +201,11 @@ def group_down(h: torch.Tensor, layer: ExpertLayer, union: Dict[str, torch.Tenso
             raise MoEError("w: expected [T, k]")
         st = _layer(dev, layer)
         o = torch.empty((T, layer.H), dtype=torch.bfloat16, device=h.device) if y is None else y
-        ws = _bytes(dev, workspace, L.load().moe_group_down_workspace(C.byref(st), T, k), h)
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(int(L.load().moe_group_down_workspace(C.byref(st), T, k)), dtype=torch.uint8, device=h.device)
+        elif ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
+            raise MoEError(f"workspace: expected contiguous bytes (uint8) on cuda:{dev}")
         args = _union_args(dev, union, ("n_unique", "unique", "offsets", "inv"), T * k, layer.E)
         _check(L.load().moe_group_down(_arg(dev, h, torch.bfloat16, (T * k, layer.I), "h"), T, k, C.byref(st), *args,
                                        _arg(dev, w, torch.float32, (T, k), "w"), _arg(dev, o, torch.bfloat16, (T, layer.H), "y"),

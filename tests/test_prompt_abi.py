@@ -93,8 +93,8 @@ def layer(pool=None, **kw):
     return L.LayerWeights(pool=None if pool is None else C.pointer(pool), **f)
 
 
-def gate_up(lib, lw, T=300, k=2, x=FAKE, n=FAKE, u=FAKE, o=FAKE, p=FAKE, h=FAKE, ws=FAKE, size=1 << 40, err=None):
-    return lib.moe_group_gate_up(x, T, k, None if lw is None else C.byref(lw), n, u, o, p, h, ws, size, err, None)
+def gate_up(lib, lw, T=300, k=2, x=FAKE, n=FAKE, u=FAKE, o=FAKE, p=FAKE, h=FAKE, err=None):
+    return lib.moe_group_gate_up(x, T, k, None if lw is None else C.byref(lw), n, u, o, p, h, err, None)
 
 
 def down(lib, lw, T=300, k=2, h=FAKE, n=FAKE, u=FAKE, o=FAKE, p=FAKE, w=FAKE, y=FAKE, ws=FAKE, size=1 << 40, err=None):
@@ -114,12 +114,11 @@ def test_group_refusals(lib, kw, T, k, want):
     assert gate_up(lib, layer(**kw), T, k) == want
     assert down(lib, layer(**kw), T, k) == want
     assert lib.moe_group_down_workspace(C.byref(layer(**kw)), T, k) == 0
-    assert lib.moe_group_gate_up_workspace(C.byref(layer(**kw)), T, k) == 0
 
 
 def test_group_pointers(lib):
     assert gate_up(lib, None) == L.MOE_ERR_ARG and down(lib, None) == L.MOE_ERR_ARG
-    assert lib.moe_group_down_workspace(None, 4, 2) == 0 and lib.moe_group_gate_up_workspace(None, 4, 2) == 0
+    assert lib.moe_group_down_workspace(None, 4, 2) == 0
     for call, names, wide in ((gate_up, "xnuoph", "xh"), (down, "hnuopwy", "hy")):
         for name in names:
             assert call(lib, layer(), **{name: None}) == L.MOE_ERR_ARG, name
@@ -127,13 +126,10 @@ def test_group_pointers(lib):
         assert call(lib, layer(), err=FAKE + 1) == L.MOE_ERR_ARG
     need = lib.moe_group_down_workspace(C.byref(layer()), 300, 2)
     assert need >= 300 * 2 * 128 * 2
-    assert lib.moe_group_gate_up_workspace(C.byref(layer()), 300, 2) >= 300 * 2 * 128 * 2  # more than 64 rows an expert
-    assert 0 < lib.moe_group_gate_up_workspace(C.byref(layer()), 256, 2) < 4096
-    for call, size in ((down, need), (gate_up, lib.moe_group_gate_up_workspace(C.byref(layer()), 300, 2))):
-        assert call(lib, layer(), size=size - 1) == L.MOE_ERR_WORKSPACE
-        assert call(lib, layer(), ws=None) == L.MOE_ERR_WORKSPACE
-        assert call(lib, layer(), ws=FAKE + 128) == L.MOE_ERR_ARG
-    assert gate_up(lib, layer(), T=0, x=None, ws=None) == L.MOE_OK and down(lib, layer(), T=0, h=None, ws=None) == L.MOE_OK
+    assert down(lib, layer(), size=need - 1) == L.MOE_ERR_WORKSPACE
+    assert down(lib, layer(), ws=None) == L.MOE_ERR_WORKSPACE
+    assert down(lib, layer(), ws=FAKE + 128) == L.MOE_ERR_ARG
+    assert gate_up(lib, layer(), T=0, x=None) == L.MOE_OK and down(lib, layer(), T=0, h=None, ws=None) == L.MOE_OK
 
 
 def test_structs_match_the_header(tmp_path):
