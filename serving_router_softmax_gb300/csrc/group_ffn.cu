@@ -59,6 +59,7 @@ struct RowMaps {
 struct Smem {
   alignas(1024) uint8_t a[kStages][kABytes];
   alignas(1024) uint8_t b[kStages][kBBytes];
+  alignas(16) uint16_t turn[4][32][32];
   float swap[2][4][16][32];   // gate/up: what a warp hands to its partner, twice
   int cum[kMaxU + 1];         // chunks before each expert of the union
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drain;
@@ -202,7 +203,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kGateUp>, 1
         (a.tiled ? dy : dx) = a.tiled ? 128 : 64;
       }
       for (int kb = 0; kb < KB; ++kb) {
-        ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait_bounded(&sm.empty[s], ph ^ 1, gave_up, kWaitNs));
+        ok = tc::mbar_sleep<true>(&sm.empty[s], ph ^ 1, gave_up, kWaitNs);
         if (!ok) break;
         if (lane == 0) {
           if (rank == 0) tc::mbar_arrive_expect_tx(&sm.full[s], bytes);
@@ -225,21 +226,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kGateUp>, 1
     if (rank == 0 && lane == 0) {
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
-      bool ok = true;
+      bool ok = true, there = false;
+      const uint64_t ad0 = tc::smem_desc_sw128(tc::smem_u32(sm.a[0])), bd0 = tc::smem_desc_sw128(tc::smem_u32(sm.b[0]));
       for (long long t = pair; t < total && ok; t += pairs) {
         walk.at(t, &x);
         const uint32_t idesc = tc::idesc_bf16_f32(256, x.N), d = tmem + acc * 256;
-        ok = tc::mbar_wait_pair(&sm.acc_empty[acc], aph ^ 1, gave_up, kWaitNs);
+        ok = tc::mbar_sleep<false>(&sm.acc_empty[acc], aph ^ 1, gave_up, kWaitNs);
         tc::tc_fence_after();
-        for (int kb = 0; kb < KB && ok; ++kb) {
-          ok = tc::mbar_wait_pair(&sm.full[s], ph, gave_up, kWaitNs);
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!there && ok) ok = tc::mbar_sleep<false>(&sm.full[s], ph, gave_up, kWaitNs);
           if (!ok) break;
           tc::tc_fence_after();
-          const uint64_t ad = tc::smem_desc_sw128(tc::smem_u32(sm.a[s])), bd = tc::smem_desc_sw128(tc::smem_u32(sm.b[s]));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tc::mma_bf16_pair(d, ad + 2 * i, bd + 2 * i, idesc, kb || i);
-          tc::mma_commit_pair(&sm.empty[s]);
+          const uint64_t ad = ad0 + s * (kABytes >> 4), bd = bd0 + s * (kBBytes >> 4);
+          uint64_t* done = &sm.empty[s];
           if (++s == kStages) s = 0, ph ^= 1;
+          tc::mma_bf16_pair(d, ad, bd, idesc, kb);
+          tc::mma_bf16_pair(d, ad + 2, bd + 2, idesc, 1);
+          // The look at the next stage's barrier (100 cycles) runs beside the products.
+          there = tc::mbar_test(&sm.full[s], ph);
+          tc::mma_bf16_pair(d, ad + 4, bd + 4, idesc, 1);
+          tc::mma_bf16_pair(d, ad + 6, bd + 6, idesc, 1);
+          tc::mma_commit_pair(done);
         }
         if (ok) tc::mma_commit_pair(&sm.acc_full[acc]);
         if (++acc == 2) acc = 0, aph ^= 1;
@@ -273,7 +280,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kGateUp>, 1
       }
       const CUtensorMap* map = &xmap.m[kGateUp ? 0 : half / 16 - 1];
       for (int kb = 0; kb < KB; ++kb) {
-        ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait_bounded(&sm.empty[s], ph ^ 1, gave_up, kWaitNs));
+        ok = tc::mbar_sleep<true>(&sm.empty[s], ph ^ 1, gave_up, kWaitNs);
         if (!ok) break;
         if (mine && !a.stall) {
           const uint32_t bar = tc::smem_of(&sm.full[s], 0);
@@ -296,8 +303,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kGateUp>, 1
     bool ok = true;
     for (long long t = pair; t < total && ok; t += pairs) {
       walk.at(t, &x);
-      ok = tc::mbar_wait_bounded(&sm.acc_full[acc], aph, gave_up, kWaitNs);
-      ok = __all_sync(0xFFFFFFFFu, ok);
+      ok = tc::mbar_sleep<true>(&sm.acc_full[acc], aph, gave_up, kWaitNs);
       // (Partners give up together: a barrier is between them.)
       if (kGateUp) {
         int both;
@@ -308,40 +314,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kGateUp>, 1
       if (!ok) break;
       tc::tc_fence_after();
       const uint32_t src = tmem + acc * 256 + lanes;
-      uint16_t* out = a.out + static_cast<size_t>(x.p) * a.N;
-      if (kGateUp) {
-        const int i = x.m * 128 + static_cast<int>(rank) * 64 + (q & 1) * 32 + lane;
-        for (int c = 0; c < x.N; c += 32) {
-          float v0[16], v1[16];
-          tc::tmem_ld16(src + c, v0);
-          tc::tmem_ld16(src + c + 16, v1);
-          tc::tmem_ld_wait();
+      // 32 output columns of this warp, for all of the chunk's rows.
+      const int i0 = kGateUp ? x.m * 128 + static_cast<int>(rank) * 64 + (q & 1) * 32 : x.m * 256 + static_cast<int>(rank) * 128 + q * 32;
+      uint16_t* out = a.out + static_cast<size_t>(x.p) * a.N + i0;
+      uint16_t(&turn)[32][32] = sm.turn[warp - 2];
+      for (int c = 0; c < x.N; c += 32) {
+        float v0[16], v1[16];
+        tc::tmem_ld16(src + c, v0);
+        tc::tmem_ld16(src + c + 16, v1);
+        tc::tmem_ld_wait();
+        // A lane has one output column and the chunk's rows side by side: through shared memory, so that a store takes 16
+        // bytes of a row (two-byte stores took 68 cycles each, as long as a tile's products).
+        __syncwarp();
+        if (kGateUp) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) sm.swap[flip][q][j][lane] = q < 2 ? v1[j] : v0[j];
           tc::named_bar_sync(1 + (q & 1), 64);
-          const int c0 = c + (q < 2 ? 0 : 16);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const float other = sm.swap[flip][q ^ 2][j][lane];
             const float g = q < 2 ? v0[j] : other, w = q < 2 ? other : v1[j];
-            const float h = __fdividef(g, 1.f + __expf(-g)) * w;
-            if (c0 + j < x.n && i < a.N) out[static_cast<size_t>(c0 + j) * a.N + i] = __bfloat16_as_ushort(__float2bfloat16_rn(h));
+            turn[j][lane] = __bfloat16_as_ushort(__float2bfloat16_rn(__fdividef(g, 1.f + __expf(-g)) * w));
           }
           flip ^= 1;
-        }
-      } else {
-        const int i = x.m * 256 + static_cast<int>(rank) * 128 + q * 32 + lane;
-        for (int c = 0; c < x.N; c += 32) {
-          float v0[16], v1[16];
-          tc::tmem_ld16(src + c, v0);
-          tc::tmem_ld16(src + c + 16, v1);
-          tc::tmem_ld_wait();
-          if (i < a.N) {
+        } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              if (c + j < x.n) out[static_cast<size_t>(c + j) * a.N + i] = __bfloat16_as_ushort(__float2bfloat16_rn(v0[j]));
-              if (c + 16 + j < x.n) out[static_cast<size_t>(c + 16 + j) * a.N + i] = __bfloat16_as_ushort(__float2bfloat16_rn(v1[j]));
-            }
+          for (int j = 0; j < 16; ++j) {
+            turn[j][lane] = __bfloat16_as_ushort(__float2bfloat16_rn(v0[j]));
+            turn[16 + j][lane] = __bfloat16_as_ushort(__float2bfloat16_rn(v1[j]));
+          }
+        }
+        __syncwarp();
+        const int c0 = c + (kGateUp && q >= 2 ? 16 : 0), part = (lane & 3) * 8;
+        if (i0 + part < a.N) {
+#pragma unroll
+          for (int j = 0; j < (kGateUp ? 16 : 32); j += 8) {
+            const int r = j + (lane >> 2);
+            if (c0 + r < x.n)
+              *reinterpret_cast<uint4*>(out + static_cast<size_t>(c0 + r) * a.N + part) = *reinterpret_cast<const uint4*>(&turn[r][part]);
           }
         }
       }

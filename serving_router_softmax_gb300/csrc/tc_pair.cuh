@@ -32,22 +32,38 @@ __device__ __forceinline__ void mbar_arrive_at(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
-// Bounded wait on a barrier of this CTA that the other one arrives on too.
-__device__ __forceinline__ bool mbar_wait_pair(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t budget_ns) {
-  auto done = [&] {
+// Whether the phase of this parity is over, without waiting; what either CTA did before it is seen.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Waits for it, asleep in hardware (warps that poll take issue slots from the one that feeds the tensor core); gives up after
+// budget_ns, or when *abort is set.  kWarp: the lanes of a warp give up together.
+template <bool kWarp>
+__device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t budget_ns) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 1;; ++n) {
     uint32_t ok;
     asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(2000u)
         : "memory");
-    return ok != 0;
-  };
-  if (done()) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t it = 1;; ++it) {
-    if (done()) return true;
-    if ((it & 255u) == 0 && (*abort || globaltimer_ns() - t0 > budget_ns)) return false;
+    if (kWarp ? __all_sync(0xFFFFFFFFu, ok) : ok) return true;
+    if ((n & 31) == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      const bool stop = *abort || now - t0 > budget_ns;
+      if (kWarp ? __any_sync(0xFFFFFFFFu, stop) : stop) {
+        *abort = 1;
+        return false;
+      }
+    }
   }
 }
 
