@@ -205,7 +205,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kGateUp>, 1
       for (int kb = 0; kb < KB; ++kb) {
         ok = tc::mbar_sleep<true>(&sm.empty[s], ph ^ 1, gave_up, kWaitNs);
         if (!ok) break;
-        if (lane == 0) {
+        if (tc::elect_one()) {
           if (rank == 0) tc::mbar_arrive_expect_tx(&sm.full[s], bytes);
           const uint32_t bar = tc::smem_of(&sm.full[s], 0);
           if (!a.stall) {
@@ -223,37 +223,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kGateUp>, 1
     if (!ok) give_up_loading(sm, a, lane);
   } else if (warp == 1) {
     // ---------------------------------------------------------- products
-    if (rank == 0 && lane == 0) {
+    // The whole warp goes through the loop and one thread of it issues: where the compiler sees one lane's branch instead, a
+    // product's operands reach its registers one by one, 710 cycles a stage whatever its size.
+    if (rank == 0) {
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       bool ok = true, there = false;
       const uint64_t ad0 = tc::smem_desc_sw128(tc::smem_u32(sm.a[0])), bd0 = tc::smem_desc_sw128(tc::smem_u32(sm.b[0]));
+      const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
       for (long long t = pair; t < total && ok; t += pairs) {
         walk.at(t, &x);
-        const uint32_t idesc = tc::idesc_bf16_f32(256, x.N), d = tmem + acc * 256;
-        ok = tc::mbar_sleep<false>(&sm.acc_empty[acc], aph ^ 1, gave_up, kWaitNs);
+        const uint32_t idesc = tc::idesc_bf16_f32(256, __shfl_sync(0xFFFFFFFFu, x.N, 0)), d = tm + acc * 256;
+        ok = tc::mbar_sleep<true>(&sm.acc_empty[acc], aph ^ 1, gave_up, kWaitNs);
         tc::tc_fence_after();
         for (int kb = 0; kb < KB; ++kb) {
-          if (!there && ok) ok = tc::mbar_sleep<false>(&sm.full[s], ph, gave_up, kWaitNs);
+          if (!there && ok) ok = tc::mbar_sleep<true>(&sm.full[s], ph, gave_up, kWaitNs);
           if (!ok) break;
           tc::tc_fence_after();
           const uint64_t ad = ad0 + s * (kABytes >> 4), bd = bd0 + s * (kBBytes >> 4);
           uint64_t* done = &sm.empty[s];
           if (++s == kStages) s = 0, ph ^= 1;
-          tc::mma_bf16_pair(d, ad, bd, idesc, kb);
-          tc::mma_bf16_pair(d, ad + 2, bd + 2, idesc, 1);
+          if (tc::elect_one()) {
+            tc::mma_bf16_pair(d, ad, bd, idesc, kb);
+            tc::mma_bf16_pair(d, ad + 2, bd + 2, idesc, 1);
+            tc::mma_bf16_pair(d, ad + 4, bd + 4, idesc, 1);
+            tc::mma_bf16_pair(d, ad + 6, bd + 6, idesc, 1);
+            tc::mma_commit_pair(done);
+          }
+          __syncwarp();
           // The look at the next stage's barrier (100 cycles) runs beside the products.
-          there = tc::mbar_test(&sm.full[s], ph);
-          tc::mma_bf16_pair(d, ad + 4, bd + 4, idesc, 1);
-          tc::mma_bf16_pair(d, ad + 6, bd + 6, idesc, 1);
-          tc::mma_commit_pair(done);
+          there = __all_sync(0xFFFFFFFFu, tc::mbar_test(&sm.full[s], ph));
         }
-        if (ok) tc::mma_commit_pair(&sm.acc_full[acc]);
+        if (ok && tc::elect_one()) tc::mma_commit_pair(&sm.acc_full[acc]);
+        __syncwarp();
         if (++acc == 2) acc = 0, aph ^= 1;
       }
-      if (!ok) {
-        *gave_up = 1;
-        flag_error(a.dev_err, MOE_DEV_TIMEOUT);
+      if (!ok && lane == 0) flag_error(a.dev_err, MOE_DEV_TIMEOUT);
+      if (!ok && tc::elect_one()) {
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(tc::smem_u32(&sm.drain)) : "memory");
         int never = 0;
         tc::mbar_wait_bounded(&sm.drain, 0, &never, kWaitNs / 100);
