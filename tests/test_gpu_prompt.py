@@ -200,7 +200,8 @@ def test_prompt_attend(mv, Hq, Hkv, D, lengths):
     qkv = randn(g, T, Hq + 2 * Hkv, D)
     q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
     attend_check(mv, q, k, v, lengths, D ** -0.5, first=2)
-    # other strides: heads outermost, and a scale of the other sign
+    # a scale of 0 (every key alike), then other strides: heads outermost, and a scale of the other sign
+    attend_check(mv, q, k, v, lengths, 0.0)
     ho = [x.transpose(0, 1).contiguous().transpose(0, 1) for x in (q, k, v)]
     attend_check(mv, *ho, lengths, -0.3 * D ** -0.5)
 

@@ -45,3 +45,15 @@ def test_group_products(mv, T):  # noqa: F811
     h = mv.group_gate_up(x, layer, u, k)
     stalled(mv, mv._lib.TEST_STALL_GROUP, lambda err: mv.group_gate_up(x, layer, u, k, dev_err=err))
     stalled(mv, mv._lib.TEST_STALL_GROUP, lambda err: mv.group_down(h, layer, u, p, dev_err=err))
+
+
+@pytest.mark.parametrize("D,lengths", [(64, [5, 0, 700]), (128, [300, 1]), (128, [2000])])
+def test_prompt_attend(mv, D, lengths):  # noqa: F811
+    g = gen(62)
+    T = sum(lengths)
+    q, k, v = randn(g, T, 8, D), randn(g, T, 2, D), randn(g, T, 2, D)
+    start = [0]
+    for n in lengths:
+        start.append(start[-1] + n)
+    st = torch.tensor(start, dtype=torch.int32, device="cuda")
+    stalled(mv, mv._lib.TEST_STALL_PROMPT, lambda err: mv.prompt_attend(q, k, v, st, dev_err=err)[0])
