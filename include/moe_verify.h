@@ -812,7 +812,7 @@ int moe_rotate(const void* q, const void* k, const int32_t* pos, const uint64_t*
  * any gives zeros and -inf).  In a value it makes that dimension of out NaN or infinite for the
  * rows that see it.  What a row does not see has no effect on it.
  * Results do not depend on timing.
- * Limits: D = 64 or 128; 0 <= T <= 2^24, n_seq <= 4096; n_q_heads a multiple of
+ * Limits: D = 64 or 128; 0 <= T <= 2^24, n_seq <= 2048; n_q_heads a multiple of
  * n_kv_heads, at most 128 times as many, n_q_heads <= 1024; strides positive multiples
  * of 8 (the token stride of one token and the head stride of one head are not used).
  * Device errors: MOE_DEV_CAPACITY (starts outside [0, T] or out of order:

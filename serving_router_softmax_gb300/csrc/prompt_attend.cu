@@ -15,22 +15,28 @@
 // rewritten in a few steps of a row instead of all; bf16 and fp32 are as good
 // anywhere in that range.
 //
-// Blocks of one sequence differ in work by their place in it.  The grid takes
-// them in falling order of it over all sequences: rank x among the items is
-// found by counting, with no plan in memory: F(b) = sum of max(0, blocks - b)
-// items lie at block b of their sequence or later.
+// Persistent, one CTA an SM: an item (such a block of a sequence and kv head)
+// begins while the one before it ends, since a block's own beginning and end
+// (13 us of launch, set-up, first loads and output) are longer than a short
+// prompt's products.  Blocks of a sequence differ in work by their place in it;
+// they are taken in falling order of it over all sequences, back and forth over
+// the CTAs.  Rank x among the items is found by counting, with no plan in memory:
+// F(b) = sum of max(0, blocks - b) items lie at block b of their sequence or later.
 //
 // What a row may not see: scores are replaced by -inf in the tiles that hold
-// any; values there that are not finite would make 0 * v a NaN, so two warps
-// look through those value tiles, put zeros in their place, and keep for each
+// any; values there that are not finite would make 0 * v a NaN, so a warp looks
+// through those value tiles, puts zeros in their place, and keeps for each
 // dimension the first such key, which makes the output of the rows that see it
 // NaN.
 //
 // Roles (384 threads): warps 0-3 and 4-7 softmax and output of a tile each,
-// warp 8 issues the products, warp 9 loads by TMA, warps 10-11 look at values.
-// Every wait is bounded.
+// warps 8 and 9 issue a tile's products each (the tensor core takes a product as
+// it begins it, so one warp's waits and signals for both tiles, 1900 cycles a step,
+// were not hidden by the 2050 of its products), warp 10 finds the items and loads
+// by TMA, warp 11 looks at values.  Every wait is bounded.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "kv4.cuh"
@@ -49,7 +55,7 @@ constexpr int kRows = 128;       // query rows of a tile, keys of a step
 constexpr int kPanel = kRows * 128;  // bytes of 64 dimensions of a tile
 constexpr float kSlack = 8.f;
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int kMaxSeqs = 4096;
+constexpr int kMaxSeqs = 2048;
 
 struct PromptArgs {
   const int32_t* start;
@@ -61,21 +67,31 @@ struct PromptArgs {
   int negative, stall;           // scale < 0; test hook
 };
 
+struct Item {
+  int begin, len;  // the sequence: first row, rows
+  int first;       // first token of the item, counted in the sequence
+  int head;        // kv head
+  int n[2];        // steps of each tile; n[0] < 0: no more items
+};
+
 template <int D>
 struct Smem {
   static constexpr int kStages = D == 128 ? 4 : 8;
   alignas(1024) uint8_t q[2][D / 64][kPanel];
-  alignas(1024) uint8_t kv[kStages][D / 64][kPanel];  // first: blocks of each sequence
-  uint64_t q_full, full[kStages], empty[kStages], v_ok[kStages], s_full[2], p_full[2], o_full[2], drain;
-  int first_bad[D], bad;
-  int sum[12], found;
+  alignas(1024) uint8_t kv[kStages][D / 64][kPanel];
+  alignas(16) uint8_t turn[8][32 * 64];               // output rows of a warp, 32 dimensions at a time
+  int blocks[kMaxSeqs];                               // of each sequence
+  uint64_t full[kStages], empty[kStages], v_ok[kStages];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2], item_full[2], item_empty[2], drain;
+  Item item[2];
+  int first_bad[2][D], bad[2];
+  int most;
   uint32_t tmem;
   int abort;
 };
 template <int D>
 constexpr size_t kSmemBytes = sizeof(Smem<D>) + 1024;
 static_assert(kSmemBytes<128> <= 227 * 1024 && kSmemBytes<64> <= 227 * 1024, "shared memory");
-static_assert(sizeof(Smem<64>::kv) >= kMaxSeqs * 4, "room for the sequences' blocks");
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float2* e) {
   asm volatile(
@@ -104,77 +120,62 @@ __device__ __forceinline__ uint64_t value_desc(uint32_t addr) {
 }
 constexpr uint32_t kValuesAlongN = 1u << 16, kNegateA = 1u << 13;
 
-// Sum over the block; every thread gets it.
-__device__ __forceinline__ int block_sum(int v, int* part) {
-  v = __reduce_add_sync(0xFFFFFFFFu, v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int s = 0;
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) s += part[i];
-  return s;
-}
+// Finds items by their rank: a warp's work.
+struct Finder {
+  const PromptArgs& a;
+  const int* blocks;
+  int top;  // a level that no later rank lies above
 
-struct Item {
-  int begin, end, first;  // rows of the sequence; its first token here, counted in the sequence
-};
-
-// Item of this rank; false if there are fewer, or if the starts are out of order.
-template <int D>
-__device__ __forceinline__ bool find_item(const PromptArgs& a, Smem<D>& sm, int rank, Item* it) {
-  int* blocks = reinterpret_cast<int*>(&sm.kv[0][0][0]);
-  const int per = 2 * a.tokens;
-  int most = 0, bad = 0;
-  for (int s = threadIdx.x; s < a.S; s += kThreads) {
-    const int b = a.start[s], e = a.start[s + 1];
-    bad |= b < 0 || e > a.T || b > e;
-    const int n = bad ? 0 : (e - b + per - 1) / per;
-    blocks[s] = n;
-    most = max(most, n);
-  }
-  if (threadIdx.x == 0) sm.found = 0;
-  if (__syncthreads_or(bad)) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) flag_error(a.dev_err, MOE_DEV_CAPACITY);
-    return false;
-  }
-  atomicMax(&sm.found, __reduce_max_sync(0xFFFFFFFFu, most));
-  __syncthreads();
-  // The last b with F(b) > rank.
-  int lo = -1, hi = sm.found, above = 0;  // F(hi) <= rank
-  while (hi - lo > 1) {
-    const int b = lo + (hi - lo) / 2;
+  // F(b).
+  __device__ __forceinline__ int at_or_above(int b, int lane) const {
     int v = 0;
-    for (int s = threadIdx.x; s < a.S; s += kThreads) v += max(0, blocks[s] - b);
-    v = block_sum(v, sm.sum);
-    if (v > rank)
-      lo = b;
-    else
-      hi = b, above = v;
+    for (int s = lane; s < a.S; s += 32) v += max(0, blocks[s] - b);
+    return __reduce_add_sync(0xFFFFFFFFu, v);
   }
-  if (lo < 0) return false;
-  // The (rank - F(lo + 1))-th sequence that has a block lo.
-  int skip = rank - above;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    int seq = -1;
-    for (int s0 = 0; s0 < a.S && seq < 0; s0 += 32) {
-      const int s = s0 + threadIdx.x;
+  __device__ __forceinline__ bool find(long long rank, Item* it, int lane) {
+    const long long r = rank / a.Hkv;
+    if (r >= at_or_above(0, lane)) return false;
+    // The last level lo with F(lo) > r.
+    int lo = 0, hi = top, above = 0;  // F(hi) <= r: 0, or counted
+    while (hi - lo > 1) {
+      const int b = lo + (hi - lo) / 2, v = at_or_above(b, lane);
+      if (v > r)
+        lo = b;
+      else
+        hi = b, above = v;
+    }
+    if (hi == top) above = at_or_above(hi, lane);
+    // The (r - F(lo + 1))-th sequence that has a block lo.
+    int skip = static_cast<int>(r) - above, seq = 0;
+    for (int s0 = 0; s0 < a.S; s0 += 32) {
+      const int s = s0 + lane;
       const uint32_t has = __ballot_sync(0xFFFFFFFFu, s < a.S && blocks[s] > lo);
       const int n = __popc(has);
       if (skip < n) {
-        const bool me = ((has >> threadIdx.x) & 1) && __popc(has & ((1u << threadIdx.x) - 1)) == skip;
+        const bool me = ((has >> lane) & 1) && __popc(has & ((1u << lane) - 1)) == skip;
         seq = s0 + __ffs(__ballot_sync(0xFFFFFFFFu, me)) - 1;
+        break;
       }
       skip -= n;
     }
-    if (threadIdx.x == 0) sm.found = seq;
+    it->begin = a.start[seq], it->len = a.start[seq + 1] - it->begin;
+    it->first = lo * 2 * a.tokens;
+    it->head = static_cast<int>(rank % a.Hkv);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int from = it->first + t * a.tokens;  // a tile's last token sees itself
+      it->n[t] = from >= it->len ? 0 : (min(from + a.tokens, it->len) + kRows - 1) / kRows;
+    }
+    return true;
   }
-  __syncthreads();
-  const int s = sm.found;
-  it->begin = a.start[s], it->end = a.start[s + 1], it->first = lo * per;
-  return true;
-}
+};
+
+// A role's place in the ring of two items.
+struct Turn {
+  int i = 0;
+  __device__ __forceinline__ int slot() const { return i & 1; }
+  __device__ __forceinline__ uint32_t parity() const { return (i >> 1) & 1; }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -185,222 +186,285 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t raw[];
   Sm& sm = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int kvh = blockIdx.x % a.Hkv;
-  Item it;
-  if (!find_item<D>(a, sm, blockIdx.x / a.Hkv, &it)) return;
 
   if (tid == 0) {
-    tc::mbar_init(&sm.q_full, 1);
-    for (int i = 0; i < NS; ++i) tc::mbar_init(&sm.full[i], 1), tc::mbar_init(&sm.empty[i], 1), tc::mbar_init(&sm.v_ok[i], 2);
-    for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.s_full[i], 1), tc::mbar_init(&sm.p_full[i], 4), tc::mbar_init(&sm.o_full[i], 1);
-    tc::mbar_init(&sm.drain, 1);
-    sm.abort = sm.bad = 0;
+    for (int i = 0; i < NS; ++i) tc::mbar_init(&sm.full[i], 1), tc::mbar_init(&sm.empty[i], 2), tc::mbar_init(&sm.v_ok[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sm.q_full[i], 1), tc::mbar_init(&sm.q_empty[i], 1);
+      tc::mbar_init(&sm.s_full[i], 1), tc::mbar_init(&sm.p_full[i], 4);
+      tc::mbar_init(&sm.o_full[i], 1), tc::mbar_init(&sm.o_empty[i], 4);
+      tc::mbar_init(&sm.item_full[i], 1), tc::mbar_init(&sm.item_empty[i], 11);
+      sm.bad[i] = 0;
+    }
+    tc::mbar_init(&sm.drain, 2);
+    sm.abort = sm.most = 0;
     tc::fence_mbar_init();
   }
-  for (int d = tid; d < D; d += kThreads) sm.first_bad[d] = 0x7FFFFFFF;
+  for (int d = tid; d < 2 * D; d += kThreads) (&sm.first_bad[0][0])[d] = 0x7FFFFFFF;
   if (warp == 8) {
     tc::tmem_alloc(&sm.tmem, 512);
     tc::tmem_relinquish();
   }
-  // (The sequences' blocks lay where the copies go.)
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  const int per = 2 * a.tokens;
+  int most = 0, out_of_order = 0;
+  for (int s = tid; s < a.S; s += kThreads) {
+    const int b = a.start[s], e = a.start[s + 1];
+    const bool wrong = b < 0 || e > a.T || b > e;
+    out_of_order |= wrong;
+    const int n = wrong ? 0 : (e - b + per - 1) / per;
+    sm.blocks[s] = n;
+    most = max(most, n);
+  }
   tc::tc_fence_before();
-  __syncthreads();
+  out_of_order = __syncthreads_or(out_of_order);
   tc::tc_fence_after();
+  most = __reduce_max_sync(0xFFFFFFFFu, most);
+  if (lane == 0 && most > 0) atomicMax(&sm.most, most);
+  __syncthreads();
+  if (out_of_order && blockIdx.x == 0 && tid == 0) flag_error(a.dev_err, MOE_DEV_CAPACITY);
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sm.tmem, 0);
   volatile int* gave_up = &sm.abort;
-  // Steps of a tile: its last token sees itself.
-  const int len = it.end - it.begin;
-  auto steps_of = [&](int t) {
-    const int from = it.first + t * a.tokens;
-    return from >= len ? 0 : (min(from + a.tokens, len) + kRows - 1) / kRows;
+  bool ok = true;
+  Turn turn;
+  // The next item, for the roles that are told of it.
+  auto next_item = [&]() -> Item {
+    ok = tc::mbar_sleep<true>(&sm.item_full[turn.slot()], turn.parity(), gave_up, kWaitNs);
+    Item it = sm.item[turn.slot()];
+    if (!ok) it.n[0] = -1;
+    return it;
   };
-  const int n0 = steps_of(0), n1 = steps_of(1), n = max(n0, n1);
+  auto item_done = [&] {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&sm.item_empty[turn.slot()]);
+    ++turn.i;
+  };
 
   if (warp < 8) {
     // ---------------------------------------------------------- softmax, output
-    const int t = warp >> 2, r = (warp & 3) * 32 + lane, steps = t ? n1 : n0;
-    const int tok = r / a.G, pos = it.first + t * a.tokens + tok;
-    const bool real = tok < a.tokens && pos < len;
-    const int limit = real ? pos + 1 : 0;  // keys that the row sees
-    const int all_see = it.first + t * a.tokens + 1;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int t = warp >> 2, r = (warp & 3) * 32 + lane, tok = r / a.G, in_group = r % a.G;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * D;
-    float ref = -INFINITY;
-    float2 l2 = make_float2(0.f, 0.f);
-    bool ok = true;
     const float2 c2 = make_float2(a.c, a.c);
-    for (int j = 0; j < steps; ++j) {
-      ok = tc::mbar_sleep<true>(&sm.s_full[t], j & 1, gave_up, kWaitNs);
-      if (!ok) break;
-      tc::tc_fence_after();
-      float2 s[64];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 16 * i);
-      tc::tmem_ld_wait();
-      if ((j + 1) * kRows > all_see) {
+    int step = 0, items = 0;  // of this tile
+    while (true) {
+      const Item it = next_item();
+      if (it.n[0] < 0) break;
+      const int steps = t ? it.n[1] : it.n[0];
+      if (steps == 0) {
+        item_done();
+        continue;
+      }
+      const int from = it.first + t * a.tokens, pos = from + tok;
+      const bool real = tok < a.tokens && pos < it.len;
+      const int limit = real ? pos + 1 : 0;  // keys that the row sees
+      float ref = -INFINITY;
+      float2 l2 = make_float2(0.f, 0.f), k2 = make_float2(0.f, 0.f);
+      for (int j = 0; j < steps; ++j, ++step) {
+        ok = tc::mbar_sleep<true>(&sm.s_full[t], step & 1, gave_up, kWaitNs);
+        if (!ok) break;
+        tc::tc_fence_after();
+        float2 s[64];
+        tmem_ld32(ts, s);
+        tmem_ld32(ts + 32, s + 16);
+        tc::tmem_ld_wait();
+        tmem_ld32(ts + 64, s + 32);
+        tmem_ld32(ts + 96, s + 48);
+        const bool masked = (j + 1) * kRows > from + 1;
         const int see = limit - j * kRows;
+        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          s[i].x = 2 * i < see ? s[i].x : -INFINITY;
-          s[i].y = 2 * i + 1 < see ? s[i].y : -INFINITY;
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1) tc::tmem_ld_wait();
+          if (masked) {
+#pragma unroll
+            for (int i = 32 * h; i < 32 * h + 32; ++i) {
+              s[i].x = 2 * i < see ? s[i].x : -INFINITY;
+              s[i].y = 2 * i + 1 < see ? s[i].y : -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int i = 32 * h; i < 32 * h + 32; ++i) m[i & 3] = kv4::max3(m[i & 3], s[i].x, s[i].y);
         }
-      }
-      float m0 = fmaxf(s[0].x, s[0].y), m1 = fmaxf(s[1].x, s[1].y), m2 = fmaxf(s[2].x, s[2].y), m3 = fmaxf(s[3].x, s[3].y);
+        const float top = fmaxf(kv4::max3(m[0], m[1], m[2]), m[3]) * a.c;
+        const bool move = top > ref + kSlack;
+        if (__any_sync(0xFFFFFFFFu, move)) {
+          const float f = move ? kv4::ex2(ref - top) : 1.f;  // (0 from -inf)
+          if (move) ref = top;
+          const float2 f2 = make_float2(f, f);
+          l2 = mul2(l2, f2), k2 = mul2(k2, f2);
+          if (j > 0) {  // (the products of the step before are over: the scores came after them)
+#pragma unroll 1
+            for (int i = 0; i < D; i += 32) {
+              float2 o[16];
+              tmem_ld32(to + i, o);
+              tc::tmem_ld_wait();
 #pragma unroll
-      for (int i = 4; i < 64; i += 4) {
-        m0 = kv4::max3(m0, s[i].x, s[i].y), m1 = kv4::max3(m1, s[i + 1].x, s[i + 1].y);
-        m2 = kv4::max3(m2, s[i + 2].x, s[i + 2].y), m3 = kv4::max3(m3, s[i + 3].x, s[i + 3].y);
-      }
-      const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * a.c;
-      const bool move = top > ref + kSlack;
-      if (__any_sync(0xFFFFFFFFu, move)) {
-        const float f = move ? kv4::ex2(ref - top) : 1.f;  // (0 from -inf)
-        if (move) ref = top;
-        const float2 f2 = make_float2(f, f);
-        l2 = mul2(l2, f2);
-        if (j > 0) {  // (the products of the step before are over: the scores came after them)
+              for (int h = 0; h < 2; ++h) {
+                uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            float2 o[16];
-            tmem_ld32(to + 32 * i, o);
-            tc::tmem_ld_wait();
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t w[16];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float2 x = mul2(o[8 * h + e], f2);
-                w[2 * e] = __float_as_uint(x.x), w[2 * e + 1] = __float_as_uint(x.y);
+                for (int e = 0; e < 8; ++e) {
+                  const float2 x = mul2(o[8 * h + e], f2);
+                  w[2 * e] = __float_as_uint(x.x), w[2 * e + 1] = __float_as_uint(x.y);
+                }
+                tc::tmem_st16(to + i + 16 * h, w);
               }
-              tc::tmem_st16(to + 32 * i + 16 * h, w);
             }
           }
         }
-      }
-      const float neg = ref == -INFINITY ? 0.f : -ref;
-      const float2 r2 = make_float2(neg, neg);
+        const float neg = ref == -INFINITY ? 0.f : -ref;
+        const float2 r2 = make_float2(neg, neg);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t w[16];
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float2 x = fma2(s[16 * i + e], c2, r2);
-          x.x = kv4::ex2(x.x), x.y = kv4::ex2(x.y);
-          l2 = add2(l2, x);
-          w[e] = pack_bf(x.x, x.y);
+          for (int e = 0; e < 16; ++e) {
+            float2 x = fma2(s[16 * i + e], c2, r2);
+            x.x = kv4::ex2(x.x), x.y = kv4::ex2(x.y);
+            if (e & 1)
+              k2 = add2(k2, x);
+            else
+              l2 = add2(l2, x);
+            w[e] = pack_bf(x.x, x.y);
+          }
+          tc::tmem_st16(ts + 16 * i, w);
         }
-        tc::tmem_st16(ts + 16 * i, w);
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.p_full[t]);
       }
-      tc::tmem_st_wait();
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sm.p_full[t]);
-    }
-    if (ok && steps > 0) ok = tc::mbar_sleep<true>(&sm.o_full[t], 0, gave_up, kWaitNs);
-    if (!ok) {
-      if (lane == 0) flag_error(a.dev_err, MOE_DEV_TIMEOUT);
-    } else if (steps > 0) {
+      if (ok) ok = tc::mbar_sleep<true>(&sm.o_full[t], items & 1, gave_up, kWaitNs);
+      if (!ok) break;
+      ++items;
       tc::tc_fence_after();
-      const float l = l2.x + l2.y;
+      const float l = (l2.x + l2.y) + (k2.x + k2.y);
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const bool some_bad = sm.bad != 0;
-      // A lane's row goes to the tile's query panel in 16-byte parts, swizzled, and from there to its place in whole rows.
-      uint8_t* stage = &sm.q[t][0][0] + (warp & 3) * 32 * D * 2;
+      const bool some_bad = sm.bad[turn.slot()] != 0;
+      const int* bad = sm.first_bad[turn.slot()];
+      const int mine = real ? tok * a.Hq * D + in_group * D : -1;
+      const size_t row0 = static_cast<size_t>(it.begin + from) * a.Hq + it.head * a.G;
+      uint16_t* out = a.out + row0 * D;
+      if (real && a.lse) a.lse[row0 + tok * a.Hq + in_group] = l == 0.f ? -INFINITY : (ref == -INFINITY ? 0.f : ref) * kv4::kLn2 + logf(l);
+      // A lane's row goes through shared memory, 32 dimensions at a time, so that a store takes 64 bytes of each of 8 rows.
+      uint8_t* buf = sm.turn[warp];
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         float2 o[16];
         tmem_ld32(to + 32 * i, o);
         tc::tmem_ld_wait();
+        if (i == D / 32 - 1) {  // the sums may be written over
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sm.o_empty[t]);
+        }
         if (some_bad) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            if (sm.first_bad[32 * i + 2 * e] < limit) o[e].x = NAN;
-            if (sm.first_bad[32 * i + 2 * e + 1] < limit) o[e].y = NAN;
+            if (bad[32 * i + 2 * e] < limit) o[e].x = NAN;
+            if (bad[32 * i + 2 * e + 1] < limit) o[e].y = NAN;
           }
         }
 #pragma unroll
-        for (int e = 0; e < 16; e += 4) {
+        for (int x = 0; x < 4; ++x) {
           uint32_t w[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) w[x] = l == 0.f ? 0u : pack_bf(o[e + x].x * inv, o[e + x].y * inv);
-          const int part = 4 * i + e / 4;
-          *reinterpret_cast<uint4*>(stage + lane * (D * 2) + ((part ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int y = 0; y < 4; ++y) w[y] = l == 0.f ? 0u : pack_bf(o[4 * x + y].x * inv, o[4 * x + y].y * inv);
+          *reinterpret_cast<uint4*>(buf + lane * 64 + ((x ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        __syncwarp();
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int row = 8 * x + (lane >> 2), part = lane & 3;
+          const int at = __shfl_sync(0xFFFFFFFFu, mine, row);
+          const uint4 v = *reinterpret_cast<const uint4*>(buf + row * 64 + ((part ^ ((row >> 1) & 3)) << 4));
+          if (at >= 0) *reinterpret_cast<uint4*>(out + at + 32 * i + part * 8) = v;
+        }
+        __syncwarp();
       }
-      const int head = r % a.G;
-      const int mine = real ? tok * a.Hq * D + head * D : -1;
-      const size_t row0 = (static_cast<size_t>(it.begin + it.first + t * a.tokens)) * a.Hq + kvh * a.G;
-      uint16_t* out = a.out + row0 * D;
-      if (real && a.lse) a.lse[row0 + tok * a.Hq + head] = l == 0.f ? -INFINITY : (ref == -INFINITY ? 0.f : ref) * kv4::kLn2 + logf(l);
-      __syncwarp();
-      constexpr int kParts = D / 8, kAtOnce = 32 / kParts;  // 16-byte parts of a row, rows a pass
-#pragma unroll 4
-      for (int i = 0; i < 32; i += kAtOnce) {
-        const int row = i + lane / kParts, part = lane % kParts;
-        const int at = __shfl_sync(0xFFFFFFFFu, mine, row);
-        if (at >= 0)
-          *reinterpret_cast<uint4*>(out + at + part * 8) =
-              *reinterpret_cast<const uint4*>(stage + row * (D * 2) + ((part ^ (row & 7)) << 4));
-      }
+      item_done();
     }
-  } else if (warp == 8) {
+    if (!ok && lane == 0) flag_error(a.dev_err, MOE_DEV_TIMEOUT);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  }
+  if (warp == 8 || warp == 9) {
     // ---------------------------------------------------------- products
+    const int t = __shfl_sync(0xFFFFFFFFu, warp - 8, 0);
     const uint32_t is = tc::idesc_bf16_f32(kRows, kRows) | (a.negative ? kNegateA : 0u);
     const uint32_t iv = tc::idesc_bf16_f32(kRows, D) | kValuesAlongN;
-    const uint64_t qd = tc::smem_desc_sw128(tc::smem_u32(sm.q[0][0])), kd = tc::smem_desc_sw128(tc::smem_u32(sm.kv[0][0]));
-    const uint64_t vd = value_desc(tc::smem_u32(sm.kv[0][0]));
     constexpr int kTile = P * kPanel >> 4;
-    bool ok = tc::mbar_sleep<true>(&sm.q_full, 0, gave_up, kWaitNs);
+    const uint64_t qd = tc::smem_desc_sw128(tc::smem_u32(sm.q[0][0])) + t * kTile, kd = tc::smem_desc_sw128(tc::smem_u32(sm.kv[0][0]));
+    const uint64_t vd = value_desc(tc::smem_u32(sm.kv[0][0]));
+    const uint32_t ts = tmem + t * 128, to = tmem + 256 + t * D;
+    int place = 0;                          // in the ring's order: keys, values, keys, ...
+    int steps_done = 0, items_done = 0;     // of this tile
     auto wait = [&](uint64_t* bar, int index) {  // its index-th phase
       if (ok) ok = tc::mbar_sleep<true>(bar, index & 1, gave_up, kWaitNs);
+    };
+    // (within one elected thread)
+    auto scores = [&](int stage) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+        tc::mma_bf16(ts, qd + (i / 4) * (kPanel >> 4) + 2 * (i % 4), kd + stage * kTile + (i / 4) * (kPanel >> 4) + 2 * (i % 4), is, i > 0);
+    };
+    // An item's first scores; keys and values that only the other tile uses are handed back as they are seen.
+    auto start = [&](int steps, int at) {
+      const int st = at % NS;
+      wait(&sm.full[st], at / NS);
+      if (steps == 0) {
+        if (ok && lane == 0) tc::mbar_arrive(&sm.empty[st]);
+        return;
+      }
+      wait(&sm.q_full[t], items_done);
       tc::tc_fence_after();
-    };
-    auto scores = [&](int t, int stage) {
       if (ok && tc::elect_one()) {
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-          tc::mma_bf16(tmem + t * 128, qd + t * kTile + (i / 4) * (kPanel >> 4) + 2 * (i % 4), kd + stage * kTile + (i / 4) * (kPanel >> 4) + 2 * (i % 4),
-                       is, i > 0);
+        scores(st);
         tc::mma_commit(&sm.s_full[t]);
+        tc::mma_commit(&sm.empty[st]);
+        if (steps == 1) tc::mma_commit(&sm.q_empty[t]);
       }
       __syncwarp();
     };
-    auto values = [&](int t, int stage, int j) {
-      if (ok && tc::elect_one()) {
+    Item it = next_item();
+    if (it.n[0] >= 0) start(t ? it.n[1] : it.n[0], 0);
+    while (it.n[0] >= 0 && ok) {
+      const int n = max(it.n[0], it.n[1]), steps = t ? it.n[1] : it.n[0];
+      for (int j = 0; j < n && ok; ++j) {
+        const int v = place + 2 * j + 1, k = v + 1, sv = v % NS, sk = k % NS;  // this step's values, the next one's keys
+        wait(&sm.v_ok[sv], v / NS);
+        if (j + 1 < n) wait(&sm.full[sk], k / NS);
+        if (j < steps) {
+          const bool more = j + 1 < steps;
+          if (j == 0) wait(&sm.o_empty[t], items_done + 1);  // (the first passes)
+          wait(&sm.p_full[t], steps_done++);
+          tc::tc_fence_after();
+          if (ok && tc::elect_one()) {
 #pragma unroll
-        for (int i = 0; i < kRows / 16; ++i)
-          mma_bf16_ts(tmem + 256 + t * D, tmem + t * 128 + 8 * i, vd + stage * kTile + i * (2048 >> 4), iv, j > 0 || i > 0);
-      }
-      __syncwarp();
-    };
-    auto commit = [&](uint64_t* bar) {
-      if (ok && tc::elect_one()) tc::mma_commit(bar);
-      __syncwarp();
-    };
-    wait(&sm.full[0], 0);
-    if (n0) scores(0, 0);
-    if (n1) scores(1, 0);
-    commit(&sm.empty[0]);
-    for (int j = 0; j < n && ok; ++j) {
-      const int v = 2 * j + 1, k = 2 * j + 2;  // places in the ring's order of this step's values and the next one's keys
-      const bool more = j + 1 < n;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int steps = t ? n1 : n0;
-        if (j >= steps) continue;
-        wait(&sm.p_full[t], j);
-        wait(&sm.v_ok[v % NS], v / NS);
-        values(t, v % NS, j);
-        if (j + 1 < steps) {
-          wait(&sm.full[k % NS], k / NS);
-          scores(t, k % NS);
-        } else {
-          commit(&sm.o_full[t]);
+            for (int i = 0; i < kRows / 16; ++i) mma_bf16_ts(to, ts + 8 * i, vd + sv * kTile + i * (2048 >> 4), iv, j > 0 || i > 0);
+            if (more) {
+              scores(sk);
+              tc::mma_commit(&sm.s_full[t]);
+              tc::mma_commit(&sm.empty[sk]);
+              if (j + 2 == steps) tc::mma_commit(&sm.q_empty[t]);
+            } else {
+              tc::mma_commit(&sm.o_full[t]);
+            }
+            tc::mma_commit(&sm.empty[sv]);
+          }
+          __syncwarp();
+          if (!more && j + 1 < n && ok && lane == 0) tc::mbar_arrive(&sm.empty[sk]);
+        } else if (ok && lane == 0) {
+          tc::mbar_arrive(&sm.empty[sv]);
+          if (j + 1 < n) tc::mbar_arrive(&sm.empty[sk]);
         }
       }
-      commit(&sm.empty[v % NS]);
-      if (more) commit(&sm.empty[k % NS]);
+      if (!ok) break;
+      items_done += steps > 0;
+      place += 2 * n;
+      item_done();
+      it = next_item();
+      if (it.n[0] >= 0) start(t ? it.n[1] : it.n[0], place);
     }
     if (!ok) {
       if (lane == 0) flag_error(a.dev_err, MOE_DEV_TIMEOUT);
@@ -411,29 +475,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
-  } else if (warp == 9) {
-    // ---------------------------------------------------------- loads
-    if (tc::elect_one()) {
-      const int row = it.begin + it.first;
-      const int tiles = n1 ? 2 : 1;
-      tc::mbar_arrive_expect_tx(&sm.q_full, tiles * P * a.G * a.tokens * 128);
-      for (int t = 0; t < tiles; ++t)
-        for (int p = 0; p < P; ++p) tc::tma_load(sm.q[t][p], &qmap, 64 * p, kvh * a.G, row + t * a.tokens, &sm.q_full);
-    }
-    __syncwarp();
-    bool ok = true;
-    for (int i = 0; i < 2 * n; ++i) {
-      const int s = i % NS;
-      ok = tc::mbar_sleep<true>(&sm.empty[s], (i / NS + 1) & 1, gave_up, kWaitNs);
+  } else if (warp == 10) {
+    // ---------------------------------------------------------- items and loads
+    Finder finder{a, sm.blocks, sm.most};
+    int place = 0, q_used[2] = {0, 0};
+    for (int i = 0;; ++i) {
+      ok = tc::mbar_sleep<true>(&sm.item_empty[turn.slot()], turn.parity() ^ 1, gave_up, kWaitNs);
       if (!ok) break;
-      if (tc::elect_one()) {
-        tc::mbar_arrive_expect_tx(&sm.full[s], P * kPanel);
-        if (!(a.stall && i == 2 * n - 2)) {
-          for (int p = 0; p < P; ++p)
-            tc::tma_load(sm.kv[s][p], i & 1 ? &vmap : &kmap, 64 * p, kvh, it.begin + (i >> 1) * kRows, &sm.full[s]);
-        }
+      const int slot = turn.slot();
+      const long long rank = static_cast<long long>(i) * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      Item it = {};
+      if (out_of_order || !finder.find(rank, &it, lane)) it.n[0] = -1;
+      if (sm.bad[slot]) {
+        for (int d = lane; d < D; d += 32) sm.first_bad[slot][d] = 0x7FFFFFFF;
+        __syncwarp();
+        if (lane == 0) sm.bad[slot] = 0;
       }
+      if (lane == 0) sm.item[slot] = it;
       __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.item_full[slot]);
+      ++turn.i;
+      if (it.n[0] < 0) break;
+      const int row = it.begin + it.first;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (it.n[t] == 0) continue;
+        if (ok) ok = tc::mbar_sleep<true>(&sm.q_empty[t], (q_used[t] + 1) & 1, gave_up, kWaitNs);
+        ++q_used[t];
+        if (ok && tc::elect_one()) {
+          tc::mbar_arrive_expect_tx(&sm.q_full[t], P * a.G * a.tokens * 128);
+          for (int p = 0; p < P; ++p) tc::tma_load(sm.q[t][p], &qmap, 64 * p, it.head * a.G, row + t * a.tokens, &sm.q_full[t]);
+        }
+        __syncwarp();
+      }
+      const int n = max(it.n[0], it.n[1]);
+      for (int x = 0; x < 2 * n && ok; ++x, ++place) {
+        const int s = place % NS;
+        ok = tc::mbar_sleep<true>(&sm.empty[s], (place / NS + 1) & 1, gave_up, kWaitNs);
+        if (ok && tc::elect_one()) {
+          tc::mbar_arrive_expect_tx(&sm.full[s], P * kPanel);
+          if (!(a.stall && x == 2 * n - 2)) {
+            for (int p = 0; p < P; ++p)
+              tc::tma_load(sm.kv[s][p], x & 1 ? &vmap : &kmap, 64 * p, it.head, it.begin + (x >> 1) * kRows, &sm.full[s]);
+          }
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
     }
     if (!ok) {
       // Copies in flight land in microseconds.
@@ -444,42 +532,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
-  } else {
+  } else if (warp == 11) {
     // ---------------------------------------------------------- values that a row may not see
-    bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const int v = 2 * j + 1, s = v % NS;
-      ok = tc::mbar_sleep<true>(&sm.full[s], (v / NS) & 1, gave_up, kWaitNs);
-      if (!ok) break;
-      if ((j + 1) * kRows > it.first + 1) {
-        bool wrote = false;
-        for (int i = tid - 320; i < P * kPanel / 16; i += 64) {
-          uint4* at = reinterpret_cast<uint4*>(&sm.kv[s][0][0]) + i;
-          const uint4 w = *at;
-          auto odd = [](uint32_t x) { return ((x & 0x7F807F80u) + 0x00800080u) & 0x80008000u; };  // exponents of ones carry over
-          if (odd(w.x) | odd(w.y) | odd(w.z) | odd(w.w)) {
-            const int row = (i >> 3) & (kRows - 1), part = (i & 7) ^ (row & 7), d0 = (i / (kPanel / 16)) * 64 + part * 8;
-            uint16_t e[8];
-            *reinterpret_cast<uint4*>(e) = w;
-            for (int x = 0; x < 8; ++x) {
-              if ((e[x] & 0x7F80) == 0x7F80) {
-                e[x] = 0;
-                atomicMin(&sm.first_bad[d0 + x], j * kRows + row);
-                sm.bad = 1;
+    int place = 0;
+    while (true) {
+      const Item it = next_item();
+      if (it.n[0] < 0) break;
+      const int n = max(it.n[0], it.n[1]), slot = turn.slot();
+      for (int j = 0; j < n; ++j) {
+        const int v = place + 2 * j + 1, s = v % NS;
+        ok = tc::mbar_sleep<true>(&sm.full[s], (v / NS) & 1, gave_up, kWaitNs);
+        if (!ok) break;
+        if ((j + 1) * kRows > it.first + 1) {
+          bool wrote = false;
+          #pragma unroll 4
+          for (int i = lane; i < P * kPanel / 16; i += 32) {
+            uint4* at = reinterpret_cast<uint4*>(&sm.kv[s][0][0]) + i;
+            const uint4 w = *at;
+            auto odd = [](uint32_t x) { return ((x & 0x7F807F80u) + 0x00800080u) & 0x80008000u; };  // exponents of ones carry over
+            if (odd(w.x) | odd(w.y) | odd(w.z) | odd(w.w)) {
+              const int row = (i >> 3) & (kRows - 1), part = (i & 7) ^ (row & 7), d0 = (i / (kPanel / 16)) * 64 + part * 8;
+              uint16_t e[8];
+              *reinterpret_cast<uint4*>(e) = w;
+              for (int x = 0; x < 8; ++x) {
+                if ((e[x] & 0x7F80) == 0x7F80) {
+                  e[x] = 0;
+                  atomicMin(&sm.first_bad[slot][d0 + x], j * kRows + row);
+                  sm.bad[slot] = 1;
+                }
               }
+              *at = *reinterpret_cast<const uint4*>(e);
+              wrote = true;
             }
-            *at = *reinterpret_cast<const uint4*>(e);
-            wrote = true;
           }
+          if (__any_sync(0xFFFFFFFFu, wrote)) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        if (__any_sync(0xFFFFFFFFu, wrote)) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.v_ok[s]);
       }
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sm.v_ok[s]);
+      if (!ok) break;
+      place += 2 * n;
+      item_done();
     }
     if (!ok && lane == 0) flag_error(a.dev_err, MOE_DEV_TIMEOUT);
     __syncwarp();
   }
+  __syncwarp();
   tc::tc_fence_before();
   __syncthreads();
   if (warp == 8) tc::tmem_dealloc(tmem, 512);
@@ -507,9 +605,8 @@ int launch(const moe_prompt_cfg& c, const void* q, const void* k, const void* v,
   if (e != MOE_OK) return e;
   // Blocks of a kv head, one more for each sequence at most.
   const long long items = (c.T / (2 * a.tokens) + static_cast<long long>(c.n_seq)) * c.n_kv_heads;
-  if (items > 0x7FFFFFFFll) return MOE_ERR_UNSUPPORTED;
   LaunchScope ls(kProfPrompt, s);
-  prompt_kernel<D><<<static_cast<unsigned>(items), kThreads, kSmemBytes<D>, s>>>(qm, km, vm, a);
+  prompt_kernel<D><<<static_cast<unsigned>(std::min<long long>(items, sm_count())), kThreads, kSmemBytes<D>, s>>>(qm, km, vm, a);
   return check_launch();
 }
 
