@@ -170,6 +170,14 @@ struct Finder {
   }
 };
 
+// Keys that tile t's last token sees.
+__device__ __forceinline__ int seen_by(const PromptArgs& a, const Item& it, int t) { return min(it.first + (t + 1) * a.tokens, it.len); }
+
+// acc += 0 * x, on two bf16.
+__device__ __forceinline__ void zero_times(uint32_t& acc, uint32_t x) {
+  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
+}
+
 // A role's place in the ring of two items.
 struct Turn {
   int i = 0;
@@ -258,6 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int from = it.first + t * a.tokens, pos = from + tok;
       const bool real = tok < a.tokens && pos < it.len;
       const int limit = real ? pos + 1 : 0;  // keys that the row sees
+      const int seen = seen_by(a, it, t);
       float ref = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f), k2 = make_float2(0.f, 0.f);
       for (int j = 0; j < steps; ++j, ++step) {
@@ -271,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(ts + 64, s + 32);
         tmem_ld32(ts + 96, s + 48);
         const bool masked = (j + 1) * kRows > from + 1;
-        const int see = limit - j * kRows;
+        const int see = limit - j * kRows, here = seen - j * kRows;  // (here: of the tile's last row; columns beyond hold anything)
         float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -316,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 r2 = make_float2(neg, neg);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+          if (32 * i >= here) break;  // no product takes them
           uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -391,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8 || warp == 9) {
     // ---------------------------------------------------------- products
     const int t = __shfl_sync(0xFFFFFFFFu, warp - 8, 0);
-    const uint32_t is = tc::idesc_bf16_f32(kRows, kRows) | (a.negative ? kNegateA : 0u);
+    const uint32_t neg = a.negative ? kNegateA : 0u;
     const uint32_t iv = tc::idesc_bf16_f32(kRows, D) | kValuesAlongN;
     constexpr int kTile = P * kPanel >> 4;
     const uint64_t qd = tc::smem_desc_sw128(tc::smem_u32(sm.q[0][0])) + t * kTile, kd = tc::smem_desc_sw128(tc::smem_u32(sm.kv[0][0]));
@@ -402,15 +412,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](uint64_t* bar, int index) {  // its index-th phase
       if (ok) ok = tc::mbar_sleep<true>(bar, index & 1, gave_up, kWaitNs);
     };
-    // (within one elected thread)
-    auto scores = [&](int stage) {
+    // (within one elected thread)  The first `keys` keys' scores, a multiple of 16.
+    auto scores = [&](int stage, int keys) {
+      const uint32_t is = tc::idesc_bf16_f32(kRows, keys) | neg;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
         tc::mma_bf16(ts, qd + (i / 4) * (kPanel >> 4) + 2 * (i % 4), kd + stage * kTile + (i / 4) * (kPanel >> 4) + 2 * (i % 4), is, i > 0);
     };
     // An item's first scores; keys and values that only the other tile uses are handed back as they are seen.
-    auto start = [&](int steps, int at) {
-      const int st = at % NS;
+    auto start = [&](const Item& it, int at) {
+      const int st = at % NS, steps = t ? it.n[1] : it.n[0];
       wait(&sm.full[st], at / NS);
       if (steps == 0) {
         if (ok && lane == 0) tc::mbar_arrive(&sm.empty[st]);
@@ -419,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait(&sm.q_full[t], items_done);
       tc::tc_fence_after();
       if (ok && tc::elect_one()) {
-        scores(st);
+        scores(st, min(kRows, (seen_by(a, it, t) + 15) & ~15));
         tc::mma_commit(&sm.s_full[t]);
         tc::mma_commit(&sm.empty[st]);
         if (steps == 1) tc::mma_commit(&sm.q_empty[t]);
@@ -427,9 +438,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     };
     Item it = next_item();
-    if (it.n[0] >= 0) start(t ? it.n[1] : it.n[0], 0);
+    if (it.n[0] >= 0) start(it, 0);
     while (it.n[0] >= 0 && ok) {
-      const int n = max(it.n[0], it.n[1]), steps = t ? it.n[1] : it.n[0];
+      const int n = max(it.n[0], it.n[1]), steps = t ? it.n[1] : it.n[0], seen = seen_by(a, it, t);
       for (int j = 0; j < n && ok; ++j) {
         const int v = place + 2 * j + 1, k = v + 1, sv = v % NS, sk = k % NS;  // this step's values, the next one's keys
         wait(&sm.v_ok[sv], v / NS);
@@ -440,10 +451,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait(&sm.p_full[t], steps_done++);
           tc::tc_fence_after();
           if (ok && tc::elect_one()) {
-#pragma unroll
-            for (int i = 0; i < kRows / 16; ++i) mma_bf16_ts(to, ts + 8 * i, vd + sv * kTile + i * (2048 >> 4), iv, j > 0 || i > 0);
             if (more) {
-              scores(sk);
+#pragma unroll
+              for (int i = 0; i < kRows / 16; ++i) mma_bf16_ts(to, ts + 8 * i, vd + sv * kTile + i * (2048 >> 4), iv, j > 0 || i > 0);
+            } else {
+              for (int i = 0; 16 * i < seen - j * kRows; ++i) mma_bf16_ts(to, ts + 8 * i, vd + sv * kTile + i * (2048 >> 4), iv, j > 0 || i > 0);
+            }
+            if (more) {
+              scores(sk, min(kRows, (seen - (j + 1) * kRows + 15) & ~15));
               tc::mma_commit(&sm.s_full[t]);
               tc::mma_commit(&sm.empty[sk]);
               if (j + 2 == steps) tc::mma_commit(&sm.q_empty[t]);
@@ -464,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       place += 2 * n;
       item_done();
       it = next_item();
-      if (it.n[0] >= 0) start(t ? it.n[1] : it.n[0], place);
+      if (it.n[0] >= 0) start(it, place);
     }
     if (!ok) {
       if (lane == 0) flag_error(a.dev_err, MOE_DEV_TIMEOUT);
@@ -543,29 +558,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int v = place + 2 * j + 1, s = v % NS;
         ok = tc::mbar_sleep<true>(&sm.full[s], (v / NS) & 1, gave_up, kWaitNs);
         if (!ok) break;
-        if ((j + 1) * kRows > it.first + 1) {
-          bool wrote = false;
-          #pragma unroll 4
-          for (int i = lane; i < P * kPanel / 16; i += 32) {
-            uint4* at = reinterpret_cast<uint4*>(&sm.kv[s][0][0]) + i;
-            const uint4 w = *at;
-            auto odd = [](uint32_t x) { return ((x & 0x7F807F80u) + 0x00800080u) & 0x80008000u; };  // exponents of ones carry over
-            if (odd(w.x) | odd(w.y) | odd(w.z) | odd(w.w)) {
-              const int row = (i >> 3) & (kRows - 1), part = (i & 7) ^ (row & 7), d0 = (i / (kPanel / 16)) * 64 + part * 8;
-              uint16_t e[8];
-              *reinterpret_cast<uint4*>(e) = w;
-              for (int x = 0; x < 8; ++x) {
-                if ((e[x] & 0x7F80) == 0x7F80) {
-                  e[x] = 0;
-                  atomicMin(&sm.first_bad[slot][d0 + x], j * kRows + row);
-                  sm.bad[slot] = 1;
-                }
-              }
-              *at = *reinterpret_cast<const uint4*>(e);
-              wrote = true;
+        // Keys from the first one that some row does not see to the last that a product takes.
+        const int lo = max(0, it.first + 1 - j * kRows) & ~7, hi = min(kRows, (seen_by(a, it, 1) - j * kRows + 15) & ~15);
+        if (lo < hi) {
+          // 0 * x + 0 is NaN for an x that is not finite, two values at a time.
+          uint32_t odd[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int p = 0; p < P; ++p) {
+            const uint4* at = reinterpret_cast<const uint4*>(sm.kv[s][p] + lo * 128) + lane;
+#pragma unroll 8
+            for (int i = 0; i < (hi - lo) * 8; i += 32) {
+              const uint4 w = at[i];
+              zero_times(odd[0], w.x), zero_times(odd[1], w.y), zero_times(odd[2], w.z), zero_times(odd[3], w.w);
             }
           }
-          if (__any_sync(0xFFFFFFFFu, wrote)) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (__any_sync(0xFFFFFFFFu, ((odd[0] | odd[1] | odd[2] | odd[3]) & 0x7FFF7FFFu) != 0)) {
+            for (int i = lane; i < P * (hi - lo) * 64; i += 32) {
+              const int d = i % (P * 64), row = lo + i / (P * 64);
+              uint16_t* e = reinterpret_cast<uint16_t*>(sm.kv[s][d / 64] + row * 128 + ((((d & 63) >> 3) ^ (row & 7)) << 4)) + (d & 7);
+              if ((*e & 0x7F80) == 0x7F80) {
+                *e = 0;
+                atomicMin(&sm.first_bad[slot][d], j * kRows + row);
+                sm.bad[slot] = 1;
+              }
+            }
+            tc::fence_async_smem();
+          }
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sm.v_ok[s]);
