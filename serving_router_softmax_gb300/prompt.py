@@ -2,7 +2,8 @@
 
 Thin like ``api``: argument checks and pointer marshalling.  Tensors are on one CUDA device, whichever is current; calls
 enqueue on that device's current stream (or ``stream``) and raise ``MoEError`` on a non-OK host status.  Device-side error
-bits land in ``dev_err`` where one is given.
+bits land in ``dev_err`` where one is given.  A small call's host time is of the order of its device time, so the argument
+structs of a shape are kept.
 """
 from __future__ import annotations
 
@@ -20,25 +21,34 @@ from .kv4 import _DTYPES, _arg, _current_device, _err, _raw_stream
 _TURN = Fraction(6283185307179586476925286766559005768394338798750211641949889, 10 ** 60)
 
 
-def _run(dev: torch.device, stream, call):
-    """The call with `dev` as the current device and `stream`, if there is one, as its stream (outputs are allocated there too)."""
-    if dev.type != "cuda":
+# Argument structs of calls of one shape (pointers are not part of them).
+_plans: Dict[tuple, tuple] = {}
+
+
+def _plan(key: tuple, make) -> tuple:
+    p = _plans.get(key)
+    if p is None:
+        if len(_plans) > 1024:
+            _plans.clear()
+        p = _plans[key] = make()
+    return p
+
+
+def _elsewhere(dev: int, stream, call):
+    """`call` with device `dev` as the current one and `stream`, if there is one, as its stream (outputs are allocated there too)."""
+    if dev < 0:
         raise MoEError("expected CUDA tensors")
-    if stream is not None and stream.device_index != dev.index:
-        raise MoEError(f"stream: expected one of {dev}")
-    if stream is None and _current_device() == dev.index:
-        return call(dev.index)
-    with torch.cuda.device(dev.index):
+    if stream is not None and stream.device_index != dev:
+        raise MoEError(f"stream: expected one of cuda:{dev}")
+    with torch.cuda.device(dev):
         if stream is None:
-            return call(dev.index)
+            return call()
         with torch.cuda.stream(stream):
-            return call(dev.index)
+            return call()
 
 
-def _rows(index: int, t: torch.Tensor, name: str, shape, dtype: torch.dtype) -> Tuple[int, int, int]:
-    """(pointer, token stride, head stride) of a tensor [tokens, heads, dim] whose last dimension is contiguous."""
-    if t.get_device() != index:
-        raise MoEError(f"{name}: expected a tensor on cuda:{index}")
+def _rows(t: torch.Tensor, name: str, shape, dtype: torch.dtype) -> Tuple[int, int]:
+    """Token and head strides of a tensor [tokens, heads, dim] whose last dimension is contiguous."""
     if t.shape != shape:
         raise MoEError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype is not dtype:
@@ -46,7 +56,13 @@ def _rows(index: int, t: torch.Tensor, name: str, shape, dtype: torch.dtype) -> 
     st = t.stride()
     if st[2] != 1 and shape[2] > 1:
         raise MoEError(f"{name}: the last dimension must be contiguous")
-    return t.data_ptr(), st[0], st[1]
+    return st[0], st[1]
+
+
+def _ptr(dev: int, t: torch.Tensor, name: str) -> int:
+    if t.get_device() != dev:
+        raise MoEError(f"{name}: expected a tensor on cuda:{dev}")
+    return t.data_ptr()
 
 
 class Rotary:
@@ -89,33 +105,40 @@ def rotate(rot: Rotary, q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.T
     """Rotates ``q`` [T, n_q_heads, head_dim] and ``k`` [T, n_k_heads, head_dim] (or None), bfloat16 or float32, by the
     positions ``pos`` (int32 [n_axes, T], or [T] with one axis); ``inverse`` turns back (the gradient).  Token and head
     strides are free (multiples of 16 bytes).  ``out_q`` / ``out_k``: may be q / k themselves; new tensors if None."""
-    if q.dim() != 3 or (k is not None and k.dim() != 3):
-        raise MoEError("q, k: expected [T, heads, head_dim]")
-    if q.dtype not in _DTYPES:
-        raise MoEError(f"q: expected bfloat16 or float32, got {q.dtype}")
-    if rot.device != q.device:
+    dev = q.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(dev, stream, lambda: rotate(rot, q, k, pos, inverse, out_q, out_k, dev_err))
+    if rot.device.index != dev:
         raise MoEError(f"q: expected a tensor on {rot.device}")
+    qs, ks = q.shape, None if k is None else k.shape
 
-    def call(dev: int):
-        T, Hq = q.shape[:2]
-        Hk = 0 if k is None else k.shape[1]
-        qp, *qs = _rows(dev, q, "q", (T, Hq, rot.head_dim), q.dtype)
-        kp, *ks = (None, 0, 0) if k is None else _rows(dev, k, "k", (T, Hk, rot.head_dim), q.dtype)
-        oq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out_q is None else out_q
-        ok = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device) if out_k is None else out_k
-        oqp, *oqs = _rows(dev, oq, "out_q", q.shape, q.dtype)
-        okp, *oks = (None, 0, 0) if k is None else _rows(dev, ok, "out_k", k.shape, q.dtype)
-        for name, x, y, xp, yp, xs, ys in (("q", q, oq, qp, oqp, qs, oqs), ("k", k, ok, kp, okp, ks, oks)):
-            if x is not None and xp == yp and xs != ys:
-                raise MoEError(f"out_{name}: expected {name} itself or memory apart from it")
-        pp = _arg(dev, pos, torch.int32, (T,) if pos.dim() == 1 and rot.n_axes == 1 else (rot.n_axes, T), "pos")
-        cfg = L.RotateCfg(T, Hq, Hk, rot.head_dim, rot.rotary_dim, rot.n_axes, int(rot.interleaved), int(inverse), _DTYPES[q.dtype],
-                          *qs, *ks, *oqs, *oks)
-        _check(L.load().moe_rotate(qp, kp, pp, rot._turns.data_ptr(), rot._axis.data_ptr(), C.byref(cfg), oqp, okp,
-                                   _err(dev, dev_err), _raw_stream(dev)), "moe_rotate")
-        return oq, ok
+    def make():
+        if q.dim() != 3 or (k is not None and k.dim() != 3):
+            raise MoEError("q, k: expected [T, heads, head_dim]")
+        if q.dtype not in _DTYPES:
+            raise MoEError(f"q: expected bfloat16 or float32, got {q.dtype}")
+        T, Hq, D = qs[0], qs[1], rot.head_dim
+        Hk = 0 if k is None else ks[1]
+        strides = [*_rows(q, "q", (T, Hq, D), q.dtype), *((0, 0) if k is None else _rows(k, "k", (T, Hk, D), q.dtype))]
+        strides += (Hq * D, D) if out_q is None else _rows(out_q, "out_q", qs, q.dtype)
+        strides += (0, 0) if k is None else (Hk * D, D) if out_k is None else _rows(out_k, "out_k", ks, q.dtype)
+        cfg = L.RotateCfg(T, Hq, Hk, D, rot.rotary_dim, rot.n_axes, int(rot.interleaved), int(inverse), _DTYPES[q.dtype], *strides)
+        return C.byref(cfg), (T,), (rot.n_axes, T), strides[:4] == strides[4:]
 
-    return _run(q.device, stream, call)
+    key = ("rotate", qs, q.stride(), q.dtype, ks, None if k is None else (k.stride(), k.dtype), rot.head_dim, rot.rotary_dim, rot.n_axes,
+           rot.interleaved, inverse, None if out_q is None else (out_q.shape, out_q.stride(), out_q.dtype),
+           None if out_k is None else (out_k.shape, out_k.stride(), out_k.dtype))
+    ref, one, many, alike = _plan(key, make)
+    oq = torch.empty(qs, dtype=q.dtype, device=q.device) if out_q is None else out_q
+    ok = None if k is None else torch.empty(ks, dtype=k.dtype, device=k.device) if out_k is None else out_k
+    qp, oqp = q.data_ptr(), _ptr(dev, oq, "out_q")
+    kp, okp = (None, None) if k is None else (_ptr(dev, k, "k"), _ptr(dev, ok, "out_k"))
+    if not alike and qs[0] and (qp == oqp and q.stride() != oq.stride() or k is not None and kp == okp and k.stride() != ok.stride()):
+        raise MoEError("out_q, out_k: expected q and k themselves or memory apart from them")
+    pp = _arg(dev, pos, torch.int32, one if rot.n_axes == 1 and pos.dim() == 1 else many, "pos")
+    _check(L.load().moe_rotate(qp, kp, pp, rot._turns.data_ptr(), rot._axis.data_ptr(), ref, oqp, okp, _err(dev, dev_err),
+                               _raw_stream(dev)), "moe_rotate")
+    return oq, ok
 
 
 def prompt_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, start: torch.Tensor, scale: Optional[float] = None,
@@ -126,60 +149,74 @@ def prompt_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, start: torc
     Sequence s is rows ``start[s]`` .. ``start[s + 1] - 1`` (int32 [n_seq + 1]) of ``q`` [T, n_q_heads, head_dim] and of
     ``k`` and ``v`` [T, n_kv_heads, head_dim] (bf16, token and head strides multiples of 8).  Rows of no sequence are left
     as they are.  ``scale``: head_dim ** -0.5 if None."""
-    if q.dim() != 3 or k.dim() != 3:
-        raise MoEError("q, k, v: expected [T, heads, head_dim]")
-    if start.dim() != 1 or start.shape[0] < 1:
-        raise MoEError("start: expected int32 [n_seq + 1]")
+    dev = q.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(dev, stream, lambda: prompt_attend(q, k, v, start, scale, out, lse, dev_err))
 
-    def call(dev: int):
+    def make():
+        if q.dim() != 3 or k.dim() != 3:
+            raise MoEError("q, k, v: expected [T, heads, head_dim]")
+        if start.dim() != 1 or start.shape[0] < 1:
+            raise MoEError("start: expected int32 [n_seq + 1]")
         T, Hq, D = q.shape
         shape = (T, k.shape[1], D)
-        qp, *qs = _rows(dev, q, "q", q.shape, torch.bfloat16)
-        kp, *ks = _rows(dev, k, "k", shape, torch.bfloat16)
-        vp, *vs = _rows(dev, v, "v", shape, torch.bfloat16)
-        o = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else out
-        z = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
-        cfg = L.PromptCfg(T, start.shape[0] - 1, Hq, k.shape[1], D, D ** -0.5 if scale is None else scale, *qs, *ks, *vs)
-        _check(L.load().moe_prompt_attend(qp, kp, vp, _arg(dev, start, torch.int32, start.shape, "start"), C.byref(cfg),
-                                          _arg(dev, o, torch.bfloat16, (T, Hq, D), "out"), _arg(dev, z, torch.float32, (T, Hq), "lse"),
-                                          _err(dev, dev_err), _raw_stream(dev)), "moe_prompt_attend")
-        return o, z
+        cfg = L.PromptCfg(T, start.shape[0] - 1, Hq, k.shape[1], D, D ** -0.5 if scale is None else scale,
+                          *_rows(q, "q", q.shape, torch.bfloat16), *_rows(k, "k", shape, torch.bfloat16),
+                          *_rows(v, "v", shape, torch.bfloat16))
+        return C.byref(cfg), (T, Hq, D), (T, Hq), start.shape
 
-    return _run(q.device, stream, call)
-
-
-def _union_args(dev: int, union: Dict[str, torch.Tensor], names, rows: int, E: int):
-    cap = min(E, rows)
-    shapes = {"n_unique": (1,), "unique": (max(cap, 1),), "offsets": (cap + 1,), "perm_token": (max(rows, 1),), "inv": (max(rows, 1),)}
-    return [_arg(dev, union[n], torch.int32, shapes[n], f"union[{n!r}]") for n in names]
+    ref, so, sl, ss = _plan(("attend", q.shape, q.stride(), q.dtype, k.shape, k.stride(), k.dtype, v.shape, v.stride(), v.dtype,
+                             start.shape, scale), make)
+    qp, kp, vp = q.data_ptr(), _ptr(dev, k, "k"), _ptr(dev, v, "v")
+    o = torch.empty(so, dtype=torch.bfloat16, device=q.device) if out is None else out
+    z = torch.empty(sl, dtype=torch.float32, device=q.device) if lse is None else lse
+    _check(L.load().moe_prompt_attend(qp, kp, vp, _arg(dev, start, torch.int32, ss, "start"), ref,
+                                      o.data_ptr() if out is None else _arg(dev, o, torch.bfloat16, so, "out"),
+                                      z.data_ptr() if lse is None else _arg(dev, z, torch.float32, sl, "lse"),
+                                      _err(dev, dev_err), _raw_stream(dev)), "moe_prompt_attend")
+    return o, z
 
 
-def _layer(dev: int, layer: ExpertLayer) -> L.LayerWeights:
+def _group_plan(rows: int, k: int, layer: ExpertLayer) -> tuple:
+    """(layer struct, shapes of x, h, y, w, and of the union's n_unique, unique, offsets and lists) of a call."""
+    def make():
+        if layer.dtype != "bf16":
+            raise MoEError(f"layer: expected bf16 weights, got {layer.dtype}")
+        if k < 1 or rows % k:
+            raise MoEError(f"expected k >= 1 rows of each token, got {rows} for k = {k}")
+        T, cap = rows // k, min(layer.E, rows)
+        return (C.byref(layer.struct()), (T, layer.H), (rows, layer.I), (T, layer.H), (T, k), (1,), (max(cap, 1),), (cap + 1,),
+                (max(rows, 1),))
+
+    if layer.pool is not None:
+        return make()
+    gu, dn = layer.gate_up, layer.down
+    return _plan(("group", rows, k, gu.data_ptr(), dn.data_ptr(), gu.shape, dn.shape, layer.dims, layer.dtype, layer.layout), make)
+
+
+def _layer_on(dev: int, layer: ExpertLayer) -> None:
     if layer.gate_up.get_device() != dev or layer.down.get_device() != dev:
         raise MoEError(f"layer: expected one on cuda:{dev}")
-    return layer.struct()
 
 
 def group_gate_up(x: torch.Tensor, layer: ExpertLayer, union: Dict[str, torch.Tensor], k: int, out: Optional[torch.Tensor] = None,
                   dev_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """h [T * k, I] bf16: silu(W_gate x) * (W_up x) for every row of the groups of ``union`` (``union_permute``'s, for the
     same T tokens' k experts), in the groups' order.  ``x`` [T, H] bf16, any T; ``layer``: bf16, either layout."""
-    if x.dim() != 2 or x.shape[1] != layer.H:
-        raise MoEError("x: expected [T, H] of the layer's H")
-
-    def call(dev: int):
-        T = x.shape[0]
-        if k < 1:
-            raise MoEError("k < 1")
-        st = _layer(dev, layer)
-        h = torch.empty((T * k, layer.I), dtype=torch.bfloat16, device=x.device) if out is None else out
-        args = _union_args(dev, union, ("n_unique", "unique", "offsets", "perm_token"), T * k, layer.E)
-        _check(L.load().moe_group_gate_up(_arg(dev, x, torch.bfloat16, x.shape, "x"), T, k, C.byref(st), *args,
-                                          _arg(dev, h, torch.bfloat16, (T * k, layer.I), "out"), _err(dev, dev_err), _raw_stream(dev)),
-               "moe_group_gate_up")
-        return h
-
-    return _run(x.device, stream, call)
+    dev = x.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(dev, stream, lambda: group_gate_up(x, layer, union, k, out, dev_err))
+    T = x.shape[0]
+    ref, sx, sh, _, _, s1, su, so, sp = _group_plan(T * k, k, layer)
+    _layer_on(dev, layer)
+    h = torch.empty(sh, dtype=torch.bfloat16, device=x.device) if out is None else out
+    i32 = torch.int32
+    _check(L.load().moe_group_gate_up(_arg(dev, x, torch.bfloat16, sx, "x"), T, k, ref, _arg(dev, union["n_unique"], i32, s1, "n_unique"),
+                                      _arg(dev, union["unique"], i32, su, "unique"), _arg(dev, union["offsets"], i32, so, "offsets"),
+                                      _arg(dev, union["perm_token"], i32, sp, "perm_token"),
+                                      h.data_ptr() if out is None else _arg(dev, h, torch.bfloat16, sh, "out"), _err(dev, dev_err),
+                                      _raw_stream(dev)), "moe_group_gate_up")
+    return h
 
 
 def group_down_workspace_bytes(layer: ExpertLayer, T: int, k: int) -> int:
@@ -192,24 +229,23 @@ def group_down(h: torch.Tensor, layer: ExpertLayer, union: Dict[str, torch.Tenso
                workspace: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y [T, H] bf16 = sum_j w[t, j] * (W_down h[inv[t, j]]): ``h`` [T * k, I] bf16 in the groups' order (``group_gate_up``'s),
     ``w`` [T, k] fp32 routing weights."""
-    if h.dim() != 2 or w.dim() != 2:
-        raise MoEError("h: expected [T * k, I], w: [T, k]")
-
-    def call(dev: int):
-        T, k = w.shape
-        if k < 1:
-            raise MoEError("w: expected [T, k]")
-        st = _layer(dev, layer)
-        o = torch.empty((T, layer.H), dtype=torch.bfloat16, device=h.device) if y is None else y
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(int(L.load().moe_group_down_workspace(C.byref(st), T, k)), dtype=torch.uint8, device=h.device)
-        elif ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
-            raise MoEError(f"workspace: expected contiguous bytes (uint8) on cuda:{dev}")
-        args = _union_args(dev, union, ("n_unique", "unique", "offsets", "inv"), T * k, layer.E)
-        _check(L.load().moe_group_down(_arg(dev, h, torch.bfloat16, (T * k, layer.I), "h"), T, k, C.byref(st), *args,
-                                       _arg(dev, w, torch.float32, (T, k), "w"), _arg(dev, o, torch.bfloat16, (T, layer.H), "y"),
-                                       ws.data_ptr(), ws.numel(), _err(dev, dev_err), _raw_stream(dev)), "moe_group_down")
-        return o
-
-    return _run(h.device, stream, call)
+    dev = h.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(dev, stream, lambda: group_down(h, layer, union, w, y, workspace, dev_err))
+    if w.dim() != 2:
+        raise MoEError("w: expected [T, k]")
+    T, k = w.shape
+    ref, _, sh, sy, sw, s1, su, so, sp = _group_plan(T * k, k, layer)
+    _layer_on(dev, layer)
+    o = torch.empty(sy, dtype=torch.bfloat16, device=h.device) if y is None else y
+    lib, i32 = L.load(), torch.int32
+    if workspace is None:
+        workspace = torch.empty((lib.moe_group_down_workspace(ref, T, k),), dtype=torch.uint8, device=h.device)
+    elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise MoEError(f"workspace: expected contiguous bytes (uint8) on cuda:{dev}")
+    _check(lib.moe_group_down(_arg(dev, h, torch.bfloat16, sh, "h"), T, k, ref, _arg(dev, union["n_unique"], i32, s1, "n_unique"),
+                              _arg(dev, union["unique"], i32, su, "unique"), _arg(dev, union["offsets"], i32, so, "offsets"),
+                              _arg(dev, union["inv"], i32, sp, "inv"), _arg(dev, w, torch.float32, sw, "w"),
+                              o.data_ptr() if y is None else _arg(dev, o, torch.bfloat16, sy, "y"), workspace.data_ptr(),
+                              workspace.numel(), _err(dev, dev_err), _raw_stream(dev)), "moe_group_down")
+    return o
