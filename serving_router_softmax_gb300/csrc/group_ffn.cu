@@ -234,7 +234,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kGateUp>, 1
       for (long long t = pair; t < total && ok; t += pairs) {
         walk.at(t, &x);
         const uint32_t idesc = tc::idesc_bf16_f32(256, __shfl_sync(0xFFFFFFFFu, x.N, 0)), d = tm + acc * 256;
-        ok = tc::mbar_sleep<true>(&sm.acc_empty[acc], aph ^ 1, gave_up, kWaitNs);
+        ok = tc::mbar_sleep<true, true>(&sm.acc_empty[acc], aph ^ 1, gave_up, kWaitNs);
         tc::tc_fence_after();
         for (int kb = 0; kb < KB; ++kb) {
           if (!there && ok) ok = tc::mbar_sleep<true>(&sm.full[s], ph, gave_up, kWaitNs);

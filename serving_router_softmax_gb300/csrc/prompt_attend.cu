@@ -5,9 +5,11 @@
 // heads of floor(128 / G) tokens each, token by token, so that any number of
 // heads fills the tiles and the heads share their keys.  Per 128 keys and tile:
 //   S [128 x 128] = Q K^T           operands in shared memory, sums in TMEM
-//   P = exp2(c S - r), l += row sums    a thread per row, P over S in TMEM as bf16
+//   P = exp2(c S - r), l += row sums    a thread per row, P in TMEM as bf16
 //   O [128 x D] += P V              P from TMEM, V as it lies ([keys][D])
-// One tile's products run while the other's exponentials do.
+// One tile's products run while the other's exponentials do.  At D = 64 TMEM has
+// room for P beside S, and the next step's S is made while this one's exponentials
+// run; at D = 128 P lies over S, and a step is a chain: S, exponentials, P V.
 //
 // The reference r of a row's exponentials need not be its maximum: any r gives
 // the same quotient O / l.  It moves (and O and l are scaled to it) only when a
@@ -29,11 +31,12 @@
 // dimension the first such key, which makes the output of the rows that see it
 // NaN.
 //
-// Roles (384 threads): warps 0-3 and 4-7 softmax and output of a tile each,
-// warps 8 and 9 issue a tile's products each (the tensor core takes a product as
-// it begins it, so one warp's waits and signals for both tiles, 1900 cycles a step,
-// were not hidden by the 2050 of its products), warp 10 finds the items and loads
-// by TMA, warp 11 looks at values.  Every wait is bounded.
+// Roles (512 threads): warps 0-3 and 4-7 softmax and output of a tile each, warps 8
+// and 9 issue a tile's products each (the tensor core takes a product as it begins
+// it, so one warp's waits and signals for both tiles, 1900 cycles a step, were not
+// hidden by the 2050 of its products; at D = 64 warps 10 and 11 issue those with V),
+// warp 12 finds the items and loads by TMA, warp 13 looks at values.  Every wait is
+// bounded.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -50,7 +53,7 @@ using tc::add2;
 using tc::fma2;
 using tc::mul2;
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kRows = 128;       // query rows of a tile, keys of a step
 constexpr int kPanel = kRows * 128;  // bytes of 64 dimensions of a tile
 constexpr float kSlack = 8.f;
@@ -64,7 +67,7 @@ struct PromptArgs {
   int32_t* dev_err;
   int T, S, Hq, Hkv, G, tokens;  // tokens: of a tile
   float c;                       // |scale| log2(e)
-  int negative, stall;           // scale < 0; test hook
+  int negative, wide, stall;     // scale < 0; out a multiple of 32 bytes; test hook
 };
 
 struct Item {
@@ -79,10 +82,9 @@ struct Smem {
   static constexpr int kStages = D == 128 ? 4 : 8;
   alignas(1024) uint8_t q[2][D / 64][kPanel];
   alignas(1024) uint8_t kv[kStages][D / 64][kPanel];
-  alignas(16) uint8_t turn[8][32 * 64];               // output rows of a warp, 32 dimensions at a time
   int blocks[kMaxSeqs];                               // of each sequence
   uint64_t full[kStages], empty[kStages], v_ok[kStages];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2], item_full[2], item_empty[2], drain;
+  uint64_t q_full[2], q_empty[2], s_full[2], s_read[2], p_full[2], pv_done[2], o_full[2], o_empty[2], item_full[2], item_empty[2], drain;
   Item item[2];
   int first_bad[2][D], bad[2];
   int most;
@@ -107,6 +109,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float2* e) {
 __device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// 32 bytes; `wide`: to an address that is a multiple of them.
+__device__ __forceinline__ void store32(uint16_t* at, const uint32_t (&w)[8], int wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+                 "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(at + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 
 // D[tmem] (+)= A[tmem] * B[smem], bf16.
@@ -191,6 +205,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const PromptArgs a) {
   using Sm = Smem<D>;
   constexpr int NS = Sm::kStages, P = D / 64;
+  constexpr bool kApart = D == 64;  // P beside S
+  // TMEM columns: S of both tiles, P (beside or over it), O.
+  constexpr int kPCol = kApart ? 256 : 0, kPStep = kApart ? 64 : 128, kOCol = kApart ? 384 : 256;
   extern __shared__ uint8_t raw[];
   Sm& sm = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -199,12 +216,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < NS; ++i) tc::mbar_init(&sm.full[i], 1), tc::mbar_init(&sm.empty[i], 2), tc::mbar_init(&sm.v_ok[i], 1);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sm.q_full[i], 1), tc::mbar_init(&sm.q_empty[i], 1);
-      tc::mbar_init(&sm.s_full[i], 1), tc::mbar_init(&sm.p_full[i], 4);
+      tc::mbar_init(&sm.s_full[i], 1), tc::mbar_init(&sm.s_read[i], 4), tc::mbar_init(&sm.pv_done[i], 1);
+      tc::mbar_init(&sm.p_full[i], 4);
       tc::mbar_init(&sm.o_full[i], 1), tc::mbar_init(&sm.o_empty[i], 4);
-      tc::mbar_init(&sm.item_full[i], 1), tc::mbar_init(&sm.item_empty[i], 11);
+      tc::mbar_init(&sm.item_full[i], 1), tc::mbar_init(&sm.item_empty[i], kApart ? 13 : 11);
       sm.bad[i] = 0;
     }
-    tc::mbar_init(&sm.drain, 2);
+    tc::mbar_init(&sm.drain, kApart ? 4 : 2);
     sm.abort = sm.most = 0;
     tc::fence_mbar_init();
   }
@@ -249,10 +267,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 8) {
     // ---------------------------------------------------------- softmax, output
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     const int t = warp >> 2, r = (warp & 3) * 32 + lane, tok = r / a.G, in_group = r % a.G;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * D;
+    const uint32_t ts = tmem + lanes + t * 128, tp = tmem + lanes + kPCol + t * kPStep, to = tmem + lanes + kOCol + t * D;
     const float2 c2 = make_float2(a.c, a.c);
     int step = 0, items = 0;  // of this tile
     while (true) {
@@ -266,7 +284,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int from = it.first + t * a.tokens, pos = from + tok;
       const bool real = tok < a.tokens && pos < it.len;
       const int limit = real ? pos + 1 : 0;  // keys that the row sees
-      const int seen = seen_by(a, it, t);
       float ref = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f), k2 = make_float2(0.f, 0.f);
       for (int j = 0; j < steps; ++j, ++step) {
@@ -274,50 +291,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc::tc_fence_after();
         float2 s[64];
-        tmem_ld32(ts, s);
-        tmem_ld32(ts + 32, s + 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 16 * i);
         tc::tmem_ld_wait();
-        tmem_ld32(ts + 64, s + 32);
-        tmem_ld32(ts + 96, s + 48);
-        const bool masked = (j + 1) * kRows > from + 1;
-        const int see = limit - j * kRows, here = seen - j * kRows;  // (here: of the tile's last row; columns beyond hold anything)
+        if (kApart) {
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sm.s_read[t]);
+        }
+        if ((j + 1) * kRows > from + 1) {
+          const int see = limit - j * kRows;
+#pragma unroll
+          for (int i = 0; i < 64; ++i) {
+            s[i].x = 2 * i < see ? s[i].x : -INFINITY;
+            s[i].y = 2 * i + 1 < see ? s[i].y : -INFINITY;
+          }
+        }
         float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h == 1) tc::tmem_ld_wait();
-          if (masked) {
-#pragma unroll
-            for (int i = 32 * h; i < 32 * h + 32; ++i) {
-              s[i].x = 2 * i < see ? s[i].x : -INFINITY;
-              s[i].y = 2 * i + 1 < see ? s[i].y : -INFINITY;
-            }
-          }
-#pragma unroll
-          for (int i = 32 * h; i < 32 * h + 32; ++i) m[i & 3] = kv4::max3(m[i & 3], s[i].x, s[i].y);
-        }
+        for (int i = 0; i < 64; ++i) m[i & 3] = kv4::max3(m[i & 3], s[i].x, s[i].y);
         const float top = fmaxf(kv4::max3(m[0], m[1], m[2]), m[3]) * a.c;
         const bool move = top > ref + kSlack;
+        if (kApart && j > 0) {  // the products of the step before (D = 128: the scores came after them)
+          ok = tc::mbar_sleep<true>(&sm.pv_done[t], (step - 1) & 1, gave_up, kWaitNs);
+          if (!ok) break;
+          tc::tc_fence_after();
+        }
         if (__any_sync(0xFFFFFFFFu, move)) {
           const float f = move ? kv4::ex2(ref - top) : 1.f;  // (0 from -inf)
           if (move) ref = top;
           const float2 f2 = make_float2(f, f);
           l2 = mul2(l2, f2), k2 = mul2(k2, f2);
-          if (j > 0) {  // (the products of the step before are over: the scores came after them)
+          if (j > 0) {
 #pragma unroll 1
-            for (int i = 0; i < D; i += 32) {
-              float2 o[16];
-              tmem_ld32(to + i, o);
+            for (int i = 0; i < D; i += 16) {
+              float o[16];
+              tc::tmem_ld16(to + i, o);
               tc::tmem_ld_wait();
+              uint32_t w[16];
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint32_t w[16];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const float2 x = mul2(o[8 * h + e], f2);
-                  w[2 * e] = __float_as_uint(x.x), w[2 * e + 1] = __float_as_uint(x.y);
-                }
-                tc::tmem_st16(to + i + 16 * h, w);
-              }
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
+              tc::tmem_st16(to + i, w);
             }
           }
         }
@@ -325,7 +339,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 r2 = make_float2(neg, neg);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (32 * i >= here) break;  // no product takes them
           uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -337,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               l2 = add2(l2, x);
             w[e] = pack_bf(x.x, x.y);
           }
-          tc::tmem_st16(ts + 16 * i, w);
+          tc::tmem_st16(tp + 16 * i, w);
         }
         tc::tmem_st_wait();
         tc::tc_fence_before();
@@ -352,72 +365,75 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const bool some_bad = sm.bad[turn.slot()] != 0;
       const int* bad = sm.first_bad[turn.slot()];
-      const int mine = real ? tok * a.Hq * D + in_group * D : -1;
       const size_t row0 = static_cast<size_t>(it.begin + from) * a.Hq + it.head * a.G;
-      uint16_t* out = a.out + row0 * D;
       if (real && a.lse) a.lse[row0 + tok * a.Hq + in_group] = l == 0.f ? -INFINITY : (ref == -INFINITY ? 0.f : ref) * kv4::kLn2 + logf(l);
-      // A lane's row goes through shared memory, 32 dimensions at a time, so that a store takes 64 bytes of each of 8 rows.
-      uint8_t* buf = sm.turn[warp];
+      float2 o[D / 2];
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        float2 o[16];
-        tmem_ld32(to + 32 * i, o);
-        tc::tmem_ld_wait();
-        if (i == D / 32 - 1) {  // the sums may be written over
-          tc::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&sm.o_empty[t]);
+      for (int i = 0; i < D / 32; ++i) tmem_ld32(to + 32 * i, o + 16 * i);
+      tc::tmem_ld_wait();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.o_empty[t]);
+      if (some_bad) {
+#pragma unroll
+        for (int e = 0; e < D / 2; ++e) {
+          if (bad[2 * e] < limit) o[e].x = NAN;
+          if (bad[2 * e + 1] < limit) o[e].y = NAN;
         }
-        if (some_bad) {
+      }
+      // A lane has a whole row: 32 bytes, a sector, to a store.  (Through shared memory, 64 bytes of 8 rows to a store, it took
+      // 3900 cycles an item.)
+      const float2 i2 = make_float2(inv, inv);
+      uint16_t* row = a.out + row0 * D + tok * a.Hq * D + in_group * D;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            if (bad[32 * i + 2 * e] < limit) o[e].x = NAN;
-            if (bad[32 * i + 2 * e + 1] < limit) o[e].y = NAN;
-          }
+      for (int e = 0; e < D / 2; e += 8) {
+        uint32_t w[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const float2 v = mul2(o[e + x], i2);
+          w[x] = l == 0.f ? 0u : pack_bf(v.x, v.y);
         }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          uint32_t w[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) w[y] = l == 0.f ? 0u : pack_bf(o[4 * x + y].x * inv, o[4 * x + y].y * inv);
-          *reinterpret_cast<uint4*>(buf + lane * 64 + ((x ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        __syncwarp();
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int row = 8 * x + (lane >> 2), part = lane & 3;
-          const int at = __shfl_sync(0xFFFFFFFFu, mine, row);
-          const uint4 v = *reinterpret_cast<const uint4*>(buf + row * 64 + ((part ^ ((row >> 1) & 3)) << 4));
-          if (at >= 0) *reinterpret_cast<uint4*>(out + at + 32 * i + part * 8) = v;
-        }
-        __syncwarp();
+        if (real) store32(row + 2 * e, w, a.wide);
       }
       item_done();
     }
     if (!ok && lane == 0) flag_error(a.dev_err, MOE_DEV_TIMEOUT);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
   }
-  if (warp == 8 || warp == 9) {
+  if (warp < 8) {
+  } else if (warp < (kApart ? 12 : 10)) {
     // ---------------------------------------------------------- products
-    const int t = __shfl_sync(0xFFFFFFFFu, warp - 8, 0);
+    const int t = __shfl_sync(0xFFFFFFFFu, warp & 1, 0);
+    const bool with_k = warp < 10, with_v = !kApart || !with_k;  // S = Q K^T, O += P V
     const uint32_t neg = a.negative ? kNegateA : 0u;
     const uint32_t iv = tc::idesc_bf16_f32(kRows, D) | kValuesAlongN;
     constexpr int kTile = P * kPanel >> 4;
     const uint64_t qd = tc::smem_desc_sw128(tc::smem_u32(sm.q[0][0])) + t * kTile, kd = tc::smem_desc_sw128(tc::smem_u32(sm.kv[0][0]));
     const uint64_t vd = value_desc(tc::smem_u32(sm.kv[0][0]));
-    const uint32_t ts = tmem + t * 128, to = tmem + 256 + t * D;
+    const uint32_t ts = tmem + t * 128, tp = tmem + kPCol + t * kPStep, to = tmem + kOCol + t * D;
     int place = 0;                          // in the ring's order: keys, values, keys, ...
     int steps_done = 0, items_done = 0;     // of this tile
     auto wait = [&](uint64_t* bar, int index) {  // its index-th phase
       if (ok) ok = tc::mbar_sleep<true>(bar, index & 1, gave_up, kWaitNs);
     };
-    // (within one elected thread)  The first `keys` keys' scores, a multiple of 16.
-    auto scores = [&](int stage, int keys) {
+    // (within one elected thread)  The scores of the first `keys` keys, a multiple of 16.
+    auto scores = [&](int stage, int keys, bool last) {
       const uint32_t is = tc::idesc_bf16_f32(kRows, keys) | neg;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
         tc::mma_bf16(ts, qd + (i / 4) * (kPanel >> 4) + 2 * (i % 4), kd + stage * kTile + (i / 4) * (kPanel >> 4) + 2 * (i % 4), is, i > 0);
+      tc::mma_commit(&sm.s_full[t]);
+      tc::mma_commit(&sm.empty[stage]);
+      if (last) tc::mma_commit(&sm.q_empty[t]);
+    };
+    auto values = [&](int stage, int parts, int j) {
+      if (parts == kRows / 16) {
+#pragma unroll
+        for (int i = 0; i < kRows / 16; ++i) mma_bf16_ts(to, tp + 8 * i, vd + stage * kTile + i * (2048 >> 4), iv, j > 0 || i > 0);
+      } else {
+        for (int i = 0; i < parts; ++i) mma_bf16_ts(to, tp + 8 * i, vd + stage * kTile + i * (2048 >> 4), iv, j > 0 || i > 0);
+      }
     };
     // An item's first scores; keys and values that only the other tile uses are handed back as they are seen.
     auto start = [&](const Item& it, int at) {
@@ -428,58 +444,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
       }
       wait(&sm.q_full[t], items_done);
+      if (kApart && steps_done) wait(&sm.s_read[t], steps_done - 1);
       tc::tc_fence_after();
-      if (ok && tc::elect_one()) {
-        scores(st, min(kRows, (seen_by(a, it, t) + 15) & ~15));
-        tc::mma_commit(&sm.s_full[t]);
-        tc::mma_commit(&sm.empty[st]);
-        if (steps == 1) tc::mma_commit(&sm.q_empty[t]);
-      }
+      if (ok && tc::elect_one()) scores(st, min(kRows, (seen_by(a, it, t) + 15) & ~15), steps == 1);
       __syncwarp();
     };
     Item it = next_item();
-    if (it.n[0] >= 0) start(it, 0);
+    if (with_k && it.n[0] >= 0) start(it, 0);
     while (it.n[0] >= 0 && ok) {
       const int n = max(it.n[0], it.n[1]), steps = t ? it.n[1] : it.n[0], seen = seen_by(a, it, t);
       for (int j = 0; j < n && ok; ++j) {
         const int v = place + 2 * j + 1, k = v + 1, sv = v % NS, sk = k % NS;  // this step's values, the next one's keys
-        wait(&sm.v_ok[sv], v / NS);
-        if (j + 1 < n) wait(&sm.full[sk], k / NS);
-        if (j < steps) {
-          const bool more = j + 1 < steps;
-          if (j == 0) wait(&sm.o_empty[t], items_done + 1);  // (the first passes)
-          wait(&sm.p_full[t], steps_done++);
-          tc::tc_fence_after();
-          if (ok && tc::elect_one()) {
-            if (more) {
-#pragma unroll
-              for (int i = 0; i < kRows / 16; ++i) mma_bf16_ts(to, ts + 8 * i, vd + sv * kTile + i * (2048 >> 4), iv, j > 0 || i > 0);
-            } else {
-              for (int i = 0; 16 * i < seen - j * kRows; ++i) mma_bf16_ts(to, ts + 8 * i, vd + sv * kTile + i * (2048 >> 4), iv, j > 0 || i > 0);
-            }
-            if (more) {
-              scores(sk, min(kRows, (seen - (j + 1) * kRows + 15) & ~15));
-              tc::mma_commit(&sm.s_full[t]);
-              tc::mma_commit(&sm.empty[sk]);
-              if (j + 2 == steps) tc::mma_commit(&sm.q_empty[t]);
-            } else {
-              tc::mma_commit(&sm.o_full[t]);
-            }
-            tc::mma_commit(&sm.empty[sv]);
+        const bool more = j + 1 < steps, other = j + 1 < n;
+        const int keys = min(kRows, (seen - (j + 1) * kRows + 15) & ~15);      // of the next step
+        if (with_k && other) wait(&sm.full[sk], k / NS);
+        if (kApart && with_k) {
+          if (more) {
+            wait(&sm.s_read[t], steps_done);
+            tc::tc_fence_after();
+            if (ok && tc::elect_one()) scores(sk, keys, j + 2 == steps);
+            __syncwarp();
+          } else if (other && ok && lane == 0) {
+            tc::mbar_arrive(&sm.empty[sk]);
           }
-          __syncwarp();
-          if (!more && j + 1 < n && ok && lane == 0) tc::mbar_arrive(&sm.empty[sk]);
-        } else if (ok && lane == 0) {
-          tc::mbar_arrive(&sm.empty[sv]);
-          if (j + 1 < n) tc::mbar_arrive(&sm.empty[sk]);
         }
+        if (with_v) {
+          wait(&sm.v_ok[sv], v / NS);
+          if (j < steps) {
+            if (j == 0) wait(&sm.o_empty[t], items_done + 1);  // (the first passes)
+            wait(&sm.p_full[t], steps_done);
+            tc::tc_fence_after();
+            if (ok && tc::elect_one()) {
+              values(sv, more ? kRows / 16 : (seen - j * kRows + 15) / 16, j);
+              if (kApart) tc::mma_commit(&sm.pv_done[t]);
+              if (!kApart && more) scores(sk, keys, j + 2 == steps);
+              if (!more) tc::mma_commit(&sm.o_full[t]);
+              tc::mma_commit(&sm.empty[sv]);
+            }
+            __syncwarp();
+            if (!kApart && !more && other && ok && lane == 0) tc::mbar_arrive(&sm.empty[sk]);
+          } else if (ok && lane == 0) {
+            tc::mbar_arrive(&sm.empty[sv]);
+            if (!kApart && other) tc::mbar_arrive(&sm.empty[sk]);
+          }
+        }
+        steps_done += j < steps;
       }
       if (!ok) break;
       items_done += steps > 0;
       place += 2 * n;
       item_done();
       it = next_item();
-      if (it.n[0] >= 0) start(it, place);
+      if (with_k && it.n[0] >= 0) start(it, place);
     }
     if (!ok) {
       if (lane == 0) flag_error(a.dev_err, MOE_DEV_TIMEOUT);
@@ -490,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
-  } else if (warp == 10) {
+  } else if (warp == 12) {
     // ---------------------------------------------------------- items and loads
     Finder finder{a, sm.blocks, sm.most};
     int place = 0, q_used[2] = {0, 0};
@@ -511,19 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) tc::mbar_arrive(&sm.item_full[slot]);
       ++turn.i;
       if (it.n[0] < 0) break;
-      const int row = it.begin + it.first;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (it.n[t] == 0) continue;
-        if (ok) ok = tc::mbar_sleep<true>(&sm.q_empty[t], (q_used[t] + 1) & 1, gave_up, kWaitNs);
-        ++q_used[t];
-        if (ok && tc::elect_one()) {
-          tc::mbar_arrive_expect_tx(&sm.q_full[t], P * a.G * a.tokens * 128);
-          for (int p = 0; p < P; ++p) tc::tma_load(sm.q[t][p], &qmap, 64 * p, it.head * a.G, row + t * a.tokens, &sm.q_full[t]);
-        }
-        __syncwarp();
-      }
-      const int n = max(it.n[0], it.n[1]);
+      const int row = it.begin + it.first, n = max(it.n[0], it.n[1]);
       for (int x = 0; x < 2 * n && ok; ++x, ++place) {
         const int s = place % NS;
         ok = tc::mbar_sleep<true>(&sm.empty[s], (place / NS + 1) & 1, gave_up, kWaitNs);
@@ -535,6 +539,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
+        if (x > 0) continue;
+        // (Behind the first keys: the queries' place is free a step later than theirs.)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (it.n[t] == 0) continue;
+          if (ok) ok = tc::mbar_sleep<true>(&sm.q_empty[t], (q_used[t] + 1) & 1, gave_up, kWaitNs);
+          ++q_used[t];
+          if (ok && tc::elect_one()) {
+            tc::mbar_arrive_expect_tx(&sm.q_full[t], P * a.G * a.tokens * 128);
+            for (int p = 0; p < P; ++p) tc::tma_load(sm.q[t][p], &qmap, 64 * p, it.head * a.G, row + t * a.tokens, &sm.q_full[t]);
+          }
+          __syncwarp();
+        }
       }
       if (!ok) break;
     }
@@ -547,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
-  } else if (warp == 11) {
+  } else if (warp == 13) {
     // ---------------------------------------------------------- values that a row may not see
     int place = 0;
     while (true) {
@@ -655,6 +672,7 @@ extern "C" int moe_prompt_attend(const void* q, const void* k, const void* v, co
   a.tokens = kRows / a.G;
   a.c = std::fmax(std::fabs(c.scale) * kv4::kLog2e, 1.17549435e-38f);  // (not 0: what is left out is -inf times this)
   a.negative = c.scale < 0.f;
+  a.wide = reinterpret_cast<uintptr_t>(out) % 32 == 0;
   a.stall = (test_stall_mask() & MOE_TEST_STALL_PROMPT) != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return c.head_dim == 64 ? launch<64>(c, q, k, v, a, s) : launch<128>(c, q, k, v, a, s);

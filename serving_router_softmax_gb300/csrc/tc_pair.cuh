@@ -35,28 +35,34 @@ __device__ __forceinline__ void mbar_arrive_at(uint32_t addr) {
 // Makes this thread's writes to shared memory visible to the tensor cores and bulk copies.
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// Whether the phase of this parity is over, without waiting; what either CTA did before it is seen.
+// Whether the phase of this parity is over, without waiting.
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok)
+               : "r"(smem_u32(bar)), "r"(parity)
+               : "memory");
   return ok != 0;
 }
 // Waits for it, asleep in hardware (warps that poll take issue slots from the one that feeds the tensor core); gives up after
-// budget_ns, or when *abort is set.  kWarp: the lanes of a warp give up together.
-template <bool kWarp>
+// budget_ns, or when *abort is set.  kWarp: the lanes of a warp give up together.  kPair: what the other CTA's threads did
+// before they arrived is seen too (some 100 cycles more a wait).
+template <bool kWarp, bool kPair = false>
 __device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t budget_ns) {
   uint64_t t0 = 0;
   for (uint32_t n = 1;; ++n) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(2000u)
-        : "memory");
+    if (kPair)
+      asm volatile(
+          "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity), "r"(2000u)
+          : "memory");
+    else
+      asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                   : "=r"(ok)
+                   : "r"(smem_u32(bar)), "r"(parity), "r"(2000u)
+                   : "memory");
     if (kWarp ? __all_sync(0xFFFFFFFFu, ok) : ok) return true;
     if ((n & 31) == 0) {
       const uint64_t now = globaltimer_ns();
