@@ -300,11 +300,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) tc::mbar_arrive(&sm.s_read[t]);
         }
         if ((j + 1) * kRows > from + 1) {
+          // (Code that runs once an item comes from far: only the groups of 32 keys that some row does not see.)
           const int see = limit - j * kRows;
 #pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            s[i].x = 2 * i < see ? s[i].x : -INFINITY;
-            s[i].y = 2 * i + 1 < see ? s[i].y : -INFINITY;
+          for (int g = 0; g < 4; ++g) {
+            if (__all_sync(0xFFFFFFFFu, see >= 32 * g + 32)) continue;
+#pragma unroll
+            for (int i = 16 * g; i < 16 * g + 16; ++i) {
+              s[i].x = 2 * i < see ? s[i].x : -INFINITY;
+              s[i].y = 2 * i + 1 < see ? s[i].y : -INFINITY;
+            }
           }
         }
         float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -362,38 +367,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++items;
       tc::tc_fence_after();
       const float l = (l2.x + l2.y) + (k2.x + k2.y);
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float inv = l == 0.f ? 0.f : kv4::rcp(l);
       const bool some_bad = sm.bad[turn.slot()] != 0;
       const int* bad = sm.first_bad[turn.slot()];
       const size_t row0 = static_cast<size_t>(it.begin + from) * a.Hq + it.head * a.G;
-      if (real && a.lse) a.lse[row0 + tok * a.Hq + in_group] = l == 0.f ? -INFINITY : (ref == -INFINITY ? 0.f : ref) * kv4::kLn2 + logf(l);
-      float2 o[D / 2];
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) tmem_ld32(to + 32 * i, o + 16 * i);
-      tc::tmem_ld_wait();
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sm.o_empty[t]);
-      if (some_bad) {
-#pragma unroll
-        for (int e = 0; e < D / 2; ++e) {
-          if (bad[2 * e] < limit) o[e].x = NAN;
-          if (bad[2 * e + 1] < limit) o[e].y = NAN;
-        }
-      }
-      // A lane has a whole row: 32 bytes, a sector, to a store.  (Through shared memory, 64 bytes of 8 rows to a store, it took
-      // 3900 cycles an item.)
-      const float2 i2 = make_float2(inv, inv);
+      if (real && a.lse)
+        a.lse[row0 + tok * a.Hq + in_group] = l == 0.f ? -INFINITY : ((ref == -INFINITY ? 0.f : ref) + kv4::lg2(l)) * kv4::kLn2;
+      // A lane has a whole row: 32 bytes, a sector, to a store.  The loop stays a loop: unrolled it took 4000 cycles an item, most of
+      // them waiting for instructions.
       uint16_t* row = a.out + row0 * D + tok * a.Hq * D + in_group * D;
-#pragma unroll
-      for (int e = 0; e < D / 2; e += 8) {
-        uint32_t w[8];
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const float2 v = mul2(o[e + x], i2);
-          w[x] = l == 0.f ? 0u : pack_bf(v.x, v.y);
+#pragma unroll 1
+      for (int i = 0; i < D; i += 32) {
+        float2 o[16];
+        tmem_ld32(to + i, o);
+        tc::tmem_ld_wait();
+        if (i + 32 == D) {
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sm.o_empty[t]);
         }
-        if (real) store32(row + 2 * e, w, a.wide);
+        if (some_bad) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            if (bad[i + 2 * e] < limit) o[e].x = NAN;
+            if (bad[i + 2 * e + 1] < limit) o[e].y = NAN;
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) w[x] = l == 0.f ? 0u : pack_bf(o[8 * h + x].x * inv, o[8 * h + x].y * inv);
+          if (real) store32(row + i + 16 * h, w, a.wide);
+        }
       }
       item_done();
     }
