@@ -123,6 +123,25 @@ __device__ __forceinline__ void store32(uint16_t* at, const uint32_t (&w)[8], in
   }
 }
 
+// Units u (bit kBit clear) and u + kBit of the four lanes of a quad: the lane whose number has the bit keeps u + kBit and takes the
+// other lane's, the other one the lower ones.  With both bits, unit k of lane g is what was unit g of lane k.
+template <int kBit>
+__device__ __forceinline__ void turn4(uint32_t (&w)[4][8], int lane) {
+  const bool high = lane & kBit;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if (u & kBit) continue;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, high ? w[u][x] : w[u + kBit][x], kBit);
+      if (high)
+        w[u][x] = got;
+      else
+        w[u + kBit][x] = got;
+    }
+  }
+}
+
 // D[tmem] (+)= A[tmem] * B[smem], bf16.
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   tc::mma_f16_ts(d, a, b, idesc, accumulate);
@@ -373,33 +392,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t row0 = static_cast<size_t>(it.begin + from) * a.Hq + it.head * a.G;
       if (real && a.lse)
         a.lse[row0 + tok * a.Hq + in_group] = l == 0.f ? -INFINITY : ((ref == -INFINITY ? 0.f : ref) + kv4::lg2(l)) * kv4::kLn2;
-      // A lane has a whole row: 32 bytes, a sector, to a store.  The loop stays a loop: unrolled it took 4000 cycles an item, most of
-      // them waiting for instructions.
-      uint16_t* row = a.out + row0 * D + tok * a.Hq * D + in_group * D;
+      // A lane has a whole row.  Four lanes turn their rows' 128 bytes about, so that a store takes whole lines: 8 rows' 128 bytes
+      // (32 bytes of each of 32 rows to a store: 3300 cycles an item).  The loop stays a loop: code that runs once an item comes
+      // from far.
+      const int mine = real ? tok * a.Hq * D + in_group * D : -1, quarter = lane & 3;
+      uint16_t* out = a.out + row0 * D + quarter * 16;
+      int at[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) at[k] = __shfl_sync(0xFFFFFFFFu, mine, (lane & ~3) + k);
 #pragma unroll 1
-      for (int i = 0; i < D; i += 32) {
-        float2 o[16];
-        tmem_ld32(to + i, o);
-        tc::tmem_ld_wait();
-        if (i + 32 == D) {
+      for (int i = 0; i < D; i += 64) {
+        uint32_t w[4][8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float2 o[16];
+          tmem_ld32(to + i + 32 * h, o);
+          tc::tmem_ld_wait();
+          if (some_bad) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              if (bad[i + 32 * h + 2 * e] < limit) o[e].x = NAN;
+              if (bad[i + 32 * h + 2 * e + 1] < limit) o[e].y = NAN;
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < 16; ++x) w[2 * h + x / 8][x % 8] = l == 0.f ? 0u : pack_bf(o[x].x * inv, o[x].y * inv);
+        }
+        if (i + 64 == D) {
           tc::tc_fence_before();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&sm.o_empty[t]);
         }
-        if (some_bad) {
+        turn4<1>(w, lane);
+        turn4<2>(w, lane);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            if (bad[i + 2 * e] < limit) o[e].x = NAN;
-            if (bad[i + 2 * e + 1] < limit) o[e].y = NAN;
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[8];
-#pragma unroll
-          for (int x = 0; x < 8; ++x) w[x] = l == 0.f ? 0u : pack_bf(o[8 * h + x].x * inv, o[8 * h + x].y * inv);
-          if (real) store32(row + i + 16 * h, w, a.wide);
-        }
+        for (int k = 0; k < 4; ++k)
+          if (at[k] >= 0) store32(out + at[k] + i, w[k], a.wide);
       }
       item_done();
     }

@@ -626,3 +626,25 @@ def test_other_streams_and_repeats(mv):
         assert torch.equal(a, b)
     for _ in range(5):
         assert all(torch.equal(a, b) for a, b in zip(pr.run(), want))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(64, 4, 128), (14, 2, 64), (8, 8, 128)])
+def test_prompt_attend_many_items(mv, Hq, Hkv, D):
+    """More blocks than CTAs, of one step and of several, again and again: no wait runs out, the same bits every time."""
+    g = gen(14)
+    lengths = [300, 20, 1, 700, 16, 16, 129, 0, 60] * 14
+    T = sum(lengths)
+    q, k, v = randn(g, T, Hq, D), randn(g, T, Hkv, D), randn(g, T, Hkv, D)
+    start = [0]
+    for n in lengths:
+        start.append(start[-1] + n)
+    st = torch.tensor(start, dtype=torch.int32, device="cuda")
+    err = mv.new_dev_err()
+    out, lse = mv.prompt_attend(q, k, v, st, dev_err=err)
+    want, z, ot, lt = attend_exact(q[:2484], k[:2484], v[:2484], start[:19], D ** -0.5)
+    within(lse[:2484], z, lt)
+    within(out[:2484], want, ot)
+    for _ in range(40):
+        o, l = mv.prompt_attend(q, k, v, st, dev_err=err)
+        assert torch.equal(o, out) and torch.equal(l, lse)
+    assert err.item() == 0
