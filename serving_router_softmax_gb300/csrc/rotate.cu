@@ -6,13 +6,19 @@
 // angle within half a turn either way, known to 2^-34 of a turn before it is
 // rounded to fp32, so cosine and sine are as good at position 2^31 as at 0.
 //
-// Bound by memory: every value is read and written once.  A thread keeps the
-// cosines and sines of one unit of pairs (16 bytes of first and 16 of second
-// halves) of one token in registers and walks the token's heads with them, in
-// 16-byte loads and stores.  How many heads it walks is a rule on the work:
-// as many as leave the device full, since a walk saves the angles and a thread
-// more hides latency.
+// Bound by memory: every value is read and written once (8192 tokens of 40 heads
+// of 128 in bf16: 28 us, 5.9 TB/s).  A block takes a few tokens, as many as give each
+// of its threads one cosine and sine to make, and these go to shared memory for all
+// of the tokens' heads (each thread making its own for up to 8 heads: 40 us).  A
+// thread keeps its 16 bytes' place in a row and steps through rows, two units' loads
+// (halves; four where a unit is one load) asked for before the first is used, the
+// first of them before the cosines; 48 registers a thread leave five blocks an SM
+// (twice as many loads in 97 registers: 40 us; an item's place worked out by division:
+// 32 us, and 30 instead of 19 for 3001 tokens of 72 fp32 heads).  With few tokens the
+// heads are split over blocks.
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 #include "common.cuh"
 
@@ -20,7 +26,8 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxWalk = 8;
+constexpr int kAhead = 2;
+constexpr int kMaxAngles = 512;
 
 struct RotateArgs {
   const uint8_t *q, *k;
@@ -30,9 +37,9 @@ struct RotateArgs {
   int32_t* dev_err;
   long long q_ts, q_hs, k_ts, k_hs, oq_ts, oq_hs, ok_ts, ok_hs;  // bytes
   int T, Hq, H, D, R, n_axes, inverse;
-  int units, turning;   // units of a row; those that turn come first
-  int walk, groups;     // heads of a thread, threads a token and unit
-  int copies;           // dimensions past R are copied
+  int units, turning;   // units of a row that is read; those that turn come first
+  int lanes_log2;       // threads a row: the units, rounded up to a power of two
+  int tokens, heads;    // of a block
 };
 
 // V values of 16 bytes as floats and back.
@@ -67,71 +74,103 @@ struct Row<__nv_bfloat16> {
   }
 };
 
-template <typename T, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateArgs a) {
-  constexpr int V = Row<T>::V;
-  const long long id = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x;
-  const int unit = static_cast<int>(id % a.units);
-  const long long rest = id / a.units;
-  const int g = static_cast<int>(rest % a.groups);
-  const long long t = rest / a.groups;
-  if (t >= a.T) return;
-  const bool turns = unit < a.turning;
-  if (!turns && !a.copies) return;
-  // Bytes of the unit's two 16-byte parts in a row (one part where it copies).
-  const int first = turns ? (kInterleaved ? unit * 32 : unit * 16) : a.R * static_cast<int>(sizeof(T)) + (unit - a.turning) * 16;
-  const int second = kInterleaved ? first + 16 : first + a.R / 2 * static_cast<int>(sizeof(T));
-  const int h0 = g * a.walk, h1 = min(a.H, h0 + a.walk);
-  float c[V], s[V];
-  if (turns) {
-    int last = -1;
-    uint64_t pos = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int ax = a.axis[unit * V + i];
-      const bool ok = ax >= 0 && ax < a.n_axes;
-      if (!ok && g == 0 && t == 0) flag_error(a.dev_err, MOE_DEV_BAD_ID);
-      if (ok && ax != last) pos = static_cast<uint64_t>(static_cast<int64_t>(a.pos[static_cast<long long>(ax) * a.T + t])), last = ax;
-      const uint64_t turn = ok ? pos * a.turns[unit * V + i] : 0;
-      // The nearest quarter turn and what is left of it, at most an eighth either way.
-      const uint64_t near = turn + (1ull << 61);
-      const int quarter = static_cast<int>(near >> 62);
-      const int64_t left = static_cast<int64_t>(turn - (static_cast<uint64_t>(quarter) << 62));
-      float sn, cs;
-      sincospif(static_cast<float>(left) * 0x1p-63f, &sn, &cs);
-      const float x = (quarter & 1) ? -sn : cs, y = (quarter & 1) ? cs : sn;
-      c[i] = (quarter & 2) ? -x : x;
-      s[i] = ((quarter & 2) != 0) != (a.inverse != 0) ? -y : y;
-    }
+// Cosine and sine (of minus the angle: `inverse`) of position pos and pair i.
+__device__ __forceinline__ float2 turn_of(const RotateArgs& a, long long t, int i, bool report) {
+  const int ax = a.axis[i];
+  if (ax < 0 || ax >= a.n_axes) {
+    if (report) flag_error(a.dev_err, MOE_DEV_BAD_ID);
+    return make_float2(1.f, 0.f);
   }
-  for (int h = h0; h < h1; ++h) {
-    const bool isq = h < a.Hq;
-    const uint8_t* in = isq ? a.q + t * a.q_ts + h * a.q_hs : a.k + t * a.k_ts + (h - a.Hq) * a.k_hs;
-    uint8_t* out = isq ? a.oq + t * a.oq_ts + h * a.oq_hs : a.ok + t * a.ok_ts + (h - a.Hq) * a.ok_hs;
-    uint4 u = *reinterpret_cast<const uint4*>(in + first);
-    if (turns) {
-      uint4 w = *reinterpret_cast<const uint4*>(in + second);
-      float x[V], y[V];
-      Row<T>::get(u, x);
-      Row<T>::get(w, y);
-      if (kInterleaved) {  // pairs side by side: the first part holds the unit's first V / 2 pairs
+  const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(a.pos[static_cast<long long>(ax) * a.T + t])) * a.turns[i];
+  // The nearest quarter turn and what is left of it, at most an eighth either way.
+  const int quarter = static_cast<int>((turn + (1ull << 61)) >> 62);
+  const int64_t left = static_cast<int64_t>(turn - (static_cast<uint64_t>(quarter) << 62));
+  float sn, cs;
+  sincospif(static_cast<float>(static_cast<int32_t>(left >> 30)) * 0x1p-33f, &sn, &cs);
+  const float x = (quarter & 1) ? -sn : cs, y = (quarter & 1) ? cs : sn;
+  return make_float2((quarter & 2) ? -x : x, ((quarter & 2) != 0) != (a.inverse != 0) ? -y : y);
+}
+
+template <typename T, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads, 5) rotate_kernel(const RotateArgs a) {
+  constexpr int V = Row<T>::V, kAt = kInterleaved ? 2 * kAhead : kAhead, kPairs = kInterleaved ? V / 2 : V;  // pairs of a unit
+  // A unit's first four and last four (of 8) lie apart, so that neighbouring units' 16 bytes lie side by side.
+  __shared__ alignas(16) float cs[kMaxAngles], sn[kMaxAngles];
+  auto slot = [](int i) { return kPairs == 8 ? ((i >> 2) & 1) * (kMaxAngles / 2) + (i >> 3) * 4 + (i & 3) : i; };
+  const int half = a.R / 2, h0 = blockIdx.y * a.heads, heads = min(a.heads, a.H - h0);
+  const long long t0 = static_cast<long long>(blockIdx.x) * a.tokens;
+  const int tokens = static_cast<int>(min(static_cast<long long>(a.tokens), a.T - t0)), rows = tokens * heads;
+  // A thread has one unit of every step-th row (a head of a token); its place in them stays.
+  const int unit = threadIdx.x & ((1 << a.lanes_log2) - 1), step = kThreads >> a.lanes_log2;
+  const bool turns = unit < a.turning, idle = unit >= a.units;
+  const int first = turns ? unit * 16 : a.R * static_cast<int>(sizeof(T)) + (unit - a.turning) * 16;
+  const int second = first + half * static_cast<int>(sizeof(T));
+  const int step_tok = step / heads, step_h = step % heads;
+  int row = threadIdx.x >> a.lanes_log2, tok = row / heads, h = row - tok * heads;
+  bool ready = false;
+  while (row < rows || !ready) {
+    uint4 u[kAt], w[kInterleaved ? 1 : kAt];
+    uint8_t* out[kAt];
+    int angle[kAt];
 #pragma unroll
-        for (int i = 0; i < V; i += 2) {
-          const float a0 = x[i], b0 = x[i + 1], a1 = y[i], b1 = y[i + 1];
-          x[i] = a0 * c[i / 2] - b0 * s[i / 2], x[i + 1] = a0 * s[i / 2] + b0 * c[i / 2];
-          y[i] = a1 * c[V / 2 + i / 2] - b1 * s[V / 2 + i / 2], y[i + 1] = a1 * s[V / 2 + i / 2] + b1 * c[V / 2 + i / 2];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float a0 = x[i], b0 = y[i];
-          x[i] = a0 * c[i] - b0 * s[i], y[i] = a0 * s[i] + b0 * c[i];
-        }
+    for (int j = 0; j < kAt; ++j) {
+      out[j] = nullptr;
+      if (row < rows && !idle) {
+        const long long t = t0 + tok;
+        const int head = h0 + h;
+        const uint8_t* in = (head < a.Hq ? a.q + t * a.q_ts + head * a.q_hs : a.k + t * a.k_ts + (head - a.Hq) * a.k_hs) + first;
+        out[j] = (head < a.Hq ? a.oq + t * a.oq_ts + head * a.oq_hs : a.ok + t * a.ok_ts + (head - a.Hq) * a.ok_hs) + first;
+        angle[j] = tok * half + unit * kPairs;
+        u[j] = *reinterpret_cast<const uint4*>(in);
+        if (!kInterleaved && turns) w[j] = *reinterpret_cast<const uint4*>(in + (second - first));
       }
-      u = Row<T>::put(x);
-      *reinterpret_cast<uint4*>(out + second) = Row<T>::put(y);
+      row += step, tok += step_tok, h += step_h;
+      if (h >= heads) h -= heads, ++tok;
     }
-    *reinterpret_cast<uint4*>(out + first) = u;
+    if (!ready) {
+      for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
+        const float2 c = turn_of(a, t0 + i / half, i % half, blockIdx.x == 0 && blockIdx.y == 0);
+        cs[slot(i)] = c.x, sn[slot(i)] = c.y;
+      }
+      __syncthreads();
+      ready = true;
+    }
+#pragma unroll
+    for (int j = 0; j < kAt; ++j) {
+      if (!out[j]) continue;
+      if (turns) {
+        float x[V], c[kPairs], s[kPairs];
+        Row<T>::get(u[j], x);
+        if (kPairs == 2) {
+          *reinterpret_cast<float2*>(c) = *reinterpret_cast<const float2*>(cs + angle[j]);
+          *reinterpret_cast<float2*>(s) = *reinterpret_cast<const float2*>(sn + angle[j]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kPairs; i += 4) {
+            *reinterpret_cast<float4*>(c + i) = *reinterpret_cast<const float4*>(cs + slot(angle[j] + i));
+            *reinterpret_cast<float4*>(s + i) = *reinterpret_cast<const float4*>(sn + slot(angle[j] + i));
+          }
+        }
+        if (kInterleaved) {  // pairs side by side
+#pragma unroll
+          for (int i = 0; i < V; i += 2) {
+            const float a0 = x[i], b0 = x[i + 1];
+            x[i] = a0 * c[i / 2] - b0 * s[i / 2], x[i + 1] = a0 * s[i / 2] + b0 * c[i / 2];
+          }
+        } else {
+          float y[V];
+          Row<T>::get(w[j], y);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float a0 = x[i], b0 = y[i];
+            x[i] = a0 * c[i] - b0 * s[i], y[i] = a0 * s[i] + b0 * c[i];
+          }
+          *reinterpret_cast<uint4*>(out[j] + (second - first)) = Row<T>::put(y);
+        }
+        u[j] = Row<T>::put(x);
+      }
+      *reinterpret_cast<uint4*>(out[j]) = u[j];
+    }
   }
 }
 
@@ -146,21 +185,25 @@ bool apart(long long ts, int T, long long hs, int H, long long D) {
 }
 
 template <typename T>
-int launch(const moe_rotate_cfg& c, RotateArgs a, cudaStream_t s) {
+int launch(const moe_rotate_cfg& c, RotateArgs a, bool copies, cudaStream_t s) {
   constexpr int V = Row<T>::V;
-  a.turning = a.R / (2 * V);
-  a.units = a.turning + (a.D - a.R) / V;
-  const long long threads = static_cast<long long>(a.T) * a.units * a.H, full = sm_count() * 2048ll;
-  a.walk = static_cast<int>(threads / full);
-  a.walk = a.walk < 1 ? 1 : a.walk > kMaxWalk ? kMaxWalk : a.walk;
-  a.groups = (a.H + a.walk - 1) / a.walk;
-  const long long blocks = (static_cast<long long>(a.T) * a.units * a.groups + kThreads - 1) / kThreads;
-  if (blocks > 0x7FFFFFFFll) return MOE_ERR_UNSUPPORTED;
+  a.turning = a.R / (c.interleaved ? V : 2 * V);
+  a.units = a.turning + (copies ? (a.D - a.R) / V : 0);
+  a.lanes_log2 = 0;
+  while ((1 << a.lanes_log2) < a.units) ++a.lanes_log2;
+  a.tokens = std::max(1, kMaxAngles / a.R);  // a cosine and a sine a thread
+  const long long across = (a.T + a.tokens - 1) / a.tokens;
+  // Twice what the SMs hold, but an item a thread at least where the heads are split.
+  const long long want = 10ll * sm_count();
+  const int most = std::max(1, a.tokens * a.H * a.units / kThreads);
+  const int split = static_cast<int>(std::min<long long>(most, std::max(1ll, want / across)));
+  a.heads = (a.H + split - 1) / split;
+  const dim3 blocks(static_cast<unsigned>(across), (a.H + a.heads - 1) / a.heads);
   LaunchScope ls(kProfRotate, s);
   if (c.interleaved)
-    rotate_kernel<T, true><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a);
+    rotate_kernel<T, true><<<blocks, kThreads, 0, s>>>(a);
   else
-    rotate_kernel<T, false><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a);
+    rotate_kernel<T, false><<<blocks, kThreads, 0, s>>>(a);
   return check_launch();
 }
 
@@ -206,7 +249,7 @@ extern "C" int moe_rotate(const void* q, const void* k, const int32_t* pos, cons
   a.ok_ts = bytes(c.ok_token_stride, c.T), a.ok_hs = bytes(c.ok_head_stride, c.n_k_heads);
   a.T = c.T, a.Hq = c.n_q_heads, a.H = c.n_q_heads + c.n_k_heads, a.D = c.head_dim, a.R = c.rotary_dim;
   a.n_axes = c.n_axes, a.inverse = c.inverse;
-  a.copies = a.R < a.D && (q != out_q || (c.n_k_heads && k != out_k));
-  return c.dtype == MOE_DTYPE_F32 ? launch<float>(c, a, static_cast<cudaStream_t>(stream))
-                                  : launch<__nv_bfloat16>(c, a, static_cast<cudaStream_t>(stream));
+  const bool copies = q != out_q || (c.n_k_heads && k != out_k);  // dimensions past R
+  return c.dtype == MOE_DTYPE_F32 ? launch<float>(c, a, copies, static_cast<cudaStream_t>(stream))
+                                  : launch<__nv_bfloat16>(c, a, copies, static_cast<cudaStream_t>(stream));
 }
