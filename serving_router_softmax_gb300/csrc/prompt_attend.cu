@@ -35,8 +35,8 @@
 // and 9 issue a tile's products each (the tensor core takes a product as it begins
 // it, so one warp's waits and signals for both tiles, 1900 cycles a step, were not
 // hidden by the 2050 of its products; at D = 64 warps 10 and 11 issue those with V),
-// warp 12 finds the items and loads by TMA, warp 13 looks at values.  Every wait is
-// bounded.
+// warp 12 loads by TMA, warp 13 looks at values, warp 14 finds the items, a few ahead.
+// Every wait is bounded.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -59,6 +59,7 @@ constexpr int kPanel = kRows * 128;  // bytes of 64 dimensions of a tile
 constexpr float kSlack = 8.f;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kMaxSeqs = 2048;
+constexpr int kItems = 4;        // items found ahead
 
 struct PromptArgs {
   const int32_t* start;
@@ -84,9 +85,9 @@ struct Smem {
   alignas(1024) uint8_t kv[kStages][D / 64][kPanel];
   int blocks[kMaxSeqs];                               // of each sequence
   uint64_t full[kStages], empty[kStages], v_ok[kStages];
-  uint64_t q_full[2], q_empty[2], s_full[2], s_read[2], p_full[2], pv_done[2], o_full[2], o_empty[2], item_full[2], item_empty[2], drain;
-  Item item[2];
-  int first_bad[2][D], bad[2];
+  uint64_t q_full[2], q_empty[2], s_full[2], s_read[2], p_full[2], pv_done[2], o_full[2], o_empty[2], item_full[kItems], item_empty[kItems], drain;
+  Item item[kItems];
+  int first_bad[kItems][D], bad[kItems];
   int most;
   uint32_t tmem;
   int abort;
@@ -211,11 +212,11 @@ __device__ __forceinline__ void zero_times(uint32_t& acc, uint32_t x) {
   asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
 }
 
-// A role's place in the ring of two items.
+// A role's place in the ring of items.
 struct Turn {
   int i = 0;
-  __device__ __forceinline__ int slot() const { return i & 1; }
-  __device__ __forceinline__ uint32_t parity() const { return (i >> 1) & 1; }
+  __device__ __forceinline__ int slot() const { return i % kItems; }
+  __device__ __forceinline__ uint32_t parity() const { return (i / kItems) & 1; }
 };
 
 template <int D>
@@ -238,14 +239,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&sm.s_full[i], 1), tc::mbar_init(&sm.s_read[i], 4), tc::mbar_init(&sm.pv_done[i], 1);
       tc::mbar_init(&sm.p_full[i], 4);
       tc::mbar_init(&sm.o_full[i], 1), tc::mbar_init(&sm.o_empty[i], 4);
-      tc::mbar_init(&sm.item_full[i], 1), tc::mbar_init(&sm.item_empty[i], kApart ? 13 : 11);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      tc::mbar_init(&sm.item_full[i], 1), tc::mbar_init(&sm.item_empty[i], kApart ? 14 : 12);  // softmax, products, loads, values
       sm.bad[i] = 0;
     }
     tc::mbar_init(&sm.drain, kApart ? 4 : 2);
     sm.abort = sm.most = 0;
     tc::fence_mbar_init();
   }
-  for (int d = tid; d < 2 * D; d += kThreads) (&sm.first_bad[0][0])[d] = 0x7FFFFFFF;
+  for (int d = tid; d < kItems * D; d += kThreads) (&sm.first_bad[0][0])[d] = 0x7FFFFFFF;
   if (warp == 8) {
     tc::tmem_alloc(&sm.tmem, 512);
     tc::tmem_relinquish();
@@ -541,25 +544,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   } else if (warp == 12) {
-    // ---------------------------------------------------------- items and loads
-    Finder finder{a, sm.blocks, sm.most};
+    // ---------------------------------------------------------- loads
     int place = 0, q_used[2] = {0, 0};
-    for (int i = 0;; ++i) {
-      ok = tc::mbar_sleep<true>(&sm.item_empty[turn.slot()], turn.parity() ^ 1, gave_up, kWaitNs);
-      if (!ok) break;
-      const int slot = turn.slot();
-      const long long rank = static_cast<long long>(i) * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-      Item it = {};
-      if (out_of_order || !finder.find(rank, &it, lane)) it.n[0] = -1;
-      if (sm.bad[slot]) {
-        for (int d = lane; d < D; d += 32) sm.first_bad[slot][d] = 0x7FFFFFFF;
-        __syncwarp();
-        if (lane == 0) sm.bad[slot] = 0;
-      }
-      if (lane == 0) sm.item[slot] = it;
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sm.item_full[slot]);
-      ++turn.i;
+    while (true) {
+      const Item it = next_item();
       if (it.n[0] < 0) break;
       const int row = it.begin + it.first, n = max(it.n[0], it.n[1]);
       for (int x = 0; x < 2 * n && ok; ++x, ++place) {
@@ -588,6 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
+      item_done();
     }
     if (!ok) {
       // Copies in flight land in microseconds.
@@ -642,6 +631,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       place += 2 * n;
       item_done();
+    }
+    if (!ok && lane == 0) flag_error(a.dev_err, MOE_DEV_TIMEOUT);
+    __syncwarp();
+  } else if (warp == 14) {
+    // ---------------------------------------------------------- items
+    Finder finder{a, sm.blocks, sm.most};
+    for (long long i = 0;; ++i) {
+      ok = tc::mbar_sleep<true>(&sm.item_empty[turn.slot()], turn.parity() ^ 1, gave_up, kWaitNs);
+      if (!ok) break;
+      const int slot = turn.slot();
+      Item it = {};
+      if (out_of_order || !finder.find(i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x), &it, lane)) it.n[0] = -1;
+      if (sm.bad[slot]) {
+        for (int d = lane; d < D; d += 32) sm.first_bad[slot][d] = 0x7FFFFFFF;
+        __syncwarp();
+        if (lane == 0) sm.bad[slot] = 0;
+      }
+      if (lane == 0) sm.item[slot] = it;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.item_full[slot]);
+      ++turn.i;
+      if (it.n[0] < 0) break;
     }
     if (!ok && lane == 0) flag_error(a.dev_err, MOE_DEV_TIMEOUT);
     __syncwarp();
