@@ -83,7 +83,7 @@ struct Smem {
   static constexpr int kStages = D == 128 ? 4 : 8;
   alignas(1024) uint8_t q[2][D / 64][kPanel];
   alignas(1024) uint8_t kv[kStages][D / 64][kPanel];
-  int blocks[kMaxSeqs];                               // of each sequence
+  int blocks[kMaxSeqs], begin[kMaxSeqs], len[kMaxSeqs];  // of each sequence
   uint64_t full[kStages], empty[kStages], v_ok[kStages];
   uint64_t q_full[2], q_empty[2], s_full[2], s_read[2], p_full[2], pv_done[2], o_full[2], o_empty[2], item_full[kItems], item_empty[kItems], drain;
   Item item[kItems];
@@ -157,7 +157,7 @@ constexpr uint32_t kValuesAlongN = 1u << 16, kNegateA = 1u << 13;
 // Finds items by their rank: a warp's work.
 struct Finder {
   const PromptArgs& a;
-  const int* blocks;
+  const int *blocks, *begin, *len;
   int top;  // a level that no later rank lies above
 
   // F(b).
@@ -166,8 +166,8 @@ struct Finder {
     for (int s = lane; s < a.S; s += 32) v += max(0, blocks[s] - b);
     return __reduce_add_sync(0xFFFFFFFFu, v);
   }
-  __device__ __forceinline__ bool find(long long rank, Item* it, int lane) {
-    const long long r = rank / a.Hkv;
+  __device__ __forceinline__ bool find(int rank, Item* it, int lane) {
+    const int r = rank / a.Hkv;
     if (r >= at_or_above(0, lane)) return false;
     // The last level lo with F(lo) > r.
     int lo = 0, hi = top, above = 0;  // F(hi) <= r: 0, or counted
@@ -180,7 +180,7 @@ struct Finder {
     }
     if (hi == top) above = at_or_above(hi, lane);
     // The (r - F(lo + 1))-th sequence that has a block lo.
-    int skip = static_cast<int>(r) - above, seq = 0;
+    int skip = r - above, seq = 0;
     for (int s0 = 0; s0 < a.S; s0 += 32) {
       const int s = s0 + lane;
       const uint32_t has = __ballot_sync(0xFFFFFFFFu, s < a.S && blocks[s] > lo);
@@ -192,9 +192,9 @@ struct Finder {
       }
       skip -= n;
     }
-    it->begin = a.start[seq], it->len = a.start[seq + 1] - it->begin;
+    it->begin = begin[seq], it->len = len[seq];
     it->first = lo * 2 * a.tokens;
-    it->head = static_cast<int>(rank % a.Hkv);
+    it->head = rank - r * a.Hkv;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int from = it->first + t * a.tokens;  // a tile's last token sees itself
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool wrong = b < 0 || e > a.T || b > e;
     out_of_order |= wrong;
     const int n = wrong ? 0 : (e - b + per - 1) / per;
-    sm.blocks[s] = n;
+    sm.blocks[s] = n, sm.begin[s] = b, sm.len[s] = e - b;
     most = max(most, n);
   }
   tc::tc_fence_before();
@@ -636,13 +636,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 14) {
     // ---------------------------------------------------------- items
-    Finder finder{a, sm.blocks, sm.most};
-    for (long long i = 0;; ++i) {
+    Finder finder{a, sm.blocks, sm.begin, sm.len, sm.most};
+    for (int i = 0;; ++i) {  // (ranks stay below 2^27)
       ok = tc::mbar_sleep<true>(&sm.item_empty[turn.slot()], turn.parity() ^ 1, gave_up, kWaitNs);
       if (!ok) break;
       const int slot = turn.slot();
       Item it = {};
-      if (out_of_order || !finder.find(i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x), &it, lane)) it.n[0] = -1;
+      if (out_of_order || !finder.find(static_cast<int>(i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x)), &it, lane)) it.n[0] = -1;
       if (sm.bad[slot]) {
         for (int d = lane; d < D; d += 32) sm.first_bad[slot][d] = 0x7FFFFFFF;
         __syncwarp();
