@@ -648,3 +648,76 @@ def test_prompt_attend_many_items(mv, Hq, Hkv, D):
         o, l = mv.prompt_attend(q, k, v, st, dev_err=err)
         assert torch.equal(o, out) and torch.equal(l, lse)
     assert err.item() == 0
+
+
+def test_two_threads_at_once(mv):
+    """Calls of several host threads, each on its own stream, beside each other."""
+    import threading
+    prs = [Prompt(mv, 60 + i, lengths) for i, lengths in enumerate(([400, 3], [64, 64, 250], [1, 1, 900]))]
+    wants = [pr.run() for pr in prs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(pr, want):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(12):
+                    got = pr.run()
+                    s.synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                        bad.append("differs")
+        except Exception as e:  # noqa: BLE001
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(prs, wants)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+# ------------------------------------------------------------------ offsets past 32 bits
+def test_far_apart_rows(mv):
+    """Token strides that put rows billions of values apart."""
+    g = gen(71)
+    T, far = 4, (1 << 30) + 64
+    near = randn(g, T, 4, 64)
+    store = torch.empty(far * (T - 1) + 4 * 64, dtype=torch.bfloat16, device="cuda")
+    x = store.as_strided((T, 4, 64), (far, 64, 1))
+    x.copy_(near)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    rot = mv.Rotary.standard(64)
+    want = mv.rotate(rot, near[:, :2], near[:, 2:], pos)
+    got = mv.rotate(rot, x[:, :2], x[:, 2:], pos, out_q=x[:, :2], out_k=x[:, 2:])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    x.copy_(near)
+    st = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    want = mv.prompt_attend(near[:, :2], near[:, 2:3], near[:, 3:], st)
+    got = mv.prompt_attend(x[:, :2], x[:, 2:3], x[:, 3:], st)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_group_products_of_many_rows(mv):
+    """As many rows as are taken: outputs of more than 2^31 values."""
+    g = gen(72)
+    T, H, I, E = 1 << 22, 64, 576, 3
+    (wg, wd), layer = make_layer(mv, g, H, I, E, False)
+    x = randn(g, T, H)
+    ids = torch.randint(0, E, (T,), generator=g, device="cuda")
+    order = torch.argsort(ids, stable=True).to(torch.int32)
+    inv = torch.empty_like(order)
+    inv[order.long()] = torch.arange(T, dtype=torch.int32, device="cuda")
+    off = torch.cat([torch.zeros(1, dtype=torch.int64, device="cuda"), torch.bincount(ids, minlength=E).cumsum(0)]).to(torch.int32)
+    u = {"n_unique": torch.tensor([E], dtype=torch.int32, device="cuda"), "unique": torch.arange(E, dtype=torch.int32, device="cuda"),
+         "offsets": off, "perm_token": order, "inv": inv}
+    err = mv.new_dev_err()
+    h = mv.group_gate_up(x, layer, u, 1, dev_err=err)
+    y = mv.group_down(h, layer, u, torch.ones((T, 1), device="cuda"), dev_err=err)
+    assert err.item() == 0
+    pick = torch.cat([torch.arange(500), torch.arange(T // 2, T // 2 + 500), torch.arange(T - 500, T)]).cuda()
+    want, tol = gate_up_exact(x[pick], wg, ids[pick][:, None], torch.arange(len(pick), device="cuda"))
+    within(h[inv[pick].long()], want, tol)
+    want, tol = down_exact(h[inv[pick].long()], wd, ids[pick][:, None], torch.arange(len(pick), device="cuda"), torch.ones((len(pick), 1), device="cuda"))
+    within(y[pick], want, tol)
