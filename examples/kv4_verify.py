@@ -1,6 +1,7 @@
 """Speculative verify rounds with the attention half of the step on the 4-bit KV cache.
 
-One layer of a small model, several sequences.  Each round
+One layer of a small model, several sequences.  First the prompts: queries and keys are rotated by their positions, every
+prompt attends over itself, keys and values go to the cache.  Then each round
   1. selects draft nodes of every sequence's tree (the control path of the MoE verify step),
   2. writes the keys and values of the verify tokens (root and selected nodes) behind the context,
   3. attends: a token sees the context, its ancestors in the tree and itself,
@@ -85,17 +86,30 @@ def main(rounds: int = 40, context: int = 180, budget: int = 256, recent: int = 
     base = [context] * cfg.nseq
     seq = t(np.repeat(np.arange(cfg.nseq), base).astype(np.int32))
     slot = t(np.concatenate([np.arange(b) for b in base]).astype(np.int32))
-    kv = rows(len(seq))
-    mv.kv4_append(cache, kv[:, Hq:Hq + Hkv], kv[:, Hq + Hkv:], seq, slot, dev_err=err)
+    qkv = rows(len(seq))
+    rot = mv.Rotary.standard(D, device=dev)
+    q, k = mv.rotate(rot, qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], slot, dev_err=err)
+    v = qkv[:, Hq + Hkv:]
+    prompts, _ = mv.prompt_attend(q, k, v, t(np.concatenate([[0], np.cumsum(base)]).astype(np.int32)), scale=scale, dev_err=err)
+    mv.kv4_append(cache, k, v, seq, slot, dev_err=err)
+    x = torch.einsum("thd,jhd->htj", q[:context].float(), k[:context].float().repeat_interleave(Hq // Hkv, 1)) * scale
+    x = torch.softmax(x.masked_fill(~torch.ones((context, context), dtype=torch.bool, device=dev).tril(), float("-inf")), 2)
+    want = torch.einsum("htj,jhd->thd", x, v[:context].float().repeat_interleave(Hq // Hkv, 1))
+    prompt = float((prompts[:context].float() - want).norm() / want.norm())
     fresh = [n + 1 for n in gamma]
     q_start = np.concatenate([[0], np.cumsum(fresh)]).astype(np.int32)
     seq = t(np.repeat(np.arange(cfg.nseq), fresh).astype(np.int32))
     worst, evictions, committed = 0.0, 0, 0
+    place = [context] * cfg.nseq  # the next token's position (evicted slots do not take positions back)
     for step in range(rounds):
         plan(*tree)
         visible = tree_masks(ancestors, plan.selected, gamma)
         qkv = rows(int(q_start[-1]))
-        q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+        # A token's position: its depth in the tree behind the committed ones.
+        depth = ((visible[:, None] >> torch.arange(64, device=dev)) & 1).sum(1) - 1
+        pos = (t(np.repeat(place, fresh)) + depth).to(torch.int32)
+        q, k = mv.rotate(rot, qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], pos, dev_err=err)
+        v = qkv[:, Hq + Hkv:]
         base_d = t(np.asarray(base, np.int32))
         slot = t(np.concatenate([b + np.arange(n) for b, n in zip(base, fresh)]).astype(np.int32))
         mv.kv4_append(cache, k, v, seq, slot, dev_err=err)
@@ -122,14 +136,15 @@ def main(rounds: int = 40, context: int = 180, budget: int = 256, recent: int = 
             mass[s, :, base[s]:base[s] + len(at)] = new[:, at]
         mv.kv4_append(cache, k, v, seq, t(slots), dev_err=err)
         base = [b + n for b, n in zip(base, kept)]
+        place = [p + n for p, n in zip(place, kept)]
         if max(base) > budget:
             new_len, _, _ = mv.kv4_evict(cache, mass, t(np.asarray(base, np.int32)), budget - 2 * max(fresh), recent, dev_err=err)
             base = new_len.tolist()
             evictions += 1
     torch.cuda.synchronize()
     assert err.item() == 0, f"device error bits {err.item()}"
-    say(f"{rounds} rounds, {committed} tokens committed, {evictions} evictions, lengths {base}, attention within {worst:.1e} of fp32")
-    return {"worst": worst, "evictions": evictions, "committed": committed, "lengths": base, "mass": mass}
+    say(f"{rounds} rounds, {committed} tokens committed, {evictions} evictions, lengths {base}, attention within {worst:.1e} of fp32, the prompts' within {prompt:.1e}")
+    return {"prompt": prompt, "worst": worst, "evictions": evictions, "committed": committed, "lengths": base, "mass": mass}
 
 
 if __name__ == "__main__":
