@@ -90,7 +90,7 @@ struct Smem {
   int first_bad[kItems][D], bad[kItems];
   int most;
   uint32_t tmem;
-  int abort;
+  int abort, issuing;
 };
 template <int D>
 constexpr size_t kSmemBytes = sizeof(Smem<D>) + 1024;
@@ -212,6 +212,15 @@ __device__ __forceinline__ void zero_times(uint32_t& acc, uint32_t x) {
   asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
 }
 
+// A tile's products are issued as a block: taken from two warps one by one in turn, both tiles' blocks take twice as long, end
+// together, and the tiles' exponentials then run at the same time as well (418 instead of 354 us for 24 ragged prompts).
+// Only the order depends on it, so who waits too long goes ahead.
+__device__ __forceinline__ void issue_alone(int* issuing) {
+  for (int n = 0; n < (1 << 20) && atomicCAS(issuing, 0, 1); ++n) {
+  }
+}
+__device__ __forceinline__ void issue_done(int* issuing) { atomicExch(issuing, 0); }
+
 // A role's place in the ring of items.
 struct Turn {
   int i = 0;
@@ -245,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm.bad[i] = 0;
     }
     tc::mbar_init(&sm.drain, kApart ? 4 : 2);
-    sm.abort = sm.most = 0;
+    sm.abort = sm.most = sm.issuing = 0;
     tc::fence_mbar_init();
   }
   for (int d = tid; d < kItems * D; d += kThreads) (&sm.first_bad[0][0])[d] = 0x7FFFFFFF;
@@ -499,7 +508,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (more) {
             wait(&sm.s_read[t], steps_done);
             tc::tc_fence_after();
-            if (ok && tc::elect_one()) scores(sk, keys, j + 2 == steps);
+            if (ok && tc::elect_one()) {
+              issue_alone(&sm.issuing);
+              scores(sk, keys, j + 2 == steps);
+              issue_done(&sm.issuing);
+            }
             __syncwarp();
           } else if (other && ok && lane == 0) {
             tc::mbar_arrive(&sm.empty[sk]);
@@ -512,11 +525,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait(&sm.p_full[t], steps_done);
             tc::tc_fence_after();
             if (ok && tc::elect_one()) {
+              issue_alone(&sm.issuing);
               values(sv, more ? kRows / 16 : (seen - j * kRows + 15) / 16, j);
               if (kApart) tc::mma_commit(&sm.pv_done[t]);
               if (!kApart && more) scores(sk, keys, j + 2 == steps);
               if (!more) tc::mma_commit(&sm.o_full[t]);
               tc::mma_commit(&sm.empty[sv]);
+              issue_done(&sm.issuing);
             }
             __syncwarp();
             if (!kApart && !more && other && ok && lane == 0) tc::mbar_arrive(&sm.empty[sk]);
