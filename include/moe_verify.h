@@ -851,7 +851,8 @@ int moe_group_gate_up(const void* x, int32_t T, int32_t k, const moe_layer_weigh
  *               are summed in slot order in fp32 and rounded once.
  * Needs moe_group_down_workspace() bytes (0: bad arguments), 256-byte aligned.
  * With n_unique outside its range (MOE_DEV_CAPACITY) or 0, y is zeros; a term whose inv is out
- * of range (MOE_DEV_BAD_ID) is left out.  Other limits and errors as above. */
+ * of range (MOE_DEV_BAD_ID) is left out.  Other limits and errors as above; the
+ * outputs of tokens routed to a group that is left out are not valid. */
 size_t moe_group_down_workspace(const moe_layer_weights* lw, int32_t T, int32_t k);
 int moe_group_down(const void* h, int32_t T, int32_t k, const moe_layer_weights* lw, const int32_t* n_unique,
                    const int32_t* unique, const int32_t* offsets, const int32_t* inv, const float* w, void* y,

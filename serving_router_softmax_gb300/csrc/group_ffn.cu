@@ -32,6 +32,10 @@
 // Roles of a CTA: warp 0 loads weights, warp 1 owns TMEM and (in the pair's first
 // CTA) issues the products, warps 2-5 take the sums out, the warps from 6 on load
 // rows.  Every wait is bounded.
+//
+// 8192 tokens of 8 of 128 experts, 4096 x 1536: gate/up 1.01 ms, 1630 TFLOP/s (tensor
+// pipe 76% busy); down 0.54 ms, 1520, and 0.09 for the sum.  300 tokens: gate/up
+// 0.47 ms, the weights' bytes at 6.9 TB/s.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -404,7 +408,12 @@ __global__ void __launch_bounds__(kThreads<kGateUp>, 1)
   if (warp == 1) tc::tmem_dealloc_pair(tmem, 512);
 }
 
-// y_t = sum_j w_tj o[inv_tj] in slot order, eight values a thread.
+// y_t = sum_j w_tj o[inv_tj] in slot order in fp32, eight values a thread.
+//
+// The products o lie between the two kernels in bf16: a rounding of 2^-8 at most of
+// each term, as the result's own is of the sum (2.3e-3 of the norm in all, 1.7e-3 with
+// that one alone).  Bound by their bytes: 91 us for 65,536 rows of 4096, 6.6 TB/s,
+// beside 0.54 ms of the product; fp32 would double them, and what the product writes.
 __global__ void __launch_bounds__(256) group_sum_kernel(const uint16_t* __restrict__ o, const int32_t* __restrict__ inv,
                                                         const float* __restrict__ w, const int32_t* __restrict__ n_unique,
                                                         uint16_t* __restrict__ y, int T, int k, int H, int cap, int32_t* dev_err) {

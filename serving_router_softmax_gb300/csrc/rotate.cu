@@ -238,6 +238,13 @@ extern "C" int moe_rotate(const void* q, const void* k, const int32_t* pos, cons
   if (rows & 15 || (reinterpret_cast<uintptr_t>(pos) | reinterpret_cast<uintptr_t>(axis) | reinterpret_cast<uintptr_t>(dev_err)) & 3 ||
       reinterpret_cast<uintptr_t>(turns) & 7)
     return MOE_ERR_ARG;
+  // In place: row on row.
+  auto astray = [&](const void* in, const void* out, long long it, long long ot, int H, long long ih, long long oh) {
+    return in == out && ((c.T > 1 && it != ot) || (H > 1 && ih != oh));
+  };
+  if (astray(q, out_q, c.q_token_stride, c.oq_token_stride, c.n_q_heads, c.q_head_stride, c.oq_head_stride) ||
+      (c.n_k_heads && astray(k, out_k, c.k_token_stride, c.ok_token_stride, c.n_k_heads, c.k_head_stride, c.ok_head_stride)))
+    return MOE_ERR_ARG;
   RotateArgs a = {};
   a.q = static_cast<const uint8_t*>(q), a.k = static_cast<const uint8_t*>(k);
   a.oq = static_cast<uint8_t*>(out_q), a.ok = static_cast<uint8_t*>(out_k);

@@ -8,7 +8,6 @@ structs of a shape are kept.
 from __future__ import annotations
 
 import ctypes as C
-from fractions import Fraction
 from typing import Dict, Optional, Sequence, Tuple
 
 import torch
@@ -18,7 +17,14 @@ from .api import ExpertLayer, MoEError, _check
 from .kv4 import _DTYPES, _arg, _current_device, _err, _raw_stream
 
 # 2 pi to 60 digits.
-_TURN = Fraction(6283185307179586476925286766559005768394338798750211641949889, 10 ** 60)
+_TURN, _TURN_UNIT = 6283185307179586476925286766559005768394338798750211641949889, 10 ** 60
+
+
+def _part_of_turn(f: float) -> int:
+    """f / (2 pi), times 2^64, to the nearest whole number, mod 2^64, as a signed 64-bit number (f is taken as it is)."""
+    a, b = f.as_integer_ratio()
+    d = b * _TURN
+    return ((((a << 65) * _TURN_UNIT + d) // (2 * d) + (1 << 63)) & ((1 << 64) - 1)) - (1 << 63)
 
 
 # Argument structs of calls of one shape (pointers are not part of them).
@@ -82,10 +88,11 @@ class Rotary:
             raise MoEError("axes: expected 0 to 3")
         if not all(abs(f) < float("inf") for f in freqs):
             raise MoEError("freqs: expected finite numbers")
-        turns = [round(Fraction(f) / _TURN * 2 ** 64) % 2 ** 64 for f in freqs]
         self.head_dim, self.rotary_dim, self.n_axes, self.interleaved = head_dim, 2 * len(freqs), max(axes) + 1, bool(interleaved)
-        self._turns = torch.tensor([t - 2 ** 64 if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
-        self._axis = torch.tensor(axes, dtype=torch.int32, device=device)
+        # (One copy: the turns, and behind them the axes, two to a word.)
+        n = len(freqs)
+        words = torch.tensor([_part_of_turn(f) for f in freqs] + [a | b << 32 for a, b in zip(axes[::2], axes[1::2])], dtype=torch.int64).to(device)
+        self._turns, self._axis = words[:n], words[n:].view(torch.int32)
         self.device = self._turns.device
 
     @classmethod

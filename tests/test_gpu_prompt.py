@@ -45,9 +45,9 @@ def rotate_exact(x, pos, freqs, axes, interleaved, inverse):
     y = x.double().clone()
     mag = y.abs()
     from fractions import Fraction
-    from serving_router_softmax_gb300.prompt import _TURN
+    whole = Fraction(6283185307179586476925286766559005768394338798750211641949889, 10 ** 60)  # 2 pi
     for i, (f, ax) in enumerate(zip(freqs, axes)):
-        turn = Fraction(float(f)) / _TURN
+        turn = Fraction(float(f)) / whole
         part = [float((turn * int(p)) % 1) for p in pos[ax].tolist()]
         ang = 2 * math.pi * torch.tensor(part, dtype=torch.float64, device=x.device)[:, None] * (-1 if inverse else 1)
         a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + n)
@@ -721,3 +721,37 @@ def test_group_products_of_many_rows(mv):
     within(h[inv[pick].long()], want, tol)
     want, tol = down_exact(h[inv[pick].long()], wd, ids[pick][:, None], torch.arange(len(pick), device="cuda"), torch.ones((len(pick), 1), device="cuda"))
     within(y[pick], want, tol)
+
+
+def test_the_first_calls_of_a_process_are_captured(mv):
+    """Nothing is looked up or raised by a first call that a capture does not allow."""
+    import subprocess
+    import sys
+    code = """
+import torch, serving_router_softmax_gb300 as mv
+g = torch.Generator(device="cuda").manual_seed(1)
+r = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)
+q, k, x = r(300, 8, 128), r(300, 2, 128), r(300, 128)
+layer = mv.ExpertLayer(r(4, 256, 128), r(4, 128, 128), "bf16")
+rot, pos = mv.Rotary.standard(128), torch.arange(300, dtype=torch.int32, device="cuda")
+st = torch.tensor([0, 100, 300], dtype=torch.int32, device="cuda")
+ids = torch.randint(0, 4, (300, 1), generator=g, device="cuda").to(torch.int32)
+w = torch.ones((300, 1), device="cuda")
+def run():
+    a, b = mv.rotate(rot, q, k, pos)
+    o, z = mv.prompt_attend(a, b, k, st)
+    u = mv.union_permute(ids, 4)
+    return o, z, mv.group_down(mv.group_gate_up(x, layer, u, 1), layer, u, w)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = run()
+graph.replay()
+want = run()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+"""
+    import os
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-2000:]

@@ -50,6 +50,9 @@ def test_rotate_pointers(lib):
         assert rotate(lib, rot(), **{name: FAKE + 2}) == L.MOE_ERR_ARG, name
     assert rotate(lib, rot(), err=FAKE + 1) == L.MOE_ERR_ARG
     assert rotate(lib, rot(T=0), q=None, k=None, pos=None) == L.MOE_OK
+    # in place with other strides than the input's
+    assert rotate(lib, rot(oq_token_stride=512), oq=FAKE) == L.MOE_ERR_ARG
+    assert rotate(lib, rot(k_head_stride=128, k_token_stride=256), ok=FAKE) == L.MOE_ERR_ARG
 
 
 # ------------------------------------------------------------------ moe_prompt_attend
