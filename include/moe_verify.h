@@ -803,7 +803,7 @@ int moe_rotate(const void* q, const void* k, const int32_t* pos, const uint64_t*
  *               (none is fine).  Rows before start[0] and from start[n_seq] on
  *               are not read, and their outputs are left as they are.
  *   out         [T, n_q_heads, D] bf16 out.
- *   lse         [T, n_q_heads] fp32 out or NULL.
+ *   lse         [T, n_q_heads] fp32 out or NULL; both apart from the inputs.
  * Scores, maxima, sums and outputs are accumulated in fp32; the probabilities
  * enter the second product as bf16 (relative to a reference within 2^8 of the
  * row's largest), the output is rounded once.
@@ -819,7 +819,7 @@ int moe_rotate(const void* q, const void* k, const int32_t* pos, const uint64_t*
  * nothing is written), MOE_DEV_TIMEOUT. */
 typedef struct {
   int32_t T, n_seq, n_q_heads, n_kv_heads, head_dim;
-  float scale;          /* finite */
+  float scale;          /* |scale| log2(e) finite */
   int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride;
 } moe_prompt_cfg;
 int moe_prompt_attend(const void* q, const void* k, const void* v, const int32_t* start,
@@ -831,8 +831,8 @@ int moe_prompt_attend(const void* q, const void* k, const void* v, const int32_t
  *   x           [T, H] bf16.
  *   lw          a bf16 layer, either layout, with or without a pool.
  *   n_unique .. perm_token   as written by moe_union_permute.
- *   h           [T * k, I] bf16 out, rows in the groups' order; rows that no
- *               group holds are left as they are.
+ *   h           [T * k, I] bf16 out, rows in the groups' order, apart from x; rows that
+ *               no group holds are left as they are.
  * fp32 accumulation on the tensor cores, one rounding per output.
  * Limits: 0 <= T, T * k <= 2^22, 1 <= k <= 16, H and I multiples of 64, E <= 1024.
  * Device errors: MOE_DEV_CAPACITY (n_unique outside [0, min(E, T*k)]: nothing is
@@ -847,7 +847,7 @@ int moe_group_gate_up(const void* x, int32_t T, int32_t k, const moe_layer_weigh
  * whose group holds that row: the second half.
  *   h           [T * k, I] bf16 in the groups' order (moe_group_gate_up's).
  *   inv, w      [T, k] int32 and fp32 as moe_union_permute and moe_route write them.
- *   y           [T, H] bf16 out.  The products, rounded to bf16 in the workspace,
+ *   y           [T, H] bf16 out, apart from h.  The products, rounded to bf16 in the workspace,
  *               are summed in slot order in fp32 and rounded once.
  * Needs moe_group_down_workspace() bytes (0: bad arguments), 256-byte aligned.
  * With n_unique outside its range (MOE_DEV_CAPACITY) or 0, y is zeros; a term whose inv is out

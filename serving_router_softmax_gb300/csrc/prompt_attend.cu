@@ -718,7 +718,7 @@ extern "C" int moe_prompt_attend(const void* q, const void* k, const void* v, co
   using namespace moe;
   if (!cfg) return MOE_ERR_ARG;
   const moe_prompt_cfg& c = *cfg;
-  if (c.T < 0 || c.n_seq < 0 || c.n_q_heads < 1 || c.n_kv_heads < 1 || !std::isfinite(c.scale)) return MOE_ERR_ARG;
+  if (c.T < 0 || c.n_seq < 0 || c.n_q_heads < 1 || c.n_kv_heads < 1 || !std::isfinite(c.scale * kv4::kLog2e)) return MOE_ERR_ARG;
   if (c.n_q_heads % c.n_kv_heads) return MOE_ERR_ARG;
   if (c.head_dim != 64 && c.head_dim != 128) return MOE_ERR_UNSUPPORTED;
   if (c.T > (1 << 24) || c.n_seq > kMaxSeqs || c.n_q_heads > 1024 || c.n_q_heads / c.n_kv_heads > 128) return MOE_ERR_UNSUPPORTED;

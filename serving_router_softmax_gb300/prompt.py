@@ -2,8 +2,8 @@
 
 Thin like ``api``: argument checks and pointer marshalling.  Tensors are on one CUDA device, whichever is current; calls
 enqueue on that device's current stream (or ``stream``) and raise ``MoEError`` on a non-OK host status.  Device-side error
-bits land in ``dev_err`` where one is given.  A small call's host time is of the order of its device time, so the argument
-structs of a shape are kept.
+bits land in ``dev_err`` where one is given.  A small call's host time is of the order of its device time, so what follows
+from the shapes of a call alone is kept.
 """
 from __future__ import annotations
 
@@ -13,7 +13,7 @@ from typing import Dict, Optional, Sequence, Tuple
 import torch
 
 from . import _lib as L
-from .api import ExpertLayer, MoEError, _check
+from .api import LAYOUTS, ExpertLayer, MoEError, _check
 from .kv4 import _DTYPES, _arg, _current_device, _err, _raw_stream
 
 # 2 pi to 60 digits.
@@ -27,7 +27,7 @@ def _part_of_turn(f: float) -> int:
     return ((((a << 65) * _TURN_UNIT + d) // (2 * d) + (1 << 63)) & ((1 << 64) - 1)) - (1 << 63)
 
 
-# Argument structs of calls of one shape (pointers are not part of them).
+# What is worked out from shapes, strides and types alone (no pointers).
 _plans: Dict[tuple, tuple] = {}
 
 
@@ -185,25 +185,35 @@ def prompt_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, start: torc
 
 
 def _group_plan(rows: int, k: int, layer: ExpertLayer) -> tuple:
-    """(layer struct, shapes of x, h, y, w, and of the union's n_unique, unique, offsets and lists) of a call."""
+    """What a layer's struct begins with; shapes of x, h, y, w, and of the union's n_unique, unique, offsets and lists."""
+    gu, dn, pool = layer.gate_up, layer.down, layer.pool
+
     def make():
         if layer.dtype != "bf16":
             raise MoEError(f"layer: expected bf16 weights, got {layer.dtype}")
         if k < 1 or rows % k:
             raise MoEError(f"expected k >= 1 rows of each token, got {rows} for k = {k}")
-        T, cap = rows // k, min(layer.E, rows)
-        return (C.byref(layer.struct()), (T, layer.H), (rows, layer.I), (T, layer.H), (T, k), (1,), (max(cap, 1),), (cap + 1,),
-                (max(rows, 1),))
+        H, I, E = layer.H, layer.I, layer.E
+        # Bytes of an expert's matrices (tiled: the rows of gate, of up and of down, each rounded up to 128).
+        up = 128 if layer.layout == "tiled" else 1
+        slots = E if pool is None else pool.n_slots
+        for t, name, n in ((gu, "gate_up", 4 * (-(-I // up) * up) * H), (dn, "down", 2 * (-(-H // up) * up) * I)):
+            if t.numel() * t.dtype.itemsize < slots * n:
+                raise MoEError(f"layer: {name} holds {t.numel() * t.dtype.itemsize} bytes of {slots * n}")
+        T, cap = rows // k, min(E, rows)
+        head = (H, I, E, L.DTYPE_BF16, LAYOUTS[layer.layout])
+        return head, (T, H), (rows, I), (T, H), (T, k), (1,), (max(cap, 1),), (cap + 1,), (max(rows, 1),)
 
-    if layer.pool is not None:
-        return make()
+    return _plan(("group", rows, k, gu.shape, gu.dtype, dn.shape, dn.dtype, layer.dims, layer.dtype, layer.layout,
+                  None if pool is None else pool.n_slots), make)
+
+
+def _layer_on(dev: int, layer: ExpertLayer, head: tuple):
+    """The layer's struct (without a pool in 2 us instead of 5)."""
     gu, dn = layer.gate_up, layer.down
-    return _plan(("group", rows, k, gu.data_ptr(), dn.data_ptr(), gu.shape, dn.shape, layer.dims, layer.dtype, layer.layout), make)
-
-
-def _layer_on(dev: int, layer: ExpertLayer) -> None:
-    if layer.gate_up.get_device() != dev or layer.down.get_device() != dev:
-        raise MoEError(f"layer: expected one on cuda:{dev}")
+    if gu.get_device() != dev or dn.get_device() != dev or not gu.is_contiguous() or not dn.is_contiguous():
+        raise MoEError(f"layer: expected contiguous weights on cuda:{dev}")
+    return C.byref(L.LayerWeights(*head, gu.data_ptr(), dn.data_ptr()) if layer.pool is None else layer.struct())
 
 
 def group_gate_up(x: torch.Tensor, layer: ExpertLayer, union: Dict[str, torch.Tensor], k: int, out: Optional[torch.Tensor] = None,
@@ -214,8 +224,8 @@ def group_gate_up(x: torch.Tensor, layer: ExpertLayer, union: Dict[str, torch.Te
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(dev, stream, lambda: group_gate_up(x, layer, union, k, out, dev_err))
     T = x.shape[0]
-    ref, sx, sh, _, _, s1, su, so, sp = _group_plan(T * k, k, layer)
-    _layer_on(dev, layer)
+    head, sx, sh, _, _, s1, su, so, sp = _group_plan(T * k, k, layer)
+    ref = _layer_on(dev, layer, head)
     h = torch.empty(sh, dtype=torch.bfloat16, device=x.device) if out is None else out
     i32 = torch.int32
     _check(L.load().moe_group_gate_up(_arg(dev, x, torch.bfloat16, sx, "x"), T, k, ref, _arg(dev, union["n_unique"], i32, s1, "n_unique"),
@@ -242,8 +252,8 @@ def group_down(h: torch.Tensor, layer: ExpertLayer, union: Dict[str, torch.Tenso
     if w.dim() != 2:
         raise MoEError("w: expected [T, k]")
     T, k = w.shape
-    ref, _, sh, sy, sw, s1, su, so, sp = _group_plan(T * k, k, layer)
-    _layer_on(dev, layer)
+    head, _, sh, sy, sw, s1, su, so, sp = _group_plan(T * k, k, layer)
+    ref = _layer_on(dev, layer, head)
     o = torch.empty(sy, dtype=torch.bfloat16, device=h.device) if y is None else y
     lib, i32 = L.load(), torch.int32
     if workspace is None:

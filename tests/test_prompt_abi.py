@@ -70,6 +70,7 @@ def attend(lib, cfg, q=FAKE, k=FAKE, v=FAKE, start=FAKE, out=FAKE, lse=FAKE, err
 @pytest.mark.parametrize("kw,want", [
     (dict(T=-1), L.MOE_ERR_ARG), (dict(n_seq=-1), L.MOE_ERR_ARG), (dict(n_kv_heads=0), L.MOE_ERR_ARG), (dict(n_q_heads=0), L.MOE_ERR_ARG),
     (dict(n_q_heads=7), L.MOE_ERR_ARG), (dict(scale=float("nan")), L.MOE_ERR_ARG), (dict(scale=float("inf")), L.MOE_ERR_ARG),
+    (dict(scale=3e38), L.MOE_ERR_ARG), (dict(scale=-3e38), L.MOE_ERR_ARG),
     (dict(head_dim=96), L.MOE_ERR_UNSUPPORTED), (dict(head_dim=256), L.MOE_ERR_UNSUPPORTED), (dict(T=(1 << 24) + 1), L.MOE_ERR_UNSUPPORTED),
     (dict(n_seq=2049), L.MOE_ERR_UNSUPPORTED), (dict(n_q_heads=258), L.MOE_ERR_UNSUPPORTED), (dict(n_q_heads=1026), L.MOE_ERR_UNSUPPORTED),
     (dict(q_token_stride=508), L.MOE_ERR_UNSUPPORTED), (dict(k_head_stride=-64), L.MOE_ERR_UNSUPPORTED), (dict(v_token_stride=1), L.MOE_ERR_UNSUPPORTED), (dict(k_head_stride=0), L.MOE_ERR_UNSUPPORTED)])

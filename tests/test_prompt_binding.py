@@ -134,3 +134,31 @@ def test_shapes_and_types_are_checked_once_known_too(machine):
             raise AssertionError(i)
     assert len(machine.lib.calls) == n
 
+
+def test_layers_smaller_than_they_say_are_refused(machine):
+    u = {"n_unique": i32(1, 0), "unique": i32(4, 0), "offsets": i32(5, 0), "perm_token": i32(6, 0), "inv": i32(6, 0)}
+    x, h, w = bf((3, 64), 0), bf((6, 128), 0), f32((3, 2), 0)
+    both = [lambda lay: prompt.group_gate_up(x, lay, u, 2), lambda lay: prompt.group_down(h, lay, u, w)]
+    # H 64, I 128, 4 experts: 4 x 256 x 64 and 4 x 64 x 128 values; tiled, 64 rows of down are 128.
+    good = [ExpertLayer(bf((4, 256, 64), 0), bf((4, 64, 128), 0), "bf16"),
+            ExpertLayer(bf((4 * 256 * 64,), 0), bf((4 * 128 * 128,), 0), "bf16", layout="tiled", dims=(64, 128, 4))]
+    for _ in range(2):
+        for lay in good:
+            for call in both:
+                call(lay)
+                at = machine.lib.calls[-1][2][3]._obj
+                assert (at.w_gate_up, at.w_down) == (lay.gate_up.at, lay.down.at)  # this layer's, not one's of its shape
+        good.append(ExpertLayer(bf((4, 256, 64), 0), bf((4, 64, 128), 0), "bf16"))
+    n = len(machine.lib.calls)
+    bad = [ExpertLayer(bf((4, 256, 64), 0), bf((3, 64, 128), 0), "bf16"), ExpertLayer(bf((4, 256, 64), 0), bf((4, 64, 127), 0), "bf16"),
+           ExpertLayer(bf((4 * 256 * 64 - 1,), 0), bf((4 * 128 * 128,), 0), "bf16", layout="tiled", dims=(64, 128, 4)),
+           ExpertLayer(bf((4 * 256 * 64,), 0), bf((4 * 64 * 128,), 0), "bf16", layout="tiled", dims=(64, 128, 4)),
+           ExpertLayer(bf((4 * 256 * 64,), 0), bf((4 * 128 * 128,), 0), "bf16", layout="tiled", dims=(64, 128, 5)),
+           ExpertLayer(bf((4 * 256 * 64,), 0), bf((4 * 128 * 128,), 0), "bf16", layout="tiled", dims=(64, 192, 4))]
+    apart = ExpertLayer(bf((4, 256, 64), 0), bf((4, 64, 128), 0), "bf16")
+    apart.down.is_contiguous = lambda: False
+    for lay in [*bad, apart]:
+        for call in both:
+            with pytest.raises(MoEError):
+                call(lay)
+    assert len(machine.lib.calls) == n
