@@ -194,6 +194,9 @@ def kv4_read(cache: Kv4Cache, seq: torch.Tensor, slot: torch.Tensor, dtype: torc
 
 def _attn_plan(cache: Kv4Cache, q: torch.Tensor, max_q: int, scale: Optional[float]):
     """(struct, workspace bytes, shapes of out, lse, q_start, base, visible) of a call with these queries."""
+    if scale is not None:
+        scale = float(scale)  # (a tensor would be looked up by its identity, whatever it holds)
+
     def make():
         if q.dim() != 3:
             raise MoEError("q: expected [T, n_q_heads, head_dim]")

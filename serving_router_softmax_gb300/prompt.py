@@ -118,6 +118,7 @@ def rotate(rot: Rotary, q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.T
     if rot.device.index != dev:
         raise MoEError(f"q: expected a tensor on {rot.device}")
     qs, ks = q.shape, None if k is None else k.shape
+    inverse = bool(inverse)  # (a tensor would be looked up by its identity, whatever it holds)
 
     def make():
         if q.dim() != 3 or (k is not None and k.dim() != 3):
@@ -159,6 +160,8 @@ def prompt_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, start: torc
     dev = q.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(dev, stream, lambda: prompt_attend(q, k, v, start, scale, out, lse, dev_err))
+    if scale is not None:
+        scale = float(scale)  # (as inverse, above)
 
     def make():
         if q.dim() != 3 or k.dim() != 3:
