@@ -16,15 +16,9 @@
 // for 65,536 rows of 4096 x 1536 matrices; four warps: 1.31; rows copied side by side
 // first: 0.1 ms for that alone.)
 //
-// Two pairs in a cluster take neighbouring row tiles of one chunk: each of the four
-// CTAs loads a quarter of the rows and sends it to the other pair too.  What bounds
-// full tiles is loading (52 bytes a clock and SM, of 64 that products without a pause
-// would take); this takes 23 of 29 KB a stage from L2: 1.10 -> 1.01 ms for those
-// 65,536 rows, though clusters of four find room on 144 of the 152 SMs only.  Where
-// the row tiles are odd in number, and few, the last one's neighbour would cost more
-// (it goes through the same tile and stores nothing): pairs stay alone.
+// What bounds full tiles is loading: 32 KB a stage and CTA, from L2.
 //
-// Persistent: cluster i takes tiles i, i + clusters, ..., in an order that has a
+// Persistent: pair i takes tiles i, i + pairs, ..., in an order that has a
 // matrix's rows go over all of their group's chunks before the next rows come,
 // and an expert's before the next expert's: what runs at the same time shares
 // weights and rows in L2.
@@ -91,7 +85,6 @@ __device__ __forceinline__ int chunk_rows(int n) {
 }
 
 struct Tile {
-  bool real;
   int u, slot, m, p, n, N;  // expert's place in the union, its weights, row tile, first row of the chunk, its rows, padded
 };
 
@@ -104,15 +97,14 @@ __device__ __forceinline__ void group_of(const GroupArgs& a, int u, int* slot, i
   *n = *slot >= 0 ? q - b : -1;
 }
 
-// Walks the tiles of one pair: `step` row tiles are a cluster's, `who` of them this pair's.
+// Walks the tiles of one pair.
 struct Walk {
   const GroupArgs& a;
   const int* cum;
-  int U, MT, step, who, u = 0, first = -1, slot, p0, n, rows, nc;
-  __device__ __forceinline__ Walk(const GroupArgs& args, const int* c, int us, int mt, int pairs, int w)
-      : a(args), cum(c), U(us), MT(mt), step(pairs), who(w) {}
+  int U, u = 0, first = -1, slot, p0, n, rows, nc;
+  __device__ __forceinline__ Walk(const GroupArgs& args, const int* c, int us) : a(args), cum(c), U(us) {}
   __device__ __forceinline__ bool at(long long t, Tile* x) {
-    while (u < U && static_cast<long long>(cum[u + 1]) * MT <= t) ++u;
+    while (u < U && static_cast<long long>(cum[u + 1]) * a.MT <= t) ++u;
     if (u >= U) return false;
     if (first != u) {
       group_of(a, u, &slot, &p0, &n);
@@ -120,10 +112,8 @@ struct Walk {
       nc = cum[u + 1] - cum[u];
       rows = chunk_rows(n);
     }
-    const int r = static_cast<int>(t - static_cast<long long>(cum[u]) * MT), c = r % nc;
-    x->u = u, x->slot = slot, x->m = r / nc * step + who;
-    x->real = x->m < a.MT;  // (an odd row tile's neighbour goes through the last one again, and stores nothing)
-    x->m = min(x->m, a.MT - 1);
+    const int r = static_cast<int>(t - static_cast<long long>(cum[u]) * a.MT), c = r % nc;
+    x->u = u, x->slot = slot, x->m = r / nc;
     x->p = p0 + c * rows;
     x->n = min(rows, n - c * rows);
     x->N = (x->n + 31) & ~31;
@@ -142,20 +132,17 @@ __device__ __noinline__ void give_up_loading(Smem& sm, const GroupArgs& a, int l
   __syncwarp();
 }
 
-template <bool kGateUp, int kPairs>
+template <bool kGateUp>
 __global__ void __launch_bounds__(kThreads<kGateUp>, 1)
     group_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ RowMaps xmap, const GroupArgs a) {
   extern __shared__ uint8_t raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // Rank in the pair, the pair's place in the cluster and its first CTA; clusters.
-  const uint32_t crank = tc::cluster_rank(), rank = crank & 1, lead = crank & ~1u, who = crank >> 1;
-  const int pair = blockIdx.x / (2 * kPairs), pairs = gridDim.x / (2 * kPairs);
-  constexpr uint32_t kAll = kPairs == 2 ? 15 : 3;
-  const int MT = kPairs == 2 ? (a.MT + 1) / 2 : a.MT;
+  const uint32_t rank = tc::cluster_rank();  // in the pair
+  const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
 
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) tc::mbar_init(&sm.full[i], 1), tc::mbar_init(&sm.empty[i], kPairs);
+    for (int i = 0; i < kStages; ++i) tc::mbar_init(&sm.full[i], 1), tc::mbar_init(&sm.empty[i], 1);
     for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.acc_full[i], 1), tc::mbar_init(&sm.acc_empty[i], 8);
     tc::mbar_init(&sm.drain, 1);
     sm.abort = 0;
@@ -197,10 +184,10 @@ __global__ void __launch_bounds__(kThreads<kGateUp>, 1)
   tc::cluster_sync();
   tc::tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  const long long total = static_cast<long long>(before) * MT;
+  const long long total = static_cast<long long>(before) * a.MT;
   const int KB = a.K / 64;
   volatile int* gave_up = &sm.abort;
-  Walk walk(a, sm.cum, U, MT, kPairs, static_cast<int>(who));
+  Walk walk(a, sm.cum, U);
   Tile x;
 
   if (warp == 0) {
@@ -227,7 +214,7 @@ __global__ void __launch_bounds__(kThreads<kGateUp>, 1)
         if (!ok) break;
         if (tc::elect_one()) {
           if (rank == 0) tc::mbar_arrive_expect_tx(&sm.full[s], bytes);
-          const uint32_t bar = tc::smem_of(&sm.full[s], lead);
+          const uint32_t bar = tc::smem_of(&sm.full[s], 0);
           if (!a.stall) {
             if (kGateUp)
               tc::tma_load_3d_pair(sm.a[s], &wmap, wx, wy, wz, bar);
@@ -268,13 +255,13 @@ __global__ void __launch_bounds__(kThreads<kGateUp>, 1)
             tc::mma_bf16_pair(d, ad + 2, bd + 2, idesc, 1);
             tc::mma_bf16_pair(d, ad + 4, bd + 4, idesc, 1);
             tc::mma_bf16_pair(d, ad + 6, bd + 6, idesc, 1);
-            tc::mma_commit_pair(done, kAll);
+            tc::mma_commit_pair(done);
           }
           __syncwarp();
           // The look at the next stage's barrier (100 cycles) runs beside the products.
           there = __all_sync(0xFFFFFFFFu, tc::mbar_test(&sm.full[s], ph));
         }
-        if (ok && tc::elect_one()) tc::mma_commit_pair(&sm.acc_full[acc], 3u << lead);
+        if (ok && tc::elect_one()) tc::mma_commit_pair(&sm.acc_full[acc]);
         __syncwarp();
         if (++acc == 2) acc = 0, aph ^= 1;
       }
@@ -293,11 +280,9 @@ __global__ void __launch_bounds__(kThreads<kGateUp>, 1)
     bool ok = true;
     for (long long t = pair; t < total && ok; t += pairs) {
       walk.at(t, &x);
-      // This CTA's part: its half of the rows, or (two pairs on the same rows) its share of that half, for itself and the
-      // other pair's CTA of the same rank.
-      const int half = x.N / 2, part = half / kPairs, off = static_cast<int>(who) * part, first = static_cast<int>(rank) * half + off;
-      const int four = (warp - 6) * (4 / kPairs) + lane;  // gate/up: rows 4 four .. 4 four + 3, by the first lanes
-      const bool mine = kGateUp ? lane < 4 / kPairs && 4 * four < part : lane == 0;
+      const int half = x.N / 2, first = static_cast<int>(rank) * half;  // this CTA's rows
+      const int four = (warp - 6) * 4 + lane;  // gate/up: rows 4 four .. 4 four + 3, by the first lanes
+      const bool mine = kGateUp ? lane < 4 && 4 * four < half : lane == 0;
       int row[4] = {x.p + first, 0, 0, 0};
       if (kGateUp && mine) {
 #pragma unroll
@@ -307,23 +292,15 @@ __global__ void __launch_bounds__(kThreads<kGateUp>, 1)
         }
       }
       const CUtensorMap* map = &xmap.m[kGateUp ? 0 : half / 16 - 1];
-      const uint32_t ctas = 5u << rank;
       for (int kb = 0; kb < KB; ++kb) {
         ok = tc::mbar_sleep<true>(&sm.empty[s], ph ^ 1, gave_up, kWaitNs);
         if (!ok) break;
         if (mine && !a.stall) {
-          const uint32_t bar = tc::smem_of(&sm.full[s], lead);
-          uint8_t* dst = sm.b[s] + off * 128 + (kGateUp ? four * 512 : 0);
-          if (kPairs == 2) {
-            if (kGateUp)
-              tc::tma_gather4_pairs(dst, map, kb * 64, row, bar, ctas);
-            else
-              tc::tma_load_2d_pairs(dst, map, kb * 64, row[0], bar, ctas);
-          } else if (kGateUp) {
-            tc::tma_gather4_pair(dst, map, kb * 64, row, bar);
-          } else {
-            tc::tma_load_2d_pair(dst, map, kb * 64, row[0], bar);
-          }
+          const uint32_t bar = tc::smem_of(&sm.full[s], 0);
+          if (kGateUp)
+            tc::tma_gather4_pair(sm.b[s] + four * 512, map, kb * 64, row, bar);
+          else
+            tc::tma_load_2d_pair(sm.b[s], map, kb * 64, row[0], bar);
         }
         __syncwarp();
         if (++s == kStages) s = 0, ph ^= 1;
@@ -382,7 +359,7 @@ __global__ void __launch_bounds__(kThreads<kGateUp>, 1)
         }
         __syncwarp();
         const int c0 = c + (kGateUp && q >= 2 ? 16 : 0), part = (lane & 3) * 8;
-        if (x.real && i0 + part < a.N) {
+        if (i0 + part < a.N) {
 #pragma unroll
           for (int j = 0; j < (kGateUp ? 16 : 32); j += 8) {
             const int r = j + (lane >> 2);
@@ -393,7 +370,7 @@ __global__ void __launch_bounds__(kThreads<kGateUp>, 1)
       }
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive_at(tc::smem_of(&sm.acc_empty[acc], lead));
+      if (lane == 0) tc::mbar_arrive_at(tc::smem_of(&sm.acc_empty[acc], 0));
       if (++acc == 2) acc = 0, aph ^= 1;
     }
     if (!ok && lane == 0) {
@@ -476,8 +453,9 @@ int group_validate(const moe_layer_weights& lw, int T, int k, const void* w) {
 }
 
 // The maps of the weights and of the rows they multiply, and the launch.
-template <bool kGateUp, int kPairs>
+template <bool kGateUp>
 int group_launch(const moe_layer_weights& lw, const void* rows, int n_rows, const void* w, GroupArgs a, cudaStream_t s) {
+  a.MT = kGateUp ? (a.N + 127) / 128 : (a.N + 255) / 256;
   a.tiled = lw.layout == MOE_LAYOUT_TILED;
   a.stall = (test_stall_mask() & MOE_TEST_STALL_GROUP) != 0;
   CUtensorMap wmap;
@@ -491,39 +469,32 @@ int group_launch(const moe_layer_weights& lw, const void* rows, int n_rows, cons
   const uint32_t wb[3] = {64, kGateUp ? 64u : 128u, 2};
   if (!tc::make_bf16_map(&wmap, w, kGateUp ? 3 : 2, wd, ws, wb)) return MOE_ERR_CUDA;
   for (uint32_t i = 0; i < (kGateUp ? 1 : 8); ++i) {
-    const uint32_t xb[2] = {64, kGateUp ? 1 : 16 / kPairs * (i + 1)};
+    const uint32_t xb[2] = {64, kGateUp ? 1 : 16 * (i + 1)};
     if (!tc::make_bf16_map(&xmap.m[i], rows, 2, xd, xs, xb)) return MOE_ERR_CUDA;
   }
-  const int e = allow_smem<group_kernel<kGateUp, kPairs>>(kSmemBytes);
+  const int e = allow_smem<group_kernel<kGateUp>>(kSmemBytes);
   if (e != MOE_OK) return e;
   // At most this many tiles (a chunk a full 256 rows, and one more for each expert).
-  const long long most = (a.rows / 256 + static_cast<long long>(a.cap)) * ((a.MT + kPairs - 1) / kPairs);
+  const long long most = (a.rows / 256 + static_cast<long long>(a.cap)) * a.MT;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2 * kPairs;
+  attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr, cfg.numAttrs = 1, cfg.stream = s;
   cfg.blockDim = dim3(kThreads<kGateUp>), cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.gridDim = dim3(2 * kPairs);
-  static std::atomic<int> found[64];  // clusters that a device holds at once
+  cfg.gridDim = dim3(2);
+  static std::atomic<int> found[64];  // pairs that a device holds at once
   int dev = 0, fits = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
   if (dev >= 0 && dev < 64) fits = found[dev].load(std::memory_order_relaxed);
   if (!fits) {
-    if (cudaOccupancyMaxActiveClusters(&fits, group_kernel<kGateUp, kPairs>, &cfg) != cudaSuccess || fits < 1) return MOE_ERR_CUDA;
+    if (cudaOccupancyMaxActiveClusters(&fits, group_kernel<kGateUp>, &cfg) != cudaSuccess || fits < 1) return MOE_ERR_CUDA;
     if (dev >= 0 && dev < 64) found[dev].store(fits, std::memory_order_relaxed);
   }
-  cfg.gridDim = dim3(2 * kPairs * static_cast<unsigned>(std::min<long long>(fits, most)));
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<long long>(fits, most)));
   LaunchScope ls(kGateUp ? kProfGroupGateUp : kProfGroupDown, s);
-  return cudaLaunchKernelEx(&cfg, group_kernel<kGateUp, kPairs>, wmap, xmap, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
-}
-
-template <bool kGateUp>
-int group_run(const moe_layer_weights& lw, const void* rows, int n_rows, const void* w, GroupArgs a, cudaStream_t s) {
-  a.MT = kGateUp ? (a.N + 127) / 128 : (a.N + 255) / 256;
-  // Two pairs on a chunk, unless an odd number of row tiles makes more than a twelfth of them idle.
-  return a.MT % 2 == 0 || a.MT > 11 ? group_launch<kGateUp, 2>(lw, rows, n_rows, w, a, s) : group_launch<kGateUp, 1>(lw, rows, n_rows, w, a, s);
+  return cudaLaunchKernelEx(&cfg, group_kernel<kGateUp>, wmap, xmap, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 bool misaligned(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) & (n - 1); }
@@ -548,7 +519,7 @@ extern "C" int moe_group_gate_up(const void* x, int32_t T, int32_t k, const moe_
   a.n_unique = n_unique, a.unique = unique, a.offsets = offsets, a.perm = perm_token, a.slot_of = slot_table(*lw);
   a.out = static_cast<uint16_t*>(h), a.dev_err = dev_err;
   a.T = T, a.rows = rows, a.E = lw->E, a.cap = cap, a.n_slots = weight_slots(*lw), a.N = lw->I, a.K = lw->H;
-  return group_run<true>(*lw, x, T, lw->w_gate_up, a, static_cast<cudaStream_t>(stream));
+  return group_launch<true>(*lw, x, T, lw->w_gate_up, a, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t moe_group_down_workspace(const moe_layer_weights* lw, int32_t T, int32_t k) {
@@ -577,7 +548,7 @@ extern "C" int moe_group_down(const void* h, int32_t T, int32_t k, const moe_lay
   a.n_unique = n_unique, a.unique = unique, a.offsets = offsets, a.slot_of = slot_table(*lw), a.out = o, a.dev_err = dev_err;
   a.T = T, a.rows = rows, a.E = lw->E, a.cap = cap, a.n_slots = weight_slots(*lw), a.N = lw->H, a.K = lw->I;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int e = group_run<false>(*lw, h, rows, lw->w_down, a, s);
+  const int e = group_launch<false>(*lw, h, rows, lw->w_down, a, s);
   if (e != MOE_OK) return e;
   LaunchScope ls(kProfGroupDown, s);
   const long long n = static_cast<long long>(T) * (lw->H / 8);

@@ -92,11 +92,11 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Arrives on the copies of `bar` of the cluster's CTAs in `ctas` once this thread's products so far have completed.
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint32_t ctas) {
+// Arrives on both CTAs' copies of `bar` once this thread's products so far have completed.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
-      "h"(static_cast<uint16_t>(ctas))
+      "h"(static_cast<uint16_t>(3))
       : "memory");
 }
 
@@ -107,7 +107,8 @@ __device__ __forceinline__ void tma_load(void* dst, const void* tmap, int x, int
       : "memory");
 }
 
-// Loads that report to a barrier of either CTA of the pair (`bar`: smem_of's).
+// Loads that report to a barrier of either CTA of the pair (`bar`: smem_of's).  Each CTA copies for itself: a copy that is sent to
+// several CTAs must not read another GPU's memory, which a caller's pointers may be, so there is none here.
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* tmap, int x, int y, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(
@@ -128,22 +129,6 @@ __device__ __forceinline__ void tma_gather4_pair(void* dst, const void* tmap, in
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4, %5, "
       "%6}], [%7];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(bar)
-      : "memory");
-}
-
-// The same copies to the same place in several CTAs of the cluster, reporting to each one's pair.
-__device__ __forceinline__ void tma_load_2d_pairs(void* dst, const void* tmap, int x, int y, uint32_t bar, uint32_t ctas) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2 [%0], [%1, {%2, %3}], "
-      "[%4], %5;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar), "h"(static_cast<uint16_t>(ctas))
-      : "memory");
-}
-__device__ __forceinline__ void tma_gather4_pairs(void* dst, const void* tmap, int x, const int (&row)[4], uint32_t bar, uint32_t ctas) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2 [%0], [%1, {%2, "
-      "%3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(bar), "h"(static_cast<uint16_t>(ctas))
       : "memory");
 }
 
