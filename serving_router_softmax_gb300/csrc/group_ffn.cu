@@ -227,6 +227,11 @@ __global__ void __launch_bounds__(kThreads<kGateUp>, 1)
         if (++s == kStages) s = 0, ph ^= 1;
       }
     }
+    // The last products' arrivals, which come from the pair's first CTA, are seen before this CTA may leave.
+    for (int i = 0; i < kStages && ok; ++i) {
+      ok = tc::mbar_sleep<true>(&sm.empty[s], ph ^ 1, gave_up, kWaitNs);
+      if (++s == kStages) s = 0, ph ^= 1;
+    }
     if (!ok) give_up_loading(sm, a, lane);
   } else if (warp == 1) {
     // ---------------------------------------------------------- products

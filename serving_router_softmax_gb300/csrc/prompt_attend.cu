@@ -399,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) tc::mbar_arrive(&sm.p_full[t]);
       }
       if (ok) ok = tc::mbar_sleep<true>(&sm.o_full[t], items & 1, gave_up, kWaitNs);
+      if (kApart && ok) ok = tc::mbar_sleep<true>(&sm.pv_done[t], (step - 1) & 1, gave_up, kWaitNs);  // (its phases are all seen)
       if (!ok) break;
       ++items;
       tc::tc_fence_after();
@@ -598,6 +599,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       item_done();
     }
+    // The last products' arrivals are seen before the CTA may leave.
+    for (int i = 0; i < NS && ok; ++i, ++place) ok = tc::mbar_sleep<true>(&sm.empty[place % NS], (place / NS + 1) & 1, gave_up, kWaitNs);
+    for (int t = 0; t < 2 && ok; ++t) ok = tc::mbar_sleep<true>(&sm.q_empty[t], (q_used[t] + 1) & 1, gave_up, kWaitNs);
     if (!ok) {
       // Copies in flight land in microseconds.
       if (lane == 0) {
