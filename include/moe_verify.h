@@ -811,6 +811,8 @@ int moe_rotate(const void* q, const void* k, const int32_t* pos, const uint64_t*
  * NaN, out and lse (a key whose score is -inf counts as not seen; a row without
  * any gives zeros and -inf).  In a value it makes that dimension of out NaN or infinite for the
  * rows that see it.  What a row does not see has no effect on it.
+ * A row whose largest score times log2(e) is 2^31 or more away from 0 is NaN, out
+ * and lse.  (From 2^24 on an fp32 score no longer tells powers of e apart.)
  * Results do not depend on timing.
  * Limits: D = 64 or 128; 0 <= T <= 2^24, n_seq <= 2048; n_q_heads a multiple of
  * n_kv_heads, at most 128 times as many, n_q_heads <= 1024; strides positive multiples

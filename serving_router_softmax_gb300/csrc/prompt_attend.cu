@@ -15,7 +15,8 @@
 // the same quotient O / l.  It moves (and O and l are scaled to it) only when a
 // score passes it by more than 8, so that powers stay below 2^8 and O is
 // rewritten in a few steps of a row instead of all; bf16 and fp32 are as good
-// anywhere in that range.
+// anywhere in that range.  r is a product rounded to fp32, the exponents c S - r are
+// not: past 2^31 the rounding alone takes P out of fp32's range, and such a row is NaN.
 //
 // Persistent, one CTA an SM: an item (such a block of a sequence and kv head)
 // begins while the one before it ends, since a block's own beginning and end
@@ -62,6 +63,7 @@ constexpr int kThreads = 512;
 constexpr int kRows = 128;       // query rows of a tile, keys of a step
 constexpr int kPanel = kRows * 128;  // bytes of 64 dimensions of a tile
 constexpr float kSlack = 8.f;
+constexpr float kFar = 2147483648.f;  // references from here on, either way: half a last place is 128 powers of two
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kMaxSeqs = 2048;
 constexpr int kItems = 4;        // items found ahead
@@ -376,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const float neg = ref == -INFINITY ? 0.f : -ref;
+        const float neg = ref <= -kFar ? 0.f : -ref;  // (P is then 0)
         const float2 r2 = make_float2(neg, neg);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -403,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       ++items;
       tc::tc_fence_after();
-      const float l = (l2.x + l2.y) + (k2.x + k2.y);
+      const float l = fabsf(ref) >= kFar && ref != -INFINITY ? NAN : (l2.x + l2.y) + (k2.x + k2.y);
       const float inv = l == 0.f ? 0.f : kv4::rcp(l);
       const bool some_bad = sm.bad[turn.slot()] != 0;
       const int* bad = sm.first_bad[turn.slot()];

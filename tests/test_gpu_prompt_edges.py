@@ -1,7 +1,9 @@
 """A prompt's calls at their edges, against plain implementations in 64 bits (tolerances as in test_gpu_prompt)."""
+import numpy as np
 import pytest
 
-from test_gpu_prompt import down_exact, gate_up_exact, gen, make_ids, make_layer, mv, randn, within  # noqa: F401  (mv: fixture)
+from test_gpu_prompt import (BF, F32, Prompt, attend_check, attend_exact, down_exact, gate_up_exact, gen, make_ids, make_layer,  # noqa: F401
+                             mv, randn, within)  # (mv: fixture)
 
 torch = pytest.importorskip("torch")
 
@@ -47,3 +49,51 @@ def test_prompt_attend_ends_with_nothing_in_flight(mv, D, lengths):  # noqa: F81
     again = [mv.prompt_attend(q, k, v, start, dev_err=err) for _ in range(30)]
     assert all(torch.equal(a, b) for got in again for a, b in zip(got, want))
     assert err.item() == 0
+
+
+# ------------------------------------------------------------------ scores far from zero
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_attend_scores_far_above_zero(mv, D):  # noqa: F811
+    """A row with a score past 2^31 (times log2 e) is NaN, up to the scores that fp32 does not hold; the rows before it are as
+    without it, and a score short of it is as good as any."""
+    g = gen(81 + D)
+    T = 300
+    q, k, v = torch.zeros((T, 2, D), device="cuda"), torch.zeros((T, 1, D), device="cuda"), randn(g, T, 1, D)
+    q[..., 0] = 1.0
+    k[:100, 0, 0] = torch.randn(100, generator=g, device="cuda")
+    st = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    want, z, ot, lt = attend_exact(q[:100].bfloat16(), k[:100].bfloat16(), v[:100], [0, 100], 1.0)
+    for low, high in ((31, 40), (60, 90), (127, 128)):
+        # powers of two between, with all the digits that bf16 has: products with the scale are rounded up and down
+        k[100:, 0, 0] = torch.exp2(torch.linspace(low, high - 0.01, T - 100, device="cuda"))
+        out, lse = mv.prompt_attend(q.bfloat16(), k.bfloat16(), v, st, scale=1.0)
+        assert out[100:].isnan().all() and lse[100:].isnan().all(), (low, high)
+        within(out[:100], want, ot)
+        within(lse[:100], z, lt)
+    # one key that all the rows behind it are sure of
+    k[100:, 0, 0] = torch.randn(T - 100, generator=g, device="cuda")
+    for far in (2.0 ** 20, 255 * 2.0 ** 20, 185 * 2.0 ** 22, 2.0 ** 30):
+        k[120, 0, 0] = far
+        out, lse = mv.prompt_attend(q.bfloat16(), k.bfloat16(), v, st, scale=1.0)
+        # its probability is 2^r for the r that the reference was rounded by: rounded to bf16, not to 1, and the result once more
+        alone = v[120:121].double().expand(T - 120, 2, D)
+        within(out[120:], alone, alone.abs() * (2 * BF + BF * BF + 2.0 ** -18), far)
+        assert ((lse[120:].double() - far).abs() <= far * 4 * F32).all(), far
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_attend_scores_far_below_zero(mv, D):  # noqa: F811
+    """Keys with scores past -2^31 (times log2 e) have no part in a row that sees others; a row with no other is NaN."""
+    g = gen(82 + D)
+    T, far = 420, 200
+    q, k, v = torch.zeros((T, 2, D), device="cuda"), torch.zeros((T, 1, D), device="cuda"), randn(g, T, 1, D)
+    q[..., 0] = 1.0
+    k[far:, 0, 0] = torch.randn(T - far, generator=g, device="cuda")
+    st = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    want, z, ot, lt = attend_exact(q[far:].bfloat16(), k[far:].bfloat16(), v[far:], [0, T - far], 1.0)
+    for low, high in ((31, 40), (60, 90), (127, 128)):
+        k[:far, 0, 0] = -torch.exp2(torch.linspace(low, high - 0.01, far, device="cuda"))
+        out, lse = mv.prompt_attend(q.bfloat16(), k.bfloat16(), v, st, scale=1.0)
+        assert out[:far].isnan().all() and lse[:far].isnan().all(), (low, high)
+        within(out[far:], want, ot, (low, high))
+        within(lse[far:], z, lt, (low, high))
