@@ -778,7 +778,10 @@ int kv4_evict(const kv4_cache* cache, const float* mass, const int32_t* lens, co
  *               the position is.
  *   axis        [rotary_dim / 2] int32, each in [0, n_axes).
  *   out_q, out_k  rows as q and k, with their own strides; either the input
- *               itself (same pointer and strides) or memory apart from it.
+ *               itself (same pointer and strides) or memory apart from both inputs,
+ *               and apart from each other: MOE_ERR_ARG otherwise.  Where the ranges
+ *               of addresses of two of them overlap (slices of one buffer), their
+ *               token strides must be the same.
  * Arithmetic in fp32; cosine and sine within 2^-22, each output rounded once.
  * Limits: 0 <= T <= 2^24; head_dim a multiple of 8 up to 512; rotary_dim a
  * multiple of 16, 16 <= rotary_dim <= head_dim; 1 <= n_axes <= 4; 1 <= n_q_heads,
@@ -803,7 +806,8 @@ int moe_rotate(const void* q, const void* k, const int32_t* pos, const uint64_t*
  *               (none is fine).  Rows before start[0] and from start[n_seq] on
  *               are not read, and their outputs are left as they are.
  *   out         [T, n_q_heads, D] bf16 out.
- *   lse         [T, n_q_heads] fp32 out or NULL; both apart from the inputs.
+ *   lse         [T, n_q_heads] fp32 out or NULL; both apart from the inputs and
+ *               from each other (MOE_ERR_ARG).
  * Scores, maxima, sums and outputs are accumulated in fp32; the probabilities
  * enter the second product as bf16 (relative to a reference within 2^8 of the
  * row's largest), the output is rounded once.
@@ -833,8 +837,8 @@ int moe_prompt_attend(const void* q, const void* k, const void* v, const int32_t
  *   x           [T, H] bf16.
  *   lw          a bf16 layer, either layout, with or without a pool.
  *   n_unique .. perm_token   as written by moe_union_permute.
- *   h           [T * k, I] bf16 out, rows in the groups' order, apart from x; rows that
- *               no group holds are left as they are.
+ *   h           [T * k, I] bf16 out, rows in the groups' order, apart from x
+ *               (MOE_ERR_ARG); rows that no group holds are left as they are.
  * fp32 accumulation on the tensor cores, one rounding per output.
  * Limits: 0 <= T, T * k <= 2^22, 1 <= k <= 16, H and I multiples of 64, E <= 1024.
  * Device errors: MOE_DEV_CAPACITY (n_unique outside [0, min(E, T*k)]: nothing is
@@ -849,7 +853,7 @@ int moe_group_gate_up(const void* x, int32_t T, int32_t k, const moe_layer_weigh
  * whose group holds that row: the second half.
  *   h           [T * k, I] bf16 in the groups' order (moe_group_gate_up's).
  *   inv, w      [T, k] int32 and fp32 as moe_union_permute and moe_route write them.
- *   y           [T, H] bf16 out, apart from h.  The products, rounded to bf16 in the workspace,
+ *   y           [T, H] bf16 out; h, y and the workspace apart from each other (MOE_ERR_ARG).  The products, rounded to bf16 in the workspace,
  *               are summed in slot order in fp32 and rounded once.
  * Needs moe_group_down_workspace() bytes (0: bad arguments), 256-byte aligned.
  * With n_unique outside its range (MOE_DEV_CAPACITY) or 0, y is zeros; a term whose inv is out

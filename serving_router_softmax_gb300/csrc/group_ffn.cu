@@ -35,6 +35,7 @@
 #include <algorithm>
 #include <atomic>
 
+#include "apart.cuh"
 #include "common.cuh"
 #include "smem_limit.cuh"
 #include "tc_pair.cuh"
@@ -520,6 +521,7 @@ extern "C" int moe_group_gate_up(const void* x, int32_t T, int32_t k, const moe_
       misaligned(perm_token, 4) || misaligned(dev_err, 4))
     return MOE_ERR_ARG;
   const int rows = T * k, cap = lw->E < rows ? lw->E : rows;
+  if (!rows_apart(whole(x, 2ll * T * lw->H), whole(h, 2ll * rows * lw->I))) return MOE_ERR_ARG;
   GroupArgs a = {};
   a.n_unique = n_unique, a.unique = unique, a.offsets = offsets, a.perm = perm_token, a.slot_of = slot_table(*lw);
   a.out = static_cast<uint16_t*>(h), a.dev_err = dev_err;
@@ -548,6 +550,9 @@ extern "C" int moe_group_down(const void* h, int32_t T, int32_t k, const moe_lay
   if (!workspace || ws_bytes < moe_group_down_workspace(lw, T, k)) return MOE_ERR_WORKSPACE;
   if (misaligned(workspace, 256)) return MOE_ERR_ARG;
   const int rows = T * k, cap = lw->E < rows ? lw->E : rows;
+  const Rows rh = whole(h, 2ll * rows * lw->I), ry = whole(y, 2ll * T * lw->H);
+  const Rows rws = whole(workspace, static_cast<long long>(moe_group_down_workspace(lw, T, k)));
+  if (!rows_apart(rh, ry) || !rows_apart(rh, rws) || !rows_apart(ry, rws)) return MOE_ERR_ARG;
   uint16_t* o = static_cast<uint16_t*>(workspace);
   GroupArgs a = {};
   a.n_unique = n_unique, a.unique = unique, a.offsets = offsets, a.slot_of = slot_table(*lw), a.out = o, a.dev_err = dev_err;

@@ -48,6 +48,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "apart.cuh"
 #include "kv4.cuh"
 #include "tc_f16.cuh"
 #include "tc_pair.cuh"
@@ -737,6 +738,15 @@ extern "C" int moe_prompt_attend(const void* q, const void* k, const void* v, co
        reinterpret_cast<uintptr_t>(out)) & 15 ||
       (reinterpret_cast<uintptr_t>(start) | reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(dev_err)) & 3)
     return MOE_ERR_ARG;
+  auto rows = [&](const void* p, int H, long long ts, long long hs) {
+    return Rows{reinterpret_cast<uintptr_t>(p), c.T, 2 * ts, H, 2 * hs, 2ll * c.head_dim};
+  };
+  const long long n_rows = static_cast<long long>(c.T) * c.n_q_heads;
+  const Rows o = whole(out, n_rows * 2 * c.head_dim), z = whole(lse, lse ? n_rows * 4 : 0);
+  for (const Rows& r : {rows(q, c.n_q_heads, c.q_token_stride, c.q_head_stride), rows(k, c.n_kv_heads, c.k_token_stride, c.k_head_stride),
+                        rows(v, c.n_kv_heads, c.v_token_stride, c.v_head_stride)})
+    if (!rows_apart(r, o) || !rows_apart(r, z)) return MOE_ERR_ARG;
+  if (!rows_apart(o, z)) return MOE_ERR_ARG;
   PromptArgs a = {};
   a.start = start, a.out = static_cast<uint16_t*>(out), a.lse = lse, a.dev_err = dev_err;
   a.T = c.T, a.S = c.n_seq, a.Hq = c.n_q_heads, a.Hkv = c.n_kv_heads, a.G = c.n_q_heads / c.n_kv_heads;

@@ -20,6 +20,7 @@
 
 #include <algorithm>
 
+#include "apart.cuh"
 #include "common.cuh"
 
 namespace moe {
@@ -233,9 +234,9 @@ extern "C" int moe_rotate(const void* q, const void* k, const int32_t* pos, cons
     return MOE_ERR_UNSUPPORTED;
   if (c.T == 0) return MOE_OK;
   if (!q || !out_q || !pos || !turns || !axis || (c.n_k_heads && (!k || !out_k))) return MOE_ERR_ARG;
-  const uintptr_t rows = reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out_q) |
+  const uintptr_t at = reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out_q) |
                          (c.n_k_heads ? reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(out_k) : 0);
-  if (rows & 15 || (reinterpret_cast<uintptr_t>(pos) | reinterpret_cast<uintptr_t>(axis) | reinterpret_cast<uintptr_t>(dev_err)) & 3 ||
+  if (at & 15 || (reinterpret_cast<uintptr_t>(pos) | reinterpret_cast<uintptr_t>(axis) | reinterpret_cast<uintptr_t>(dev_err)) & 3 ||
       reinterpret_cast<uintptr_t>(turns) & 7)
     return MOE_ERR_ARG;
   // In place: row on row.
@@ -244,6 +245,14 @@ extern "C" int moe_rotate(const void* q, const void* k, const int32_t* pos, cons
   };
   if (astray(q, out_q, c.q_token_stride, c.oq_token_stride, c.n_q_heads, c.q_head_stride, c.oq_head_stride) ||
       (c.n_k_heads && astray(k, out_k, c.k_token_stride, c.ok_token_stride, c.n_k_heads, c.k_head_stride, c.ok_head_stride)))
+    return MOE_ERR_ARG;
+  auto rows = [&](const void* p, int H, long long ts, long long hs) {
+    return Rows{reinterpret_cast<uintptr_t>(p), c.T, ts * size, H, hs * size, D * size};
+  };
+  const Rows rq = rows(q, c.n_q_heads, c.q_token_stride, c.q_head_stride), rk = rows(k, c.n_k_heads, c.k_token_stride, c.k_head_stride);
+  const Rows roq = rows(out_q, c.n_q_heads, c.oq_token_stride, c.oq_head_stride), rok = rows(out_k, c.n_k_heads, c.ok_token_stride, c.ok_head_stride);
+  if ((q != out_q && !rows_apart(rq, roq)) || (k != out_k && !rows_apart(rk, rok)) || !rows_apart(rq, rok) || !rows_apart(rk, roq) ||
+      !rows_apart(roq, rok))
     return MOE_ERR_ARG;
   RotateArgs a = {};
   a.q = static_cast<const uint8_t*>(q), a.k = static_cast<const uint8_t*>(k);

@@ -97,3 +97,40 @@ def test_prompt_attend_scores_far_below_zero(mv, D):  # noqa: F811
         assert out[:far].isnan().all() and lse[:far].isnan().all(), (low, high)
         within(out[far:], want, ot, (low, high))
         within(lse[far:], z, lt, (low, high))
+
+
+# ------------------------------------------------------------------ outputs and inputs in one memory
+def test_outputs_on_inputs_are_refused(mv):  # noqa: F811
+    g = gen(91)
+    T = 40
+    rot, pos, st = mv.Rotary.standard(64), torch.arange(T, dtype=torch.int32, device="cuda"), torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    q, k = randn(g, T, 4, 64), randn(g, T, 4, 64)
+    _, layer = make_layer(mv, g, 128, 128, 2, False)
+    x, u = randn(g, T, 128), mv.union_permute(make_ids(g, T, 2, 1, 0.0), 2)
+    w, more = torch.ones((T, 1), device="cuda"), torch.empty(T * 4 * 64 * 2 + T * 4 * 4, dtype=torch.uint8, device="cuda")
+    both = more[:T * 4 * 64 * 2].view(torch.bfloat16).view(T, 4, 64)
+    before = [t.clone() for t in (q, k, x)]
+    for call in (lambda: mv.rotate(rot, q, k, pos, out_q=k, out_k=q), lambda: mv.rotate(rot, q, k, pos, out_q=both, out_k=both),
+                 lambda: mv.rotate(rot, q, q, pos, out_q=q), lambda: mv.rotate(rot, q[1:], None, pos[1:], out_q=q[:-1]),
+                 lambda: mv.prompt_attend(q, k, k, st, out=q), lambda: mv.prompt_attend(q, k, k, st, out=k),
+                 lambda: mv.prompt_attend(q, k, k, st, out=both, lse=more[:T * 16].view(torch.float32).view(T, 4)),
+                 lambda: mv.group_gate_up(x, layer, u, 1, out=x), lambda: mv.group_down(x, layer, u, w, y=x),
+                 lambda: mv.group_down(x, layer, u, w, workspace=x.view(torch.uint8).view(-1).repeat(4), y=x)):
+        with pytest.raises(mv.MoEError):
+            call()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((q, k, x), before))
+
+
+def test_rotate_in_place_in_one_buffer(mv):  # noqa: F811
+    """Queries, keys and values as slices of one buffer, tokens or heads outermost, parts behind one another or head by head."""
+    g = gen(92)
+    T, H, D = 33, 6, 64
+    rot, pos = mv.Rotary.standard(D), torch.arange(T, dtype=torch.int32, device="cuda")
+    for shape, order in (((T, 3, H, D), (0, 2, 1, 3)), ((T, H, 3, D), (0, 1, 2, 3)), ((3, H, T, D), (2, 1, 0, 3)), ((H, 3, T, D), (2, 0, 1, 3))):
+        x = randn(g, *shape)
+        parts = x.permute(*order)  # [T, H, 3, D]
+        q, k, v = (parts[:, :, i] for i in range(3))
+        want, held = mv.rotate(rot, q, k, pos), v.clone()
+        got = mv.rotate(rot, q, k, pos, out_q=q, out_k=k)
+        assert got[0].data_ptr() == q.data_ptr() and torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(v, held)
