@@ -853,8 +853,11 @@ int moe_group_gate_up(const void* x, int32_t T, int32_t k, const moe_layer_weigh
  * whose group holds that row: the second half.
  *   h           [T * k, I] bf16 in the groups' order (moe_group_gate_up's).
  *   inv, w      [T, k] int32 and fp32 as moe_union_permute and moe_route write them.
- *   y           [T, H] bf16 out; h, y and the workspace apart from each other (MOE_ERR_ARG).  The products, rounded to bf16 in the workspace,
- *               are summed in slot order in fp32 and rounded once.
+ *   y           [T, H] bf16 out; h, y and the workspace apart from each other (MOE_ERR_ARG).
+ * The products o_j, summed in fp32 and rounded to bf16 in the workspace, are summed in slot
+ * order in fp32 and rounded once: y is off by up to 2^-8 of sum_j |w[t, j] o_j| and 2^-8 of
+ * itself.  Where a token's terms cancel, that is more of y than of moe_verify_ffn's, which
+ * keeps them in fp32.
  * Needs moe_group_down_workspace() bytes (0: bad arguments), 256-byte aligned.
  * With n_unique outside its range (MOE_DEV_CAPACITY) or 0, y is zeros; a term whose inv is out
  * of range (MOE_DEV_BAD_ID) is left out.  Other limits and errors as above; the

@@ -393,10 +393,12 @@ __global__ void __launch_bounds__(kThreads<kGateUp>, 1)
 
 // y_t = sum_j w_tj o[inv_tj] in slot order in fp32, eight values a thread.
 //
-// The products o lie between the two kernels in bf16: a rounding of 2^-8 at most of
-// each term, as the result's own is of the sum (2.3e-3 of the norm in all, 1.7e-3 with
-// that one alone).  Bound by their bytes: 91 us for 65,536 rows of 4096, 6.6 TB/s,
-// beside 0.54 ms of the product; fp32 would double them, and what the product writes.
+// The products o lie between the two kernels in bf16: off by 2^-8 of each term at most,
+// so y by 2^-8 sum_j |w_tj o_j| and 2^-8 |y_t| of its own rounding.  Where terms cancel
+// that is more than 2^-8 of y, by any factor; with weights that are all positive it is
+// 2.3e-3 of y's norm in all, 1.7e-3 with the result's rounding alone.  (moe_verify_ffn
+// keeps its terms in fp32.)  Bound by their bytes: 91 us for 65,536 rows of 4096, 6.6
+// TB/s, behind the product; fp32 would double them, and what the product writes.
 __global__ void __launch_bounds__(256) group_sum_kernel(const uint16_t* __restrict__ o, const int32_t* __restrict__ inv,
                                                         const float* __restrict__ w, const int32_t* __restrict__ n_unique,
                                                         uint16_t* __restrict__ y, int T, int k, int H, int cap, int32_t* dev_err) {

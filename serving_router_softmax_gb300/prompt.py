@@ -248,7 +248,8 @@ def group_down_workspace_bytes(layer: ExpertLayer, T: int, k: int) -> int:
 def group_down(h: torch.Tensor, layer: ExpertLayer, union: Dict[str, torch.Tensor], w: torch.Tensor, y: Optional[torch.Tensor] = None,
                workspace: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y [T, H] bf16 = sum_j w[t, j] * (W_down h[inv[t, j]]): ``h`` [T * k, I] bf16 in the groups' order (``group_gate_up``'s),
-    ``w`` [T, k] fp32 routing weights."""
+    ``w`` [T, k] fp32 routing weights.  The terms are rounded to bf16 before they are summed in fp32: ``y`` is off by up to
+    2^-8 of the sum of their sizes (``verify_ffn`` keeps them in fp32)."""
     dev = h.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(dev, stream, lambda: group_down(h, layer, union, w, y, workspace, dev_err))

@@ -134,3 +134,35 @@ def test_rotate_in_place_in_one_buffer(mv):  # noqa: F811
         want, held = mv.rotate(rot, q, k, pos), v.clone()
         got = mv.rotate(rot, q, k, pos, out_q=q, out_k=k)
         assert got[0].data_ptr() == q.data_ptr() and torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(v, held)
+
+
+# ------------------------------------------------------------------ sums whose terms cancel
+@pytest.mark.parametrize("tiled", [False, True])
+def test_group_down_terms_that_cancel(mv, tiled):  # noqa: F811
+    """Two experts that are nearly alike, with weights of 1 and -1: an output is off by 2^-8 of its terms' sizes and of itself."""
+    g = gen(101)
+    T, H, I, E, k = 400, 256, 320, 4, 2
+    wg, wd = randn(g, E, 2 * I, H, std=H ** -0.5), randn(g, E, H, I, std=I ** -0.5)
+    wg[1::2], wd[1::2] = wg[::2], (wd[::2].float() * (1 + 2.0 ** -6)).to(torch.bfloat16)
+    layer = mv.ExpertLayer(wg, wd, "bf16")
+    if tiled:
+        layer = mv.pack_tiled(layer)
+    pair = 2 * torch.randint(0, E // 2, (T, 1), generator=g, device="cuda")
+    ids = torch.cat([pair, pair + 1], 1).to(torch.int32)
+    w = torch.tensor([[1.0, -1.0]], device="cuda").repeat(T, 1)
+    err = mv.new_dev_err()
+    u = mv.union_permute(ids, E, dev_err=err)
+    h = mv.group_gate_up(randn(g, T, H), layer, u, k, dev_err=err)
+    y = mv.group_down(h, layer, u, w, dev_err=err)
+    assert err.item() == 0
+    want, size, sums = (torch.zeros((T, H), dtype=torch.float64, device="cuda") for _ in range(3))
+    place = u["inv"].long().view(T, k)
+    for e in range(E):
+        t, j = torch.nonzero(ids == e, as_tuple=True)
+        hd, wt = h[place[t, j]].double(), wd[e].double()
+        want[t] += w[t, j].double()[:, None] * (hd @ wt.t())
+        size[t] += (hd @ wt.t()).abs()
+        sums[t] += hd.abs() @ wt.abs().t()
+    assert want.abs().sum() < 0.05 * size.sum()
+    # products of I terms in fp32; each rounded to bf16; their sum of k in fp32; the result rounded
+    within(y, want, (1 + BF) * ((BF + k * F32) * size + (1 + BF) * I * F32 * sums) + BF * want.abs(), "y")
