@@ -166,3 +166,86 @@ def test_group_down_terms_that_cancel(mv, tiled):  # noqa: F811
     assert want.abs().sum() < 0.05 * size.sum()
     # products of I terms in fp32; each rounded to bf16; their sum of k in fp32; the result rounded
     within(y, want, (1 + BF) * ((BF + k * F32) * size + (1 + BF) * I * F32 * sums) + BF * want.abs(), "y")
+
+
+# ------------------------------------------------------------------ beside the cache's attention and the verify step
+def test_prompt_attend_and_the_cache_give_the_same(mv):  # noqa: F811
+    """A prompt through both attentions: outputs and log-sums are as near each other as each one's roundings, and the exact
+    difference that rounding the held values to bf16 makes, allow."""
+    from oracle import kv_cache as okv
+    g = gen(111)
+    T, Hq, Hkv, D, page = 300, 8, 2, 128, 64
+    q, k, v = randn(g, T, Hq, D), randn(g, T, Hkv, D), randn(g, T, Hkv, D)
+    cache = mv.Kv4Cache.new(8, Hkv, page, D, 1, 6)
+    cache.table[0] = torch.tensor([5, 0, 7, 2, 1, 3], dtype=torch.int32, device="cuda")
+    i = torch.arange(T, dtype=torch.int32, device="cuda")
+    mv.kv4_append(cache, k, v, torch.zeros_like(i), i)
+    kh, vh = mv.kv4_read(cache, torch.zeros_like(i), i)
+    st = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    out, lse = mv.prompt_attend(q, kh, vh, st)
+    o4, l4 = mv.kv4_attend(cache, q, st, torch.zeros(1, dtype=torch.int32, device="cuda"), T)
+    mine = attend_exact(q, kh, vh, [0, T], D ** -0.5)
+    pages = okv.Pages(cache.pages.cpu().numpy(), cache.table.cpu().numpy(), page, D)
+    theirs = okv.attend(pages, q.float().cpu().numpy(), [0, T], [0], D ** -0.5)
+    want, z, ot, lt = (torch.from_numpy(theirs[n]).cuda() for n in (0, 1, 3, 4))
+    within(out, mine[0], mine[2], "prompt_attend")
+    within(o4, want, ot, "kv4_attend")
+    within(out, o4.double(), mine[2] + ot + (mine[0] - want).abs(), "out")
+    within(lse, l4.double(), mine[3] + lt + (mine[1] - z).abs(), "lse")
+    # the bounds tell a key more or less: they are far below what the last key of a row is worth
+    assert (mine[3] + lt + (mine[1] - z).abs()).max() < 2.0 ** -6 and (lse - l4).abs().max() < 2.0 ** -6
+
+
+def test_the_step_after_a_prompts_pass(mv):  # noqa: F811
+    """The keys and values that a pass has written are in their slots, and the next step's tokens attend over them."""
+    from oracle import kv_cache as okv
+    lengths, Hq, Hkv, D = [150, 1, 64, 333], 8, 2, 64
+    pr = Prompt(mv, 32, lengths)
+    k = pr.run()[1]
+    v = pr.qkv[:, Hq + Hkv:]
+    # the same rows in a cache of other pages
+    other = mv.Kv4Cache.new(4 * 12, Hkv, 32, D, 4, 12)
+    other.table.copy_(torch.arange(48, dtype=torch.int32).flip(0).view(4, 12))
+    held = mv.kv4_append(other, k, v, pr.seq, pr.slot, held=True)
+    assert all(torch.equal(a, b) for a, b in zip(mv.kv4_read(pr.cache, pr.seq, pr.slot), held))
+    g = gen(112)
+    qkv, four = randn(g, 4, Hq + 2 * Hkv, D), torch.arange(5, dtype=torch.int32, device="cuda")
+    base = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    pos = torch.stack([base, base + 7, base + 9]).contiguous()
+    q, k = mv.rotate(pr.rot, qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], pos)
+    mv.kv4_append(pr.cache, k, qkv[:, Hq + Hkv:], four[:4], base)
+    out, lse = mv.kv4_attend(pr.cache, q, four, base, 1)
+    pages = okv.Pages(pr.cache.pages.cpu().numpy(), pr.cache.table.cpu().numpy(), 32, D)
+    want, z, _, ot, lt, _ = okv.attend(pages, q.float().cpu().numpy(), range(5), lengths, D ** -0.5)
+    assert np.all(np.abs(out.float().cpu().numpy() - want) <= ot) and np.all(np.abs(lse.cpu().numpy() - z) <= lt)
+
+
+# ------------------------------------------------------------------ the largest sizes
+@pytest.mark.parametrize("Hq,Hkv,D,lengths", [
+    (1, 1, 64, [9001]), (2, 1, 128, [6007, 3]), (3, 1, 64, [4097]),                       # long sequences
+    (2, 1, 64, [(i * 29) % 11 for i in range(2048)]), (4, 4, 128, [(i * 5) % 3 for i in range(2048)]),  # as many as are taken
+    (1024, 8, 64, [3, 70]), (1024, 1024, 128, [40, 91]), (1024, 512, 64, [129]),          # query heads
+])
+def test_prompt_attend_largest(mv, Hq, Hkv, D, lengths):  # noqa: F811
+    g = gen(sum(lengths) + Hq)
+    T = sum(lengths) + 3
+    attend_check(mv, randn(g, T, Hq, D), randn(g, T, Hkv, D), randn(g, T, Hkv, D), lengths, D ** -0.5, first=1)
+
+
+@pytest.mark.parametrize("tiled", [False, True])
+@pytest.mark.parametrize("T,H,I,E,k", [(300, 3264, 192, 3, 2), (130, 192, 3264, 2, 1), (40, 3264, 3264, 2, 1)])
+def test_group_products_of_odd_row_tiles(mv, T, H, I, E, k, tiled):  # noqa: F811
+    """Matrices of an odd number of row tiles, the last one part of a tile."""
+    g = gen(T + H)
+    (wg, wd), layer = make_layer(mv, g, H, I, E, tiled)
+    x, ids = randn(g, T, H), make_ids(g, T, E, k, 0.3)
+    err = mv.new_dev_err()
+    u = mv.union_permute(ids, E, dev_err=err)
+    h = mv.group_gate_up(x, layer, u, k, dev_err=err)
+    want, tol = gate_up_exact(x, wg, ids, u["inv"])
+    within(h, want, tol, "gate_up")
+    p = torch.rand((T, k), generator=g, device="cuda") - 0.3
+    y = mv.group_down(h, layer, u, p, dev_err=err)
+    want, tol = down_exact(h, wd, ids, u["inv"], p)
+    within(y, want, tol, "down")
+    assert err.item() == 0
