@@ -174,7 +174,8 @@ int moe_route(const float* logits, const float* w_conf, const moe_route_cfg* cfg
  *   perm_slot   [T*k] int32 out: the slot j with ids[t, j] == expert.
  *   inv         [T*k] int32 out: inv[t*k + j] = perm position of (t, j).
  *   reuse_ratio [1] fp32 out: U / (T*k) rounded once to fp32; 0 when T == 0.
- * Limits: 1 <= k <= 16, 1 <= E <= 1024, T*k <= 65536, T*E <= 1048576.
+ * Limits: 1 <= k <= 16, 1 <= E <= 1024, T*k <= 65536, T*ceil(E/32) <= 32768.
+ * (One CTA, made for a verify step's tokens: its time grows with T*T*k.)
  * Device errors: MOE_DEV_BAD_ID, MOE_DEV_DUP_ID (then n_unique = 0).
  */
 int moe_union_permute(const int32_t* ids, int32_t T, int32_t k, int32_t E,
@@ -804,7 +805,7 @@ int moe_rotate(const void* q, const void* k, const int32_t* pos, const uint64_t*
  *               cfg says, 16-byte aligned.
  *   start       [n_seq + 1] int32: sequence s is rows start[s] .. start[s + 1] - 1
  *               (none is fine).  Rows before start[0] and from start[n_seq] on
- *               are not read, and their outputs are left as they are.
+ *               have no effect, and their outputs are left as they are.
  *   out         [T, n_q_heads, D] bf16 out.
  *   lse         [T, n_q_heads] fp32 out or NULL; both apart from the inputs and
  *               from each other (MOE_ERR_ARG).
@@ -833,10 +834,13 @@ int moe_prompt_attend(const void* q, const void* k, const void* v, const int32_t
 
 /* moe_group_gate_up -- h[p] = silu(W_gate,e x_t) * (W_up,e x_t) for every row p
  * of the union's groups (offsets[u] <= p < offsets[u+1], e = unique[u],
- * t = perm_token[p]): the first half of moe_verify_ffn, for any number of tokens.
+ * t = perm_token[p]): the first half of moe_verify_ffn, for a prompt's tokens.
  *   x           [T, H] bf16.
  *   lw          a bf16 layer, either layout, with or without a pool.
- *   n_unique .. perm_token   as written by moe_union_permute.
+ *   n_unique .. perm_token   as written by moe_union_permute, whose limits are
+ *               tighter than this call's (8,192 tokens of 128 experts): more tokens
+ *               go through in parts, each with a union of its own, or with a union
+ *               in the same form from elsewhere.
  *   h           [T * k, I] bf16 out, rows in the groups' order, apart from x
  *               (MOE_ERR_ARG); rows that no group holds are left as they are.
  * fp32 accumulation on the tensor cores, one rounding per output.

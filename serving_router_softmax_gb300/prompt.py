@@ -222,7 +222,8 @@ def _layer_on(dev: int, layer: ExpertLayer, head: tuple):
 def group_gate_up(x: torch.Tensor, layer: ExpertLayer, union: Dict[str, torch.Tensor], k: int, out: Optional[torch.Tensor] = None,
                   dev_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """h [T * k, I] bf16: silu(W_gate x) * (W_up x) for every row of the groups of ``union`` (``union_permute``'s, for the
-    same T tokens' k experts), in the groups' order.  ``x`` [T, H] bf16, any T; ``layer``: bf16, either layout."""
+    same T tokens' k experts), in the groups' order.  ``x`` [T, H] bf16; ``layer``: bf16, either layout.  T * k may be up to
+    2^22; ``union_permute`` takes T * k <= 65536 and T * ceil(E / 32) <= 32768, so more tokens go through in parts."""
     dev = x.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(dev, stream, lambda: group_gate_up(x, layer, union, k, out, dev_err))

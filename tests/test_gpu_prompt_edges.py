@@ -249,3 +249,36 @@ def test_group_products_of_odd_row_tiles(mv, T, H, I, E, k, tiled):  # noqa: F81
     want, tol = down_exact(h, wd, ids, u["inv"], p)
     within(y, want, tol, "down")
     assert err.item() == 0
+
+
+@pytest.mark.parametrize("T,E,k", [(8192, 128, 8), (4096, 256, 16), (32768, 8, 2)])
+def test_the_largest_union(mv, T, E, k):  # noqa: F811
+    """Routing, union and products of as many tokens as union_permute takes; a token more is refused, and goes in a second part."""
+    g = gen(E)
+    H, I = 64, 64
+    (wg, wd), layer = make_layer(mv, g, H, I, E, True)
+    x, gate = randn(g, T + 1, H), randn(g, E, H, std=0.1)
+    err = mv.new_dev_err()
+
+    def experts(x):
+        ids, w = mv.route(mv.router_logits(x, gate), k, dev_err=err)
+        u = mv.union_permute(ids, E, dev_err=err)
+        h = mv.group_gate_up(x, layer, u, k, dev_err=err)
+        return ids, w, u, h, mv.group_down(h, layer, u, w, dev_err=err)
+
+    ids, w, u, h, y = experts(x[:T])
+    assert err.item() == 0
+    order = torch.argsort(ids.view(-1).long(), stable=True)
+    assert torch.equal(u["perm_token"].long(), order // k) and torch.equal(u["perm_slot"].long(), order % k)
+    want, tol = gate_up_exact(x[:T], wg, ids, u["inv"])
+    within(h, want, tol, "gate_up")
+    want, tol = down_exact(h, wd, ids, u["inv"], w)
+    within(y, want, tol, "down")
+    with pytest.raises(mv.MoEError):
+        experts(x)
+    half = T // 2
+    for part in (x[:half], x[half:]):
+        ids, w, u, h, y = experts(part)
+        want, tol = down_exact(h, wd, ids, u["inv"], w)
+        within(y, want, tol, "a part")
+    assert err.item() == 0
