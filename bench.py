@@ -1335,6 +1335,18 @@ def reference(args, rank, ws):
     }
 
 
+LONG = ("workloads", "cost_model", "residency")
+
+
+def emit(res):
+    """The result as one JSON line of some KB on standard output, the last that is written; the long records, which are measured
+    beside it, as one line each on standard error before it.  (With them it was 25 KB, and a reader of the output's end saw no line.)"""
+    for k in LONG:
+        if res.get(k) is not None:
+            print(json.dumps({k: res[k]}), file=sys.stderr, flush=True)
+    print(json.dumps({k: v for k, v in res.items() if k not in LONG}), flush=True)
+
+
 def main():
     args = parse()
     if args.impl == "reference":
@@ -1342,7 +1354,7 @@ def main():
         rank = int(os.environ.get("RANK", "0"))
         res = reference(args, rank, ws)
         if res is not None:
-            print(json.dumps(res))
+            emit(res)
         return
     rank, ws, local = dist_setup(args.gpus)
     res, wl, cfg, y_first = ours(args, rank, ws, local)
@@ -1355,7 +1367,7 @@ def main():
                                "parity_layer0": ffn_errors(y_first.numpy().astype(np.float64), y_oracle,
                                                            cfg.dtype)}
     if rank == 0:
-        print(json.dumps(res))
+        emit(res)
     if ws > 1:
         import torch.distributed as dist
         dist.destroy_process_group()
