@@ -99,7 +99,9 @@ class Rotary:
     def standard(cls, head_dim: int, base: float = 10000.0, sections: Optional[Sequence[int]] = None,
                  rotary_dim: Optional[int] = None, interleaved: bool = False, device="cuda") -> "Rotary":
         """freqs[i] = base ** (-2 i / rotary_dim); ``sections``: how many pairs, in order, take each axis."""
-        n = (head_dim if rotary_dim is None else rotary_dim) // 2
+        n, odd = divmod(head_dim if rotary_dim is None else rotary_dim, 2)
+        if odd:
+            raise MoEError("rotary_dim: expected an even number")
         if sections is not None and sum(sections) != n:
             raise MoEError(f"sections: expected a sum of {n}")
         axes = None if sections is None else [a for a, m in enumerate(sections) for _ in range(m)]

@@ -7,6 +7,7 @@ from test_kv4_binding import Tensor, cache_on, i32, queries
 torch = pytest.importorskip("torch")
 
 from serving_router_softmax_gb300 import kv4, prompt  # noqa: E402
+from serving_router_softmax_gb300.api import MoEError  # noqa: E402
 
 
 def test_numbers_are_taken_as_they_are_now(machine):  # noqa: F811
@@ -29,3 +30,11 @@ def test_numbers_are_taken_as_they_are_now(machine):  # noqa: F811
         back.fill_(value)
         prompt.rotate(Rot(0), q, k, pos, inverse=back)
         assert machine.lib.calls[-1][2][5]._obj.inverse == value
+
+
+def test_an_odd_number_of_turned_dimensions_is_refused():
+    """(Not rounded down to the pairs that fit: their frequencies would be another embedding's.)"""
+    for odd in (33, 49, 17):
+        with pytest.raises(MoEError):
+            prompt.Rotary.standard(64, rotary_dim=odd, device="cpu")
+    assert prompt.Rotary.standard(64, rotary_dim=48, device="cpu").rotary_dim == 48
