@@ -817,7 +817,7 @@ int moe_rotate(const void* q, const void* k, const int32_t* pos, const uint64_t*
  * any gives zeros and -inf).  In a value it makes that dimension of out NaN or infinite for the
  * rows that see it.  What a row does not see has no effect on it.
  * A row whose largest score times log2(e) is 2^31 or more away from 0 is NaN, out
- * and lse.  (From 2^24 on an fp32 score no longer tells powers of e apart.)
+ * and lse; q . k is summed in fp32 before it is scaled.  (From 2^24 on an fp32 score no longer tells powers of e apart.)
  * Results do not depend on timing.
  * Limits: D = 64 or 128; 0 <= T <= 2^24, n_seq <= 2048; n_q_heads a multiple of
  * n_kv_heads, at most 128 times as many, n_q_heads <= 1024; strides positive multiples

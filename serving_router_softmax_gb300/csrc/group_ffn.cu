@@ -16,7 +16,9 @@
 // for 65,536 rows of 4096 x 1536 matrices; four warps: 1.31; rows copied side by side
 // first: 0.1 ms for that alone.)
 //
-// What bounds full tiles is loading: 32 KB a stage and CTA, from L2.
+// What bounds full tiles is loading, 32 KB a stage and CTA from L2.  (Rows loaded once for
+// two pairs and sent to both took gate/up from 1.11 to 1.01 ms; a copy to several CTAs must
+// not read another GPU's memory, which a caller's pointers may be.)
 //
 // Persistent: pair i takes tiles i, i + pairs, ..., in an order that has a
 // matrix's rows go over all of their group's chunks before the next rows come,
@@ -27,9 +29,9 @@
 // CTA) issues the products, warps 2-5 take the sums out, the warps from 6 on load
 // rows.  Every wait is bounded.
 //
-// 8192 tokens of 8 of 128 experts, 4096 x 1536: gate/up 1.01 ms, 1630 TFLOP/s (tensor
-// pipe 76% busy); down 0.54 ms, 1520, and 0.09 for the sum.  300 tokens: gate/up
-// 0.47 ms, the weights' bytes at 6.9 TB/s.
+// 8192 tokens of 8 of 128 experts, 4096 x 1536, on the device: gate/up 1.11 ms, 1480
+// TFLOP/s; down 0.54 ms, 1520, and 0.09 for the sum.  (Tensor pipe 66% and 70% busy with
+// 4096 tokens of 2 of 16.)  300 tokens: gate/up 0.465 ms, the weights' bytes at 6.9 TB/s.
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -41,8 +41,8 @@
 //
 // Bound by a step's chain: at D = 128 some 3050 cycles, 2050 of them products of the
 // two tiles, which take turns; at D = 64 2600 against 1110.  2 prompts of up to 12,001
-// tokens, 32 query heads on 8, D 128: 1.28 ms, 1597 TFLOP/s; 24 ragged ones of up to
-// 1500, 64 heads on 4: 0.36 ms, 1069; one of 8192, 32 on 8, D 64: 0.29 ms, 943.
+// tokens, 32 query heads on 8, D 128: 1.28 ms, 1590 TFLOP/s; 24 ragged ones of up to
+// 1500, 64 heads on 4: 0.36 ms, 1060; one of 8192, 32 on 8, D 64: 0.30 ms, 920.
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -7,7 +7,7 @@
 // rounded to fp32, so cosine and sine are as good at position 2^31 as at 0.
 //
 // Bound by memory: every value is read and written once (8192 tokens of 40 heads
-// of 128 in bf16: 28 us, 5.9 TB/s).  A block takes a few tokens, as many as give each
+// of 128 in bf16: 29 us, 5.8 TB/s).  A block takes a few tokens, as many as give each
 // of its threads one cosine and sine to make, and these go to shared memory for all
 // of the tokens' heads (each thread making its own for up to 8 heads: 40 us).  A
 // thread keeps its 16 bytes' place in a row and steps through rows, two units' loads
