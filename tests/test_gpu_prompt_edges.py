@@ -282,3 +282,50 @@ def test_the_largest_union(mv, T, E, k):  # noqa: F811
         want, tol = down_exact(h, wd, ids, u["inv"], w)
         within(y, want, tol, "a part")
     assert err.item() == 0
+
+
+@pytest.mark.parametrize("T,H,I,E,k,tiled", [(500, 64, 128, 1024, 16, True), (90, 128, 64, 1000, 8, False), (3, 1 << 18, 64, 2, 1, False),
+                                             (2, 64, 1 << 18, 2, 2, True)])
+def test_group_products_of_many_experts_and_long_rows(mv, T, H, I, E, k, tiled):  # noqa: F811
+    g = gen(T + E)
+    (wg, wd), layer = make_layer(mv, g, H, I, E, tiled)
+    x, ids = randn(g, T, H), make_ids(g, T, E, k, 0.0)
+    err = mv.new_dev_err()
+    u = mv.union_permute(ids, E, dev_err=err)
+    h = mv.group_gate_up(x, layer, u, k, dev_err=err)
+    want, tol = gate_up_exact(x, wg, ids, u["inv"])
+    within(h, want, tol, "gate_up")
+    p = torch.rand((T, k), generator=g, device="cuda") - 0.3
+    y = mv.group_down(h, layer, u, p, dev_err=err)
+    want, tol = down_exact(h, wd, ids, u["inv"], p)
+    within(y, want, tol, "down")
+    assert err.item() == 0
+
+
+def test_rotate_largest(mv):  # noqa: F811
+    """As many tokens, and as many heads, as are taken: rows far behind the first turn as they do alone."""
+    g = gen(121)
+    for T, Hq, Hk, D in ((1 << 24, 1, 0, 16), (1 << 24, 1, 1, 64), (40, 4000, 96, 64), (70001, 300, 20, 128)):
+        rot = mv.Rotary.standard(D)
+        x = randn(g, T, Hq + Hk, D)
+        pos = torch.arange(T, dtype=torch.int32, device="cuda") * 3
+        q, k = mv.rotate(rot, x[:, :Hq], x[:, Hq:] if Hk else None, pos)
+        for part in (slice(0, 30), slice(T // 2, T // 2 + 20), slice(T - 33, T)):
+            a, b = mv.rotate(rot, x[part, :Hq], x[part, Hq:] if Hk else None, pos[part])
+            assert torch.equal(q[part], a) and (b is None or torch.equal(k[part], b)), (T, part)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,n", [(1 << 24, 1, 1, 64, 8192), (40000, 1024, 8, 128, 100)])
+def test_prompt_attend_most_rows(mv, T, Hq, Hkv, D, n):  # noqa: F811
+    """As many tokens as are taken, and outputs of more than 2^31 values."""
+    g = gen(122)
+    q, k, v = randn(g, T, Hq, D), randn(g, T, Hkv, D), randn(g, T, Hkv, D)
+    start = list(range(0, T + 1, n))
+    err = mv.new_dev_err()
+    out, lse = mv.prompt_attend(q, k, v, torch.tensor(start, dtype=torch.int32, device="cuda"), dev_err=err)
+    assert err.item() == 0
+    for s in (0, len(start) // 2, len(start) - 2):
+        at = slice(start[s], start[s + 1])
+        want, z, ot, lt = attend_exact(q[at], k[at], v[at], [0, n], D ** -0.5)
+        within(lse[at], z, lt, s)
+        within(out[at], want, ot, s)
